@@ -38,6 +38,9 @@ EXPORTED = ("nvfp4_scale_bytes", "nvfp4_quantize_workspace_size", "nvfp4_quantiz
             "nvfp4_requantize_col_rht", "nvfp4_gemm_lora", "nvfp4_gemm_lora_workspace_size",
             "nvfp4_gemm_amax", "nvfp4_quantize_row_col_rht_amax", "nvfp4_gemm_axpby",
             "nvfp4_newton_schulz_workspace_size", "nvfp4_newton_schulz_step",
+            "nvfp4_qk_norm_rope", "nvfp4_qk_norm_rope_backward_workspace_size", "nvfp4_qk_norm_rope_backward",
+            "nvfp4_attention_spans", "nvfp4_attention", "nvfp4_attention_backward_workspace_size",
+            "nvfp4_attention_backward",
             "nvfp4_testing_arm_gemm_timeout", "nvfp4_testing_bounds_violations",
             "nvfp4_testing_bounds_shrink")
 
@@ -47,6 +50,16 @@ class nvfp4_tensor(ctypes.Structure):
                 ("amax", ctypes.c_void_p), ("global_scale", ctypes.c_void_p),
                 ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
                 ("ld_codes", ctypes.c_int64)]
+
+
+class nvfp4_heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("ld_token", ctypes.c_int64), ("ld_head", ctypes.c_int64)]
+
+
+class nvfp4_attention_desc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("slopes", ctypes.c_void_p), ("spans", ctypes.c_void_p)]
 
 
 class NVFP4Error(RuntimeError):
@@ -101,6 +114,21 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.nvfp4_newton_schulz_workspace_size.restype = sz
     L.nvfp4_newton_schulz_step.argtypes = [vp, i64, i64, i64, f32, f32, f32, u16, vp, i64, vp, sz, vp]
     L.nvfp4_newton_schulz_step.restype = i32
+    hp, dp = ctypes.POINTER(nvfp4_heads), ctypes.POINTER(nvfp4_attention_desc)
+    c32 = ctypes.c_int32
+    rope = [vp, i64, i64, c32, c32, c32, vp, vp, f32, vp, vp, i64, c32, c32, vp]
+    L.nvfp4_qk_norm_rope.argtypes = rope + [hp, hp, vp]
+    L.nvfp4_qk_norm_rope.restype = i32
+    L.nvfp4_qk_norm_rope_backward_workspace_size.argtypes = [c32]
+    L.nvfp4_qk_norm_rope_backward_workspace_size.restype = sz
+    L.nvfp4_qk_norm_rope_backward.argtypes = [hp, hp] + rope + [vp, i64, vp, vp, vp, sz, vp]
+    L.nvfp4_qk_norm_rope_backward.restype = i32
+    L.nvfp4_attention_spans.argtypes, L.nvfp4_attention_spans.restype = [vp, i64, vp, c32, i64, vp, vp], i32
+    L.nvfp4_attention.argtypes, L.nvfp4_attention.restype = [dp, hp, hp, hp, hp, vp, vp], i32
+    L.nvfp4_attention_backward_workspace_size.argtypes = [i64, c32]
+    L.nvfp4_attention_backward_workspace_size.restype = sz
+    L.nvfp4_attention_backward.argtypes = [dp, hp, hp, hp, hp, hp, vp, hp, hp, hp, vp, sz, vp]
+    L.nvfp4_attention_backward.restype = i32
     L.nvfp4_dequantize.argtypes = [tp, vp, i64, i32, vp]
     L.nvfp4_dequantize.restype = i32
     L.nvfp4_status_string.argtypes, L.nvfp4_status_string.restype = [i32], ctypes.c_char_p
@@ -208,6 +236,46 @@ def nvfp4_newton_schulz_step(X, m, n, ldx, a, b, c, rht_sign_mask, X_out, ld_out
 
 def nvfp4_dequantize(q, y, ldy, out_dtype, stream):
     return load().nvfp4_dequantize(_ref(q), y, ldy, out_dtype, stream)
+
+
+def nvfp4_qk_norm_rope(qkv, ld_qkv, tokens, q_heads, kv_heads, head_dim, q_weight, k_weight, eps, cos, sin,
+                       table_rows, rotary_dim, interleaved, positions, q_out, k_out, stream):
+    """RMS norm of every query and key head with the position rotation in the same pass."""
+    return load().nvfp4_qk_norm_rope(qkv, ld_qkv, tokens, q_heads, kv_heads, head_dim, q_weight, k_weight, eps, cos,
+                                     sin, table_rows, rotary_dim, interleaved, positions, _ref(q_out), _ref(k_out),
+                                     stream)
+
+
+def nvfp4_qk_norm_rope_backward_workspace_size(head_dim):
+    return load().nvfp4_qk_norm_rope_backward_workspace_size(head_dim)
+
+
+def nvfp4_qk_norm_rope_backward(dq, dk, qkv, ld_qkv, tokens, q_heads, kv_heads, head_dim, q_weight, k_weight, eps,
+                                cos, sin, table_rows, rotary_dim, interleaved, positions, dqkv, ld_dqkv, dq_weight,
+                                dk_weight, workspace, workspace_bytes, stream):
+    """Gradients of nvfp4_qk_norm_rope's input columns and weights."""
+    return load().nvfp4_qk_norm_rope_backward(_ref(dq), _ref(dk), qkv, ld_qkv, tokens, q_heads, kv_heads, head_dim,
+                                              q_weight, k_weight, eps, cos, sin, table_rows, rotary_dim, interleaved,
+                                              positions, dqkv, ld_dqkv, dq_weight, dk_weight, workspace,
+                                              workspace_bytes, stream)
+
+
+def nvfp4_attention_spans(offsets, documents, prefix, causal, tokens, spans, stream):
+    """The key interval of every token of packed documents."""
+    return load().nvfp4_attention_spans(offsets, documents, prefix, causal, tokens, spans, stream)
+
+
+def nvfp4_attention(desc, q, k, v, out, lse, stream):
+    return load().nvfp4_attention(_ref(desc), _ref(q), _ref(k), _ref(v), _ref(out), lse, stream)
+
+
+def nvfp4_attention_backward_workspace_size(tokens, q_heads):
+    return load().nvfp4_attention_backward_workspace_size(tokens, q_heads)
+
+
+def nvfp4_attention_backward(desc, dout, q, k, v, out, lse, dq, dk, dv, workspace, workspace_bytes, stream):
+    return load().nvfp4_attention_backward(_ref(desc), _ref(dout), _ref(q), _ref(k), _ref(v), _ref(out), lse, _ref(dq),
+                                           _ref(dk), _ref(dv), workspace, workspace_bytes, stream)
 
 
 def nvfp4_status_string(status):

@@ -129,6 +129,83 @@ nvfp4::GemmOperand to_operand(const nvfp4_tensor* t) {
     return nvfp4::GemmOperand{t->codes, t->ld_codes, t->scales, t->global_scale, t->rows, t->cols};
 }
 
+// Head vectors of a call: [tokens][heads][head_dim] with positive strides.
+nvfp4_status check_heads(const nvfp4_heads* t, int32_t head_dim) {
+    if (!t || !t->data) return NVFP4_ERR_INVALID_ARG;
+    if (t->ld_token < head_dim || t->ld_head < head_dim) return NVFP4_ERR_SHAPE;
+    if (!aligned16(t->data) || t->ld_token % 8 != 0 || t->ld_head % 8 != 0) return NVFP4_ERR_ALIGNMENT;
+    return NVFP4_OK;
+}
+
+nvfp4::HeadsView to_heads(const nvfp4_heads* t) {
+    return nvfp4::HeadsView{static_cast<uint16_t*>(t->data), t->ld_token, t->ld_head};
+}
+
+constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 256;
+
+nvfp4_status check_head_shape(int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
+    if (tokens < 0 || tokens >= kMaxTokens || q_heads < 1 || kv_heads < 1) return NVFP4_ERR_SHAPE;
+    if (head_dim < 8 || head_dim > 128 || head_dim % 8 != 0) return NVFP4_ERR_SHAPE;
+    if (q_heads > 65535 || kv_heads > 65535) return NVFP4_ERR_UNSUPPORTED;
+    return NVFP4_OK;
+}
+
+// The arguments the two norm entry points share.
+nvfp4_status check_norm_rope(const nvfp4::NormRope& a) {
+    nvfp4_status s;
+    if ((s = check_head_shape(a.tokens, a.q_heads, a.kv_heads, a.head_dim)) != NVFP4_OK) return s;
+    if (a.rotary_dim < 0 || a.rotary_dim > a.head_dim || a.rotary_dim % 16 != 0) return NVFP4_ERR_SHAPE;
+    if (!std::isfinite(a.eps) || a.eps < 0.0f) return NVFP4_ERR_INVALID_ARG;
+    if (!a.q_weight || !a.k_weight) return NVFP4_ERR_INVALID_ARG;
+    if (!aligned16(a.q_weight) || !aligned16(a.k_weight)) return NVFP4_ERR_ALIGNMENT;
+    if (a.rotary_dim > 0) {
+        if (!a.cos || !a.sin) return NVFP4_ERR_INVALID_ARG;
+        if (a.table_rows < 1) return NVFP4_ERR_SHAPE;
+        if (!aligned16(a.cos) || !aligned16(a.sin)) return NVFP4_ERR_ALIGNMENT;
+        if (a.tokens > 0 && !a.positions) return NVFP4_ERR_INVALID_ARG;
+        if ((reinterpret_cast<uintptr_t>(a.positions) & 3u) != 0) return NVFP4_ERR_ALIGNMENT;
+    }
+    if (a.tokens > 0) {
+        if (!a.qkv) return NVFP4_ERR_INVALID_ARG;
+        if (a.ld_qkv < (int64_t)(a.q_heads + a.kv_heads) * a.head_dim) return NVFP4_ERR_SHAPE;
+        if (!aligned16(a.qkv) || a.ld_qkv % 8 != 0) return NVFP4_ERR_ALIGNMENT;
+    }
+    return NVFP4_OK;
+}
+
+// The arguments the two attention entry points share; *a gets the shape.
+nvfp4_status check_attention(const nvfp4_attention_desc* d, const nvfp4_heads* q, const nvfp4_heads* k,
+                             const nvfp4_heads* v, const nvfp4_heads* out, const float* lse, nvfp4::Attention* a) {
+    if (!d) return NVFP4_ERR_INVALID_ARG;
+    nvfp4_status s;
+    if ((s = check_head_shape(d->tokens, d->q_heads, d->kv_heads, d->head_dim)) != NVFP4_OK) return s;
+    if (d->q_heads % d->kv_heads != 0) return NVFP4_ERR_SHAPE;
+    if (!std::isfinite(d->scale) || !(d->scale > 0.0f) || !std::isfinite(d->softcap) || d->softcap < 0.0f)
+        return NVFP4_ERR_INVALID_ARG;
+    *a = nvfp4::Attention{};
+    a->tokens = d->tokens;
+    a->q_heads = d->q_heads;
+    a->kv_heads = d->kv_heads;
+    a->head_dim = d->head_dim;
+    a->scale = d->scale;
+    a->softcap = d->softcap;
+    a->slopes = d->slopes;
+    a->spans = d->spans;
+    if (d->tokens == 0) return NVFP4_OK;
+    if (!d->spans || !lse) return NVFP4_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(d->spans) & 7u) != 0 || (reinterpret_cast<uintptr_t>(d->slopes) & 3u) != 0 ||
+        (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
+        return NVFP4_ERR_ALIGNMENT;
+    for (const nvfp4_heads* t : {q, k, v, out})
+        if ((s = check_heads(t, d->head_dim)) != NVFP4_OK) return s;
+    a->q = to_heads(q);
+    a->k = to_heads(k);
+    a->v = to_heads(v);
+    a->out = to_heads(out);
+    a->lse = const_cast<float*>(lse);
+    return NVFP4_OK;
+}
+
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // Carves one [rows][cols] NVFP4 operand (codes with a 16-byte multiple row
@@ -468,6 +545,125 @@ nvfp4_status nvfp4_dequantize(const nvfp4_tensor* q, void* y, int64_t ldy, nvfp4
     return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
+nvfp4_status nvfp4_qk_norm_rope(const void* qkv, int64_t ld_qkv, int64_t tokens, int32_t q_heads, int32_t kv_heads,
+                                int32_t head_dim, const float* q_weight, const float* k_weight, float eps,
+                                const float* cos, const float* sin, int64_t table_rows, int32_t rotary_dim,
+                                int32_t interleaved, const int32_t* positions, const nvfp4_heads* q_out,
+                                const nvfp4_heads* k_out, nvfp4_stream_t stream) {
+    const ApiRange range("nvfp4_qk_norm_rope");
+    nvfp4::NormRope a{static_cast<const uint16_t*>(qkv), ld_qkv, tokens, q_heads, kv_heads, head_dim, rotary_dim,
+                      interleaved != 0, q_weight, k_weight, eps, cos, sin, table_rows, positions};
+    nvfp4_status s;
+    if ((s = check_norm_rope(a)) != NVFP4_OK) return s;
+    if (tokens == 0) return NVFP4_OK;
+    if ((s = check_heads(q_out, head_dim)) != NVFP4_OK) return s;
+    if ((s = check_heads(k_out, head_dim)) != NVFP4_OK) return s;
+    a.q = to_heads(q_out);
+    a.k = to_heads(k_out);
+    return nvfp4::launch_norm_rope(a, false, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? NVFP4_OK
+                                                                                                    : NVFP4_ERR_CUDA;
+}
+
+size_t nvfp4_qk_norm_rope_backward_workspace_size(int32_t head_dim) {
+    if (head_dim <= 0) return 0;
+    return (size_t)nvfp4::kNormRopeMaxBlocks * 2 * (size_t)head_dim * sizeof(float);
+}
+
+nvfp4_status nvfp4_qk_norm_rope_backward(const nvfp4_heads* dq, const nvfp4_heads* dk, const void* qkv,
+                                         int64_t ld_qkv, int64_t tokens, int32_t q_heads, int32_t kv_heads,
+                                         int32_t head_dim, const float* q_weight, const float* k_weight, float eps,
+                                         const float* cos, const float* sin, int64_t table_rows, int32_t rotary_dim,
+                                         int32_t interleaved, const int32_t* positions, void* dqkv, int64_t ld_dqkv,
+                                         float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes,
+                                         nvfp4_stream_t stream) {
+    const ApiRange range("nvfp4_qk_norm_rope_backward");
+    nvfp4::NormRope a{static_cast<const uint16_t*>(qkv), ld_qkv, tokens, q_heads, kv_heads, head_dim, rotary_dim,
+                      interleaved != 0, q_weight, k_weight, eps, cos, sin, table_rows, positions};
+    nvfp4_status s;
+    if ((s = check_norm_rope(a)) != NVFP4_OK) return s;
+    if (!dq_weight || !dk_weight) return NVFP4_ERR_INVALID_ARG;
+    if (((reinterpret_cast<uintptr_t>(dq_weight) | reinterpret_cast<uintptr_t>(dk_weight)) & 3u) != 0)
+        return NVFP4_ERR_ALIGNMENT;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (tokens == 0)   // an empty sum
+        return cudaMemsetAsync(dq_weight, 0, (size_t)head_dim * sizeof(float), st) == cudaSuccess &&
+                       cudaMemsetAsync(dk_weight, 0, (size_t)head_dim * sizeof(float), st) == cudaSuccess
+                   ? NVFP4_OK
+                   : NVFP4_ERR_CUDA;
+    if ((s = check_heads(dq, head_dim)) != NVFP4_OK) return s;
+    if ((s = check_heads(dk, head_dim)) != NVFP4_OK) return s;
+    if (!dqkv) return NVFP4_ERR_INVALID_ARG;
+    if (ld_dqkv < (int64_t)(q_heads + kv_heads) * head_dim) return NVFP4_ERR_SHAPE;
+    if (!aligned16(dqkv) || ld_dqkv % 8 != 0) return NVFP4_ERR_ALIGNMENT;
+    if (dqkv == qkv && ld_dqkv != ld_qkv) return NVFP4_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < nvfp4_qk_norm_rope_backward_workspace_size(head_dim))
+        return NVFP4_ERR_WORKSPACE;
+    a.q = to_heads(dq);
+    a.k = to_heads(dk);
+    a.dqkv = static_cast<uint16_t*>(dqkv);
+    a.ld_dqkv = ld_dqkv;
+    a.dq_weight = dq_weight;
+    a.dk_weight = dk_weight;
+    a.partials = static_cast<float*>(workspace);
+    return nvfp4::launch_norm_rope(a, true, st) == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+}
+
+nvfp4_status nvfp4_attention_spans(const int32_t* offsets, int64_t documents, const int32_t* prefix, int32_t causal,
+                                   int64_t tokens, int32_t* spans, nvfp4_stream_t stream) {
+    const ApiRange range("nvfp4_attention_spans");
+    if (documents < 0 || tokens < 0 || tokens >= kMaxTokens) return NVFP4_ERR_SHAPE;
+    if (tokens == 0) return NVFP4_OK;
+    if (!spans || (documents > 0 && !offsets)) return NVFP4_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(spans) & 7u) != 0 ||
+        ((reinterpret_cast<uintptr_t>(offsets) | reinterpret_cast<uintptr_t>(prefix)) & 3u) != 0)
+        return NVFP4_ERR_ALIGNMENT;
+    return nvfp4::launch_attention_spans(offsets, documents, prefix, causal != 0, tokens, spans,
+                                         reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? NVFP4_OK
+               : NVFP4_ERR_CUDA;
+}
+
+nvfp4_status nvfp4_attention(const nvfp4_attention_desc* desc, const nvfp4_heads* q, const nvfp4_heads* k,
+                             const nvfp4_heads* v, const nvfp4_heads* out, float* lse, nvfp4_stream_t stream) {
+    const ApiRange range("nvfp4_attention");
+    nvfp4::Attention a;
+    nvfp4_status s;
+    if ((s = check_attention(desc, q, k, v, out, lse, &a)) != NVFP4_OK) return s;
+    if (a.tokens == 0) return NVFP4_OK;
+    return nvfp4::launch_attention(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? NVFP4_OK
+                                                                                             : NVFP4_ERR_CUDA;
+}
+
+size_t nvfp4_attention_backward_workspace_size(int64_t tokens, int32_t q_heads) {
+    if (tokens <= 0 || q_heads <= 0) return 0;
+    return nvfp4::attention_backward_workspace_bytes(tokens, q_heads);
+}
+
+nvfp4_status nvfp4_attention_backward(const nvfp4_attention_desc* desc, const nvfp4_heads* dout, const nvfp4_heads* q,
+                                      const nvfp4_heads* k, const nvfp4_heads* v, const nvfp4_heads* out,
+                                      const float* lse, const nvfp4_heads* dq, const nvfp4_heads* dk,
+                                      const nvfp4_heads* dv, void* workspace, size_t workspace_bytes,
+                                      nvfp4_stream_t stream) {
+    const ApiRange range("nvfp4_attention_backward");
+    nvfp4::Attention a;
+    nvfp4_status s;
+    if ((s = check_attention(desc, q, k, v, out, lse, &a)) != NVFP4_OK) return s;
+    if (a.tokens == 0) return NVFP4_OK;
+    for (const nvfp4_heads* t : {dout, dq, dk, dv})
+        if ((s = check_heads(t, a.head_dim)) != NVFP4_OK) return s;
+    if (!workspace || !aligned16(workspace) ||
+        workspace_bytes < nvfp4_attention_backward_workspace_size(a.tokens, a.q_heads))
+        return NVFP4_ERR_WORKSPACE;
+    a.dout = to_heads(dout);
+    a.dq = to_heads(dq);
+    a.dk = to_heads(dk);
+    a.dv = to_heads(dv);
+    a.workspace = static_cast<float*>(workspace);
+    return nvfp4::launch_attention_backward(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? NVFP4_OK
+               : NVFP4_ERR_CUDA;
+}
+
 const char* nvfp4_status_string(nvfp4_status status) {
     switch (status) {
         case NVFP4_OK: return "NVFP4_OK";
@@ -495,7 +691,9 @@ nvfp4_status nvfp4_testing_bounds_violations(uint64_t* count) {
     uint64_t n = 0;
     if (nvfp4::quantize_bounds_read_and_clear(&n) != cudaSuccess ||
         nvfp4::gemm_bounds_read_and_clear(&n) != cudaSuccess ||
-        nvfp4::dequantize_bounds_read_and_clear(&n) != cudaSuccess)
+        nvfp4::dequantize_bounds_read_and_clear(&n) != cudaSuccess ||
+        nvfp4::norm_rope_bounds_read_and_clear(&n) != cudaSuccess ||
+        nvfp4::attention_bounds_read_and_clear(&n) != cudaSuccess)
         return NVFP4_ERR_CUDA;
     *count = n;
     return NVFP4_OK;

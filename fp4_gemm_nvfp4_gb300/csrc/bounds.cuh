@@ -15,6 +15,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "kernels.h"
+
 namespace nvfp4 {
 
 // Bytes [lo, hi) a kernel may write in one output buffer.
@@ -30,6 +32,13 @@ Extent extent_of(const void* p, int64_t bytes);
 // `row_bytes` bytes in use (the last row ends after them).
 inline Extent extent_rows(const void* p, int64_t rows, int64_t ld_bytes, int64_t row_bytes) {
     return extent_of(p, rows > 0 ? (rows - 1) * ld_bytes + row_bytes : 0);
+}
+
+// Host: the range of [tokens][heads][head_dim] BF16 head vectors.
+inline Extent extent_heads(const HeadsView& v, int64_t tokens, int64_t heads, int64_t head_dim) {
+    return extent_of(v.data, tokens > 0 && heads > 0
+                                 ? 2 * ((tokens - 1) * v.ld_token + (heads - 1) * v.ld_head + head_dim)
+                                 : 0);
 }
 
 #ifdef NVFP4_BOUNDS_CHECK

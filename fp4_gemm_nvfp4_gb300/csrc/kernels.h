@@ -97,6 +97,8 @@ cudaError_t gemm_read_and_clear_status(unsigned int* status);
 cudaError_t quantize_bounds_read_and_clear(uint64_t* n);
 cudaError_t gemm_bounds_read_and_clear(uint64_t* n);
 cudaError_t dequantize_bounds_read_and_clear(uint64_t* n);
+cudaError_t norm_rope_bounds_read_and_clear(uint64_t* n);
+cudaError_t attention_bounds_read_and_clear(uint64_t* n);
 
 // Test support: the next GEMM launch waits at most timeout_ns per barrier and
 // its leader CTA leaves out one scale-warp arrival, so one wait runs out.
@@ -105,6 +107,51 @@ void arm_gemm_fault(uint64_t timeout_ns);
 cudaError_t launch_dequantize(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales, const float* sg,
                               int64_t rows, int64_t cols, void* y, int64_t ldy, bool out_fp32,
                               cudaStream_t stream);
+
+// BF16 head vectors [tokens][heads][head_dim], head_dim contiguous; strides
+// in elements.
+struct HeadsView {
+    uint16_t* data;
+    int64_t ld_token, ld_head;
+};
+
+// Per-head RMS norm with position rotation (norm_rope.cu).  q and k: the
+// outputs forward, the outputs' gradients backward.
+constexpr int kNormRopeMaxBlocks = 1024;   // partial sums of the weights' gradients: 2 * head_dim floats each
+struct NormRope {
+    const uint16_t* qkv;         // [tokens][ld_qkv], the first (q_heads + kv_heads) * head_dim columns
+    int64_t ld_qkv, tokens;
+    int q_heads, kv_heads, head_dim, rotary_dim;
+    bool interleaved;
+    const float *q_weight, *k_weight;
+    float eps;
+    const float *cos, *sin;      // [table_rows][rotary_dim / 2]
+    int64_t table_rows;
+    const int32_t* positions;    // [tokens]
+    HeadsView q, k;
+    uint16_t* dqkv;              // backward only, as qkv
+    int64_t ld_dqkv;
+    float *dq_weight, *dk_weight, *partials;
+};
+cudaError_t launch_norm_rope(const NormRope& a, bool backward, cudaStream_t stream);
+
+// Attention whose mask is one key interval per query row (attention.cu).
+struct Attention {
+    int64_t tokens;
+    int q_heads, kv_heads, head_dim;
+    float scale, softcap;        // softcap 0: none
+    const float* slopes;         // [q_heads] or null
+    const int32_t* spans;        // [tokens][2]: first key, one past the last
+    HeadsView q, k, v, out;
+    float* lse;                  // [q_heads][tokens]
+    HeadsView dout, dq, dk, dv;  // backward only
+    float* workspace;            // backward only
+};
+cudaError_t launch_attention_spans(const int32_t* offsets, int64_t documents, const int32_t* prefix, bool causal,
+                                   int64_t tokens, int32_t* spans, cudaStream_t stream);
+cudaError_t launch_attention(const Attention& a, cudaStream_t stream);
+size_t attention_backward_workspace_bytes(int64_t tokens, int64_t q_heads);
+cudaError_t launch_attention_backward(const Attention& a, cudaStream_t stream);
 
 // cuTensorMapEncodeTiled from the driver (null if unavailable).
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,

@@ -264,5 +264,174 @@ def dequantize(q: NVFP4Operand, out_dtype=torch.float32, stream=None) -> torch.T
     return y
 
 
+def rope_tables(positions: int, rotary_dim: int, base: float = 10000.0, device="cuda"
+                ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Cosines and sines of pos * base^(-2 i / rotary_dim), float32 [positions][rotary_dim / 2] each
+    (angles in float64); a program makes them once."""
+    i = torch.arange(rotary_dim // 2, dtype=torch.float64, device=device)
+    angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * base ** (-2.0 * i / max(1, rotary_dim))
+    return angle.cos().float(), angle.sin().float()
+
+
+def _heads(x: torch.Tensor, tokens: int, heads: int, dim: int, what: str) -> capi.nvfp4_heads:
+    """A bf16 [tokens, heads, dim] tensor as the ABI's strided view."""
+    if x.dtype != torch.bfloat16 or x.shape != (tokens, heads, dim):
+        raise ValueError(f"{what}: bfloat16 [{tokens}, {heads}, {dim}] expected, got {x.dtype} {list(x.shape)}")
+    st, sh, sd = x.stride()
+    if sd != 1:
+        raise ValueError(f"{what}: the head dimension must be contiguous")
+    # the stride of an axis of one element says nothing
+    return capi.nvfp4_heads(x.data_ptr(), st if tokens > 1 else heads * dim, sh if heads > 1 else dim)
+
+
+def _norm_rope_args(qkv, q_weight, k_weight, cos, sin, positions, q_heads, kv_heads, eps, interleaved):
+    if qkv.dtype != torch.bfloat16 or qkv.dim() != 2 or qkv.stride(1) != 1:
+        raise ValueError("qkv: a bfloat16 matrix with contiguous rows expected")
+    tokens, dim = qkv.shape[0], q_weight.numel()
+    if qkv.shape[1] < (q_heads + kv_heads) * dim:
+        raise ValueError(f"qkv: at least {(q_heads + kv_heads) * dim} columns expected, got {qkv.shape[1]}")
+    for name, t, shape in (("q_weight", q_weight, (dim,)), ("k_weight", k_weight, (dim,)), ("sin", sin, cos.shape)):
+        if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name}: contiguous float32 {list(shape)} expected, got {t.dtype} {list(t.shape)}")
+    if cos.dtype != torch.float32 or cos.dim() != 2 or not cos.is_contiguous():
+        raise ValueError("cos: contiguous float32 [positions, rotary_dim / 2] expected")
+    if positions.dtype != torch.int32 or positions.shape != (tokens,) or not positions.is_contiguous():
+        raise ValueError(f"positions: contiguous int32 [{tokens}] expected")
+    return (qkv.data_ptr(), qkv.stride(0) if tokens > 1 else qkv.shape[1], tokens, q_heads, kv_heads, dim,
+            q_weight.data_ptr(), k_weight.data_ptr(), eps, cos.data_ptr(), sin.data_ptr(), cos.shape[0],
+            2 * cos.shape[1], 1 if interleaved else 0, positions.data_ptr())
+
+
+def qk_norm_rope(qkv: torch.Tensor, q_weight: torch.Tensor, k_weight: torch.Tensor, cos: torch.Tensor,
+                 sin: torch.Tensor, positions: torch.Tensor, *, q_heads: int, kv_heads: int, eps: float = 1e-6,
+                 interleaved: bool = False, out_q: Optional[torch.Tensor] = None,
+                 out_k: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """RMS norm of every query and key head of the QKV projection's output, then the position rotation
+    (nvfp4_qk_norm_rope): q [tokens, q_heads, dim], k [tokens, kv_heads, dim], bf16.  The weights are
+    float32 [dim], the tables those of rope_tables."""
+    args = _norm_rope_args(qkv, q_weight, k_weight, cos, sin, positions, q_heads, kv_heads, eps, interleaved)
+    tokens, dim = args[2], args[5]
+    if out_q is None:
+        out_q = torch.empty((tokens, q_heads, dim), dtype=torch.bfloat16, device=qkv.device)
+    if out_k is None:
+        out_k = torch.empty((tokens, kv_heads, dim), dtype=torch.bfloat16, device=qkv.device)
+    status = capi.nvfp4_qk_norm_rope(*args, _heads(out_q, tokens, q_heads, dim, "out_q"),
+                                     _heads(out_k, tokens, kv_heads, dim, "out_k"), stream_handle(stream))
+    capi.check(status, "nvfp4_qk_norm_rope")
+    return out_q, out_k
+
+
+def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor, qkv: torch.Tensor, q_weight: torch.Tensor,
+                          k_weight: torch.Tensor, cos: torch.Tensor, sin: torch.Tensor, positions: torch.Tensor, *,
+                          eps: float = 1e-6, interleaved: bool = False, dqkv: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None, stream=None
+                          ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Gradients of qk_norm_rope (nvfp4_qk_norm_rope_backward): (dqkv, dq_weight, dk_weight).  dqkv's first
+    (q_heads + kv_heads) * dim columns are written; without one given it has just those."""
+    q_heads, kv_heads = dq.shape[1], dk.shape[1]
+    args = _norm_rope_args(qkv, q_weight, k_weight, cos, sin, positions, q_heads, kv_heads, eps, interleaved)
+    tokens, dim = args[2], args[5]
+    if dqkv is None:
+        dqkv = torch.empty((tokens, (q_heads + kv_heads) * dim), dtype=torch.bfloat16, device=qkv.device)
+    elif (dqkv.dtype != torch.bfloat16 or dqkv.dim() != 2 or dqkv.shape[0] != tokens or dqkv.stride(1) != 1 or
+          dqkv.shape[1] < (q_heads + kv_heads) * dim):
+        raise ValueError(f"dqkv: bfloat16 [{tokens}, >= {(q_heads + kv_heads) * dim}] expected")
+    nbytes = capi.nvfp4_qk_norm_rope_backward_workspace_size(dim)
+    if workspace is None or workspace.numel() < nbytes:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=qkv.device)
+    dw = torch.empty((2, dim), dtype=torch.float32, device=qkv.device)
+    status = capi.nvfp4_qk_norm_rope_backward(
+        _heads(dq, tokens, q_heads, dim, "dq"), _heads(dk, tokens, kv_heads, dim, "dk"), *args, dqkv.data_ptr(),
+        dqkv.stride(0) if tokens > 1 else dqkv.shape[1], dw.data_ptr(), dw.data_ptr() + 4 * dim,
+        workspace.data_ptr(), workspace.numel(), stream_handle(stream))
+    capi.check(status, "nvfp4_qk_norm_rope_backward")
+    return dqkv, dw[0], dw[1]
+
+
+def attention_spans(offsets: torch.Tensor, tokens: int, *, causal: bool = True, prefix: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The key interval of every token of packed documents, int32 [tokens, 2] (nvfp4_attention_spans).
+    offsets: int32 [documents + 1] on the device; prefix: int32 [documents]."""
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 1 or not offsets.is_contiguous():
+        raise ValueError("offsets: contiguous int32 [documents + 1] expected")
+    documents = offsets.numel() - 1
+    if prefix is not None and (prefix.dtype != torch.int32 or prefix.shape != (documents,) or
+                               not prefix.is_contiguous()):
+        raise ValueError(f"prefix: contiguous int32 [{documents}] expected")
+    if out is None:
+        out = torch.empty((tokens, 2), dtype=torch.int32, device=offsets.device)
+    elif out.dtype != torch.int32 or out.shape != (tokens, 2) or not out.is_contiguous():
+        raise ValueError(f"out: contiguous int32 [{tokens}, 2] expected")
+    status = capi.nvfp4_attention_spans(offsets.data_ptr(), documents, None if prefix is None else prefix.data_ptr(),
+                                        1 if causal else 0, tokens, out.data_ptr(), stream_handle(stream))
+    capi.check(status, "nvfp4_attention_spans")
+    return out
+
+
+def _attention_desc(q, k, spans, scale, softcap, slopes) -> capi.nvfp4_attention_desc:
+    tokens, q_heads, dim = q.shape
+    if spans.dtype != torch.int32 or spans.shape != (tokens, 2) or not spans.is_contiguous():
+        raise ValueError(f"spans: contiguous int32 [{tokens}, 2] expected")
+    if slopes is not None and (slopes.dtype != torch.float32 or slopes.shape != (q_heads,) or
+                               not slopes.is_contiguous()):
+        raise ValueError(f"slopes: contiguous float32 [{q_heads}] expected")
+    return capi.nvfp4_attention_desc(tokens, q_heads, k.shape[1], dim, dim ** -0.5 if scale is None else scale,
+                                     softcap, None if slopes is None else slopes.data_ptr(), spans.data_ptr())
+
+
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, spans: torch.Tensor, *,
+              scale: Optional[float] = None, softcap: float = 0.0, slopes: Optional[torch.Tensor] = None,
+              out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, stream=None
+              ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of bf16 q [tokens, q_heads, dim] over k, v [tokens, kv_heads, dim] (nvfp4_attention): token i
+    sees the keys spans[i, 0] <= j < spans[i, 1].  scale defaults to dim^-1/2; softcap > 0 caps the scores
+    by softcap * tanh(score / softcap); slopes (float32 [q_heads]) take slope * |i - j| off them.
+    Returns (out bf16 like q, lse float32 [q_heads, tokens])."""
+    desc = _attention_desc(q, k, spans, scale, softcap, slopes)
+    tokens, q_heads, kv_heads, dim = desc.tokens, desc.q_heads, desc.kv_heads, desc.head_dim
+    if out is None:
+        out = torch.empty((tokens, q_heads, dim), dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty((q_heads, tokens), dtype=torch.float32, device=q.device)
+    elif lse.dtype != torch.float32 or lse.shape != (q_heads, tokens) or not lse.is_contiguous():
+        raise ValueError(f"lse: contiguous float32 [{q_heads}, {tokens}] expected")
+    status = capi.nvfp4_attention(desc, _heads(q, tokens, q_heads, dim, "q"), _heads(k, tokens, kv_heads, dim, "k"),
+                                  _heads(v, tokens, kv_heads, dim, "v"), _heads(out, tokens, q_heads, dim, "out"),
+                                  lse.data_ptr(), stream_handle(stream))
+    capi.check(status, "nvfp4_attention")
+    return out, lse
+
+
+def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                       lse: torch.Tensor, spans: torch.Tensor, *, scale: Optional[float] = None,
+                       softcap: float = 0.0, slopes: Optional[torch.Tensor] = None,
+                       dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
+                       dv: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None
+                       ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Gradients (dq, dk, dv) of attention from dout and the forward pass's inputs, out and lse
+    (nvfp4_attention_backward); dv may be a view of the QKV projection's output gradient."""
+    desc = _attention_desc(q, k, spans, scale, softcap, slopes)
+    tokens, q_heads, kv_heads, dim = desc.tokens, desc.q_heads, desc.kv_heads, desc.head_dim
+    if lse.dtype != torch.float32 or lse.shape != (q_heads, tokens) or not lse.is_contiguous():
+        raise ValueError(f"lse: contiguous float32 [{q_heads}, {tokens}] expected")
+    if dq is None:
+        dq = torch.empty((tokens, q_heads, dim), dtype=torch.bfloat16, device=q.device)
+    if dk is None:
+        dk = torch.empty((tokens, kv_heads, dim), dtype=torch.bfloat16, device=q.device)
+    if dv is None:
+        dv = torch.empty((tokens, kv_heads, dim), dtype=torch.bfloat16, device=q.device)
+    nbytes = capi.nvfp4_attention_backward_workspace_size(tokens, q_heads)
+    if workspace is None or workspace.numel() < nbytes:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    status = capi.nvfp4_attention_backward(
+        desc, _heads(dout, tokens, q_heads, dim, "dout"), _heads(q, tokens, q_heads, dim, "q"),
+        _heads(k, tokens, kv_heads, dim, "k"), _heads(v, tokens, kv_heads, dim, "v"),
+        _heads(out, tokens, q_heads, dim, "out"), lse.data_ptr(), _heads(dq, tokens, q_heads, dim, "dq"),
+        _heads(dk, tokens, kv_heads, dim, "dk"), _heads(dv, tokens, kv_heads, dim, "dv"), workspace.data_ptr(),
+        workspace.numel(), stream_handle(stream))
+    capi.check(status, "nvfp4_attention_backward")
+    return dq, dk, dv
+
+
 def device_error(stream=None) -> int:
     return capi.nvfp4_device_error(stream_handle(stream))

@@ -401,6 +401,144 @@ NVFP4_API nvfp4_status nvfp4_quantize_noalloc(const void *x, int64_t rows, int64
                                               const nvfp4_tensor *out_row, const nvfp4_tensor *out_col,
                                               nvfp4_stream_t stream);
 
+/*
+ * ---- Between the QKV and the O projection -----------------------------------
+ *
+ * The attention half of a block [FS: a grouped-query transformer, 24 query
+ * and 12 key/value heads of 128]: the QKV projection's output, nvfp4_gemm's
+ * BF16 [tokens][(q_heads + 2 kv_heads) * head_dim], goes through
+ * nvfp4_qk_norm_rope and nvfp4_attention to the O projection's input, and
+ * back through the two _backward calls.  Tensors are BF16, statistics FP32.
+ *
+ * A set of head vectors: BF16 [tokens][heads][head_dim] with head_dim
+ * contiguous; ld_token and ld_head are the strides in elements between
+ * tokens and between heads (any order of the two, multiples of 8), so that
+ * columns of the QKV projection's output are used where they are.
+ */
+typedef struct {
+    void    *data;       /* device, 16-byte aligned */
+    int64_t  ld_token;
+    int64_t  ld_head;
+} nvfp4_heads;
+
+/*
+ * nvfp4_qk_norm_rope -- RMS norm of every query and key head, then the
+ * position rotation, in one pass.  For head vector x of one token:
+ *   n = x / sqrt(mean(x^2) + eps) * w,
+ *   y1 = n1 cos - n2 sin, y2 = n2 cos + n1 sin  over the pairs (1, 2) of the
+ * first rotary_dim dims; y = n past them.  Binary32 throughout, one rounding.
+ *  qkv          BF16 [tokens][ld_qkv]: q_heads query heads, then kv_heads key
+ *               heads, of head_dim columns each (what follows is not read).
+ *  q_weight, k_weight  FP32 [head_dim].
+ *  cos, sin     FP32 [table_rows][rotary_dim / 2] of the positions' angles.
+ *  positions    int32 [tokens], rows of the tables (held to the last row if
+ *               they are past it).
+ *  interleaved  0: pairs (i, i + rotary_dim / 2); 1: pairs (2i, 2i + 1).
+ *  q_out, k_out [tokens][q_heads][head_dim], [tokens][kv_heads][head_dim].
+ * Requirements: 8 <= head_dim <= 128 and head_dim % 8 == 0, rotary_dim % 16
+ * == 0 and 0 <= rotary_dim <= head_dim, q_heads, kv_heads >= 1 [SHAPE];
+ * every pointer 16-byte aligned (positions 4), strides multiples of 8
+ * [ALIGNMENT]; finite eps >= 0 [INVALID_ARG].
+ */
+NVFP4_API nvfp4_status nvfp4_qk_norm_rope(const void *qkv, int64_t ld_qkv, int64_t tokens, int32_t q_heads,
+                                          int32_t kv_heads, int32_t head_dim, const float *q_weight,
+                                          const float *k_weight, float eps, const float *cos, const float *sin,
+                                          int64_t table_rows, int32_t rotary_dim, int32_t interleaved,
+                                          const int32_t *positions, const nvfp4_heads *q_out,
+                                          const nvfp4_heads *k_out, nvfp4_stream_t stream);
+
+/*
+ * nvfp4_qk_norm_rope_backward -- the gradients of nvfp4_qk_norm_rope's inputs
+ * from those of its outputs.  With dn = dq (dk) turned back, r = 1 / sqrt(
+ * mean(x^2) + eps), xh = x r, g = w dn:
+ *   dx = r (g - xh mean(g xh)),  dw = sum over tokens and heads of dn xh.
+ *  dqkv         BF16 [tokens][ld_dqkv]: the first (q_heads + kv_heads) *
+ *               head_dim columns are written, what follows keeps its values
+ *               (nvfp4_attention_backward writes dv there).  May be qkv.
+ *  dq_weight, dk_weight  FP32 [head_dim], overwritten (0 for no tokens).
+ *  workspace    nvfp4_qk_norm_rope_backward_workspace_size(head_dim) bytes,
+ *               16-byte aligned.
+ * The sums run in a fixed order: equal inputs give equal bits.
+ */
+NVFP4_API size_t nvfp4_qk_norm_rope_backward_workspace_size(int32_t head_dim);
+NVFP4_API nvfp4_status nvfp4_qk_norm_rope_backward(const nvfp4_heads *dq, const nvfp4_heads *dk, const void *qkv,
+                                                   int64_t ld_qkv, int64_t tokens, int32_t q_heads,
+                                                   int32_t kv_heads, int32_t head_dim, const float *q_weight,
+                                                   const float *k_weight, float eps, const float *cos,
+                                                   const float *sin, int64_t table_rows, int32_t rotary_dim,
+                                                   int32_t interleaved, const int32_t *positions, void *dqkv,
+                                                   int64_t ld_dqkv, float *dq_weight, float *dk_weight,
+                                                   void *workspace, size_t workspace_bytes, nvfp4_stream_t stream);
+
+/*
+ * What one attention call computes:
+ *   z_ij = scale q_i.k_j;  s_ij = softcap tanh(z_ij / softcap) if softcap > 0,
+ *   else z_ij;  s_ij -= slopes[h] |i - j| if slopes;  token i attends to the
+ *   keys spans[i][0] <= j < spans[i][1];
+ *   out_i = sum_j softmax_j(s_ij) v_j,  lse_i = log sum_j exp(s_ij).
+ * Query head h reads key/value head h / (q_heads / kv_heads).  Causal,
+ * document, prefix and window masks and padding are all such intervals
+ * (nvfp4_attention_spans writes the common ones); a row whose interval is
+ * empty gets out = 0, lse = -inf and gradients 0.  Intervals are cut to
+ * [0, tokens).  Work is spent only on 128 x 128 tiles that some interval
+ * reaches.  Inputs are finite; the rows of keys and values that no interval of a
+ * tile of 128 queries reaches, and of queries with an empty interval, may
+ * hold anything.
+ */
+typedef struct {
+    int64_t        tokens;
+    int32_t        q_heads, kv_heads, head_dim;
+    float          scale;      /* > 0 */
+    float          softcap;    /* >= 0; 0: no cap */
+    const float   *slopes;     /* device [q_heads], or NULL: no distance bias */
+    const int32_t *spans;      /* device [tokens][2], 8-byte aligned */
+} nvfp4_attention_desc;
+
+/*
+ * nvfp4_attention_spans -- the intervals of packed documents.  Document d is
+ * the tokens offsets[d] <= i < offsets[d + 1]; its tokens attend to the whole
+ * document, or if causal to the tokens up to their own and to the document's
+ * first prefix[d] tokens.  Tokens outside every document get [0, 0).
+ *  offsets      device int32 [documents + 1], ascending.
+ *  prefix       device int32 [documents], or NULL.
+ *  spans        device int32 [tokens][2], 8-byte aligned.
+ */
+NVFP4_API nvfp4_status nvfp4_attention_spans(const int32_t *offsets, int64_t documents, const int32_t *prefix,
+                                             int32_t causal, int64_t tokens, int32_t *spans,
+                                             nvfp4_stream_t stream);
+
+/*
+ * nvfp4_attention -- the forward pass.
+ *  q            [tokens][q_heads][head_dim];  k, v [tokens][kv_heads][head_dim].
+ *  out          [tokens][q_heads][head_dim];  lse FP32 [q_heads][tokens].
+ * Scores, softmax statistics and sums are FP32; the probabilities are rounded
+ * to BF16 for their product with v (relative error at most 2^-8 each, as
+ * out's own rounding), the result once more to BF16.
+ * Requirements: head_dim as for nvfp4_qk_norm_rope, q_heads a multiple of
+ * kv_heads, tokens < 2^31 - 256 [SHAPE]; data 16-byte aligned, strides positive
+ * multiples of 8 [ALIGNMENT]; finite scale > 0 and softcap >= 0
+ * [INVALID_ARG].  tokens = 0 enqueues nothing.
+ */
+NVFP4_API nvfp4_status nvfp4_attention(const nvfp4_attention_desc *desc, const nvfp4_heads *q, const nvfp4_heads *k,
+                                       const nvfp4_heads *v, const nvfp4_heads *out, float *lse,
+                                       nvfp4_stream_t stream);
+
+/*
+ * nvfp4_attention_backward -- dq, dk, dv from dout, the forward pass's inputs
+ * and its out and lse.  dk and dv sum over the query heads that share their
+ * head.  Everything is recomputed from lse; sums run in a fixed order: equal
+ * inputs give equal bits.  The probabilities and the scores' gradients are
+ * rounded to BF16 for their products, sums are FP32.
+ *  workspace    nvfp4_attention_backward_workspace_size(tokens, q_heads)
+ *               bytes, 16-byte aligned.
+ */
+NVFP4_API size_t nvfp4_attention_backward_workspace_size(int64_t tokens, int32_t q_heads);
+NVFP4_API nvfp4_status nvfp4_attention_backward(const nvfp4_attention_desc *desc, const nvfp4_heads *dout,
+                                                const nvfp4_heads *q, const nvfp4_heads *k, const nvfp4_heads *v,
+                                                const nvfp4_heads *out, const float *lse, const nvfp4_heads *dq,
+                                                const nvfp4_heads *dk, const nvfp4_heads *dv, void *workspace,
+                                                size_t workspace_bytes, nvfp4_stream_t stream);
+
 /* Human-readable name of a status. */
 NVFP4_API const char *nvfp4_status_string(nvfp4_status status);
 
