@@ -19,8 +19,8 @@ LIB = os.path.join(OUT_DIR, "libnvfp4.so")
 OUT_DIR_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_DEBUG = os.path.join(OUT_DIR_DEBUG, "libnvfp4_debug.so")
 SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "dequantize.cu", "quantize_noalloc.cu", "norm_rope.cu",
-           "attention.cu"]
-HEADERS = ["device_common.cuh", "kernels.h", "bounds.cuh"]
+           "attention.cu", "attention_forward.cu"]
+HEADERS = ["device_common.cuh", "kernels.h", "bounds.cuh", "mma_common.cuh", "attention_common.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "-Xcompiler", "-fvisibility=hidden", "-I", os.path.join(ROOT, "include")]

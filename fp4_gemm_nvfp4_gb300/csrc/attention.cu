@@ -101,43 +101,6 @@ __global__ void __launch_bounds__(256) spans_kernel(const int32_t* __restrict__ 
     store_out(spans + i, s, xs);
 }
 
-// One warp per query row and head: lanes take keys for the scores, then dims
-// for the products.
-__global__ void __launch_bounds__(kThreads) attention_kernel(const __grid_constant__ Params p) {
-    const Attention& a = p.a;
-    const int64_t w = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
-    const int lane = threadIdx.x & 31, D = a.head_dim;
-    if (w >= a.tokens * a.q_heads) return;
-    const int64_t i = w / a.q_heads;
-    const int h = (int)(w % a.q_heads), g = h / (a.q_heads / a.kv_heads);
-    const uint16_t* q = a.q.data + i * a.q.ld_token + h * a.q.ld_head;
-    const float slope = a.slopes ? a.slopes[h] : 0.0f;
-    int64_t lo, hi;
-    span_of(a, i, lo, hi);
-    float m = -INFINITY, l = 0.0f, o[kPer] = {};
-    for (int64_t j0 = lo; j0 < hi; j0 += 32) {
-        const int64_t j = j0 + lane;
-        float s = -INFINITY, th;
-        if (j < hi) s = score(a, dot_row(q, a.k.data + j * a.k.ld_token + g * a.k.ld_head, D), slope, i - j, &th);
-        const float mn = fmaxf(m, warp_max(s));
-        const float f = __expf(m - mn);
-        const float e = __expf(s - mn);
-        l = l * f + warp_sum(e);
-        m = mn;
-        for (int c = 0; c < kPer; ++c) o[c] *= f;
-        for (int k = 0; k < 32 && j0 + k < hi; ++k) {
-            const float pk = __shfl_sync(0xFFFFFFFFu, e, k);
-            const uint16_t* v = a.v.data + (j0 + k) * a.v.ld_token + g * a.v.ld_head;
-            for (int c = 0; c < kPer; ++c)
-                if (lane + 32 * c < D) o[c] = fmaf(pk, bf16_at(v + lane + 32 * c), o[c]);
-        }
-    }
-    uint16_t* out = a.out.data + i * a.out.ld_token + h * a.out.ld_head;
-    for (int c = 0; c < kPer; ++c)
-        if (lane + 32 * c < D) store_bf16(out + lane + 32 * c, l > 0.0f ? o[c] / l : 0.0f, p.xo);
-    if (lane == 0) store_out(a.lse + h * a.tokens + i, l > 0.0f ? m + logf(l) : -INFINITY, p.xlse);
-}
-
 // One warp per query row and head: delta into the workspace, dq.
 __global__ void __launch_bounds__(kThreads) attention_dq_kernel(const __grid_constant__ Params p) {
     const Attention& a = p.a;
@@ -237,15 +200,6 @@ cudaError_t launch_attention_spans(const int32_t* offsets, int64_t documents, co
     spans_kernel<<<(unsigned)((tokens + 255) / 256), 256, 0, stream>>>(offsets, documents, prefix, causal ? 1 : 0, tokens,
                                                                        reinterpret_cast<int2*>(spans),
                                                                        extent_of(spans, tokens * 8));
-    return cudaGetLastError();
-}
-
-cudaError_t launch_attention(const Attention& a, cudaStream_t stream) {
-    Params p{};
-    p.a = a;
-    p.xo = extent_heads(a.out, a.tokens, a.q_heads, a.head_dim);
-    p.xlse = extent_of(a.lse, a.tokens * a.q_heads * 4);
-    attention_kernel<<<warp_blocks(a.tokens * a.q_heads), kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
