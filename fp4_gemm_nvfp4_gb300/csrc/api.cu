@@ -693,7 +693,7 @@ nvfp4_status nvfp4_testing_bounds_violations(uint64_t* count) {
         nvfp4::gemm_bounds_read_and_clear(&n) != cudaSuccess ||
         nvfp4::dequantize_bounds_read_and_clear(&n) != cudaSuccess ||
         nvfp4::norm_rope_bounds_read_and_clear(&n) != cudaSuccess ||
-        nvfp4::attention_bounds_read_and_clear(&n) != cudaSuccess ||
+        nvfp4::attention_spans_bounds_read_and_clear(&n) != cudaSuccess ||
         nvfp4::attention_forward_bounds_read_and_clear(&n) != cudaSuccess)
         return NVFP4_ERR_CUDA;
     *count = n;
@@ -720,7 +720,8 @@ nvfp4_status nvfp4_device_error(nvfp4_stream_t stream) {
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return NVFP4_ERR_CUDA;
     unsigned int status = 0;
     if (nvfp4::gemm_read_and_clear_status(&status) != cudaSuccess ||
-        nvfp4::attention_forward_status_read_and_clear(&status) != cudaSuccess)
+        nvfp4::attention_forward_status_read_and_clear(&status) != cudaSuccess ||
+        nvfp4::attention_backward_status_read_and_clear(&status) != cudaSuccess)
         return NVFP4_ERR_CUDA;
     return (status & nvfp4::kStatusTimeoutBit) ? NVFP4_ERR_TIMEOUT : NVFP4_OK;
 }

@@ -93,6 +93,7 @@ cudaError_t gemm_read_and_clear_status(unsigned int* status);
 
 // As gemm_read_and_clear_status, for the attention kernels: or-ed into *status.
 cudaError_t attention_forward_status_read_and_clear(unsigned int* status);
+cudaError_t attention_backward_status_read_and_clear(unsigned int* status);
 
 // Add the stores that the debug build's bounds check skipped in one source
 // file's kernels to *n and clear that count (synchronous; in the regular
@@ -101,7 +102,7 @@ cudaError_t quantize_bounds_read_and_clear(uint64_t* n);
 cudaError_t gemm_bounds_read_and_clear(uint64_t* n);
 cudaError_t dequantize_bounds_read_and_clear(uint64_t* n);
 cudaError_t norm_rope_bounds_read_and_clear(uint64_t* n);
-cudaError_t attention_bounds_read_and_clear(uint64_t* n);
+cudaError_t attention_spans_bounds_read_and_clear(uint64_t* n);
 cudaError_t attention_forward_bounds_read_and_clear(uint64_t* n);
 
 // Test support: the next GEMM launch waits at most timeout_ns per barrier and
@@ -139,7 +140,7 @@ struct NormRope {
 };
 cudaError_t launch_norm_rope(const NormRope& a, bool backward, cudaStream_t stream);
 
-// Attention whose mask is one key interval per query row (attention.cu).
+// Attention whose mask is one key interval per query row (attention_*.cu).
 struct Attention {
     int64_t tokens;
     int q_heads, kv_heads, head_dim;
