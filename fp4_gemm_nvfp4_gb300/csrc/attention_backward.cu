@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     TileSpan* parts = reinterpret_cast<TileSpan*>(tmem_slot + 4);   // [4]
     float* exchange = vec;                                       // dq: [128], the vectors' place is unused there
 
-    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
+    const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31u;
     // the longest first under a causal mask: the last queries, the first keys
     const int32_t head = (int32_t)(blockIdx.x % (uint32_t)p.heads);
     const int32_t at = (int32_t)(blockIdx.x / (uint32_t)p.heads);
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (threadIdx.x == 0 && head == 0) p.ws.spans[tile] = ts;
     }
     const int head0 = kKeys ? head * p.group : head / p.group;        // first streamed head
-    const int total = kKeys ? count * p.group : count;
+    const int total = __shfl_sync(0xFFFFFFFFu, kKeys ? count * p.group : count, 0);
 
     if (warp < kFirstSoftmaxWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" ::: "memory");
@@ -256,40 +256,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t n = issued - 1 - back;
                 (void)mbar_wait(&full[n % kSlots], (n / kSlots) & 1u, p.timeout_ns);
             }
-        } else if (warp == 1 && lane == 0 && total > 0) {
+        } else if (warp == 1 && total > 0) {
             // --------------------------------------------------- MMA issue
             constexpr uint32_t kIdS = idesc_bf16(128, 128, false);
             constexpr uint32_t kIdAcc = idesc_bf16(128, kD, true);
+            const uint32_t elected = elect_one();
+            const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+            const uint32_t f_lo = desc_k_major(smem_u32(smem)), xk_lo = desc_k_major(smem_u32(ring)),
+                           xn_lo = desc_n_major(smem_u32(ring));
             bool ok = true;
             auto await = [&](uint64_t* bar, uint32_t parity) {
-                if (ok && !mbar_wait_or_abort(bar, parity, p.timeout_ns, abort_flag)) ok = false;
+                if (ok && !warp_wait_or_abort(bar, parity, p.timeout_ns, abort_flag)) ok = false;
                 tc_fence_after();
             };
-            auto place = [&](uint32_t n) { return smem_u32(ring) + (n % kSlots) * S::kTile; };
             // the scores of streamed tile i (x = 0: S, 1: dP)
-            auto scores = [&](int i, int x) {
-                const uint32_t n = 2 * (uint32_t)i + x;
-                await(&full[n % kSlots], (n / kSlots) & 1u);
+            auto scores = [&](int i, uint32_t x) {
+                const uint32_t n = 2 * (uint32_t)i + x, slot = n % kSlots;
+                await(&full[slot], (n / kSlots) & 1u);
                 if (!ok) return;
-                const uint64_t a = desc_k_major(smem_u32(smem) + x * S::kTile), b = desc_k_major(place(n));
-#pragma unroll
-                for (uint32_t j = 0; j < kD / 16; ++j)
-                    mma_bf16_ss(tmem + (x ? kDpCol : kSCol), a + k_major_step(j), b + k_major_step(j), kIdS, j ? 1u : 0u);
-                tc_commit(x ? dp_full : s_full);
-                if (!kKeys && x == 1) tc_commit(&empty[n % kSlots]);   // dq: v is needed for dP alone
+                mma_scores<kIdS, kD>(tm + (x ? kDpCol : kSCol), f_lo + x * (S::kTile >> 4),
+                                     xk_lo + slot * (S::kTile >> 4), elected);
+                tc_commit(x ? dp_full : s_full, elected);
+                if (!kKeys && x == 1) tc_commit(&empty[slot], elected);   // dq: v is needed for dP alone
             };
-            auto product = [&](int i, int acc) {
-                const uint32_t n = 2 * (uint32_t)i + (kKeys && acc == 0 ? 1u : 0u);
+            auto product = [&](int i, uint32_t acc) {
+                const uint32_t n = 2 * (uint32_t)i + (kKeys && acc == 0 ? 1u : 0u), slot = n % kSlots;
                 await(acc ? dz_full : p_full, (uint32_t)i & 1u);
                 if (!ok) return;
-                const uint32_t a = tmem + (acc ? kDpCol : kSCol);
-                const uint64_t b = desc_n_major(place(n));
                 // the 64 columns of each half of S hold 64 rows' BF16 in their first 32
-#pragma unroll
-                for (uint32_t j = 0; j < 8; ++j)
-                    mma_bf16_ts(tmem + (acc ? kAcc2Col : kAcc1Col), a + (j >> 2) * 64 + (j & 3u) * 8, b + n_major_step(j),
-                                kIdAcc, (i || j) ? 1u : 0u);
-                if (kKeys || acc == 1) tc_commit(&empty[n % kSlots]);
+                mma_sum<kIdAcc, 4, 64>(tm + (acc ? kAcc2Col : kAcc1Col), tm + (acc ? kDpCol : kSCol),
+                                       xn_lo + slot * (S::kTile >> 4), i ? 1u : 0u, elected);
+                if (kKeys || acc == 1) tc_commit(&empty[slot], elected);
             };
             await(f_full, 0);
             scores(0, 0);
@@ -300,13 +297,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 product(i, 1);
                 if (i + 1 < total) scores(i + 1, 1);
             }
-            if (ok) tc_commit(acc_full);
-            if (!ok) {
+            if (ok) tc_commit(acc_full, elected);
+            if (!ok && elected) {
                 *abort_flag = 1u;
                 atomicOr(&g_attention_status, kStatusTimeoutBit);
             }
             // every product is done before tensor memory is freed
-            tc_commit(drain);
+            tc_commit(drain, elected);
             (void)mbar_wait(drain, 0, p.timeout_ns);
         }
     } else {

@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile uint32_t* abort_flag = tmem_slot + 1;
     TileSpan* parts = reinterpret_cast<TileSpan*>(tmem_slot + 4);   // [8]
 
-    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
+    const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31u;
     // the last tiles first: with a causal mask they are the longest
     const uint32_t item = blockIdx.x % p.items_per_tile;
     const int32_t ti = p.tiles - 1 - (int32_t)(blockIdx.x / p.items_per_tile);
@@ -139,8 +139,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int x = 0; x < 2; ++x) {
         ts[x] = join_spans(parts + 4 * x);
         const bool some = ts[x].lo < ts[x].hi;
-        first[x] = some ? ts[x].lo >> 7 : INT32_MAX;
-        last[x] = some ? (ts[x].hi + 127) >> 7 : 0;
+        first[x] = __shfl_sync(0xFFFFFFFFu, some ? ts[x].lo >> 7 : INT32_MAX, 0);
+        last[x] = __shfl_sync(0xFFFFFFFFu, some ? (ts[x].hi + 127) >> 7 : 0, 0);
     }
     const int begin = min(first[0], first[1]), end = max(last[0], last[1]);
 
@@ -190,16 +190,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t n = issued - 1 - back;
                 (void)mbar_wait(&full[n % S::kSlots], (n / S::kSlots) & 1u, p.timeout_ns);
             }
-        } else if (warp == 1 && lane == 0) {
+        } else if (warp == 1) {
             // --------------------------------------------------- MMA issue
             constexpr uint32_t kIdS = idesc_bf16(128, 128, false);
             constexpr uint32_t kIdO = idesc_bf16(128, kD, true);
+            const uint32_t elected = elect_one();
+            const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+            const uint32_t q_lo = desc_k_major(smem_u32(smem)), k_lo = desc_k_major(smem_u32(ring)),
+                           v_lo = desc_n_major(smem_u32(ring));
             Ring r;
             bool ok = true;
             uint32_t p_phase[2] = {0, 0};
             bool started[2] = {false, false};
             auto await = [&](uint64_t* bar, uint32_t parity) {
-                if (ok && !mbar_wait_or_abort(bar, parity, p.timeout_ns, abort_flag)) ok = false;
+                if (ok && !warp_wait_or_abort(bar, parity, p.timeout_ns, abort_flag)) ok = false;
             };
             auto in = [&](int x, int kt) { return kt >= first[x] && kt < last[x]; };
             auto advance = [&](Ring& q) {
@@ -209,12 +213,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             auto scores = [&](int x, uint32_t slot) {
-                const uint64_t a = desc_k_major(smem_u32(smem + x * S::kTile));
-                const uint64_t b = desc_k_major(smem_u32(ring + slot * S::kTile));
-#pragma unroll
-                for (uint32_t j = 0; j < kD / 16; ++j)
-                    mma_bf16_ss(tmem + kScoreCol + 128 * x, a + k_major_step(j), b + k_major_step(j), kIdS, j ? 1u : 0u);
-                tc_commit(&s_full[x]);
+                mma_scores<kIdS, kD>(tm + kScoreCol + 128 * x, q_lo + x * (S::kTile >> 4), k_lo + slot * (S::kTile >> 4),
+                                     elected);
+                tc_commit(&s_full[x], elected);
             };
             int kt = begin;
 #pragma unroll
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int x = 0; x < 2; ++x)
                         if (in(x, kt)) scores(x, r.slot);
                 }
-                if (ok) tc_commit(&empty[r.slot]);
+                if (ok) tc_commit(&empty[r.slot], elected);
                 advance(r);
             }
             while (kt < end && ok) {
@@ -245,13 +246,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         p_phase[x] ^= 1u;
                         if (!ok) break;
                         tc_fence_after();
-                        const uint64_t b = desc_n_major(smem_u32(ring + v.slot * S::kTile));
-#pragma unroll
-                        for (uint32_t j = 0; j < 8; ++j)
-                            mma_bf16_ts(tmem + kOutCol + 128 * x, tmem + kScoreCol + 128 * x + 8 * j,
-                                        b + n_major_step(j), kIdO, (started[x] || j) ? 1u : 0u);
+                        mma_sum<kIdO, 8, 64>(tm + kOutCol + 128 * x, tm + kScoreCol + 128 * x,
+                                             v_lo + v.slot * (S::kTile >> 4), started[x] ? 1u : 0u, elected);
                         started[x] = true;
-                        if (kt + 1 == last[x]) tc_commit(&o_full[x]);
+                        if (kt + 1 == last[x]) tc_commit(&o_full[x], elected);
                     }
                     if (nk < end && in(x, nk)) {
                         await(&full[k.slot], k.phase);
@@ -261,19 +259,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (!ok) break;
-                tc_commit(&empty[v.slot]);
+                tc_commit(&empty[v.slot], elected);
                 if (nk < end) {
-                    tc_commit(&empty[k.slot]);
+                    tc_commit(&empty[k.slot], elected);
                     advance(r);
                 }
                 kt = nk;
             }
-            if (!ok) {
+            if (!ok && elected) {
                 *abort_flag = 1u;
                 atomicOr(&g_attention_status, kStatusTimeoutBit);
             }
             // every product is done before tensor memory is freed
-            tc_commit(drain);
+            tc_commit(drain, elected);
             (void)mbar_wait(drain, 0, p.timeout_ns);
         }
     } else {

@@ -21,10 +21,23 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
-// Arrive on the mbarrier once this thread's MMAs so far have completed.
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
+// The MMA warp runs as a whole, with every value uniform, and one elected lane
+// issues: operand addresses then live in uniform registers, where the
+// instruction wants them.  (One lane on its own needed a move per operand
+// and 110 cycles per MMA, against 64 that a 128 x 128 x 16 product takes.)
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e;
+}
+
+// Arrive on the mbarrier once the elected lane's MMAs so far have completed.
+__device__ __forceinline__ void tc_commit(uint64_t* bar, uint32_t elected) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(elected)
+        : "memory");
 }
 
 // Instruction descriptor of kind::f16: FP32 D (bit 4), BF16 A and B (format 1
@@ -34,40 +47,69 @@ __host__ __device__ constexpr uint32_t idesc_bf16(uint32_t m, uint32_t n, bool b
     return (1u << 4) | (1u << 7) | (1u << 10) | ((b_n_major ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
-// D (+)= A B^T, both operands in shared memory.
-__device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
-                                            uint32_t accumulate) {
+// Tiles of 128 rows in shared memory: 64 dims (128 bytes) by 128 rows per
+// 16 KiB chunk, 128-byte swizzle, chunk after chunk.  A descriptor's high
+// word is the same for both uses: 8-row groups 1024 bytes apart, version 1,
+// 128-byte swizzle.
+constexpr uint32_t kChunkBytes = 128 * 128;
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+// As a K-major operand (the dims are summed over): a step of 16 dims is 32
+// bytes, the fifth starts the next chunk.
+__device__ __forceinline__ uint32_t desc_k_major(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+__host__ __device__ constexpr uint32_t k_major_step(uint32_t step) {
+    return (step >> 2) * (kChunkBytes >> 4) + (step & 3u) * 2u;
+}
+// As an N-major operand (the rows are summed over): 64 dims per chunk; a step
+// of 16 rows is 2048 bytes.
+__device__ __forceinline__ uint32_t desc_n_major(uint32_t addr) { return (addr >> 4) | ((kChunkBytes >> 4) << 16); }
+__host__ __device__ constexpr uint32_t n_major_step(uint32_t step) { return step * (2048u >> 4); }
+
+// D (+)= A B^T over one step of 16, both operands in shared memory;
+// descriptors by their low words.
+template <uint32_t kIdesc, uint32_t kA, uint32_t kB>
+__device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t accumulate,
+                                            uint32_t elected) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, e;\n\t.reg .b32 a, b;\n\t.reg .b64 da, db;\n\t"
+        "setp.ne.b32 p, %3, 0;\n\tsetp.ne.b32 e, %4, 0;\n\t"
+        "add.u32 a, %1, %5;\n\tadd.u32 b, %2, %6;\n\tmov.b64 da, {a, %7};\n\tmov.b64 db, {b, %7};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %8, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(accumulate), "r"(elected), "n"(kA), "n"(kB), "r"(kDescHi), "r"(kIdesc)
         : "memory");
 }
 
 // D (+)= A B, A (two BF16 per column, row = lane) in tensor memory.
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
-                                            uint32_t accumulate) {
+template <uint32_t kIdesc, uint32_t kA, uint32_t kB>
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t accumulate,
+                                            uint32_t elected) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, e;\n\t.reg .b32 a, b;\n\t.reg .b64 db;\n\t"
+        "setp.ne.b32 p, %3, 0;\n\tsetp.ne.b32 e, %4, 0;\n\t"
+        "add.u32 a, %1, %5;\n\tadd.u32 b, %2, %6;\n\tmov.b64 db, {b, %7};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %8, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(accumulate), "r"(elected), "n"(kA), "n"(kB), "r"(kDescHi), "r"(kIdesc)
         : "memory");
 }
 
-// Tiles of 128 rows in shared memory: 64 dims (128 bytes) by 128 rows per
-// 16 KiB chunk, 128-byte swizzle, chunk after chunk.
-constexpr uint32_t kChunkBytes = 128 * 128;
-
-// As a K-major operand (the dims are summed over): 8-row groups 1024 bytes
-// apart; a step of 16 dims is 32 bytes, the fifth starts the next chunk.
-__device__ __forceinline__ uint64_t desc_k_major(uint32_t addr) { return smem_desc(addr, 16, 1024, 2); }
-__device__ __forceinline__ uint64_t k_major_step(uint32_t step) {
-    return (step >> 2) * (kChunkBytes >> 4) + (step & 3u) * 2u;
+// All steps of a 128-row product: scores over kD dims, and the sum over 128
+// rows whose BF16 left operand lies in runs of kRun steps, kRunCols columns
+// apart.
+template <uint32_t kIdesc, uint32_t kD, uint32_t kStep = 0>
+__device__ __forceinline__ void mma_scores(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t elected) {
+    if constexpr (kStep < kD / 16) {
+        mma_bf16_ss<kIdesc, k_major_step(kStep), k_major_step(kStep)>(d_tmem, a_lo, b_lo, kStep ? 1u : 0u, elected);
+        mma_scores<kIdesc, kD, kStep + 1>(d_tmem, a_lo, b_lo, elected);
+    }
 }
-// As an N-major operand (the rows are summed over): 64 dims per chunk, 8-row
-// groups 1024 bytes apart; a step of 16 rows is 2048 bytes.
-__device__ __forceinline__ uint64_t desc_n_major(uint32_t addr) { return smem_desc(addr, kChunkBytes, 1024, 2); }
-__device__ __forceinline__ uint64_t n_major_step(uint32_t step) { return step * (2048u >> 4); }
+template <uint32_t kIdesc, uint32_t kRun, uint32_t kRunCols, uint32_t kStep = 0, uint32_t kEnd = 8>
+__device__ __forceinline__ void mma_sum(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t accumulate,
+                                        uint32_t elected) {
+    if constexpr (kStep < kEnd) {
+        mma_bf16_ts<kIdesc, kStep / kRun * kRunCols + kStep % kRun * 8, n_major_step(kStep)>(
+            d_tmem, a_tmem, b_lo, kStep ? 1u : accumulate, elected);
+        mma_sum<kIdesc, kRun, kRunCols, kStep + 1, kEnd>(d_tmem, a_tmem, b_lo, accumulate, elected);
+    }
+}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
