@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         first = range[0] < range[1] ? range[0] : 0;
         count = range[0] < range[1] ? range[1] - first : 0;
     } else {
-        ts = join_spans(parts);
+        ts = join_spans(join_spans(parts[0], parts[1]), join_spans(parts[2], parts[3]));
         if (ts.lo < ts.hi) {
             first = ts.lo >> 7;
             count = ((ts.hi + 127) >> 7) - first;

@@ -58,8 +58,7 @@ struct TileSpan {
     int lo, hi, all_lo, all_hi;
 };
 
-// The TileSpan of 128 rows, one per thread of four consecutive warps; each
-// warp leaves its part in parts[warp], join_spans joins them after a barrier.
+// The TileSpan of 32 rows, one per lane; join_spans makes the tile's of four.
 // Rows past the end take no part in all_lo and all_hi.
 __device__ __forceinline__ TileSpan warp_span(int2 s, bool row) {
     TileSpan t;
@@ -71,16 +70,12 @@ __device__ __forceinline__ TileSpan warp_span(int2 s, bool row) {
     return t;
 }
 
-__device__ __forceinline__ TileSpan join_spans(const TileSpan* parts) {
-    TileSpan t = parts[0];
-#pragma unroll
-    for (int i = 1; i < 4; ++i) {
-        t.lo = min(t.lo, parts[i].lo);
-        t.hi = max(t.hi, parts[i].hi);
-        t.all_lo = max(t.all_lo, parts[i].all_lo);
-        t.all_hi = min(t.all_hi, parts[i].all_hi);
-    }
-    return t;
+__device__ __forceinline__ TileSpan join_spans(TileSpan a, const TileSpan& b) {
+    a.lo = min(a.lo, b.lo);
+    a.hi = max(a.hi, b.hi);
+    a.all_lo = max(a.all_lo, b.all_lo);
+    a.all_hi = min(a.all_hi, b.all_hi);
+    return a;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {

@@ -9,8 +9,11 @@
 // row.  Per key tile and query tile: S = Q K^T (FP32, tensor memory), P as
 // BF16 over S's own columns, O += P V with P read from tensor memory.  While
 // the softmax of one query tile runs on its four warps, the tensor cores work
-// on the other.  Warps: 0 TMA loads, 1 MMA issue, 4-7 and 8-11 the softmax of
-// the two tiles, one row per thread.
+// on the other; P is handed over in two halves.  Warps: 0 TMA loads, 1 MMA
+// issue, 2 the next item, 4-7 and 8-11 the softmax of the two tiles, one row
+// per thread.  A CTA goes on to blocks of the grid that have not started
+// (cluster launch control), so that the loads and first scores of the next
+// item run under the epilogue of the last.
 //
 // O is rescaled only when a row's maximum has risen by more than 8 (in
 // log2) since it was last scaled: until then P is at most 2^8, which BF16
@@ -35,16 +38,18 @@ template <int kD>
 struct Shape {
     static constexpr uint32_t kChunks = kD / 64;
     static constexpr uint32_t kTile = kChunks * kChunkBytes;
-    static constexpr uint32_t kSlots = kD == 128 ? 5 : 8;   // key and value tiles in flight
-    static constexpr size_t kSmem = (size_t)(2 + kSlots) * kTile + 1024 /*align*/ + 512 /*barriers, spans*/;
+    static constexpr uint32_t kSlots = kD == 128 ? 4 : 8;   // key and value tiles in flight
+    static constexpr uint32_t kStageAt = (2 + kSlots) * kTile;
+    static constexpr uint32_t kBarAt = kStageAt + 8 * 4096;  // 32 rows x 64 dims of output per softmax warp
+    static constexpr size_t kSmem = kBarAt + 1024;           // dynamic shared memory starts 1024-byte aligned (checked)
 };
 static_assert(Shape<128>::kSmem <= 232448 && Shape<64>::kSmem <= 232448, "shared memory budget");
 
 struct Params {
     int64_t tokens;
-    int32_t q_heads, group;          // query heads per key head
-    int32_t pair_heads;              // the CTA's tiles: two heads of one tile, or two tiles of one head
-    int32_t tiles;                   // work items along the tokens
+    int32_t group;                   // query heads per key head
+    int32_t pair_heads;              // an item's tiles: two heads of one tile, or two tiles of one head
+    int32_t tiles;                   // items along the tokens
     uint32_t items_per_tile;         // ... and across heads
     Scores sc;
     const float* slopes;
@@ -52,6 +57,15 @@ struct Params {
     float* lse;
     Extent xlse;
     uint64_t timeout_ns;
+};
+
+// One item: two query tiles, the key tiles [first, last) each of them sees
+// (first >= last: none) and their spans.
+struct Item {
+    int valid, kv_head;
+    int head[2], tile[2], first[2], last[2];
+    TileSpan span[2];
+    int pad[2];
 };
 
 struct Ring {
@@ -64,36 +78,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                              const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o,
                              const __grid_constant__ Params p) {
     using S = Shape<kD>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* ring = smem + 2 * S::kTile;
-    uint64_t* full = reinterpret_cast<uint64_t*>(ring + S::kSlots * S::kTile);
+    Item* items = reinterpret_cast<Item*>(smem + S::kBarAt);     // [2] the current and the next
+    uint4* answer = reinterpret_cast<uint4*>(items + 2);
+    uint64_t* full = reinterpret_cast<uint64_t*>(answer + 1);
     uint64_t* empty = full + S::kSlots;
     uint64_t* q_full = empty + S::kSlots;        // [2]
-    uint64_t* s_full = q_full + 2;               // [2] scores written
-    uint64_t* p_full = s_full + 2;               // [2] probabilities written, scores read
-    uint64_t* o_full = p_full + 2;               // [2] the last product done
-    uint64_t* drain = o_full + 2;
+    uint64_t* q_empty = q_full + 2;              // [2] the item's scores done
+    uint64_t* s_full = q_empty + 2;              // [2] scores written
+    uint64_t* p_half = s_full + 2;               // [2] scores read, the first 64 columns of P written
+    uint64_t* p_full = p_half + 2;               // [2] all of P written
+    uint64_t* o_full = p_full + 2;               // [2] the item's last product done
+    uint64_t* o_empty = o_full + 2;              // [2] its result read
+    uint64_t* item_full = o_empty + 2;           // [2]
+    uint64_t* item_empty = item_full + 2;        // [2] read by loads, MMA and softmax warps
+    uint64_t* answered = item_empty + 2;
+    uint64_t* drain = answered + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile uint32_t* abort_flag = tmem_slot + 1;
-    TileSpan* parts = reinterpret_cast<TileSpan*>(tmem_slot + 4);   // [8]
 
     const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31u;
-    // the last tiles first: with a causal mask they are the longest
-    const uint32_t item = blockIdx.x % p.items_per_tile;
-    const int32_t ti = p.tiles - 1 - (int32_t)(blockIdx.x / p.items_per_tile);
-    int32_t head[2], tile[2];
-    if (p.pair_heads) {
-        head[0] = 2 * (int32_t)item;
-        head[1] = head[0] + 1;
-        tile[0] = tile[1] = ti;
-    } else {
-        head[0] = head[1] = (int32_t)item;
-        tile[0] = 2 * ti;
-        tile[1] = tile[0] + 1;
-    }
-    const int32_t kv_head = head[0] / p.group;
-
     if (threadIdx.x == 0) {
         for (uint32_t i = 0; i < S::kSlots; ++i) {
             mbar_init(&full[i], 1);
@@ -101,10 +106,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1);
             mbar_init(&s_full[i], 1);
+            mbar_init(&p_half[i], 4);
             mbar_init(&p_full[i], 4);
             mbar_init(&o_full[i], 1);
+            mbar_init(&o_empty[i], 4);
+            mbar_init(&item_full[i], 1);
+            mbar_init(&item_empty[i], 10);
         }
+        mbar_init(answered, 1);
         mbar_init(drain, 1);
         *abort_flag = 0u;
         fence_barrier_init();
@@ -119,73 +130,66 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(tmem_slot, kTmemCols);
         tmem_relinquish();
     }
-    const uint32_t mine = (warp - kFirstSoftmaxWarp) >> 2;            // softmax warps: which tile
-    const uint32_t row = (warp & 3u) * 32 + lane;                     // ... and row
-    int2 span = make_int2(0, 0);
-    int64_t token = 0;
-    if (warp >= kFirstSoftmaxWarp) {
-        token = (int64_t)(mine ? tile[1] : tile[0]) * 128 + row;
-        span = span_of(p.spans, token, p.tokens);
-        const TileSpan t = warp_span(span, token < p.tokens);
-        if (lane == 0) parts[warp - kFirstSoftmaxWarp] = t;
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    TileSpan ts[2];
-    int first[2], last[2];                                            // key tiles [first, last) of each query tile
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        ts[x] = join_spans(parts + 4 * x);
-        const bool some = ts[x].lo < ts[x].hi;
-        first[x] = __shfl_sync(0xFFFFFFFFu, some ? ts[x].lo >> 7 : INT32_MAX, 0);
-        last[x] = __shfl_sync(0xFFFFFFFFu, some ? (ts[x].hi + 127) >> 7 : 0, 0);
-    }
-    const int begin = min(first[0], first[1]), end = max(last[0], last[1]);
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
+
+    auto give_up = [&](bool one) {
+        if (one) {
+            *abort_flag = 1u;
+            atomicOr(&g_attention_status, kStatusTimeoutBit);
+        }
+    };
 
     if (warp < kFirstSoftmaxWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" ::: "memory");
         if (warp == 0 && lane == 0) {
             // ------------------------------------------------------- loads
-            uint32_t issued = 0;   // loads into the ring
+            uint32_t issued = 0, q_loads[2] = {0, 0};
             Ring r;
             bool ok = true;
+            auto await = [&](uint64_t* bar, uint32_t parity) {
+                if (ok && !mbar_wait_or_abort(bar, parity, p.timeout_ns, abort_flag)) ok = false;
+                return ok;
+            };
+            for (uint32_t it = 0; await(&item_full[it & 1u], (it >> 1) & 1u); ++it) {
+                const Item item = items[it & 1u];
+                mbar_arrive(&item_empty[it & 1u]);
+                if (!item.valid) break;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                if (first[x] >= last[x]) continue;
-                mbar_arrive_expect_tx(&q_full[x], S::kTile);
-                for (uint32_t c = 0; c < S::kChunks; ++c)
-                    tma_load_3d(smem + x * S::kTile + c * kChunkBytes, &map_q, &q_full[x], (int32_t)c * 64, head[x],
-                                tile[x] * 128);
-            }
-            for (int kt = begin; kt < end && ok; ++kt) {
-                if (!(kt >= first[0] && kt < last[0]) && !(kt >= first[1] && kt < last[1])) continue;
-                for (int kv = 0; kv < 2 && ok; ++kv) {
-                    if (!mbar_wait_or_abort(&empty[r.slot], r.phase ^ 1u, p.timeout_ns, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_arrive_expect_tx(&full[r.slot], S::kTile);
+                for (int x = 0; x < 2; ++x) {
+                    if (item.first[x] >= item.last[x]) continue;
+                    if (!await(&q_empty[x], (q_loads[x] & 1u) ^ 1u)) break;
+                    ++q_loads[x];
+                    mbar_arrive_expect_tx(&q_full[x], S::kTile);
                     for (uint32_t c = 0; c < S::kChunks; ++c)
-                        tma_load_3d(ring + r.slot * S::kTile + c * kChunkBytes, kv ? &map_v : &map_k, &full[r.slot],
-                                    (int32_t)c * 64, kv_head, kt * 128);
-                    ++issued;
-                    if (++r.slot == S::kSlots) {
-                        r.slot = 0;
-                        r.phase ^= 1u;
+                        tma_load_3d(smem + x * S::kTile + c * kChunkBytes, &map_q, &q_full[x], (int32_t)c * 64,
+                                    item.head[x], item.tile[x] * 128);
+                }
+                const int end = max(item.last[0], item.last[1]);
+                for (int kt = min(item.first[0], item.first[1]); kt < end && ok; ++kt) {
+                    if (!(kt >= item.first[0] && kt < item.last[0]) && !(kt >= item.first[1] && kt < item.last[1])) continue;
+                    for (int kv = 0; kv < 2; ++kv) {
+                        if (!await(&empty[r.slot], r.phase ^ 1u)) break;
+                        mbar_arrive_expect_tx(&full[r.slot], S::kTile);
+                        for (uint32_t c = 0; c < S::kChunks; ++c)
+                            tma_load_3d(ring + r.slot * S::kTile + c * kChunkBytes, kv ? &map_v : &map_k,
+                                        &full[r.slot], (int32_t)c * 64, item.kv_head, kt * 128);
+                        ++issued;
+                        if (++r.slot == S::kSlots) {
+                            r.slot = 0;
+                            r.phase ^= 1u;
+                        }
                     }
                 }
             }
-            if (!ok) {
-                *abort_flag = 1u;
-                atomicOr(&g_attention_status, kStatusTimeoutBit);
-            }
+            give_up(!ok);
             // every load has landed before the CTA exits (at once, unless a
             // wait ran out: then nothing else waits for them)
 #pragma unroll
             for (int x = 0; x < 2; ++x)
-                if (first[x] < last[x]) (void)mbar_wait(&q_full[x], 0, p.timeout_ns);
+                if (q_loads[x]) (void)mbar_wait(&q_full[x], (q_loads[x] - 1) & 1u, p.timeout_ns);
             for (uint32_t back = 0; back < S::kSlots && back < issued; ++back) {
                 const uint32_t n = issued - 1 - back;
                 (void)mbar_wait(&full[n % S::kSlots], (n / S::kSlots) & 1u, p.timeout_ns);
@@ -195,237 +199,323 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t kIdS = idesc_bf16(128, 128, false);
             constexpr uint32_t kIdO = idesc_bf16(128, kD, true);
             const uint32_t elected = elect_one();
-            const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
             const uint32_t q_lo = desc_k_major(smem_u32(smem)), k_lo = desc_k_major(smem_u32(ring)),
                            v_lo = desc_n_major(smem_u32(ring));
             Ring r;
             bool ok = true;
-            uint32_t p_phase[2] = {0, 0};
-            bool started[2] = {false, false};
+            uint32_t p_phase[2] = {0, 0}, q_items[2] = {0, 0}, o_items[2] = {0, 0};
             auto await = [&](uint64_t* bar, uint32_t parity) {
                 if (ok && !warp_wait_or_abort(bar, parity, p.timeout_ns, abort_flag)) ok = false;
+                return ok;
             };
-            auto in = [&](int x, int kt) { return kt >= first[x] && kt < last[x]; };
             auto advance = [&](Ring& q) {
                 if (++q.slot == S::kSlots) {
                     q.slot = 0;
                     q.phase ^= 1u;
                 }
             };
-            auto scores = [&](int x, uint32_t slot) {
-                mma_scores<kIdS, kD>(tm + kScoreCol + 128 * x, q_lo + x * (S::kTile >> 4), k_lo + slot * (S::kTile >> 4),
-                                     elected);
-                tc_commit(&s_full[x], elected);
-            };
-            int kt = begin;
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-                if (first[x] < last[x]) await(&q_full[x], 0);
-            if (kt < end) {
-                await(&full[r.slot], r.phase);
-                tc_fence_after();
-                if (ok) {
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        if (in(x, kt)) scores(x, r.slot);
-                }
-                if (ok) tc_commit(&empty[r.slot], elected);
-                advance(r);
-            }
-            while (kt < end && ok) {
-                int nk = kt + 1;
-                while (nk < end && !in(0, nk) && !in(1, nk)) ++nk;
-                const Ring v = r;
-                advance(r);
-                const Ring k = r;
-                await(&full[v.slot], v.phase);
+            for (uint32_t it = 0; await(&item_full[it & 1u], (it >> 1) & 1u); ++it) {
+                const Item& item = items[it & 1u];
+                const int valid = __shfl_sync(0xFFFFFFFFu, item.valid, 0);
+                int first[2], last[2];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    if (in(x, kt)) {
-                        await(&p_full[x], p_phase[x]);
-                        p_phase[x] ^= 1u;
-                        if (!ok) break;
-                        tc_fence_after();
-                        mma_sum<kIdO, 8, 64>(tm + kOutCol + 128 * x, tm + kScoreCol + 128 * x,
-                                             v_lo + v.slot * (S::kTile >> 4), started[x] ? 1u : 0u, elected);
-                        started[x] = true;
-                        if (kt + 1 == last[x]) tc_commit(&o_full[x], elected);
-                    }
-                    if (nk < end && in(x, nk)) {
-                        await(&full[k.slot], k.phase);
-                        if (!ok) break;
-                        tc_fence_after();
-                        scores(x, k.slot);
-                    }
+                    first[x] = __shfl_sync(0xFFFFFFFFu, item.first[x], 0);
+                    last[x] = __shfl_sync(0xFFFFFFFFu, item.last[x], 0);
                 }
-                if (!ok) break;
-                tc_commit(&empty[v.slot], elected);
-                if (nk < end) {
-                    tc_commit(&empty[k.slot], elected);
+                if (lane == 0) mbar_arrive(&item_empty[it & 1u]);
+                if (!valid) break;
+                bool started[2] = {false, false};
+                auto in = [&](int x, int kt) { return kt >= first[x] && kt < last[x]; };
+                auto scores = [&](int x, int kt, uint32_t slot) {
+                    mma_scores<kIdS, kD>(tmem + kScoreCol + 128 * x, q_lo + x * (S::kTile >> 4),
+                                         k_lo + slot * (S::kTile >> 4), elected);
+                    tc_commit(&s_full[x], elected);
+                    if (kt + 1 == last[x]) tc_commit(&q_empty[x], elected);
+                };
+                int kt = min(first[0], first[1]);
+                const int end = max(last[0], last[1]);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    if (first[x] < last[x]) await(&q_full[x], q_items[x]++ & 1u);
+                if (kt < end) {
+                    await(&full[r.slot], r.phase);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        if (in(x, kt)) scores(x, kt, r.slot);
+                    tc_commit(&empty[r.slot], elected);
                     advance(r);
                 }
-                kt = nk;
+                while (kt < end && ok) {
+                    int nk = kt + 1;
+                    while (nk < end && !in(0, nk) && !in(1, nk)) ++nk;
+                    const Ring v = r;
+                    advance(r);
+                    const Ring k = r;
+                    await(&full[v.slot], v.phase);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if (ok && in(x, kt)) {
+                            // O still holds the last item's result until it has been read
+                            if (!started[x]) await(&o_empty[x], (o_items[x]++ & 1u) ^ 1u);
+                            const uint32_t o = tmem + kOutCol + 128 * x, pr = tmem + kScoreCol + 128 * x,
+                                           vl = v_lo + v.slot * (S::kTile >> 4);
+                            if (await(&p_half[x], p_phase[x])) {
+                                tc_fence_after();
+                                mma_sum<kIdO, 8, 64, 0, 4>(o, pr, vl, started[x] ? 1u : 0u, elected);
+                            }
+                            if (await(&p_full[x], p_phase[x])) {
+                                tc_fence_after();
+                                mma_sum<kIdO, 8, 64, 4, 8>(o, pr, vl, 1u, elected);
+                                if (kt + 1 == last[x]) tc_commit(&o_full[x], elected);
+                            }
+                            p_phase[x] ^= 1u;
+                            started[x] = true;
+                        }
+                        if (nk < end && in(x, nk) && await(&full[k.slot], k.phase)) {
+                            tc_fence_after();
+                            scores(x, nk, k.slot);
+                        }
+                    }
+                    if (!ok) break;
+                    tc_commit(&empty[v.slot], elected);
+                    if (nk < end) {
+                        tc_commit(&empty[k.slot], elected);
+                        advance(r);
+                    }
+                    kt = nk;
+                }
             }
-            if (!ok && elected) {
-                *abort_flag = 1u;
-                atomicOr(&g_attention_status, kStatusTimeoutBit);
-            }
+            give_up(!ok && elected);
             // every product is done before tensor memory is freed
             tc_commit(drain, elected);
             (void)mbar_wait(drain, 0, p.timeout_ns);
+        } else if (warp == 2) {
+            // ------------------------------------------------------- items
+            // The CTA's own block first, then blocks that have not started,
+            // taken over one ahead of the work: loads and scores of the next
+            // item run under the last one's epilogue.
+            uint32_t block = blockIdx.x;
+            bool valid = true, ok = true;
+            for (uint32_t it = 0;; ++it) {
+                Item item{};
+                item.valid = valid ? 1 : 0;
+                if (valid) {
+                    // the last tiles first: with a causal mask they are the longest
+                    const int n = (int)(block % p.items_per_tile), ti = p.tiles - 1 - (int)(block / p.items_per_tile);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        item.head[x] = p.pair_heads ? 2 * n + x : n;
+                        item.tile[x] = p.pair_heads ? ti : 2 * ti + x;
+                    }
+                    item.kv_head = item.head[0] / p.group;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if (x == 1 && p.pair_heads) {
+                            item.span[1] = item.span[0];
+                        } else {
+                            TileSpan t{INT32_MAX, 0, 0, INT32_MAX};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const int64_t token = (int64_t)item.tile[x] * 128 + 32 * j + lane;
+                                t = join_spans(t, warp_span(span_of(p.spans, token, p.tokens), token < p.tokens));
+                            }
+                            item.span[x] = t;
+                        }
+                        const bool some = item.span[x].lo < item.span[x].hi;
+                        item.first[x] = some ? item.span[x].lo >> 7 : INT32_MAX;
+                        item.last[x] = some ? (item.span[x].hi + 127) >> 7 : 0;
+                    }
+                }
+                ok = warp_wait_or_abort(&item_empty[it & 1u], ((it >> 1) & 1u) ^ 1u, p.timeout_ns, abort_flag);
+                if (!ok) break;
+                if (lane == 0) {
+                    items[it & 1u] = item;
+                    mbar_arrive(&item_full[it & 1u]);
+                    if (valid) {
+                        mbar_arrive_expect_tx(answered, 16);
+                        claim_block(answer, answered);
+                    }
+                }
+                if (!valid) break;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(answered, it & 1u, p.timeout_ns));
+                if (!ok) break;
+                valid = claimed_block(answer, block);
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            give_up(!ok && lane == 0);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
         // --------------------------------------------------------- softmax
-        const uint32_t x = mine;
-        const TileSpan my = x ? ts[1] : ts[0];
-        const int my_first = x ? first[1] : first[0], my_last = x ? last[1] : last[0];
-        const int32_t my_head = x ? head[1] : head[0];
+        const uint32_t x = (warp - kFirstSoftmaxWarp) >> 2, row = (warp & 3u) * 32 + lane;
         const uint32_t lanes = tmem + (((warp & 3u) * 32u) << 16);
         const uint32_t s_at = lanes + kScoreCol + 128 * x, o_at = lanes + kOutCol + 128 * x;
-        const float slope = p.slopes ? p.slopes[my_head] * kLog2e : 0.0f;
+        uint8_t* stage = smem + S::kStageAt + (warp - kFirstSoftmaxWarp) * 4096;
         const bool plain = !p.sc.capped && !p.slopes;
         const float c = plain ? p.sc.mult : 1.0f;      // scores in registers times c are in log2
-        float m = -INFINITY, l = 0.0f;                 // maximum (log2) that P and O are scaled by; sum
-        uint32_t phase = 0, n = 0;                     // n: key tiles of the CTA so far
+        uint32_t s_phase = 0, o_phase = 0, n = 0;      // n: key tiles of the CTA so far
         bool ok = true;
-        for (int kt = begin; kt < end; ++kt) {
-            const bool in0 = kt >= first[0] && kt < last[0], in1 = kt >= first[1] && kt < last[1];
-            if (!in0 && !in1) continue;
-            const uint32_t load = 2 * n++ + 1;         // the value tile's place among the loads
-            if (!(x ? in1 : in0)) continue;
-            if (!warp_wait_or_abort(&s_full[x], phase, p.timeout_ns, abort_flag)) {
-                ok = false;
-                break;
-            }
-            phase ^= 1u;
-            tc_fence_after();
-            const int k0 = kt * 128;
-            float s[128];
-            {
-                uint32_t* r = reinterpret_cast<uint32_t*>(s);
+        for (uint32_t it = 0;; ++it) {
+            ok = warp_wait_or_abort(&item_full[it & 1u], (it >> 1) & 1u, p.timeout_ns, abort_flag);
+            if (!ok) break;
+            const Item& item = items[it & 1u];
+            const bool valid = item.valid != 0;
+            const int first = item.first[x], last = item.last[x], first2 = item.first[x ^ 1u], last2 = item.last[x ^ 1u];
+            const int all_lo = item.span[x].all_lo, all_hi = item.span[x].all_hi;
+            const int cta_lo = min(item.span[0].lo, item.span[1].lo), cta_hi = max(item.span[0].hi, item.span[1].hi);
+            const int head = item.head[x], tile = item.tile[x];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&item_empty[it & 1u]);
+            if (!valid) break;
+            const int64_t token = (int64_t)tile * 128 + row;
+            const int2 span = span_of(p.spans, token, p.tokens);
+            const float slope = p.slopes ? p.slopes[head] * kLog2e : 0.0f;
+            float m = -INFINITY, l = 0.0f;             // maximum (log2) that P and O are scaled by; sum
+            const int end = max(last, last2);
+            for (int kt = min(first, first2); kt < end; ++kt) {
+                const bool mine = kt >= first && kt < last;
+                if (!mine && !(kt >= first2 && kt < last2)) continue;
+                const uint32_t load = 2 * n++ + 1;     // the value tile's place among the loads
+                if (!mine) continue;
+                ok = warp_wait_or_abort(&s_full[x], s_phase, p.timeout_ns, abort_flag);
+                if (!ok) break;
+                s_phase ^= 1u;
+                tc_fence_after();
+                const int k0 = kt * 128;
+                float s[128];
+                {
+                    uint32_t* r = reinterpret_cast<uint32_t*>(s);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(s_at + 32 * i, r + 32 * i);
-                tmem_ld_wait();
-            }
-            if (p.sc.capped) {
+                    for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(s_at + 32 * i, r + 32 * i);
+                    tmem_ld_wait();
+                }
+                if (p.sc.capped) {
 #pragma unroll
-                for (int j = 0; j < 128; ++j) s[j] = capped_tanh(s[j], p.sc.mult) * p.sc.cap_log2;
-            }
-            if (p.slopes) {
-                const float f = p.sc.capped ? 1.0f : p.sc.mult, d = (float)((int)token - k0);
+                    for (int j = 0; j < 128; ++j) s[j] = capped_tanh(s[j], p.sc.mult) * p.sc.cap_log2;
+                }
+                if (p.slopes) {
+                    const float f = p.sc.capped ? 1.0f : p.sc.mult, d = (float)((int)token - k0);
 #pragma unroll
-                for (int j = 0; j < 128; ++j) s[j] = fmaf(-slope, fabsf(d - (float)j), s[j] * f);
-            }
-            if (k0 < my.all_lo || k0 + 128 > my.all_hi) {
-                const int lo = span.x - k0, hi = span.y - k0;
+                    for (int j = 0; j < 128; ++j) s[j] = fmaf(-slope, fabsf(d - (float)j), s[j] * f);
+                }
+                if (k0 < all_lo || k0 + 128 > all_hi) {
+                    const int lo = span.x - k0, hi = span.y - k0;
 #pragma unroll
-                for (int j = 0; j < 128; ++j)
-                    if (j < lo || j >= hi) s[j] = -INFINITY;
-            }
-            float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-            for (int j = 4; j < 128; j += 4) {
-                mx[0] = fmaxf(mx[0], s[j]);
-                mx[1] = fmaxf(mx[1], s[j + 1]);
-                mx[2] = fmaxf(mx[2], s[j + 2]);
-                mx[3] = fmaxf(mx[3], s[j + 3]);
-            }
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-            // rescale what has been summed when the maximum has risen far
-            // enough (the first finite one counts as such)
-            const bool rise = top > m + kRescale;
-            if (__any_sync(0xFFFFFFFFu, rise)) {
-                const float f = rise ? ex2(m - top) : 1.0f;   // m = -inf: nothing summed yet, f = 0
-                if (rise) m = top;
-                l *= f;
-                if (kt != my_first) {
-#pragma unroll
-                    for (int i = 0; i < kD / 32; ++i) {
-                        uint32_t o[32];
-                        tmem_ld_32x32b_x32(o_at + 32 * i, o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                        tmem_st_32x32b_x32(o_at + 32 * i, o);
+                    for (int j = 0; j < 128; ++j)
+                        if (j < lo || j >= hi) s[j] = -INFINITY;
+                    // value rows that no row of the CTA reads may hold anything
+                    // (their P is 0): they are zeroed for the product
+                    if (k0 < cta_lo || k0 + 128 > cta_hi) {
+                        const uint32_t slot = load % S::kSlots;
+                        ok = warp_wait_or_abort(&full[slot], (load / S::kSlots) & 1u, p.timeout_ns, abort_flag);
+                        if (!ok) break;
+                        const int key = k0 + (int)row;
+                        if (key < cta_lo || key >= cta_hi) zero_tile_row(ring + slot * S::kTile, row, S::kChunks);
+                        fence_proxy_async_smem();
                     }
                 }
-            }
-            const float base = m == -INFINITY ? 0.0f : m;     // a row with no key so far: ex2(-inf) = 0
-            float sum[4] = {};
-            uint32_t pk[64];
+                float mx[4] = {max3(s[0], s[1], s[2]), max3(s[3], s[4], s[5]), max3(s[6], s[7], s[8]), s[9]};
 #pragma unroll
-            for (int j = 0; j < 128; j += 4) {
-                const float e0 = ex2(fmaf(s[j], c, -base)), e1 = ex2(fmaf(s[j + 1], c, -base));
-                const float e2 = ex2(fmaf(s[j + 2], c, -base)), e3 = ex2(fmaf(s[j + 3], c, -base));
-                sum[0] += e0;
-                sum[1] += e1;
-                sum[2] += e2;
-                sum[3] += e3;
-                pk[j / 2] = pack_bf16(e0, e1);
-                pk[j / 2 + 1] = pack_bf16(e2, e3);
-            }
-            tmem_st_32x32b_x32(s_at, pk);
-            tmem_st_32x32b_x32(s_at + 32, pk + 32);
-            // value rows that no row of the CTA reads may hold anything (their
-            // P is 0): they are zeroed for the product
-            const int lo_all = min(ts[0].lo, ts[1].lo), hi_all = max(ts[0].hi, ts[1].hi);
-            if (k0 < lo_all || k0 + 128 > hi_all) {
-                if (!warp_wait_or_abort(&full[load % S::kSlots], (load / S::kSlots) & 1u, p.timeout_ns, abort_flag)) {
-                    ok = false;
-                    break;
+                for (int j = 10; j < 122; j += 8) {
+                    mx[0] = max3(mx[0], s[j], s[j + 1]);
+                    mx[1] = max3(mx[1], s[j + 2], s[j + 3]);
+                    mx[2] = max3(mx[2], s[j + 4], s[j + 5]);
+                    mx[3] = max3(mx[3], s[j + 6], s[j + 7]);
                 }
-                const int key = k0 + (int)row;
-                if (key < lo_all || key >= hi_all)
-                    zero_tile_row(ring + (load % S::kSlots) * S::kTile, row, S::kChunks);
-                fence_proxy_async_smem();
+                mx[0] = max3(mx[0], s[122], s[123]);
+                mx[1] = max3(mx[1], s[124], s[125]);
+                mx[2] = max3(mx[2], s[126], s[127]);
+                const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
+                // rescale what has been summed when the maximum has risen far
+                // enough (the first finite one counts as such)
+                const bool rise = top > m + kRescale;
+                if (__any_sync(0xFFFFFFFFu, rise)) {
+                    const float f = rise ? ex2(m - top) : 1.0f;   // m = -inf: nothing summed yet, f = 0
+                    if (rise) m = top;
+                    l *= f;
+                    if (kt != first) {
+#pragma unroll 1
+                        for (uint32_t i = 0; i < kD; i += 16) {
+                            uint32_t o[16];
+                            tmem_ld_32x32b_x16(o_at + i, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            tmem_st_32x32b_x16(o_at + i, o);
+                        }
+                    }
+                }
+                const float base = m == -INFINITY ? 0.0f : m;     // a row with no key so far: ex2(-inf) = 0
+                const uint64_t c2 = pair(c, c), b2 = pair(-base, -base);
+                uint64_t sum[2] = {pair(l, 0.0f), 0};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const int j = 64 * h + 2 * i;
+                        float e0, e1;
+                        unpair(fma2(pair(s[j], s[j + 1]), c2, b2), e0, e1);
+                        e0 = ex2(e0);
+                        e1 = ex2(e1);
+                        sum[i & 1] = add2(sum[i & 1], pair(e0, e1));
+                        pk[i] = pack_bf16(e0, e1);
+                    }
+                    tmem_st_32x32b_x32(s_at + 32 * h, pk);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(h ? &p_full[x] : &p_half[x]);
+                }
+                float l0, l1;
+                unpair(add2(sum[0], sum[1]), l0, l1);
+                l = l0 + l1;
             }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[x]);
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        }
-        // ------------------------------------------------------- epilogue
-        if (ok && my_first < my_last) ok = warp_wait_or_abort(&o_full[x], 0, p.timeout_ns, abort_flag);
-        if (!ok && lane == 0) {
-            *abort_flag = 1u;
-            atomicOr(&g_attention_status, kStatusTimeoutBit);
-        }
-        const int64_t row0 = token - lane;
-        if (ok && row0 < p.tokens) {
+            // --------------------------------------------------- epilogue
+            if (ok && first < last) {
+                ok = warp_wait_or_abort(&o_full[x], o_phase, p.timeout_ns, abort_flag);
+                o_phase ^= 1u;
+            }
+            if (!ok) break;
             tc_fence_after();
-            const float f = l > 0.0f ? 1.0f / l : 0.0f;
-            uint8_t* stage = smem + x * S::kTile;      // the query tile's place: its products are done
+            const bool some = l > 0.0f;
+            const float f = some ? 1.0f / l : 0.0f;
+            const int64_t row0 = token - lane;
+#pragma unroll 1
+            for (uint32_t ch = 0; ch < S::kChunks; ++ch) {
+                if (lane == 0) bulk_wait_read_all();   // the place's last store
+                __syncwarp();
 #pragma unroll
-            for (int i = 0; i < kD / 32; ++i) {
-                uint32_t o[32];
-                if (my_first < my_last) {
-                    tmem_ld_32x32b_x32(o_at + 32 * i, o);
+                for (uint32_t h = 0; h < 2; ++h) {
+                    uint32_t o[32];
+                    tmem_ld_32x32b_x32(o_at + 64 * ch + 32 * h, o);
                     tmem_ld_wait();
-                } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = 0;
+                    for (int j = 0; j < 32; ++j)
+                        if (!some) o[j] = 0;           // nothing summed: the columns may hold anything
+                    stage_row_32(stage, lane, h, o, f);
                 }
-                if (!(l > 0.0f)) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = 0;
+                if (first < last && ch + 1 == S::kChunks) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&o_empty[x]);
                 }
-                stage_row_32(stage + (i >> 1) * kChunkBytes, row, i & 1, o, f);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                for (uint32_t ch = 0; ch < S::kChunks; ++ch)
-                    tma_store_3d(&map_o, stage + ch * kChunkBytes + (warp & 3u) * 4096, (int32_t)ch * 64, my_head,
-                                 (int32_t)row0);
-                bulk_commit_group();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0 && row0 < p.tokens) {
+                    tma_store_3d(&map_o, stage, (int32_t)ch * 64, head, (int32_t)row0);
+                    bulk_commit_group();
+                }
             }
             if (token < p.tokens)
-                store_out(p.lse + (int64_t)my_head * p.tokens + token,
-                          l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY, p.xlse);
-            if (lane == 0) bulk_wait_all();
+                store_out(p.lse + (int64_t)head * p.tokens + token, some ? (m + log2f(l)) * kLn2 : -INFINITY, p.xlse);
         }
+        give_up(!ok && lane == 0);
+        if (lane == 0) bulk_wait_all();
     }
     __syncwarp();
     tc_fence_before();
@@ -445,7 +535,10 @@ cudaError_t prepare_kernel() {
     if (done[dev]) return cudaSuccess;
     cudaFuncAttributes f;
     cudaError_t e = cudaFuncGetAttributes(&f, attention_forward_kernel<kD>);
-    if (e == cudaSuccess && f.numRegs * kThreads < 128 * 80 + 256 * 208) e = cudaErrorInvalidConfiguration;
+    // the tiles' swizzle needs dynamic shared memory to start on 1024 bytes:
+    // it does when there is no static shared memory before it
+    if (e == cudaSuccess && (f.numRegs * kThreads < 128 * 80 + 256 * 208 || f.sharedSizeBytes != 0))
+        e = cudaErrorInvalidConfiguration;
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(attention_forward_kernel<kD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)Shape<kD>::kSmem);
@@ -465,7 +558,6 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     Params p{};
     p.tokens = a.tokens;
-    p.q_heads = a.q_heads;
     p.group = a.q_heads / a.kv_heads;
     // two heads with the same keys have the same mask; an odd group has none to spare
     p.pair_heads = p.group % 2 == 0 ? 1 : 0;
