@@ -9,7 +9,7 @@
 // row.  Per key tile and query tile: S = Q K^T (FP32, tensor memory), P as
 // BF16 over S's own columns, O += P V with P read from tensor memory.  While
 // the softmax of one query tile runs on its four warps, the tensor cores work
-// on the other; P is handed over in two halves.  Warps: 0 TMA loads, 1 MMA
+// on the other.  Warps: 0 TMA loads, 1 MMA
 // issue, 2 the next item, 4-7 and 8-11 the softmax of the two tiles, one row
 // per thread.  A CTA goes on to blocks of the grid that have not started
 // (cluster launch control), so that the loads and first scores of the next
@@ -38,8 +38,10 @@ template <int kD>
 struct Shape {
     static constexpr uint32_t kChunks = kD / 64;
     static constexpr uint32_t kTile = kChunks * kChunkBytes;
-    static constexpr uint32_t kSlots = kD == 128 ? 4 : 8;   // key and value tiles in flight
-    static constexpr uint32_t kStageAt = (2 + kSlots) * kTile;
+    // A stage of the ring holds what one step of the MMA warp needs: the value
+    // tile of the step before, then the key tile of this one.
+    static constexpr uint32_t kStages = kD == 128 ? 2 : 4;
+    static constexpr uint32_t kStageAt = (2 + 2 * kStages) * kTile;
     static constexpr uint32_t kBarAt = kStageAt + 8 * 4096;  // 32 rows x 64 dims of output per softmax warp
     static constexpr size_t kSmem = kBarAt + 1024;           // dynamic shared memory starts 1024-byte aligned (checked)
 };
@@ -60,7 +62,8 @@ struct Params {
 };
 
 // One item: two query tiles, the key tiles [first, last) each of them sees
-// (first >= last: none) and their spans.
+// (first >= last: none) and their spans.  The key tiles from the lower first
+// to the higher last are loaded; a query tile passes over those not its own.
 struct Item {
     int valid, kv_head;
     int head[2], tile[2], first[2], last[2];
@@ -83,12 +86,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     Item* items = reinterpret_cast<Item*>(smem + S::kBarAt);     // [2] the current and the next
     uint4* answer = reinterpret_cast<uint4*>(items + 2);
     uint64_t* full = reinterpret_cast<uint64_t*>(answer + 1);
-    uint64_t* empty = full + S::kSlots;
-    uint64_t* q_full = empty + S::kSlots;        // [2]
+    uint64_t* empty = full + S::kStages;
+    uint64_t* q_full = empty + S::kStages;        // [2]
     uint64_t* q_empty = q_full + 2;              // [2] the item's scores done
     uint64_t* s_full = q_empty + 2;              // [2] scores written
-    uint64_t* p_half = s_full + 2;               // [2] scores read, the first 64 columns of P written
-    uint64_t* p_full = p_half + 2;               // [2] all of P written
+    uint64_t* p_full = s_full + 2;               // [2] scores read, P written
     uint64_t* o_full = p_full + 2;               // [2] the item's last product done
     uint64_t* o_empty = o_full + 2;              // [2] its result read
     uint64_t* item_full = o_empty + 2;           // [2]
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31u;
     if (threadIdx.x == 0) {
-        for (uint32_t i = 0; i < S::kSlots; ++i) {
+        for (uint32_t i = 0; i < S::kStages; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
@@ -108,7 +110,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&q_full[i], 1);
             mbar_init(&q_empty[i], 1);
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_half[i], 4);
             mbar_init(&p_full[i], 4);
             mbar_init(&o_full[i], 1);
             mbar_init(&o_empty[i], 4);
@@ -153,6 +154,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ok && !mbar_wait_or_abort(bar, parity, p.timeout_ns, abort_flag)) ok = false;
                 return ok;
             };
+            int v_head = 0, v_tile = -1;   // the value tile that goes with the next stage
+            auto stage = [&](bool with_key, int head, int kt) {
+                if (!await(&empty[r.slot], r.phase ^ 1u)) return;
+                uint8_t* to = ring + r.slot * 2 * S::kTile;
+                mbar_arrive_expect_tx(&full[r.slot], (with_key ? S::kTile : 0u) + (v_tile >= 0 ? S::kTile : 0u));
+                for (uint32_t c = 0; c < S::kChunks; ++c) {
+                    if (v_tile >= 0)
+                        tma_load_3d(to + c * kChunkBytes, &map_v, &full[r.slot], (int32_t)c * 64, v_head, v_tile * 128);
+                    if (with_key)
+                        tma_load_3d(to + S::kTile + c * kChunkBytes, &map_k, &full[r.slot], (int32_t)c * 64, head, kt * 128);
+                }
+                ++issued;
+                if (++r.slot == S::kStages) {
+                    r.slot = 0;
+                    r.phase ^= 1u;
+                }
+            };
             for (uint32_t it = 0; await(&item_full[it & 1u], (it >> 1) & 1u); ++it) {
                 const Item item = items[it & 1u];
                 mbar_arrive(&item_empty[it & 1u]);
@@ -169,52 +187,57 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const int end = max(item.last[0], item.last[1]);
                 for (int kt = min(item.first[0], item.first[1]); kt < end && ok; ++kt) {
-                    if (!(kt >= item.first[0] && kt < item.last[0]) && !(kt >= item.first[1] && kt < item.last[1])) continue;
-                    for (int kv = 0; kv < 2; ++kv) {
-                        if (!await(&empty[r.slot], r.phase ^ 1u)) break;
-                        mbar_arrive_expect_tx(&full[r.slot], S::kTile);
-                        for (uint32_t c = 0; c < S::kChunks; ++c)
-                            tma_load_3d(ring + r.slot * S::kTile + c * kChunkBytes, kv ? &map_v : &map_k,
-                                        &full[r.slot], (int32_t)c * 64, item.kv_head, kt * 128);
-                        ++issued;
-                        if (++r.slot == S::kSlots) {
-                            r.slot = 0;
-                            r.phase ^= 1u;
-                        }
-                    }
+                    stage(true, item.kv_head, kt);
+                    v_head = item.kv_head;
+                    v_tile = kt;
                 }
             }
+            if (ok && v_tile >= 0) stage(false, 0, 0);
             give_up(!ok);
             // every load has landed before the CTA exits (at once, unless a
             // wait ran out: then nothing else waits for them)
 #pragma unroll
             for (int x = 0; x < 2; ++x)
                 if (q_loads[x]) (void)mbar_wait(&q_full[x], (q_loads[x] - 1) & 1u, p.timeout_ns);
-            for (uint32_t back = 0; back < S::kSlots && back < issued; ++back) {
+            for (uint32_t back = 0; back < S::kStages && back < issued; ++back) {
                 const uint32_t n = issued - 1 - back;
-                (void)mbar_wait(&full[n % S::kSlots], (n / S::kSlots) & 1u, p.timeout_ns);
+                (void)mbar_wait(&full[n % S::kStages], (n / S::kStages) & 1u, p.timeout_ns);
             }
         } else if (warp == 1) {
             // --------------------------------------------------- MMA issue
+            // Per step (a key tile) and query tile x: the product P V of the step
+            // before, then S of this step, which overwrites P behind the product
+            // that reads it (MMAs of one thread run in order).  The order of the
+            // two query tiles keeps their softmaxes half a step apart, and an
+            // item's first scores follow the last item's last products.
             constexpr uint32_t kIdS = idesc_bf16(128, 128, false);
             constexpr uint32_t kIdO = idesc_bf16(128, kD, true);
             const uint32_t elected = elect_one();
-            const uint32_t q_lo = desc_k_major(smem_u32(smem)), k_lo = desc_k_major(smem_u32(ring)),
+            const uint32_t q_lo = desc_k_major(smem_u32(smem)), k_lo = desc_k_major(smem_u32(ring) + S::kTile),
                            v_lo = desc_n_major(smem_u32(ring));
-            Ring r;
+            const uint32_t full0 = smem_u32(full);
+            uint32_t slot = 0, phase = 0, p_phase[2] = {0, 0}, q_items[2] = {0, 0}, o_items[2] = {0, 0};
             bool ok = true;
-            uint32_t p_phase[2] = {0, 0}, q_items[2] = {0, 0}, o_items[2] = {0, 0};
-            auto await = [&](uint64_t* bar, uint32_t parity) {
-                if (ok && !warp_wait_or_abort(bar, parity, p.timeout_ns, abort_flag)) ok = false;
-                return ok;
+            auto await = [&](uint32_t bar, uint32_t parity) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity)))
+                    ok = ok && warp_wait_or_abort_addr(bar, parity, p.timeout_ns, abort_flag);
             };
-            auto advance = [&](Ring& q) {
-                if (++q.slot == S::kSlots) {
-                    q.slot = 0;
-                    q.phase ^= 1u;
-                }
+            // the products of the step before
+            bool due[2] = {false, false}, due_start[2] = {false, false}, due_end[2] = {false, false};
+            auto product = [&](int x, uint32_t vl) {
+                // O holds the last item's result until it has been read
+                if (due_start[x]) await(smem_u32(&o_empty[x]), (o_items[x]++ & 1u) ^ 1u);
+                await(smem_u32(&p_full[x]), p_phase[x]);
+                p_phase[x] ^= 1u;
+                tc_fence_after();
+                if (ok)
+                    mma_sum<kIdO, 8, 64>(tmem + kOutCol + 128 * x, tmem + kScoreCol + 128 * x, vl,
+                                         due_start[x] ? 0u : 1u, elected);
+                if (ok && due_end[x]) tc_commit(&o_full[x], elected);
             };
-            for (uint32_t it = 0; await(&item_full[it & 1u], (it >> 1) & 1u); ++it) {
+            for (uint32_t it = 0;; ++it) {
+                await(smem_u32(&item_full[it & 1u]), (it >> 1) & 1u);
+                if (!ok) break;
                 const Item& item = items[it & 1u];
                 const int valid = __shfl_sync(0xFFFFFFFFu, item.valid, 0);
                 int first[2], last[2];
@@ -225,68 +248,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (lane == 0) mbar_arrive(&item_empty[it & 1u]);
                 if (!valid) break;
-                bool started[2] = {false, false};
-                auto in = [&](int x, int kt) { return kt >= first[x] && kt < last[x]; };
-                auto scores = [&](int x, int kt, uint32_t slot) {
-                    mma_scores<kIdS, kD>(tmem + kScoreCol + 128 * x, q_lo + x * (S::kTile >> 4),
-                                         k_lo + slot * (S::kTile >> 4), elected);
-                    tc_commit(&s_full[x], elected);
-                    if (kt + 1 == last[x]) tc_commit(&q_empty[x], elected);
-                };
-                int kt = min(first[0], first[1]);
                 const int end = max(last[0], last[1]);
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    if (first[x] < last[x]) await(&q_full[x], q_items[x]++ & 1u);
-                if (kt < end) {
-                    await(&full[r.slot], r.phase);
-                    if (!ok) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        if (in(x, kt)) scores(x, kt, r.slot);
-                    tc_commit(&empty[r.slot], elected);
-                    advance(r);
-                }
-                while (kt < end && ok) {
-                    int nk = kt + 1;
-                    while (nk < end && !in(0, nk) && !in(1, nk)) ++nk;
-                    const Ring v = r;
-                    advance(r);
-                    const Ring k = r;
-                    await(&full[v.slot], v.phase);
+                for (int kt = min(first[0], first[1]); kt < end && ok; ++kt) {
+                    await(full0 + 8 * slot, phase);
+                    const uint32_t kl = k_lo + slot * (2 * S::kTile >> 4), vl = v_lo + slot * (2 * S::kTile >> 4);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        if (ok && in(x, kt)) {
-                            // O still holds the last item's result until it has been read
-                            if (!started[x]) await(&o_empty[x], (o_items[x]++ & 1u) ^ 1u);
-                            const uint32_t o = tmem + kOutCol + 128 * x, pr = tmem + kScoreCol + 128 * x,
-                                           vl = v_lo + v.slot * (S::kTile >> 4);
-                            if (await(&p_half[x], p_phase[x])) {
-                                tc_fence_after();
-                                mma_sum<kIdO, 8, 64, 0, 4>(o, pr, vl, started[x] ? 1u : 0u, elected);
-                            }
-                            if (await(&p_full[x], p_phase[x])) {
-                                tc_fence_after();
-                                mma_sum<kIdO, 8, 64, 4, 8>(o, pr, vl, 1u, elected);
-                                if (kt + 1 == last[x]) tc_commit(&o_full[x], elected);
-                            }
-                            p_phase[x] ^= 1u;
-                            started[x] = true;
-                        }
-                        if (nk < end && in(x, nk) && await(&full[k.slot], k.phase)) {
+                        if (due[x]) product(x, vl);
+                        due[x] = kt >= first[x] && kt < last[x];
+                        due_start[x] = kt == first[x];
+                        due_end[x] = kt + 1 == last[x];
+                        if (due[x]) {
+                            if (due_start[x]) await(smem_u32(&q_full[x]), q_items[x]++ & 1u);
                             tc_fence_after();
-                            scores(x, nk, k.slot);
+                            if (!ok) break;
+                            mma_scores<kIdS, kD>(tmem + kScoreCol + 128 * x, q_lo + x * (S::kTile >> 4), kl, elected);
+                            tc_commit(&s_full[x], elected);
+                            if (due_end[x]) tc_commit(&q_empty[x], elected);
                         }
                     }
                     if (!ok) break;
-                    tc_commit(&empty[v.slot], elected);
-                    if (nk < end) {
-                        tc_commit(&empty[k.slot], elected);
-                        advance(r);
+                    tc_commit(&empty[slot], elected);
+                    if (++slot == S::kStages) {
+                        slot = 0;
+                        phase ^= 1u;
                     }
-                    kt = nk;
                 }
+                if (!ok) break;
+            }
+            if (ok && (due[0] || due[1])) {
+                await(full0 + 8 * slot, phase);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    if (ok && due[x]) product(x, v_lo + slot * (2 * S::kTile >> 4));
             }
             give_up(!ok && elected);
             // every product is done before tensor memory is freed
@@ -357,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* stage = smem + S::kStageAt + (warp - kFirstSoftmaxWarp) * 4096;
         const bool plain = !p.sc.capped && !p.slopes;
         const float c = plain ? p.sc.mult : 1.0f;      // scores in registers times c are in log2
-        uint32_t s_phase = 0, o_phase = 0, n = 0;      // n: key tiles of the CTA so far
+        uint32_t s_phase = 0, o_phase = 0, n = 0;      // n: steps of the CTA so far
         bool ok = true;
         for (uint32_t it = 0;; ++it) {
             ok = warp_wait_or_abort(&item_full[it & 1u], (it >> 1) & 1u, p.timeout_ns, abort_flag);
@@ -377,10 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = -INFINITY, l = 0.0f;             // maximum (log2) that P and O are scaled by; sum
             const int end = max(last, last2);
             for (int kt = min(first, first2); kt < end; ++kt) {
-                const bool mine = kt >= first && kt < last;
-                if (!mine && !(kt >= first2 && kt < last2)) continue;
-                const uint32_t load = 2 * n++ + 1;     // the value tile's place among the loads
-                if (!mine) continue;
+                const uint32_t load = ++n;             // the value tile comes with the next stage
+                if (kt < first || kt >= last) continue;
                 ok = warp_wait_or_abort(&s_full[x], s_phase, p.timeout_ns, abort_flag);
                 if (!ok) break;
                 s_phase ^= 1u;
@@ -410,11 +402,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // value rows that no row of the CTA reads may hold anything
                     // (their P is 0): they are zeroed for the product
                     if (k0 < cta_lo || k0 + 128 > cta_hi) {
-                        const uint32_t slot = load % S::kSlots;
-                        ok = warp_wait_or_abort(&full[slot], (load / S::kSlots) & 1u, p.timeout_ns, abort_flag);
+                        const uint32_t slot = load % S::kStages;
+                        ok = warp_wait_or_abort(&full[slot], (load / S::kStages) & 1u, p.timeout_ns, abort_flag);
                         if (!ok) break;
                         const int key = k0 + (int)row;
-                        if (key < cta_lo || key >= cta_hi) zero_tile_row(ring + slot * S::kTile, row, S::kChunks);
+                        if (key < cta_lo || key >= cta_hi) zero_tile_row(ring + slot * 2 * S::kTile, row, S::kChunks);
                         fence_proxy_async_smem();
                     }
                 }
@@ -466,11 +458,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pk[i] = pack_bf16(e0, e1);
                     }
                     tmem_st_32x32b_x32(s_at + 32 * h, pk);
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(h ? &p_full[x] : &p_half[x]);
                 }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[x]);
                 float l0, l1;
                 unpair(add2(sum[0], sum[1]), l0, l1);
                 l = l0 + l1;
@@ -485,34 +477,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool some = l > 0.0f;
             const float f = some ? 1.0f / l : 0.0f;
             const int64_t row0 = token - lane;
-#pragma unroll 1
-            for (uint32_t ch = 0; ch < S::kChunks; ++ch) {
+            uint32_t pk[kD / 2];
+#pragma unroll
+            for (int h = 0; h < kD / 32; ++h) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(o_at + 32 * h, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j)   // nothing summed: the columns may hold anything
+                    pk[16 * h + j] = some ? pack_bf16(__uint_as_float(o[2 * j]) * f, __uint_as_float(o[2 * j + 1]) * f) : 0u;
+            }
+            if (first < last) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&o_empty[x]);
+            }
+#pragma unroll
+            for (int ch = 0; ch < (int)S::kChunks; ++ch) {
                 if (lane == 0) bulk_wait_read_all();   // the place's last store
                 __syncwarp();
 #pragma unroll
-                for (uint32_t h = 0; h < 2; ++h) {
-                    uint32_t o[32];
-                    tmem_ld_32x32b_x32(o_at + 64 * ch + 32 * h, o);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (!some) o[j] = 0;           // nothing summed: the columns may hold anything
-                    stage_row_32(stage, lane, h, o, f);
-                }
-                if (first < last && ch + 1 == S::kChunks) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&o_empty[x]);
-                }
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((i ^ (lane & 7u)) * 16)) =
+                        make_uint4(pk[32 * ch + 4 * i], pk[32 * ch + 4 * i + 1], pk[32 * ch + 4 * i + 2],
+                                   pk[32 * ch + 4 * i + 3]);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0 && row0 < p.tokens) {
                     tma_store_3d(&map_o, stage, (int32_t)ch * 64, head, (int32_t)row0);
                     bulk_commit_group();
                 }
+                if (ch == 0 && token < p.tokens)
+                    store_out(p.lse + (int64_t)head * p.tokens + token, some ? (m + log2f(l)) * kLn2 : -INFINITY, p.xlse);
             }
-            if (token < p.tokens)
-                store_out(p.lse + (int64_t)head * p.tokens + token, some ? (m + log2f(l)) * kLn2 : -INFINITY, p.xlse);
         }
         give_up(!ok && lane == 0);
         if (lane == 0) bulk_wait_all();

@@ -188,9 +188,8 @@ __device__ __forceinline__ bool claimed_block(const void* answer, uint32_t& bloc
 }
 
 // A bounded wait that also ends when another warp has given up.
-__device__ __forceinline__ bool mbar_wait_or_abort(uint64_t* bar, uint32_t parity, uint64_t timeout_ns,
-                                                   const volatile uint32_t* abort_flag) {
-    const uint32_t a = smem_u32(bar);
+__device__ __forceinline__ bool mbar_wait_or_abort_addr(uint32_t a, uint32_t parity, uint64_t timeout_ns,
+                                                        const volatile uint32_t* abort_flag) {
     if (mbar_try_wait(a, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (;;) {
@@ -201,8 +200,17 @@ __device__ __forceinline__ bool mbar_wait_or_abort(uint64_t* bar, uint32_t parit
     }
 }
 
+__device__ __forceinline__ bool mbar_wait_or_abort(uint64_t* bar, uint32_t parity, uint64_t timeout_ns,
+                                                   const volatile uint32_t* abort_flag) {
+    return mbar_wait_or_abort_addr(smem_u32(bar), parity, timeout_ns, abort_flag);
+}
+
 // The same by a whole warp: true only if every lane's wait ended well, so that
 // the warp stays together.
+__device__ __forceinline__ bool warp_wait_or_abort_addr(uint32_t a, uint32_t parity, uint64_t timeout_ns,
+                                                        const volatile uint32_t* abort_flag) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait_or_abort_addr(a, parity, timeout_ns, abort_flag));
+}
 __device__ __forceinline__ bool warp_wait_or_abort(uint64_t* bar, uint32_t parity, uint64_t timeout_ns,
                                                    const volatile uint32_t* abort_flag) {
     return __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar, parity, timeout_ns, abort_flag));
