@@ -125,7 +125,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.nvfp4_qk_norm_rope_backward.restype = i32
     L.nvfp4_attention_spans.argtypes, L.nvfp4_attention_spans.restype = [vp, i64, vp, c32, i64, vp, vp], i32
     L.nvfp4_attention.argtypes, L.nvfp4_attention.restype = [dp, hp, hp, hp, hp, vp, vp], i32
-    L.nvfp4_attention_backward_workspace_size.argtypes = [i64, c32]
+    L.nvfp4_attention_backward_workspace_size.argtypes = [i64, c32, c32, c32]
     L.nvfp4_attention_backward_workspace_size.restype = sz
     L.nvfp4_attention_backward.argtypes = [dp, hp, hp, hp, hp, hp, vp, hp, hp, hp, vp, sz, vp]
     L.nvfp4_attention_backward.restype = i32
@@ -269,8 +269,8 @@ def nvfp4_attention(desc, q, k, v, out, lse, stream):
     return load().nvfp4_attention(_ref(desc), _ref(q), _ref(k), _ref(v), _ref(out), lse, stream)
 
 
-def nvfp4_attention_backward_workspace_size(tokens, q_heads):
-    return load().nvfp4_attention_backward_workspace_size(tokens, q_heads)
+def nvfp4_attention_backward_workspace_size(tokens, q_heads, kv_heads, head_dim):
+    return load().nvfp4_attention_backward_workspace_size(tokens, q_heads, kv_heads, head_dim)
 
 
 def nvfp4_attention_backward(desc, dout, q, k, v, out, lse, dq, dk, dv, workspace, workspace_bytes, stream):

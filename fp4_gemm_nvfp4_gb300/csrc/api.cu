@@ -634,9 +634,9 @@ nvfp4_status nvfp4_attention(const nvfp4_attention_desc* desc, const nvfp4_heads
                                                                                              : NVFP4_ERR_CUDA;
 }
 
-size_t nvfp4_attention_backward_workspace_size(int64_t tokens, int32_t q_heads) {
-    if (tokens <= 0 || q_heads <= 0) return 0;
-    return nvfp4::attention_backward_workspace_bytes(tokens, q_heads);
+size_t nvfp4_attention_backward_workspace_size(int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
+    if (tokens <= 0 || check_head_shape(tokens, q_heads, kv_heads, head_dim) != NVFP4_OK) return 0;
+    return nvfp4::attention_backward_workspace_bytes(tokens, q_heads, kv_heads, head_dim);
 }
 
 nvfp4_status nvfp4_attention_backward(const nvfp4_attention_desc* desc, const nvfp4_heads* dout, const nvfp4_heads* q,
@@ -652,7 +652,7 @@ nvfp4_status nvfp4_attention_backward(const nvfp4_attention_desc* desc, const nv
     for (const nvfp4_heads* t : {dout, dq, dk, dv})
         if ((s = check_heads(t, a.head_dim)) != NVFP4_OK) return s;
     if (!workspace || !aligned16(workspace) ||
-        workspace_bytes < nvfp4_attention_backward_workspace_size(a.tokens, a.q_heads))
+        workspace_bytes < nvfp4::attention_backward_workspace_bytes(a.tokens, a.q_heads, a.kv_heads, a.head_dim))
         return NVFP4_ERR_WORKSPACE;
     a.dout = to_heads(dout);
     a.dq = to_heads(dq);
@@ -694,7 +694,8 @@ nvfp4_status nvfp4_testing_bounds_violations(uint64_t* count) {
         nvfp4::dequantize_bounds_read_and_clear(&n) != cudaSuccess ||
         nvfp4::norm_rope_bounds_read_and_clear(&n) != cudaSuccess ||
         nvfp4::attention_spans_bounds_read_and_clear(&n) != cudaSuccess ||
-        nvfp4::attention_forward_bounds_read_and_clear(&n) != cudaSuccess)
+        nvfp4::attention_forward_bounds_read_and_clear(&n) != cudaSuccess ||
+        nvfp4::attention_backward_bounds_read_and_clear(&n) != cudaSuccess)
         return NVFP4_ERR_CUDA;
     *count = n;
     return NVFP4_OK;

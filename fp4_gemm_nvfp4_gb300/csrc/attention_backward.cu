@@ -23,8 +23,9 @@
 // the exact delta = sum_j P dP in FP32; with P' = P (1 - tanh^2) its acc1
 // turns dq for the difference, dq = scale (acc2 + (delta~ - delta) acc1), and
 // the dk dv kernel uses the exact delta.  That product is a seventh of the
-// work.  Warps: 0 TMA loads, 1 MMA issue, 4-11 softmax (a lane one row, each
-// group of four warps half of the columns).
+// work.  Warps: 0 TMA loads, 1 MMA issue, 2 the next item, 4-19 softmax (a
+// lane one row, each group of four warps 32 of the columns).  As in the
+// forward pass a CTA goes on to blocks that have not started.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -34,9 +35,10 @@
 namespace nvfp4 {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
 constexpr int kFirstSoftmaxWarp = 4;
-constexpr uint32_t kSoftmaxWarps = 8;
+constexpr uint32_t kSoftmaxWarps = 16;
+constexpr int kControlRegs = 64, kSoftmaxRegs = 104;   // per thread, of the launch's 96
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 0, kDpCol = 128, kAcc1Col = 256, kAcc2Col = 384;
 // Streamed tiles in flight.  With five, the place of X2(i + 2) is that of
@@ -44,6 +46,7 @@ constexpr uint32_t kSCol = 0, kDpCol = 128, kAcc1Col = 256, kAcc2Col = 384;
 // need two places.
 constexpr uint32_t kSlots = 5;
 constexpr uint32_t kVecBytes = 2 * 128 * sizeof(float);
+constexpr uint32_t kMaxSplits = 8;
 
 template <int kD>
 struct Shape {
@@ -57,17 +60,21 @@ static_assert(Shape<128>::kSmem <= 232448, "shared memory budget");
 
 // The workspace: per query head and row (rounded up to tiles) lse in log2 (inf
 // for a row without keys) and the exact delta, then the tiles' spans.
+// With the dk dv kernel's sums split, also the parts: FP32 [splits][dv, dk]
+// [tokens][kv_heads][head_dim].
 struct Workspace {
     float* lse2;
     float* delta;
     TileSpan* spans;
-    int64_t ld;   // rows per head
+    float* parts;
+    int64_t ld;         // rows per head
+    int64_t part_size;  // floats of one part of dv or dk
 };
 
 struct Params {
     int64_t tokens;
     int32_t heads, group;            // heads the CTAs own; query heads per key head
-    int32_t tiles;
+    int32_t tiles, splits;           // splits of an owner's streamed tiles
     float scale;
     Scores sc;
     const float* slopes;
@@ -79,14 +86,22 @@ struct Params {
     uint64_t timeout_ns;
 };
 
+// One item: an owned tile, and the streamed tiles first .. first + count - 1
+// of each streamed head from head0 on; of these, in order, `total` from
+// number `from` on.
+struct Item {
+    int valid, head, tile, split;
+    int head0, first, count, from, total;
+    TileSpan span;   // dq
+    int pad[3];
+};
+
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                      smem_u32(dst)),
                  "l"(src), "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
 }
-
-__device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 __device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float t) {
     t = fmaf(bf16lo(a.x), bf16lo(b.x), t);
@@ -110,43 +125,54 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* ring = smem + 2 * S::kTile;
     float* vec = reinterpret_cast<float*>(smem + S::kVecAt);     // [2][lse2, delta][128] of the streamed rows
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBarAt);
+    // dq: quarters of the rows' deltas, [4][128] from out in the vectors' place
+    // (unused there), and [2 items][4][128] exact ones in that of the own tiles
+    // once they are done with
+    float* exact_parts = reinterpret_cast<float*>(smem + S::kTile);
+    Item* items = reinterpret_cast<Item*>(smem + S::kBarAt);     // [2] the current and the next
+    uint4* answer = reinterpret_cast<uint4*>(items + 2);
+    uint64_t* full = reinterpret_cast<uint64_t*>(answer + 1);
     uint64_t* empty = full + kSlots;
-    uint64_t* f_full = empty + kSlots;
-    uint64_t* s_full = f_full + 1;
+    uint64_t* f_full = empty + kSlots;           // the item's own tiles loaded
+    uint64_t* f_empty = f_full + 1;              // ... and their place free: it stages the results
+    uint64_t* s_full = f_empty + 1;
     uint64_t* dp_full = s_full + 1;
     uint64_t* p_full = dp_full + 1;
     uint64_t* dz_full = p_full + 1;
     uint64_t* acc_full = dz_full + 1;
-    uint64_t* drain = acc_full + 1;
+    uint64_t* item_full = acc_full + 1;          // [2]
+    uint64_t* item_empty = item_full + 2;        // [2]
+    uint64_t* loaded = item_empty + 2;           // the item's loads issued
+    uint64_t* delta_full = loaded + 1;           // dq: the quarters of the deltas written
+    uint64_t* exact_full = delta_full + 1;       // ... of the exact ones
+    uint64_t* answered = exact_full + 1;
+    uint64_t* drain = answered + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile uint32_t* abort_flag = tmem_slot + 1;
-    int* range = reinterpret_cast<int*>(tmem_slot + 2);          // [2]
-    TileSpan* parts = reinterpret_cast<TileSpan*>(tmem_slot + 4);   // [4]
-    float* exchange = vec;                                       // dq: [128], the vectors' place is unused there
 
     const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31u;
-    // the longest first under a causal mask: the last queries, the first keys
-    const int32_t head = (int32_t)(blockIdx.x % (uint32_t)p.heads);
-    const int32_t at = (int32_t)(blockIdx.x / (uint32_t)p.heads);
-    const int32_t tile = kKeys ? at : p.tiles - 1 - at;
-    const int own0 = tile * 128;
-
     if (threadIdx.x == 0) {
         for (uint32_t i = 0; i < kSlots; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
         mbar_init(f_full, 1);
+        mbar_init(f_empty, kSoftmaxWarps);
         mbar_init(s_full, 1);
         mbar_init(dp_full, 1);
         mbar_init(p_full, kSoftmaxWarps);
         mbar_init(dz_full, kSoftmaxWarps);
         mbar_init(acc_full, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&item_full[i], 1);
+            mbar_init(&item_empty[i], 2 + kSoftmaxWarps);
+        }
+        mbar_init(loaded, 1);
+        mbar_init(delta_full, kSoftmaxWarps);
+        mbar_init(exact_full, kSoftmaxWarps);
+        mbar_init(answered, 1);
         mbar_init(drain, 1);
         *abort_flag = 0u;
-        range[0] = INT32_MAX;
-        range[1] = 0;
         fence_barrier_init();
     }
     if (warp == 0 && lane == 0) {
@@ -159,405 +185,502 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(tmem_slot, kTmemCols);
         tmem_relinquish();
     }
-    const uint32_t half = (warp - kFirstSoftmaxWarp) >> 2;            // softmax warps: columns 64 half ..
-    const uint32_t row = (warp & 3u) * 32 + lane;                     // ... of this row
-    const int64_t own = own0 + (int64_t)row;
-    int2 span = make_int2(0, 0);
-    if constexpr (!kKeys) {
-        if (warp >= kFirstSoftmaxWarp) {
-            span = span_of(p.spans, own, p.tokens);
-            const TileSpan t = warp_span(span, own < p.tokens);
-            if (half == 0 && lane == 0) parts[warp - kFirstSoftmaxWarp] = t;
-        }
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    TileSpan ts{};
-    int first = 0, count = 0;      // streamed tiles first .. first + count - 1, per streamed head
-    if constexpr (kKeys) {
-        // the query tiles with a row that reaches these keys
-        int a = INT32_MAX, b = 0;
-        for (int t = (int)threadIdx.x; t < p.tiles; t += kThreads) {
-            const TileSpan q = p.ws.spans[t];
-            if (q.lo < own0 + 128 && q.hi > own0 && q.lo < q.hi) {
-                a = min(a, t);
-                b = max(b, t + 1);
-            }
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
+
+    auto give_up = [&](bool one) {
+        if (one) {
+            *abort_flag = 1u;
+            atomicOr(&g_attention_status, kStatusTimeoutBit);
         }
-        a = __reduce_min_sync(0xFFFFFFFFu, a);
-        b = __reduce_max_sync(0xFFFFFFFFu, b);
-        if (lane == 0 && a < b) {
-            atomicMin(&range[0], a);
-            atomicMax(&range[1], b);
-        }
-        __syncthreads();
-        first = range[0] < range[1] ? range[0] : 0;
-        count = range[0] < range[1] ? range[1] - first : 0;
-    } else {
-        ts = join_spans(join_spans(parts[0], parts[1]), join_spans(parts[2], parts[3]));
-        if (ts.lo < ts.hi) {
-            first = ts.lo >> 7;
-            count = ((ts.hi + 127) >> 7) - first;
-        }
-        if (threadIdx.x == 0 && head == 0) p.ws.spans[tile] = ts;
-    }
-    const int head0 = kKeys ? head * p.group : head / p.group;        // first streamed head
-    const int total = __shfl_sync(0xFFFFFFFFu, kKeys ? count * p.group : count, 0);
+    };
 
     if (warp < kFirstSoftmaxWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" ::: "memory");
-        if (warp == 0 && lane == 0 && total > 0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs) : "memory");
+        if (warp == 0 && lane == 0) {
             // ------------------------------------------------------- loads
-            mbar_arrive_expect_tx(f_full, 2 * S::kTile);
-            for (uint32_t c = 0; c < S::kChunks; ++c) {
-                tma_load_3d(smem + c * kChunkBytes, &map_f1, f_full, (int32_t)c * 64, head, own0);
-                tma_load_3d(smem + S::kTile + c * kChunkBytes, &map_f2, f_full, (int32_t)c * 64, head, own0);
-            }
-            uint32_t slot = 0, phase = 0, issued = 0;
-            int h = head0, t = first;
+            uint32_t slot = 0, phase = 0, issued = 0, own_loads = 0, n = 0;   // n: streamed tiles so far
             bool ok = true;
-            for (int i = 0; i < total && ok; ++i) {
-                for (int x = 0; x < 2; ++x) {
-                    if (!mbar_wait_or_abort(&empty[slot], phase ^ 1u, p.timeout_ns, abort_flag)) {
-                        ok = false;
-                        break;
+            auto await = [&](uint64_t* bar, uint32_t parity) {
+                if (ok && !mbar_wait_or_abort(bar, parity, p.timeout_ns, abort_flag)) ok = false;
+                return ok;
+            };
+            for (uint32_t it = 0; await(&item_full[it & 1u], (it >> 1) & 1u); ++it) {
+                const Item item = items[it & 1u];
+                mbar_arrive(&item_empty[it & 1u]);
+                if (!item.valid) break;
+                // the streamed tiles need not wait for the owned ones' place:
+                // the first pair goes ahead
+                int h = item.head0 + item.from / max(item.count, 1), t = item.first + item.from % max(item.count, 1);
+                for (int i = 0; i < item.total && ok; ++i, ++n) {
+                    for (int x = 0; x < 2; ++x) {
+                        if (!await(&empty[slot], phase ^ 1u)) break;
+                        const bool vectors = kKeys && x == 1;
+                        mbar_arrive_expect_tx(&full[slot], S::kTile + (vectors ? kVecBytes : 0u));
+                        for (uint32_t c = 0; c < S::kChunks; ++c)
+                            tma_load_3d(ring + slot * S::kTile + c * kChunkBytes, x ? &map_x2 : &map_x1, &full[slot],
+                                        (int32_t)c * 64, h, t * 128);
+                        if (vectors) {
+                            float* to = vec + (n & 1u) * 256;
+                            const int64_t from = (int64_t)h * p.ws.ld + t * 128;
+                            bulk_load(to, p.ws.lse2 + from, 512, &full[slot]);
+                            bulk_load(to + 128, p.ws.delta + from, 512, &full[slot]);
+                        }
+                        ++issued;
+                        if (++slot == kSlots) {
+                            slot = 0;
+                            phase ^= 1u;
+                        }
                     }
-                    const bool vectors = kKeys && x == 1;
-                    mbar_arrive_expect_tx(&full[slot], S::kTile + (vectors ? kVecBytes : 0u));
-                    for (uint32_t c = 0; c < S::kChunks; ++c)
-                        tma_load_3d(ring + slot * S::kTile + c * kChunkBytes, x ? &map_x2 : &map_x1, &full[slot],
-                                    (int32_t)c * 64, h, t * 128);
-                    if (vectors) {
-                        float* to = vec + (i & 1) * 256;
-                        const int64_t from = (int64_t)h * p.ws.ld + t * 128;
-                        bulk_load(to, p.ws.lse2 + from, 512, &full[slot]);
-                        bulk_load(to + 128, p.ws.delta + from, 512, &full[slot]);
+                    if (ok && i == 0 && await(f_empty, (it & 1u) ^ 1u)) {
+                        ++own_loads;
+                        mbar_arrive_expect_tx(f_full, 2 * S::kTile);
+                        for (uint32_t c = 0; c < S::kChunks; ++c) {
+                            tma_load_3d(smem + c * kChunkBytes, &map_f1, f_full, (int32_t)c * 64, item.head, item.tile * 128);
+                            tma_load_3d(smem + S::kTile + c * kChunkBytes, &map_f2, f_full, (int32_t)c * 64, item.head,
+                                        item.tile * 128);
+                        }
                     }
-                    ++issued;
-                    if (++slot == kSlots) {
-                        slot = 0;
-                        phase ^= 1u;
+                    if (++t == item.first + item.count) {
+                        t = item.first;
+                        ++h;
                     }
                 }
-                if (++t == first + count) {
-                    t = first;
-                    ++h;
-                }
+                if (item.total == 0) await(f_empty, (it & 1u) ^ 1u);
+                if (ok) mbar_arrive(loaded);
             }
-            if (!ok) {
-                *abort_flag = 1u;
-                atomicOr(&g_attention_status, kStatusTimeoutBit);
-            }
+            give_up(!ok);
             // every load has landed before the CTA exits
-            (void)mbar_wait(f_full, 0, p.timeout_ns);
+            if (own_loads) (void)mbar_wait(f_full, (own_loads - 1) & 1u, p.timeout_ns);
             for (uint32_t back = 0; back < kSlots && back < issued; ++back) {
-                const uint32_t n = issued - 1 - back;
-                (void)mbar_wait(&full[n % kSlots], (n / kSlots) & 1u, p.timeout_ns);
+                const uint32_t m = issued - 1 - back;
+                (void)mbar_wait(&full[m % kSlots], (m / kSlots) & 1u, p.timeout_ns);
             }
-        } else if (warp == 1 && total > 0) {
+        } else if (warp == 1) {
             // --------------------------------------------------- MMA issue
             constexpr uint32_t kIdS = idesc_bf16(128, 128, false);
             constexpr uint32_t kIdAcc = idesc_bf16(128, kD, true);
             const uint32_t elected = elect_one();
-            const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
             const uint32_t f_lo = desc_k_major(smem_u32(smem)), xk_lo = desc_k_major(smem_u32(ring)),
                            xn_lo = desc_n_major(smem_u32(ring));
+            const uint32_t full0 = smem_u32(full);
             bool ok = true;
-            auto await = [&](uint64_t* bar, uint32_t parity) {
-                if (ok && !warp_wait_or_abort(bar, parity, p.timeout_ns, abort_flag)) ok = false;
+            auto await = [&](uint32_t bar, uint32_t parity) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity)))
+                    ok = ok && warp_wait_or_abort_addr(bar, parity, p.timeout_ns, abort_flag);
                 tc_fence_after();
             };
-            // the scores of streamed tile i (x = 0: S, 1: dP)
-            auto scores = [&](int i, uint32_t x) {
-                const uint32_t n = 2 * (uint32_t)i + x, slot = n % kSlots;
-                await(&full[slot], (n / kSlots) & 1u);
+            // places of X1(i), X2(i) for the products, of the next X1 for S and dP
+            uint32_t n = 0, x1 = 0, x2 = 0, at = 0, at_phase = 0, own_tiles = 0;
+            auto scores = [&](uint32_t x) {
+                const uint32_t slot = at;
+                (x ? x2 : x1) = slot;
+                await(full0 + 8 * slot, at_phase);
+                if (++at == kSlots) {
+                    at = 0;
+                    at_phase ^= 1u;
+                }
                 if (!ok) return;
-                mma_scores<kIdS, kD>(tm + (x ? kDpCol : kSCol), f_lo + x * (S::kTile >> 4),
+                mma_scores<kIdS, kD>(tmem + (x ? kDpCol : kSCol), f_lo + x * (S::kTile >> 4),
                                      xk_lo + slot * (S::kTile >> 4), elected);
                 tc_commit(x ? dp_full : s_full, elected);
                 if (!kKeys && x == 1) tc_commit(&empty[slot], elected);   // dq: v is needed for dP alone
             };
-            auto product = [&](int i, uint32_t acc) {
-                const uint32_t n = 2 * (uint32_t)i + (kKeys && acc == 0 ? 1u : 0u), slot = n % kSlots;
-                await(acc ? dz_full : p_full, (uint32_t)i & 1u);
+            auto product = [&](uint32_t acc, uint32_t slot, bool start) {
+                await(smem_u32(acc ? dz_full : p_full), n & 1u);
                 if (!ok) return;
-                // the 64 columns of each half of S hold 64 rows' BF16 in their first 32
-                mma_sum<kIdAcc, 4, 64>(tm + (acc ? kAcc2Col : kAcc1Col), tm + (acc ? kDpCol : kSCol),
-                                       xn_lo + slot * (S::kTile >> 4), i ? 1u : 0u, elected);
+                // each 32 columns of S hold 32 rows' BF16 in their first 16
+                mma_sum<kIdAcc, 2, 32>(tmem + (acc ? kAcc2Col : kAcc1Col), tmem + (acc ? kDpCol : kSCol),
+                                       xn_lo + slot * (S::kTile >> 4), start ? 0u : 1u, elected);
                 if (kKeys || acc == 1) tc_commit(&empty[slot], elected);
             };
-            await(f_full, 0);
-            scores(0, 0);
-            scores(0, 1);
-            for (int i = 0; i < total && ok; ++i) {
-                product(i, 0);
-                if (i + 1 < total) scores(i + 1, 0);
-                product(i, 1);
-                if (i + 1 < total) scores(i + 1, 1);
+            for (uint32_t it = 0;; ++it) {
+                await(smem_u32(&item_full[it & 1u]), (it >> 1) & 1u);
+                if (!ok) break;
+                const int valid = __shfl_sync(0xFFFFFFFFu, items[it & 1u].valid, 0);
+                const int total = __shfl_sync(0xFFFFFFFFu, items[it & 1u].total, 0);
+                if (lane == 0) mbar_arrive(&item_empty[it & 1u]);
+                if (!valid) break;
+                if (total == 0) continue;
+                await(smem_u32(f_full), own_tiles++ & 1u);
+                scores(0);
+                scores(1);
+                for (int i = 0; i < total && ok; ++i, ++n) {
+                    const uint32_t c1 = x1, c2 = x2;
+                    product(0, kKeys ? c2 : c1, i == 0);
+                    if (i + 1 < total) scores(0);
+                    product(1, c1, i == 0);
+                    if (i + 1 < total) scores(1);
+                }
+                if (!ok) break;
+                tc_commit(acc_full, elected);
             }
-            if (ok) tc_commit(acc_full, elected);
-            if (!ok && elected) {
-                *abort_flag = 1u;
-                atomicOr(&g_attention_status, kStatusTimeoutBit);
-            }
+            give_up(!ok && elected);
             // every product is done before tensor memory is freed
             tc_commit(drain, elected);
             (void)mbar_wait(drain, 0, p.timeout_ns);
-        }
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
-        // --------------------------------------------------------- softmax
-        const uint32_t lanes = tmem + (((warp & 3u) * 32u) << 16);
-        const uint32_t s_at = lanes + kSCol + 64 * half, dp_at = lanes + kDpCol + 64 * half;
-        const bool biased = p.slopes != nullptr;
-        const float c = p.sc.capped || biased ? 1.0f : p.sc.mult;
-        float lse2 = INFINITY, delta = 0.0f;           // dq: of this row
-        if constexpr (!kKeys) {
-            // delta from out: each group of warps takes half of the dims
-            const bool alive = span.x < span.y;
-            float part = 0.0f;
-            if (alive) {
-                const uint16_t* o = p.out.data + own * p.out.ld_token + (int64_t)head * p.out.ld_head;
-                const uint16_t* d = p.dout.data + own * p.dout.ld_token + (int64_t)head * p.dout.ld_head;
-#pragma unroll
-                for (int i = 0; i < kD / 16; ++i) {
-                    const int at8 = 8 * (i + (int)half * (kD / 16));
-                    if (at8 < p.head_dim) part = dot8(ld_nc_v4(o + at8), ld_nc_v4(d + at8), part);
-                }
-                lse2 = p.lse[(int64_t)head * p.tokens + own] * kLog2e;
-            }
-            exchange[half * 128 + row] = part;
-            softmax_bar();
-            delta = exchange[row] + exchange[128 + row];
-            softmax_bar();
-        }
-        float exact = 0.0f;                            // dq: sum of P dP
-        bool ok = true;
-        int h = head0, t = first;
-        for (int i = 0; i < total; ++i) {
-            const int x0 = t * 128;                    // first streamed row
-            const uint32_t n2 = 2 * (uint32_t)i + 1;
-            float slope = 0.0f;
-            if (biased) slope = p.slopes[kKeys ? h : head] * kLog2e;
-            if constexpr (kKeys) ts = p.ws.spans[t];
-            const bool masked = kKeys ? (own0 < ts.all_lo || own0 + 128 > ts.all_hi)
-                                      : (x0 < ts.all_lo || x0 + 128 > ts.all_hi);
-            const float* v_lse = vec + (i & 1) * 256 + 64 * half;
-            const float* v_delta = v_lse + 128;
-            if constexpr (kKeys) ok = warp_wait_or_abort(&full[n2 % kSlots], (n2 / kSlots) & 1u, p.timeout_ns, abort_flag);
-            ok = ok && warp_wait_or_abort(s_full, (uint32_t)i & 1u, p.timeout_ns, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            float e[64], damp[64];
-            {
-                uint32_t* r = reinterpret_cast<uint32_t*>(e);
-                tmem_ld_32x32b_x32(s_at, r);
-                tmem_ld_32x32b_x32(s_at + 32, r + 32);
-                tmem_ld_wait();
-            }
-            if (p.sc.capped) {
-#pragma unroll
-                for (int j = 0; j < 64; ++j) {
-                    const float th = capped_tanh(e[j], p.sc.mult);
-                    e[j] = th * p.sc.cap_log2;
-                    damp[j] = fmaf(-th, th, 1.0f);
-                }
-            }
-            if (biased) {
-                const float f = p.sc.capped ? 1.0f : p.sc.mult, d = (float)((int)own - x0 - 64 * (int)half);
-#pragma unroll
-                for (int j = 0; j < 64; ++j) e[j] = fmaf(-slope, fabsf(d - (float)j), e[j] * f);
-            }
-            if constexpr (kKeys) {
-#pragma unroll
-                for (int j = 0; j < 64; j += 4) {
-                    const float4 l4 = *reinterpret_cast<const float4*>(v_lse + j);
-                    e[j] = ex2(fmaf(e[j], c, -l4.x));
-                    e[j + 1] = ex2(fmaf(e[j + 1], c, -l4.y));
-                    e[j + 2] = ex2(fmaf(e[j + 2], c, -l4.z));
-                    e[j + 3] = ex2(fmaf(e[j + 3], c, -l4.w));
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 64; ++j) e[j] = ex2(fmaf(e[j], c, -lse2));
-            }
-            if (masked) {
-                if constexpr (kKeys) {
-#pragma unroll
-                    for (int j = 0; j < 64; ++j) {
-                        const int2 s = span_of(p.spans, x0 + 64 * (int)half + j, p.tokens);
-                        if (own < s.x || own >= s.y) e[j] = 0.0f;
-                    }
-                    // rows of queries without keys may hold anything (their P
-                    // and dZ are 0): they are zeroed for the products
-                    if (half == 0 && ts.all_hi == 0) {
-                        const int64_t q = x0 + (int64_t)row;
-                        const int2 s = span_of(p.spans, q, p.tokens);
-                        if (s.x >= s.y) {
-                            zero_tile_row(ring + ((n2 - 1) % kSlots) * S::kTile, row, S::kChunks);
-                            zero_tile_row(ring + (n2 % kSlots) * S::kTile, row, S::kChunks);
+        } else if (warp == 2) {
+            // ------------------------------------------------------- items
+            // As in the forward pass: the CTA's own block, then blocks that have
+            // not started, each taken over when the last one's loads are issued.
+            uint32_t block = blockIdx.x;
+            bool valid = true, ok = true;
+            for (uint32_t it = 0;; ++it) {
+                Item item{};
+                item.valid = valid ? 1 : 0;
+                if (valid) {
+                    // the longest first under a causal mask: the last queries, the first keys
+                    item.head = (int)(block % (uint32_t)p.heads);
+                    const int rest = (int)(block / (uint32_t)p.heads);
+                    item.split = rest % p.splits;
+                    item.tile = kKeys ? rest / p.splits : p.tiles - 1 - rest / p.splits;
+                    const int own0 = item.tile * 128;
+                    if constexpr (kKeys) {
+                        // the query tiles with a row that reaches these keys
+                        int a = INT32_MAX, b = 0;
+                        for (int t = (int)lane; t < p.tiles; t += 32) {
+                            const TileSpan q = p.ws.spans[t];
+                            if (q.lo < own0 + 128 && q.hi > own0 && q.lo < q.hi) {
+                                a = min(a, t);
+                                b = max(b, t + 1);
+                            }
                         }
-                        fence_proxy_async_smem();
-                    }
-                } else {
-                    const int lo = span.x - x0 - 64 * (int)half, hi = span.y - x0 - 64 * (int)half;
-#pragma unroll
-                    for (int j = 0; j < 64; ++j)
-                        if (j < lo || j >= hi) e[j] = 0.0f;
-                    // so may keys that no row of the tile reads
-                    if (half == 0 && (x0 < ts.lo || x0 + 128 > ts.hi)) {
-                        const int key = x0 + (int)row;
-                        if (key < ts.lo || key >= ts.hi)
-                            zero_tile_row(ring + ((n2 - 1) % kSlots) * S::kTile, row, S::kChunks);
-                        fence_proxy_async_smem();
-                    }
-                }
-            }
-            {
-                uint32_t pk[32];
-                if (!kKeys && p.sc.capped) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) pk[j] = pack_bf16(e[2 * j] * damp[2 * j], e[2 * j + 1] * damp[2 * j + 1]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) pk[j] = pack_bf16(e[2 * j], e[2 * j + 1]);
-                }
-                tmem_st_32x32b_x32(s_at, pk);
-                tmem_st_wait();
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(p_full);
-
-            if (!warp_wait_or_abort(dp_full, (uint32_t)i & 1u, p.timeout_ns, abort_flag)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            float g[64];
-            {
-                uint32_t* r = reinterpret_cast<uint32_t*>(g);
-                tmem_ld_32x32b_x32(dp_at, r);
-                tmem_ld_32x32b_x32(dp_at + 32, r + 32);
-                tmem_ld_wait();
-            }
-            if (masked) {
-                // a masked place's dP may be anything
-#pragma unroll
-                for (int j = 0; j < 64; ++j)
-                    if (e[j] == 0.0f) g[j] = 0.0f;
-            }
-            if constexpr (kKeys) {
-#pragma unroll
-                for (int j = 0; j < 64; j += 4) {
-                    const float4 d4 = *reinterpret_cast<const float4*>(v_delta + j);
-                    g[j] = e[j] * (g[j] - d4.x);
-                    g[j + 1] = e[j + 1] * (g[j + 1] - d4.y);
-                    g[j + 2] = e[j + 2] * (g[j + 2] - d4.z);
-                    g[j + 3] = e[j + 3] * (g[j + 3] - d4.w);
-                }
-            } else {
-                float sum[2] = {};
-#pragma unroll
-                for (int j = 0; j < 64; j += 2) {
-                    sum[0] = fmaf(e[j], g[j], sum[0]);
-                    sum[1] = fmaf(e[j + 1], g[j + 1], sum[1]);
-                    g[j] = e[j] * (g[j] - delta);
-                    g[j + 1] = e[j + 1] * (g[j + 1] - delta);
-                }
-                exact += sum[0] + sum[1];
-            }
-            if (p.sc.capped) {
-#pragma unroll
-                for (int j = 0; j < 64; ++j) g[j] *= damp[j];
-            }
-            {
-                uint32_t pk[32];
-#pragma unroll
-                for (int j = 0; j < 32; ++j) pk[j] = pack_bf16(g[2 * j], g[2 * j + 1]);
-                tmem_st_32x32b_x32(dp_at, pk);
-                tmem_st_wait();
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(dz_full);
-            if (++t == first + count) {
-                t = first;
-                ++h;
-            }
-        }
-        // ------------------------------------------------------- epilogue
-        if (ok && total > 0) ok = warp_wait_or_abort(acc_full, 0, p.timeout_ns, abort_flag);
-        if (!ok && lane == 0) {
-            *abort_flag = 1u;
-            atomicOr(&g_attention_status, kStatusTimeoutBit);
-        }
-        tc_fence_after();
-        const uint32_t rows0 = (warp & 3u) * 32;
-        const int64_t tok0 = own0 + (int64_t)rows0;
-        if constexpr (kKeys) {
-            // dv by the first four warps, dk by the others, through the ring
-            uint8_t* stage = ring + half * S::kTile;
-            const float f = half ? p.scale : 1.0f;
-            if (ok && tok0 < p.tokens) {
-#pragma unroll
-                for (int i = 0; i < kD / 32; ++i) {
-                    uint32_t o[32];
-                    if (total > 0) {
-                        tmem_ld_32x32b_x32(lanes + (half ? kAcc2Col : kAcc1Col) + 32 * i, o);
-                        tmem_ld_wait();
+                        a = __reduce_min_sync(0xFFFFFFFFu, a);
+                        b = __reduce_max_sync(0xFFFFFFFFu, b);
+                        item.first = a < b ? a : 0;
+                        item.count = a < b ? b - a : 0;
+                        item.head0 = item.head * p.group;
+                        const int all = item.count * p.group, per = (all + p.splits - 1) / p.splits;
+                        item.from = min(item.split * per, all);
+                        item.total = min(per, all - item.from);
                     } else {
+                        TileSpan t{INT32_MAX, 0, 0, INT32_MAX};
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = 0;
+                        for (int j = 0; j < 4; ++j) {
+                            const int64_t q = own0 + 32 * j + (int)lane;
+                            t = join_spans(t, warp_span(span_of(p.spans, q, p.tokens), q < p.tokens));
+                        }
+                        item.span = t;
+                        if (t.lo < t.hi) {
+                            item.first = t.lo >> 7;
+                            item.count = ((t.hi + 127) >> 7) - item.first;
+                        }
+                        item.total = item.count;
+                        item.head0 = item.head / p.group;
+                        if (lane == 0 && item.head == 0) p.ws.spans[item.tile] = t;
                     }
-                    stage_row_32(stage + (i >> 1) * kChunkBytes, row, i & 1, o, f);
                 }
+                ok = warp_wait_or_abort(&item_empty[it & 1u], ((it >> 1) & 1u) ^ 1u, p.timeout_ns, abort_flag);
+                if (!ok) break;
+                if (lane == 0) {
+                    items[it & 1u] = item;
+                    mbar_arrive(&item_full[it & 1u]);
+                }
+                if (!valid) break;
+                ok = warp_wait_or_abort(loaded, it & 1u, p.timeout_ns, abort_flag);
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(answered, 16);
+                    claim_block(answer, answered);
+                }
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(answered, it & 1u, p.timeout_ns));
+                if (!ok) break;
+                valid = claimed_block(answer, block);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) {
-                    for (uint32_t ch = 0; ch < S::kChunks; ++ch)
-                        tma_store_3d(half ? &map_out2 : &map_out1, stage + ch * kChunkBytes + rows0 * 128,
-                                     (int32_t)ch * 64, head, (int32_t)tok0);
-                    bulk_commit_group();
-                    bulk_wait_all();
+            }
+            give_up(!ok && lane == 0);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs) : "memory");
+        // --------------------------------------------------------- softmax
+        const uint32_t quarter = (warp - kFirstSoftmaxWarp) >> 2;         // columns 32 quarter ..
+        const uint32_t row = (warp & 3u) * 32 + lane;                     // ... of this row
+        const uint32_t lanes = tmem + (((warp & 3u) * 32u) << 16);
+        const uint32_t s_at = lanes + kSCol + 32 * quarter, dp_at = lanes + kDpCol + 32 * quarter;
+        const bool biased = p.slopes != nullptr;
+        const float c = p.sc.capped || biased ? 1.0f : p.sc.mult;
+        uint32_t n = 0, results = 0;               // streamed tiles, items with a result so far
+        bool ok = true;
+        for (uint32_t it = 0;; ++it) {
+            ok = warp_wait_or_abort(&item_full[it & 1u], (it >> 1) & 1u, p.timeout_ns, abort_flag);
+            if (!ok) break;
+            const Item& item = items[it & 1u];
+            const bool valid = item.valid != 0;
+            const int head = item.head, own0 = item.tile * 128, total = item.total, first = item.first,
+                      last = item.first + item.count, split = item.split;
+            int h = item.head0 + item.from / max(item.count, 1), t = first + item.from % max(item.count, 1);
+            TileSpan ts = item.span;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&item_empty[it & 1u]);
+            if (!valid) break;
+            const int64_t own = own0 + (int64_t)row;
+            int2 span = make_int2(0, 0);
+            float lse2 = INFINITY, delta = 0.0f;           // dq: of this row
+            if constexpr (!kKeys) {
+                // delta from out: this group's quarter of the dims, kD / 32 lanes
+                // to a row, then the quarters together
+                span = span_of(p.spans, own, p.tokens);
+                constexpr int kPerRow = kD / 32, kRows = 32 / kPerRow;
+                const int dim = (int)quarter * (kD / 4) + (int)(lane % kPerRow) * 8;
+#pragma unroll
+                for (int j = 0; j < kPerRow; ++j) {
+                    const int64_t r = own - lane + kRows * j + lane / kPerRow;
+                    float part = 0.0f;
+                    if (r < p.tokens && dim < p.head_dim)
+                        part = dot8(ld_nc_v4(p.out.data + r * p.out.ld_token + (int64_t)head * p.out.ld_head + dim),
+                                    ld_nc_v4(p.dout.data + r * p.dout.ld_token + (int64_t)head * p.dout.ld_head + dim), 0.0f);
+#pragma unroll
+                    for (int o = kPerRow / 2; o > 0; o >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, o);
+                    if (lane % kPerRow == 0) vec[quarter * 128 + (warp & 3u) * 32 + kRows * j + lane / kPerRow] = part;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(delta_full);
+                ok = warp_wait_or_abort(delta_full, it & 1u, p.timeout_ns, abort_flag);
+                if (!ok) break;
+                if (span.x < span.y) {
+                    delta = (vec[row] + vec[128 + row]) + (vec[256 + row] + vec[384 + row]);
+                    lse2 = p.lse[(int64_t)head * p.tokens + own] * kLog2e;
                 }
             }
-        } else {
-            const bool alive = span.x < span.y;
-            exchange[half * 128 + row] = exact;
-            softmax_bar();
-            exact = alive ? exchange[row] + exchange[128 + row] : 0.0f;
-            const float turn = alive ? delta - exact : 0.0f;
+            float exact = 0.0f;                            // dq: sum of P dP
+            for (int i = 0; i < total; ++i, ++n) {
+                const int x0 = t * 128;                    // first streamed row
+                const uint32_t n2 = 2 * n + 1;             // X2's place among the loads
+                float slope = 0.0f;
+                if (biased) slope = p.slopes[kKeys ? h : head] * kLog2e;
+                if constexpr (kKeys) ts = p.ws.spans[t];
+                const bool masked = kKeys ? (own0 < ts.all_lo || own0 + 128 > ts.all_hi)
+                                          : (x0 < ts.all_lo || x0 + 128 > ts.all_hi);
+                const float* v_lse = vec + (n & 1u) * 256 + 32 * quarter;
+                const float* v_delta = v_lse + 128;
+                if constexpr (kKeys)
+                    ok = warp_wait_or_abort(&full[n2 % kSlots], (n2 / kSlots) & 1u, p.timeout_ns, abort_flag);
+                ok = ok && warp_wait_or_abort(s_full, n & 1u, p.timeout_ns, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                float e[32], damp[32];
+                tmem_ld_32x32b_x32(s_at, reinterpret_cast<uint32_t*>(e));
+                tmem_ld_wait();
+                if (p.sc.capped) {
 #pragma unroll
-            for (int i = 0; i < kD / 64; ++i) {
-                const uint32_t col = half * (kD / 2) + 32 * i;     // this group's columns
-                uint32_t a1[32], a2[32];
-                if (total > 0) {
-                    tmem_ld_32x32b_x32(lanes + kAcc1Col + col, a1);
-                    tmem_ld_32x32b_x32(lanes + kAcc2Col + col, a2);
-                    tmem_ld_wait();
+                    for (int j = 0; j < 32; ++j) {
+                        const float th = capped_tanh(e[j], p.sc.mult);
+                        e[j] = th * p.sc.cap_log2;
+                        damp[j] = fmaf(-th, th, 1.0f);
+                    }
                 }
+                if (biased) {
+                    const float f = p.sc.capped ? 1.0f : p.sc.mult, d = (float)((int)own - x0 - 32 * (int)quarter);
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    a2[j] = total > 0 ? __float_as_uint(fmaf(turn, __uint_as_float(a1[j]), __uint_as_float(a2[j]))) : 0u;
-                stage_row_32(ring + (col >> 6) * kChunkBytes, row, (col >> 5) & 1u, a2, p.scale);
+                    for (int j = 0; j < 32; ++j) e[j] = fmaf(-slope, fabsf(d - (float)j), e[j] * f);
+                }
+                if constexpr (kKeys) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 l4 = *reinterpret_cast<const float4*>(v_lse + j);
+                        e[j] = ex2(fmaf(e[j], c, -l4.x));
+                        e[j + 1] = ex2(fmaf(e[j + 1], c, -l4.y));
+                        e[j + 2] = ex2(fmaf(e[j + 2], c, -l4.z));
+                        e[j + 3] = ex2(fmaf(e[j + 3], c, -l4.w));
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) e[j] = ex2(fmaf(e[j], c, -lse2));
+                }
+                if (masked) {
+                    if constexpr (kKeys) {
+                        // each lane makes one query's mask over the warp's 32 keys,
+                        // which the lanes then take in turn
+                        const int2 s = span_of(p.spans, x0 + 32 * (int)quarter + (int)lane, p.tokens);
+                        const int k0 = own0 + (int)(warp & 3u) * 32;
+                        const int lo = min(max(s.x - k0, 0), 32), hi = min(max(s.y - k0, 0), 32);
+                        const uint32_t bits = lo < hi ? (0xFFFFFFFFu >> (32 - (hi - lo))) << lo : 0u;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (!((__shfl_sync(0xFFFFFFFFu, bits, j) >> lane) & 1u)) e[j] = 0.0f;
+                        // rows of queries without keys may hold anything (their P
+                        // and dZ are 0): they are zeroed for the products
+                        if (ts.all_hi == 0) {
+                            if (quarter == (warp & 3u) && s.x >= s.y) {
+                                const uint32_t r = 32 * quarter + lane;
+                                zero_tile_row(ring + ((n2 - 1) % kSlots) * S::kTile, r, S::kChunks);
+                                zero_tile_row(ring + (n2 % kSlots) * S::kTile, r, S::kChunks);
+                            }
+                            fence_proxy_async_smem();
+                        }
+                    } else {
+                        const int lo = span.x - x0 - 32 * (int)quarter, hi = span.y - x0 - 32 * (int)quarter;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j < lo || j >= hi) e[j] = 0.0f;
+                        // so may keys that no row of the tile reads
+                        if (quarter == 0 && (x0 < ts.lo || x0 + 128 > ts.hi)) {
+                            const int key = x0 + (int)row;
+                            if (key < ts.lo || key >= ts.hi)
+                                zero_tile_row(ring + ((n2 - 1) % kSlots) * S::kTile, row, S::kChunks);
+                            fence_proxy_async_smem();
+                        }
+                    }
+                }
+                uint32_t pk[16];
+                if (!kKeys && p.sc.capped) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(e[2 * j] * damp[2 * j], e[2 * j + 1] * damp[2 * j + 1]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(e[2 * j], e[2 * j + 1]);
+                }
+                tmem_st_32x32b_x16(s_at, pk);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full);
+
+                ok = warp_wait_or_abort(dp_full, n & 1u, p.timeout_ns, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int half = 0; half < 32; half += 16) {
+                    float g[16];
+                    tmem_ld_32x32b_x16(dp_at + half, reinterpret_cast<uint32_t*>(g));
+                    tmem_ld_wait();
+                    if (masked) {
+                        // a masked place's dP may be anything
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (e[half + j] == 0.0f) g[j] = 0.0f;
+                    }
+                    if constexpr (kKeys) {
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 d4 = *reinterpret_cast<const float4*>(v_delta + half + j);
+                            g[j] = e[half + j] * (g[j] - d4.x);
+                            g[j + 1] = e[half + j + 1] * (g[j + 1] - d4.y);
+                            g[j + 2] = e[half + j + 2] * (g[j + 2] - d4.z);
+                            g[j + 3] = e[half + j + 3] * (g[j + 3] - d4.w);
+                        }
+                    } else {
+                        float sum[2] = {};
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            sum[0] = fmaf(e[half + j], g[j], sum[0]);
+                            sum[1] = fmaf(e[half + j + 1], g[j + 1], sum[1]);
+                            g[j] = e[half + j] * (g[j] - delta);
+                            g[j + 1] = e[half + j + 1] * (g[j + 1] - delta);
+                        }
+                        exact += sum[0] + sum[1];
+                    }
+                    if (p.sc.capped) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) g[j] *= damp[half + j];
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) pk[half / 2 + j] = pack_bf16(g[2 * j], g[2 * j + 1]);
+                }
+                tmem_st_32x32b_x16(dp_at, pk);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(dz_full);
+                if (++t == last) {
+                    t = first;
+                    ++h;
+                }
+            }
+            // --------------------------------------------------- epilogue
+            if (ok && total > 0) ok = warp_wait_or_abort(acc_full, results++ & 1u, p.timeout_ns, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t rows0 = (warp & 3u) * 32;
+            const int64_t tok0 = own0 + (int64_t)rows0;
+            if constexpr (kKeys) {
+                // 64 dims by each group: dv by the first, dk by the others
+                const uint32_t k = quarter / S::kChunks, ch = quarter % S::kChunks;
+                const float f = k ? p.scale : 1.0f;
+                const uint32_t acc = lanes + (k ? kAcc2Col : kAcc1Col) + 64 * ch;
+                if (k < 2 && p.splits > 1) {
+                    // this split's part, in FP32
+                    float* to = p.ws.parts + (2 * split + k) * p.ws.part_size + (own * p.heads + head) * p.head_dim;
+#pragma unroll 1
+                    for (int i = 0; i < 64; i += 16) {
+                        uint32_t o[16];
+                        tmem_ld_32x32b_x16(acc + i, o);
+                        tmem_ld_wait();
+                        const int dim = 64 * (int)ch + i;
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4)
+                            if (own < p.tokens && dim + j < p.head_dim)
+                                *reinterpret_cast<float4*>(to + dim + j) =
+                                    total > 0 ? make_float4(__uint_as_float(o[j]) * f, __uint_as_float(o[j + 1]) * f,
+                                                            __uint_as_float(o[j + 2]) * f, __uint_as_float(o[j + 3]) * f)
+                                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    }
+                } else if (k < 2) {
+                    uint8_t* stage = smem + k * S::kTile + ch * kChunkBytes;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t o[32];
+                        tmem_ld_32x32b_x32(acc + 32 * i, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (total == 0) o[j] = 0;
+                        stage_row_32(stage, row, i, o, f);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && tok0 < p.tokens) {
+                        tma_store_3d(k ? &map_out2 : &map_out1, stage + rows0 * 128, (int32_t)ch * 64, head, (int32_t)tok0);
+                        bulk_commit_group();
+                        bulk_wait_read_all();
+                    }
+                }
+            } else {
+                const bool alive = span.x < span.y;
+                float* parts = exact_parts + (it & 1u) * 512;
+                parts[quarter * 128 + row] = exact;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(exact_full);
+                ok = warp_wait_or_abort(exact_full, it & 1u, p.timeout_ns, abort_flag);
+                if (!ok) break;
+                exact = alive ? (parts[row] + parts[128 + row]) + (parts[256 + row] + parts[384 + row]) : 0.0f;
+                const float turn = alive ? delta - exact : 0.0f;
+                if (quarter < S::kChunks) {
+                    uint8_t* stage = smem + quarter * kChunkBytes;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t col = 64 * quarter + 16 * i;
+                        uint32_t a1[16], a2[16];
+                        tmem_ld_32x32b_x16(lanes + kAcc1Col + col, a1);
+                        tmem_ld_32x32b_x16(lanes + kAcc2Col + col, a2);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            a2[j] = total > 0 ? __float_as_uint(fmaf(turn, __uint_as_float(a1[j]), __uint_as_float(a2[j]))) : 0u;
+                        stage_row_16(stage, row, i, a2, p.scale);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && tok0 < p.tokens) {
+                        tma_store_3d(&map_out1, stage + rows0 * 128, (int32_t)quarter * 64, head, (int32_t)tok0);
+                        bulk_commit_group();
+                        bulk_wait_read_all();
+                    }
+                }
+                if (quarter == 3) {
+                    p.ws.lse2[(int64_t)head * p.ws.ld + own] = alive ? lse2 : INFINITY;
+                    p.ws.delta[(int64_t)head * p.ws.ld + own] = exact;
+                }
             }
             fence_proxy_async_smem();
-            softmax_bar();
-            if (half == 0) {
-                p.ws.lse2[(int64_t)head * p.ws.ld + own] = alive ? lse2 : INFINITY;
-                p.ws.delta[(int64_t)head * p.ws.ld + own] = exact;
-                if (ok && tok0 < p.tokens && lane == 0) {
-                    for (uint32_t ch = 0; ch < S::kChunks; ++ch)
-                        tma_store_3d(&map_out1, ring + ch * kChunkBytes + rows0 * 128, (int32_t)ch * 64, head,
-                                     (int32_t)tok0);
-                    bulk_commit_group();
-                    bulk_wait_all();
-                }
-            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(f_empty);
         }
+        give_up(!ok && lane == 0);
+        if (lane == 0) bulk_wait_all();
     }
     __syncwarp();
     tc_fence_before();
@@ -566,8 +689,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
-// As in the forward pass: 128 * 80 + 256 * 208 registers of the launch's
-// 384 * 168.
+// dv and dk from their parts, summed in the order of the splits: a thread
+// takes 8 dims of one head vector.
+__global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ Params p, const HeadsView dv,
+                                                         const HeadsView dk, const Extent xdv, const Extent xdk) {
+    const uint32_t pieces = (uint32_t)p.head_dim / 8;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= p.tokens * p.heads * pieces) return;
+    const bool k = blockIdx.y != 0;
+    float sum[8] = {};
+    for (int s = 0; s < p.splits; ++s) {
+        const float* from = p.ws.parts + (2 * s + (k ? 1 : 0)) * p.ws.part_size + 8 * i;
+        const float4 a = *reinterpret_cast<const float4*>(from), b = *reinterpret_cast<const float4*>(from + 4);
+        sum[0] += a.x;
+        sum[1] += a.y;
+        sum[2] += a.z;
+        sum[3] += a.w;
+        sum[4] += b.x;
+        sum[5] += b.y;
+        sum[6] += b.z;
+        sum[7] += b.w;
+    }
+    const int64_t vector = i / pieces, token = vector / p.heads;
+    const HeadsView& out = k ? dk : dv;
+    uint16_t* to = out.data + token * out.ld_token + (vector - token * p.heads) * out.ld_head + (i - vector * pieces) * 8;
+    store_out(reinterpret_cast<uint4*>(to),
+              make_uint4(pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3]), pack_bf16(sum[4], sum[5]),
+                         pack_bf16(sum[6], sum[7])),
+              k ? xdk : xdv);
+}
+
+// As in the forward pass: a build whose launch has too few registers for the
+// groups' shares is not launched.
 template <int kD, bool kKeys>
 cudaError_t prepare_kernel() {
     static bool done[64];
@@ -578,7 +731,7 @@ cudaError_t prepare_kernel() {
     cudaError_t e = cudaFuncGetAttributes(&f, attention_backward_kernel<kD, kKeys>);
     // the tiles' swizzle needs dynamic shared memory to start on 1024 bytes:
     // it does when there is no static shared memory before it
-    if (e == cudaSuccess && (f.numRegs * kThreads < 128 * 80 + 256 * 208 || f.sharedSizeBytes != 0))
+    if (e == cudaSuccess && (f.numRegs * kThreads < 128 * kControlRegs + 512 * kSoftmaxRegs || f.sharedSizeBytes != 0))
         e = cudaErrorInvalidConfiguration;
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(attention_backward_kernel<kD, kKeys>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -587,12 +740,30 @@ cudaError_t prepare_kernel() {
     return e;
 }
 
-Workspace carve(float* base, int64_t tokens, int64_t q_heads) {
+// The dk dv kernel has an item per key tile and key head; where these are too
+// few for the SMs (few key heads, short sequences) each is split over its
+// streamed tiles, at the cost of FP32 parts written and summed.  Two items
+// per SM even out the items' lengths.
+int split_count(int64_t tokens, int q_heads, int kv_heads) {
+    const int64_t tiles = (tokens + 127) / 128, items = tiles * kv_heads;
+    const int64_t want = 2 * (int64_t)device_sm_count();
+    if (2 * items > want) return 1;
+    const int64_t most = tiles * (q_heads / kv_heads);       // streamed tiles of the longest item
+    int64_t splits = want / items;
+    splits = splits < kMaxSplits ? splits : kMaxSplits;
+    return (int)(splits < most ? splits : most);
+}
+
+Workspace carve(float* base, int64_t tokens, int q_heads, int kv_heads, int head_dim, int splits, size_t* bytes) {
     Workspace w;
     w.ld = (tokens + 127) / 128 * 128;
+    w.part_size = tokens * kv_heads * head_dim;
     w.lse2 = base;
     w.delta = base + w.ld * q_heads;
     w.spans = reinterpret_cast<TileSpan*>(w.delta + w.ld * q_heads);
+    w.parts = reinterpret_cast<float*>(w.spans + w.ld / 128);
+    if (bytes)
+        *bytes = (size_t)((w.ld * q_heads * 2 + w.ld / 32 + (splits > 1 ? 2 * splits * w.part_size : 0)) * 4);
     return w;
 }
 
@@ -622,7 +793,9 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
     p.out = a.out;
     p.dout = a.dout;
     p.head_dim = a.head_dim;
-    p.ws = carve(a.workspace, a.tokens, a.q_heads);
+    const int splits = split_count(a.tokens, a.q_heads, a.kv_heads);
+    p.ws = carve(a.workspace, a.tokens, a.q_heads, a.kv_heads, a.head_dim, splits, nullptr);
+    p.splits = 1;
     p.timeout_ns = kAttentionTimeoutNs;
     if ((uint64_t)p.tiles * (uint64_t)a.q_heads > 0x7FFFFFFFull) return cudaErrorInvalidValue;
     p.heads = a.q_heads;
@@ -631,21 +804,31 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     p.heads = a.kv_heads;
-    attention_backward_kernel<kD, true><<<(unsigned)(p.tiles * a.kv_heads), kThreads, Shape<kD>::kSmem, stream>>>(
+    p.splits = splits;
+    attention_backward_kernel<kD, true><<<(unsigned)(p.tiles * a.kv_heads * splits), kThreads, Shape<kD>::kSmem, stream>>>(
         mk, mv, mq, mdo, mdv, mdk, p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || splits == 1) return e;
+    const int64_t pieces = a.tokens * a.kv_heads * (a.head_dim / 8);
+    join_parts_kernel<<<dim3((unsigned)((pieces + 255) / 256), 2), 256, 0, stream>>>(
+        p, a.dv, a.dk, extent_heads(a.dv, a.tokens, a.kv_heads, a.head_dim),
+        extent_heads(a.dk, a.tokens, a.kv_heads, a.head_dim));
     return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t attention_backward_workspace_bytes(int64_t tokens, int64_t q_heads) {
-    const int64_t tiles = (tokens + 127) / 128;
-    return (size_t)(tiles * 128 * q_heads * 2) * sizeof(float) + (size_t)tiles * sizeof(TileSpan);
+size_t attention_backward_workspace_bytes(int64_t tokens, int q_heads, int kv_heads, int head_dim) {
+    size_t bytes = 0;
+    carve(nullptr, tokens, q_heads, kv_heads, head_dim, split_count(tokens, q_heads, kv_heads), &bytes);
+    return bytes;
 }
 
 cudaError_t launch_attention_backward(const Attention& a, cudaStream_t stream) {
     return a.head_dim <= 64 ? launch<64>(a, stream) : launch<128>(a, stream);
 }
+
+cudaError_t attention_backward_bounds_read_and_clear(uint64_t* n) { return bounds_read_and_clear_local(n); }
 
 cudaError_t attention_backward_status_read_and_clear(unsigned int* status) {
     return attention_status_read_and_clear_local(status);

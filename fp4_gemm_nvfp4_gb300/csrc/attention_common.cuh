@@ -97,18 +97,22 @@ __device__ __forceinline__ void zero_tile_row(uint8_t* tile, uint32_t row, uint3
             *reinterpret_cast<uint4*>(tile + c * kChunkBytes + row * 128 + i * 16) = make_uint4(0, 0, 0, 0);
 }
 
-// 32 FP32 values of a tensor-memory row, times f, as BF16 into half a chunk
-// of the row's 128 bytes (half: 0 or 1) of a swizzled tile.
-__device__ __forceinline__ void stage_row_32(uint8_t* chunk, uint32_t row, uint32_t half, const uint32_t* v, float f) {
+// 16 FP32 values of a tensor-memory row, times f, as BF16 into a quarter of
+// the row's 128 bytes of a swizzled chunk.
+__device__ __forceinline__ void stage_row_16(uint8_t* chunk, uint32_t row, uint32_t quarter, const uint32_t* v, float f) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
         uint4 o;
         o.x = pack_bf16(__uint_as_float(v[8 * i]) * f, __uint_as_float(v[8 * i + 1]) * f);
         o.y = pack_bf16(__uint_as_float(v[8 * i + 2]) * f, __uint_as_float(v[8 * i + 3]) * f);
         o.z = pack_bf16(__uint_as_float(v[8 * i + 4]) * f, __uint_as_float(v[8 * i + 5]) * f);
         o.w = pack_bf16(__uint_as_float(v[8 * i + 6]) * f, __uint_as_float(v[8 * i + 7]) * f);
-        *reinterpret_cast<uint4*>(chunk + row * 128 + (((4 * half + i) ^ (row & 7u)) * 16)) = o;
+        *reinterpret_cast<uint4*>(chunk + row * 128 + (((2 * quarter + i) ^ (row & 7u)) * 16)) = o;
     }
+}
+__device__ __forceinline__ void stage_row_32(uint8_t* chunk, uint32_t row, uint32_t half, const uint32_t* v, float f) {
+    stage_row_16(chunk, row, 2 * half, v, f);
+    stage_row_16(chunk, row, 2 * half + 1, v + 16, f);
 }
 
 // Map of head vectors [tokens][heads][head_dim]: boxes of 64 dims by one head

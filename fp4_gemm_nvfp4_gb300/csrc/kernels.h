@@ -104,6 +104,7 @@ cudaError_t dequantize_bounds_read_and_clear(uint64_t* n);
 cudaError_t norm_rope_bounds_read_and_clear(uint64_t* n);
 cudaError_t attention_spans_bounds_read_and_clear(uint64_t* n);
 cudaError_t attention_forward_bounds_read_and_clear(uint64_t* n);
+cudaError_t attention_backward_bounds_read_and_clear(uint64_t* n);
 
 // Test support: the next GEMM launch waits at most timeout_ns per barrier and
 // its leader CTA leaves out one scale-warp arrival, so one wait runs out.
@@ -155,7 +156,7 @@ struct Attention {
 cudaError_t launch_attention_spans(const int32_t* offsets, int64_t documents, const int32_t* prefix, bool causal,
                                    int64_t tokens, int32_t* spans, cudaStream_t stream);
 cudaError_t launch_attention(const Attention& a, cudaStream_t stream);
-size_t attention_backward_workspace_bytes(int64_t tokens, int64_t q_heads);
+size_t attention_backward_workspace_bytes(int64_t tokens, int q_heads, int kv_heads, int head_dim);
 cudaError_t launch_attention_backward(const Attention& a, cudaStream_t stream);
 
 // cuTensorMapEncodeTiled from the driver (null if unavailable).

@@ -420,7 +420,7 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
         dk = torch.empty((tokens, kv_heads, dim), dtype=torch.bfloat16, device=q.device)
     if dv is None:
         dv = torch.empty((tokens, kv_heads, dim), dtype=torch.bfloat16, device=q.device)
-    nbytes = capi.nvfp4_attention_backward_workspace_size(tokens, q_heads)
+    nbytes = capi.nvfp4_attention_backward_workspace_size(tokens, q_heads, kv_heads, dim)
     if workspace is None or workspace.numel() < nbytes:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
     status = capi.nvfp4_attention_backward(

@@ -529,10 +529,11 @@ NVFP4_API nvfp4_status nvfp4_attention(const nvfp4_attention_desc *desc, const n
  * head.  Everything is recomputed from lse; sums run in a fixed order: equal
  * inputs give equal bits.  The probabilities and the scores' gradients are
  * rounded to BF16 for their products, sums are FP32.
- *  workspace    nvfp4_attention_backward_workspace_size(tokens, q_heads)
- *               bytes, 16-byte aligned.
+ *  workspace    nvfp4_attention_backward_workspace_size() bytes, 16-byte
+ *               aligned (0 bytes for a shape that is refused).
  */
-NVFP4_API size_t nvfp4_attention_backward_workspace_size(int64_t tokens, int32_t q_heads);
+NVFP4_API size_t nvfp4_attention_backward_workspace_size(int64_t tokens, int32_t q_heads, int32_t kv_heads,
+                                                         int32_t head_dim);
 NVFP4_API nvfp4_status nvfp4_attention_backward(const nvfp4_attention_desc *desc, const nvfp4_heads *dout,
                                                 const nvfp4_heads *q, const nvfp4_heads *k, const nvfp4_heads *v,
                                                 const nvfp4_heads *out, const float *lse, const nvfp4_heads *dq,

@@ -229,7 +229,7 @@ def test_other_stream_and_graph():
     spans = _causal(300)
     o, lse = ops.attention(q, k, v, spans)
     want = (o, lse, *ops.attention_backward(do, q, k, v, o, lse, spans))
-    ws = torch.empty(capi.nvfp4_attention_backward_workspace_size(300, 4), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(capi.nvfp4_attention_backward_workspace_size(300, 4, 2, 64), dtype=torch.uint8, device="cuda")
     outs = [torch.zeros_like(x) for x in want]
 
     def step(stream):
