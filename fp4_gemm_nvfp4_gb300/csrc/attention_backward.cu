@@ -41,10 +41,10 @@ constexpr uint32_t kSoftmaxWarps = 16;
 constexpr int kControlRegs = 64, kSoftmaxRegs = 104;   // per thread, of the launch's 96
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 0, kDpCol = 128, kAcc1Col = 256, kAcc2Col = 384;
-// Streamed tiles in flight.  With five, the place of X2(i + 2) is that of
-// X1(i), free only when dZ(i) has been formed: its rows' lse and delta then
-// need two places.
-constexpr uint32_t kSlots = 5;
+// Streamed tiles in flight.  With four, the place of X1(i + 2) is that of
+// X1(i), free only when dZ(i) has been formed: its rows' lse and delta, which
+// come with X1, then need two places.
+constexpr uint32_t kSlots = 4;
 constexpr uint32_t kVecBytes = 2 * 128 * sizeof(float);
 constexpr uint32_t kMaxSplits = 8;
 
@@ -52,11 +52,12 @@ template <int kD>
 struct Shape {
     static constexpr uint32_t kChunks = kD / 64;
     static constexpr uint32_t kTile = kChunks * kChunkBytes;
-    static constexpr uint32_t kVecAt = (2 + kSlots) * kTile;
+    static constexpr uint32_t kStageAt = (2 + kSlots) * kTile;   // 32 rows x 32 dims of results per softmax warp
+    static constexpr uint32_t kVecAt = kStageAt + kSoftmaxWarps * 2048;
     static constexpr uint32_t kBarAt = kVecAt + 2 * kVecBytes;
     static constexpr size_t kSmem = kBarAt + 1024;   // dynamic shared memory starts 1024-byte aligned (checked)
 };
-static_assert(Shape<128>::kSmem <= 232448, "shared memory budget");
+static_assert(Shape<128>::kSmem <= 232448 && Shape<64>::kSmem <= 232448, "shared memory budget");
 
 // The workspace: per query head and row (rounded up to tiles) lse in log2 (inf
 // for a row without keys) and the exact delta, then the tiles' spans.
@@ -81,6 +82,8 @@ struct Params {
     const int32_t* spans;
     const float* lse;
     HeadsView out, dout;
+    HeadsView dv, dk;                // joined from their parts
+    Extent xdv, xdk;
     int32_t head_dim;
     Workspace ws;
     uint64_t timeout_ns;
@@ -125,16 +128,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* ring = smem + 2 * S::kTile;
     float* vec = reinterpret_cast<float*>(smem + S::kVecAt);     // [2][lse2, delta][128] of the streamed rows
-    // dq: quarters of the rows' deltas, [4][128] from out in the vectors' place
-    // (unused there), and [2 items][4][128] exact ones in that of the own tiles
-    // once they are done with
-    float* exact_parts = reinterpret_cast<float*>(smem + S::kTile);
+    float* exact_parts = vec;                                    // dq, instead: [4][128] quarters of exact deltas
     Item* items = reinterpret_cast<Item*>(smem + S::kBarAt);     // [2] the current and the next
     uint4* answer = reinterpret_cast<uint4*>(items + 2);
     uint64_t* full = reinterpret_cast<uint64_t*>(answer + 1);
     uint64_t* empty = full + kSlots;
     uint64_t* f_full = empty + kSlots;           // the item's own tiles loaded
-    uint64_t* f_empty = f_full + 1;              // ... and their place free: it stages the results
+    uint64_t* f_empty = f_full + 1;              // ... and their last scores done
     uint64_t* s_full = f_empty + 1;
     uint64_t* dp_full = s_full + 1;
     uint64_t* p_full = dp_full + 1;
@@ -143,12 +143,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* item_full = acc_full + 1;          // [2]
     uint64_t* item_empty = item_full + 2;        // [2]
     uint64_t* loaded = item_empty + 2;           // the item's loads issued
-    uint64_t* delta_full = loaded + 1;           // dq: the quarters of the deltas written
-    uint64_t* exact_full = delta_full + 1;       // ... of the exact ones
+    uint64_t* delta_full = loaded + 1;           // dq: the rows' deltas written
+    uint64_t* exact_full = delta_full + 1;       // ... the quarters of the exact ones
     uint64_t* answered = exact_full + 1;
     uint64_t* drain = answered + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile uint32_t* abort_flag = tmem_slot + 1;
+    float* row_delta = reinterpret_cast<float*>(smem + S::kBarAt + 512);   // dq: [128]
 
     const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31u;
     if (threadIdx.x == 0) {
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&empty[i], 1);
         }
         mbar_init(f_full, 1);
-        mbar_init(f_empty, kSoftmaxWarps);
+        mbar_init(f_empty, 1);
         mbar_init(s_full, 1);
         mbar_init(dp_full, 1);
         mbar_init(p_full, kSoftmaxWarps);
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < item.total && ok; ++i, ++n) {
                     for (int x = 0; x < 2; ++x) {
                         if (!await(&empty[slot], phase ^ 1u)) break;
-                        const bool vectors = kKeys && x == 1;
+                        const bool vectors = kKeys && x == 0;
                         mbar_arrive_expect_tx(&full[slot], S::kTile + (vectors ? kVecBytes : 0u));
                         for (uint32_t c = 0; c < S::kChunks; ++c)
                             tma_load_3d(ring + slot * S::kTile + c * kChunkBytes, x ? &map_x2 : &map_x1, &full[slot],
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             phase ^= 1u;
                         }
                     }
-                    if (ok && i == 0 && await(f_empty, (it & 1u) ^ 1u)) {
+                    if (ok && i == 0 && await(f_empty, (own_loads & 1u) ^ 1u)) {
                         ++own_loads;
                         mbar_arrive_expect_tx(f_full, 2 * S::kTile);
                         for (uint32_t c = 0; c < S::kChunks; ++c) {
@@ -248,7 +249,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ++h;
                     }
                 }
-                if (item.total == 0) await(f_empty, (it & 1u) ^ 1u);
                 if (ok) mbar_arrive(loaded);
             }
             give_up(!ok);
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // places of X1(i), X2(i) for the products, of the next X1 for S and dP
             uint32_t n = 0, x1 = 0, x2 = 0, at = 0, at_phase = 0, own_tiles = 0;
-            auto scores = [&](uint32_t x) {
+            auto scores = [&](uint32_t x, bool last) {
                 const uint32_t slot = at;
                 (x ? x2 : x1) = slot;
                 await(full0 + 8 * slot, at_phase);
@@ -287,6 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      xk_lo + slot * (S::kTile >> 4), elected);
                 tc_commit(x ? dp_full : s_full, elected);
                 if (!kKeys && x == 1) tc_commit(&empty[slot], elected);   // dq: v is needed for dP alone
+                if (last) tc_commit(f_empty, elected);
             };
             auto product = [&](uint32_t acc, uint32_t slot, bool start) {
                 await(smem_u32(acc ? dz_full : p_full), n & 1u);
@@ -305,14 +306,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!valid) break;
                 if (total == 0) continue;
                 await(smem_u32(f_full), own_tiles++ & 1u);
-                scores(0);
-                scores(1);
+                scores(0, false);
+                scores(1, total == 1);
                 for (int i = 0; i < total && ok; ++i, ++n) {
                     const uint32_t c1 = x1, c2 = x2;
                     product(0, kKeys ? c2 : c1, i == 0);
-                    if (i + 1 < total) scores(0);
+                    if (i + 1 < total) scores(0, false);
                     product(1, c1, i == 0);
-                    if (i + 1 < total) scores(1);
+                    if (i + 1 < total) scores(1, i + 2 == total);
                 }
                 if (!ok) break;
                 tc_commit(acc_full, elected);
@@ -404,7 +405,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float c = p.sc.capped || biased ? 1.0f : p.sc.mult;
         uint32_t n = 0, results = 0;               // streamed tiles, items with a result so far
         bool ok = true;
-        for (uint32_t it = 0;; ++it) {
+        // dq: an item's delta~ is formed before the epilogue of the item before, 8
+        // rows by each warp, kD / 8 lanes to a row.
+        constexpr int kPerRow = kD / 8, kRows = 32 / kPerRow, kTurns = 8 / kRows;
+        int2 span = make_int2(0, 0);
+        float lse = 0.0f;
+        auto prepare = [&](const Item& item) {
+            const uint32_t row8 = (warp & 3u) * 32 + quarter * 8 + lane / kPerRow;
+            const int64_t own0 = (int64_t)item.tile * 128;
+            const int dim = (int)(lane % kPerRow) * 8;
+            const uint16_t* o = p.out.data + (int64_t)item.head * p.out.ld_head + dim;
+            const uint16_t* d = p.dout.data + (int64_t)item.head * p.dout.ld_head + dim;
+            uint4 op[kTurns], dp[kTurns];
+#pragma unroll
+            for (int j = 0; j < kTurns; ++j) {
+                const int64_t r = own0 + row8 + kRows * j;
+                const bool on = r < p.tokens && dim < p.head_dim;
+                op[j] = on ? ld_nc_v4(o + r * p.out.ld_token) : make_uint4(0, 0, 0, 0);
+                dp[j] = on ? ld_nc_v4(d + r * p.dout.ld_token) : make_uint4(0, 0, 0, 0);
+            }
+            span = span_of(p.spans, own0 + row, p.tokens);
+            if (own0 + row < p.tokens) lse = p.lse[(int64_t)item.head * p.tokens + own0 + row];
+#pragma unroll
+            for (int j = 0; j < kTurns; ++j) {
+                float part = dot8(op[j], dp[j], 0.0f);
+#pragma unroll
+                for (int o2 = kPerRow / 2; o2 > 0; o2 >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, o2);
+                if (lane % kPerRow == 0) row_delta[row8 + kRows * j] = part;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(delta_full);
+        };
+        if constexpr (!kKeys) {
+            ok = warp_wait_or_abort(&item_full[0], 0, p.timeout_ns, abort_flag);
+            if (ok) prepare(items[0]);
+        }
+        uint8_t* stage = smem + S::kStageAt + (warp - kFirstSoftmaxWarp) * 2048;
+        for (uint32_t it = 0; ok; ++it) {
             ok = warp_wait_or_abort(&item_full[it & 1u], (it >> 1) & 1u, p.timeout_ns, abort_flag);
             if (!ok) break;
             const Item& item = items[it & 1u];
@@ -417,32 +454,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&item_empty[it & 1u]);
             if (!valid) break;
             const int64_t own = own0 + (int64_t)row;
-            int2 span = make_int2(0, 0);
             float lse2 = INFINITY, delta = 0.0f;           // dq: of this row
             if constexpr (!kKeys) {
-                // delta from out: this group's quarter of the dims, kD / 32 lanes
-                // to a row, then the quarters together
-                span = span_of(p.spans, own, p.tokens);
-                constexpr int kPerRow = kD / 32, kRows = 32 / kPerRow;
-                const int dim = (int)quarter * (kD / 4) + (int)(lane % kPerRow) * 8;
-#pragma unroll
-                for (int j = 0; j < kPerRow; ++j) {
-                    const int64_t r = own - lane + kRows * j + lane / kPerRow;
-                    float part = 0.0f;
-                    if (r < p.tokens && dim < p.head_dim)
-                        part = dot8(ld_nc_v4(p.out.data + r * p.out.ld_token + (int64_t)head * p.out.ld_head + dim),
-                                    ld_nc_v4(p.dout.data + r * p.dout.ld_token + (int64_t)head * p.dout.ld_head + dim), 0.0f);
-#pragma unroll
-                    for (int o = kPerRow / 2; o > 0; o >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, o);
-                    if (lane % kPerRow == 0) vec[quarter * 128 + (warp & 3u) * 32 + kRows * j + lane / kPerRow] = part;
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(delta_full);
                 ok = warp_wait_or_abort(delta_full, it & 1u, p.timeout_ns, abort_flag);
                 if (!ok) break;
+                // a row without keys may hold anything
                 if (span.x < span.y) {
-                    delta = (vec[row] + vec[128 + row]) + (vec[256 + row] + vec[384 + row]);
-                    lse2 = p.lse[(int64_t)head * p.tokens + own] * kLog2e;
+                    delta = row_delta[row];
+                    lse2 = lse * kLog2e;
                 }
             }
             float exact = 0.0f;                            // dq: sum of P dP
@@ -456,9 +475,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                           : (x0 < ts.all_lo || x0 + 128 > ts.all_hi);
                 const float* v_lse = vec + (n & 1u) * 256 + 32 * quarter;
                 const float* v_delta = v_lse + 128;
-                if constexpr (kKeys)
-                    ok = warp_wait_or_abort(&full[n2 % kSlots], (n2 / kSlots) & 1u, p.timeout_ns, abort_flag);
-                ok = ok && warp_wait_or_abort(s_full, n & 1u, p.timeout_ns, abort_flag);
+                ok = warp_wait_or_abort(s_full, n & 1u, p.timeout_ns, abort_flag);
+                // (X1 is there, S was made of it; this makes its rows' vectors visible)
+                if (kKeys && ok)
+                    ok = warp_wait_or_abort(&full[(n2 - 1) % kSlots], ((n2 - 1) / kSlots) & 1u, p.timeout_ns, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
                 float e[32], damp[32];
@@ -504,6 +524,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // rows of queries without keys may hold anything (their P
                         // and dZ are 0): they are zeroed for the products
                         if (ts.all_hi == 0) {
+                            ok = warp_wait_or_abort(&full[n2 % kSlots], (n2 / kSlots) & 1u, p.timeout_ns, abort_flag);
+                            if (!ok) break;
                             if (quarter == (warp & 3u) && s.x >= s.y) {
                                 const uint32_t r = 32 * quarter + lane;
                                 zero_tile_row(ring + ((n2 - 1) % kSlots) * S::kTile, r, S::kChunks);
@@ -590,97 +612,86 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++h;
                 }
             }
+            if (!ok) break;
+            const bool alive = span.x < span.y;
+            if constexpr (!kKeys) {
+                const uint32_t next = it + 1;
+                ok = warp_wait_or_abort(&item_full[next & 1u], (next >> 1) & 1u, p.timeout_ns, abort_flag);
+                if (!ok) break;
+                if (items[next & 1u].valid) prepare(items[next & 1u]);
+            }
             // --------------------------------------------------- epilogue
-            if (ok && total > 0) ok = warp_wait_or_abort(acc_full, results++ & 1u, p.timeout_ns, abort_flag);
+            if (total > 0) ok = warp_wait_or_abort(acc_full, results++ & 1u, p.timeout_ns, abort_flag);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t rows0 = (warp & 3u) * 32;
-            const int64_t tok0 = own0 + (int64_t)rows0;
+            // 32 rows x 32 dims of a result at a time through the warp's place
+            auto store = [&](const CUtensorMap* map, uint32_t col, const uint32_t* v) {
+                if (lane == 0) bulk_wait_read_all();   // the place's last store
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3u)) * 16)) =
+                        make_uint4(pack_bf16(__uint_as_float(v[8 * i]), __uint_as_float(v[8 * i + 1])),
+                                   pack_bf16(__uint_as_float(v[8 * i + 2]), __uint_as_float(v[8 * i + 3])),
+                                   pack_bf16(__uint_as_float(v[8 * i + 4]), __uint_as_float(v[8 * i + 5])),
+                                   pack_bf16(__uint_as_float(v[8 * i + 6]), __uint_as_float(v[8 * i + 7])));
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0 && own < p.tokens) {
+                    tma_store_3d(map, stage, (int32_t)col, head, (int32_t)own);
+                    bulk_commit_group();
+                }
+            };
             if constexpr (kKeys) {
-                // 64 dims by each group: dv by the first, dk by the others
-                const uint32_t k = quarter / S::kChunks, ch = quarter % S::kChunks;
-                const float f = k ? p.scale : 1.0f;
-                const uint32_t acc = lanes + (k ? kAcc2Col : kAcc1Col) + 64 * ch;
-                if (k < 2 && p.splits > 1) {
-                    // this split's part, in FP32
-                    float* to = p.ws.parts + (2 * split + k) * p.ws.part_size + (own * p.heads + head) * p.head_dim;
+                // dv, then dk, 32 dims by each group in turn
 #pragma unroll 1
-                    for (int i = 0; i < 64; i += 16) {
-                        uint32_t o[16];
-                        tmem_ld_32x32b_x16(acc + i, o);
-                        tmem_ld_wait();
-                        const int dim = 64 * (int)ch + i;
+                for (uint32_t u = quarter; u < 2 * (kD / 32); u += 4) {
+                    const uint32_t k = u / (kD / 32), col = 32 * (u % (kD / 32));
+                    uint32_t o[32];
+                    tmem_ld_32x32b_x32(lanes + (k ? kAcc2Col : kAcc1Col) + col, o);
+                    tmem_ld_wait();
+                    const float f = k ? p.scale : 1.0f;
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4)
-                            if (own < p.tokens && dim + j < p.head_dim)
-                                *reinterpret_cast<float4*>(to + dim + j) =
-                                    total > 0 ? make_float4(__uint_as_float(o[j]) * f, __uint_as_float(o[j + 1]) * f,
-                                                            __uint_as_float(o[j + 2]) * f, __uint_as_float(o[j + 3]) * f)
-                                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    }
-                } else if (k < 2) {
-                    uint8_t* stage = smem + k * S::kTile + ch * kChunkBytes;
+                    for (int j = 0; j < 32; ++j) o[j] = total > 0 ? __float_as_uint(__uint_as_float(o[j]) * f) : 0u;
+                    if (p.splits > 1) {
+                        // this split's part, in FP32
+                        float* part = p.ws.parts + (2 * split + k) * p.ws.part_size + (own * p.heads + head) * p.head_dim + col;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t o[32];
-                        tmem_ld_32x32b_x32(acc + 32 * i, o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (total == 0) o[j] = 0;
-                        stage_row_32(stage, row, i, o, f);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0 && tok0 < p.tokens) {
-                        tma_store_3d(k ? &map_out2 : &map_out1, stage + rows0 * 128, (int32_t)ch * 64, head, (int32_t)tok0);
-                        bulk_commit_group();
-                        bulk_wait_read_all();
+                        for (int j = 0; j < 32; j += 4)
+                            if (own < p.tokens && (int)col + j < p.head_dim)
+                                *reinterpret_cast<uint4*>(part + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                    } else {
+                        store(k ? &map_out2 : &map_out1, col, o);
                     }
                 }
             } else {
-                const bool alive = span.x < span.y;
-                float* parts = exact_parts + (it & 1u) * 512;
-                parts[quarter * 128 + row] = exact;
+                exact_parts[quarter * 128 + row] = exact;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(exact_full);
                 ok = warp_wait_or_abort(exact_full, it & 1u, p.timeout_ns, abort_flag);
                 if (!ok) break;
-                exact = alive ? (parts[row] + parts[128 + row]) + (parts[256 + row] + parts[384 + row]) : 0.0f;
+                exact = alive ? (exact_parts[row] + exact_parts[128 + row]) + (exact_parts[256 + row] + exact_parts[384 + row])
+                              : 0.0f;
                 const float turn = alive ? delta - exact : 0.0f;
-                if (quarter < S::kChunks) {
-                    uint8_t* stage = smem + quarter * kChunkBytes;
+                if (quarter < kD / 32) {
+                    uint32_t a1[32], a2[32];
+                    tmem_ld_32x32b_x32(lanes + kAcc1Col + 32 * quarter, a1);
+                    tmem_ld_32x32b_x32(lanes + kAcc2Col + 32 * quarter, a2);
+                    tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t col = 64 * quarter + 16 * i;
-                        uint32_t a1[16], a2[16];
-                        tmem_ld_32x32b_x16(lanes + kAcc1Col + col, a1);
-                        tmem_ld_32x32b_x16(lanes + kAcc2Col + col, a2);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            a2[j] = total > 0 ? __float_as_uint(fmaf(turn, __uint_as_float(a1[j]), __uint_as_float(a2[j]))) : 0u;
-                        stage_row_16(stage, row, i, a2, p.scale);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0 && tok0 < p.tokens) {
-                        tma_store_3d(&map_out1, stage + rows0 * 128, (int32_t)quarter * 64, head, (int32_t)tok0);
-                        bulk_commit_group();
-                        bulk_wait_read_all();
-                    }
+                    for (int j = 0; j < 32; ++j)
+                        a2[j] = total > 0 ? __float_as_uint(fmaf(turn, __uint_as_float(a1[j]), __uint_as_float(a2[j])) * p.scale)
+                                          : 0u;
+                    store(&map_out1, 32 * quarter, a2);
                 }
                 if (quarter == 3) {
-                    p.ws.lse2[(int64_t)head * p.ws.ld + own] = alive ? lse2 : INFINITY;
+                    p.ws.lse2[(int64_t)head * p.ws.ld + own] = lse2;
                     p.ws.delta[(int64_t)head * p.ws.ld + own] = exact;
                 }
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(f_empty);
         }
-        give_up(!ok && lane == 0);
         if (lane == 0) bulk_wait_all();
+        give_up(!ok && lane == 0);
     }
     __syncwarp();
     tc_fence_before();
@@ -691,8 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // dv and dk from their parts, summed in the order of the splits: a thread
 // takes 8 dims of one head vector.
-__global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ Params p, const HeadsView dv,
-                                                         const HeadsView dk, const Extent xdv, const Extent xdk) {
+__global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ Params p) {
     const uint32_t pieces = (uint32_t)p.head_dim / 8;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= p.tokens * p.heads * pieces) return;
@@ -711,12 +721,12 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__
         sum[7] += b.w;
     }
     const int64_t vector = i / pieces, token = vector / p.heads;
-    const HeadsView& out = k ? dk : dv;
+    const HeadsView& out = k ? p.dk : p.dv;
     uint16_t* to = out.data + token * out.ld_token + (vector - token * p.heads) * out.ld_head + (i - vector * pieces) * 8;
     store_out(reinterpret_cast<uint4*>(to),
               make_uint4(pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3]), pack_bf16(sum[4], sum[5]),
                          pack_bf16(sum[6], sum[7])),
-              k ? xdk : xdv);
+              k ? p.xdk : p.xdv);
 }
 
 // As in the forward pass: a build whose launch has too few registers for the
@@ -777,9 +787,9 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
         !make_heads_map(&mk, a.k, a.tokens, a.kv_heads, a.head_dim, 128) ||
         !make_heads_map(&mv, a.v, a.tokens, a.kv_heads, a.head_dim, 128) ||
         !make_heads_map(&mdo, a.dout, a.tokens, a.q_heads, a.head_dim, 128) ||
-        !make_heads_map(&mdq, a.dq, a.tokens, a.q_heads, a.head_dim, 32) ||
-        !make_heads_map(&mdk, a.dk, a.tokens, a.kv_heads, a.head_dim, 32) ||
-        !make_heads_map(&mdv, a.dv, a.tokens, a.kv_heads, a.head_dim, 32))
+        !make_heads_map(&mdq, a.dq, a.tokens, a.q_heads, a.head_dim, 32, 32) ||
+        !make_heads_map(&mdk, a.dk, a.tokens, a.kv_heads, a.head_dim, 32, 32) ||
+        !make_heads_map(&mdv, a.dv, a.tokens, a.kv_heads, a.head_dim, 32, 32))
         return cudaErrorInvalidValue;
     Params p{};
     p.tokens = a.tokens;
@@ -804,15 +814,17 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     p.heads = a.kv_heads;
+    p.dv = a.dv;
+    p.dk = a.dk;
+    p.xdv = extent_heads(a.dv, a.tokens, a.kv_heads, a.head_dim);
+    p.xdk = extent_heads(a.dk, a.tokens, a.kv_heads, a.head_dim);
     p.splits = splits;
     attention_backward_kernel<kD, true><<<(unsigned)(p.tiles * a.kv_heads * splits), kThreads, Shape<kD>::kSmem, stream>>>(
         mk, mv, mq, mdo, mdv, mdk, p);
     e = cudaGetLastError();
     if (e != cudaSuccess || splits == 1) return e;
     const int64_t pieces = a.tokens * a.kv_heads * (a.head_dim / 8);
-    join_parts_kernel<<<dim3((unsigned)((pieces + 255) / 256), 2), 256, 0, stream>>>(
-        p, a.dv, a.dk, extent_heads(a.dv, a.tokens, a.kv_heads, a.head_dim),
-        extent_heads(a.dk, a.tokens, a.kv_heads, a.head_dim));
+    join_parts_kernel<<<dim3((unsigned)((pieces + 255) / 256), 2), 256, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -97,38 +97,20 @@ __device__ __forceinline__ void zero_tile_row(uint8_t* tile, uint32_t row, uint3
             *reinterpret_cast<uint4*>(tile + c * kChunkBytes + row * 128 + i * 16) = make_uint4(0, 0, 0, 0);
 }
 
-// 16 FP32 values of a tensor-memory row, times f, as BF16 into a quarter of
-// the row's 128 bytes of a swizzled chunk.
-__device__ __forceinline__ void stage_row_16(uint8_t* chunk, uint32_t row, uint32_t quarter, const uint32_t* v, float f) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        uint4 o;
-        o.x = pack_bf16(__uint_as_float(v[8 * i]) * f, __uint_as_float(v[8 * i + 1]) * f);
-        o.y = pack_bf16(__uint_as_float(v[8 * i + 2]) * f, __uint_as_float(v[8 * i + 3]) * f);
-        o.z = pack_bf16(__uint_as_float(v[8 * i + 4]) * f, __uint_as_float(v[8 * i + 5]) * f);
-        o.w = pack_bf16(__uint_as_float(v[8 * i + 6]) * f, __uint_as_float(v[8 * i + 7]) * f);
-        *reinterpret_cast<uint4*>(chunk + row * 128 + (((2 * quarter + i) ^ (row & 7u)) * 16)) = o;
-    }
-}
-__device__ __forceinline__ void stage_row_32(uint8_t* chunk, uint32_t row, uint32_t half, const uint32_t* v, float f) {
-    stage_row_16(chunk, row, 2 * half, v, f);
-    stage_row_16(chunk, row, 2 * half + 1, v + 16, f);
-}
-
-// Map of head vectors [tokens][heads][head_dim]: boxes of 64 dims by one head
-// by `rows` tokens, 128-byte swizzle; dims past head_dim and tokens past the
-// end read as zero and are not written.
+// Map of head vectors [tokens][heads][head_dim]: boxes of `dims` (64 or 32)
+// dims by one head by `rows` tokens, swizzled over the box's 128 or 64 bytes;
+// dims past head_dim and tokens past the end read as zero and are not written.
 inline bool make_heads_map(CUtensorMap* map, const HeadsView& v, int64_t tokens, int heads, int head_dim,
-                           uint32_t rows) {
+                           uint32_t rows, uint32_t dims_per_box = 64) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)heads, (cuuint64_t)tokens};
     const cuuint64_t strides[2] = {(cuuint64_t)v.ld_head * 2, (cuuint64_t)v.ld_token * 2};
-    const cuuint32_t box[3] = {64, 1, rows};
+    const cuuint32_t box[3] = {dims_per_box, 1, rows};
     const cuuint32_t elem[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, v.data, dims, strides, box, elem,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              CU_TENSOR_MAP_INTERLEAVE_NONE, dims_per_box == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace nvfp4
