@@ -52,8 +52,11 @@ def alloc_operand(rows: int, cols: int, device="cuda") -> NVFP4Operand:
 
 
 def stream_handle(stream: Optional[torch.cuda.Stream] = None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # torch.cuda.current_stream().cuda_stream without the Stream object, which
+    # costs as much as a kernel launch
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 class Workspace:
@@ -416,9 +419,11 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
         raise ValueError(f"lse: contiguous float32 [{q_heads}, {tokens}] expected")
     if dq is None:
         dq = torch.empty((tokens, q_heads, dim), dtype=torch.bfloat16, device=q.device)
-    if dk is None:
+    if dk is None and dv is None:
+        dk, dv = torch.empty((2, tokens, kv_heads, dim), dtype=torch.bfloat16, device=q.device).unbind(0)
+    elif dk is None:
         dk = torch.empty((tokens, kv_heads, dim), dtype=torch.bfloat16, device=q.device)
-    if dv is None:
+    elif dv is None:
         dv = torch.empty((tokens, kv_heads, dim), dtype=torch.bfloat16, device=q.device)
     nbytes = capi.nvfp4_attention_backward_workspace_size(tokens, q_heads, kv_heads, dim)
     if workspace is None or workspace.numel() < nbytes:
