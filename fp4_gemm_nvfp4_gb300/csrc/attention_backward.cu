@@ -485,10 +485,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld_32x32b_x32(s_at, reinterpret_cast<uint32_t*>(e));
                 tmem_ld_wait();
                 if (p.sc.capped) {
+                    cap_scores<32>(e, p.sc);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
-                        const float th = capped_tanh(e[j], p.sc.mult);
-                        e[j] = th * p.sc.cap_log2;
+                        const float th = e[j] * p.sc.over_cap;
                         damp[j] = fmaf(-th, th, 1.0f);
                     }
                 }

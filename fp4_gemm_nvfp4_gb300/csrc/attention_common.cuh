@@ -26,22 +26,103 @@ inline cudaError_t attention_status_read_and_clear_local(unsigned int* status) {
     return e;
 }
 
-// How a product q.k becomes a score in units of log2 (exp becomes ex2):
-//  no cap:  s = mult * dot                   (mult = scale log2e)
-//  cap:     th = tanh(scale dot / cap) = 1 - 2 / (ex2(mult * dot) + 1), mult = 2 log2e scale / cap;
-//           s = cap_log2 * th                (its absolute error, 2^-22 of the cap, is what counts)
+// How a product q.k becomes a score in units of log2 (exp becomes ex2), with
+// u = scale dot / cap:
+//  no cap:  s = mult * dot (mult = scale log2e)
+//  cap:     s = cap_log2 tanh(u).  For |u| <= kSmallCap by an odd polynomial, whose
+//           relative error (2e-7 in FP32) is what a row of few keys needs;
+//           beyond, tanh(u) = 1 - 2 i with i = 1 / (ex2(mult * dot) + 1), mult = 2 log2e scale / cap.
+//           1 - tanh^2 = 1 - (s / cap_log2)^2.
 //  bias:    s -= slope_log2 |i - j|
+// tanh(u) / u as a polynomial in u^2 on [0, 0.75^2], interpolated at its
+// Chebyshev points: relative error 3e-8.
+constexpr float kSmallCap = 0.75f;
+constexpr int kCapTerms = 6;
+
 struct Scores {
-    float mult, cap_log2;
+    float mult, cap_log2, over_cap, kappa, small;   // kappa = scale / cap, small = kSmallCap / kappa
+    float poly[kCapTerms];                          // times cap_log2
     int capped;
 };
 
 inline Scores make_scores(float scale, float softcap) {
-    if (softcap > 0.0f) return {2.0f * kLog2e * scale / softcap, softcap * kLog2e, 1};
-    return {scale * kLog2e, 0.0f, 0};
+    Scores s{};
+    if (!(softcap > 0.0f)) {
+        s.mult = scale * kLog2e;
+        return s;
+    }
+    const double c[kCapTerms] = {0.9999999704657849,    -0.33332954098406786, 0.1332533884815183,
+                                 -0.053341115329099964, 0.019576216425263346, -0.004711522234826275};
+    const double cap_log2 = (double)softcap * (double)kLog2e, kappa = (double)scale / softcap;
+    s.mult = (float)(2.0 * (double)kLog2e * kappa);
+    s.cap_log2 = (float)cap_log2;
+    s.over_cap = (float)(1.0 / cap_log2);
+    s.kappa = (float)kappa;
+    s.small = (float)(kSmallCap / kappa);
+    for (int i = 0; i < kCapTerms; ++i) s.poly[i] = (float)(cap_log2 * c[i]);
+    s.capped = 1;
+    return s;
 }
 
-__device__ __forceinline__ float capped_tanh(float dot, float mult) { return fmaf(-2.0f, rcp(ex2(dot * mult) + 1.0f), 1.0f); }
+__device__ __forceinline__ float cap_small(float dot, const Scores& sc) {
+    const float u = dot * sc.kappa, w = u * u;
+    float r = sc.poly[kCapTerms - 1];
+#pragma unroll
+    for (int i = kCapTerms - 2; i >= 0; --i) r = fmaf(r, w, sc.poly[i]);
+    return r * u;
+}
+
+// Four values of i at once: one reciprocal of the product of the four
+// denominators, and the products of the others (a reciprocal takes as long as
+// two ex2 or eight multiplications).  The exponent is held to 30, where tanh
+// is 1 to the last bit, so that the product stays finite; a NaN (a masked
+// key's) becomes 30 too and does not reach the other three.
+__device__ __forceinline__ void cap_inverse_x4(float* v, float mult) {
+    float d[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) d[k] = ex2(fminf(v[k] * mult, 30.0f)) + 1.0f;
+    const float ab = d[0] * d[1], cd = d[2] * d[3];
+    const float r = rcp(ab * cd);
+    const float rab = r * cd, rcd = r * ab;
+    v[0] = rab * d[1];
+    v[1] = rab * d[0];
+    v[2] = rcd * d[3];
+    v[3] = rcd * d[2];
+}
+
+// kN products of a lane's row to capped scores; a warp whose products are all
+// small takes the polynomial alone.
+template <int kN>
+__device__ __forceinline__ void cap_scores(float* s, const Scores& sc) {
+    float top = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kN; j += 2) top = max3(top, fabsf(s[j]), fabsf(s[j + 1]));
+    if (!__any_sync(0xFFFFFFFFu, top > sc.small)) {
+        const uint64_t kappa = pair(sc.kappa, sc.kappa);
+        uint64_t c[kCapTerms];
+#pragma unroll
+        for (int i = 0; i < kCapTerms; ++i) c[i] = pair(sc.poly[i], sc.poly[i]);
+#pragma unroll
+        for (int j = 0; j < kN; j += 2) {
+            const uint64_t u = mul2(pair(s[j], s[j + 1]), kappa), w = mul2(u, u);
+            uint64_t r = c[kCapTerms - 1];
+#pragma unroll
+            for (int i = kCapTerms - 2; i >= 0; --i) r = fma2(r, w, c[i]);
+            unpair(mul2(r, u), s[j], s[j + 1]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kN; j += 4) {
+            float i[4] = {s[j], s[j + 1], s[j + 2], s[j + 3]};
+            cap_inverse_x4(i, sc.mult);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float small = cap_small(s[j + k], sc);
+                s[j + k] = fabsf(s[j + k]) > sc.small ? fmaf(-2.0f * sc.cap_log2, i[k], sc.cap_log2) : small;
+            }
+        }
+    }
+}
 
 // The keys a row attends to, cut to [0, tokens); rows past the end see none.
 __device__ __forceinline__ int2 span_of(const int32_t* spans, int64_t i, int64_t tokens) {

@@ -393,10 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(s_at + 32 * i, r + 32 * i);
                     tmem_ld_wait();
                 }
-                if (p.sc.capped) {
-#pragma unroll
-                    for (int j = 0; j < 128; ++j) s[j] = capped_tanh(s[j], p.sc.mult) * p.sc.cap_log2;
-                }
+                if (p.sc.capped) cap_scores<128>(s, p.sc);
                 if (p.slopes) {
                     const float f = p.sc.capped ? 1.0f : p.sc.mult, d = (float)((int)token - k0);
 #pragma unroll
