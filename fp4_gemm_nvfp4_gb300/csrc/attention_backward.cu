@@ -15,8 +15,9 @@
 //           F1  F2  X1  X2  acc1 (B1)     acc2 (B2)
 //   dq      q   do  k   v   P' k  (k)     dZ k    (k)
 //   dk dv   k   v   q   do  P^T do (do)   dZ^T q  (q)
-// The tensor cores run acc1(i), S(i+1), acc2(i), dP(i+1) in turn, so the
-// softmax warps have two products' time for each of their two halves.
+// The tensor cores run acc1(i), S(i+1), acc2(i), dP(i+1) in turn (with 64 dims
+// S(i+1) first), so the softmax warps have two products' time for each of their
+// two halves.
 //
 // delta from the BF16 out is off by out's rounding, which is as large as dS
 // itself in rows that one key dominates.  The dq kernel therefore also sums
@@ -40,11 +41,6 @@ constexpr int kFirstSoftmaxWarp = 4;
 constexpr uint32_t kSoftmaxWarps = 16;
 constexpr int kControlRegs = 64, kSoftmaxRegs = 104;   // per thread, of the launch's 96
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kSCol = 0, kDpCol = 128, kAcc1Col = 256, kAcc2Col = 384;
-// Streamed tiles in flight.  With four, the place of X1(i + 2) is that of
-// X1(i), free only when dZ(i) has been formed: its rows' lse and delta, which
-// come with X1, then need two places.
-constexpr uint32_t kSlots = 4;
 constexpr uint32_t kVecBytes = 2 * 128 * sizeof(float);
 constexpr uint32_t kMaxSplits = 8;
 
@@ -52,20 +48,31 @@ template <int kD>
 struct Shape {
     static constexpr uint32_t kChunks = kD / 64;
     static constexpr uint32_t kTile = kChunks * kChunkBytes;
+    // Tensor memory: S (P over it), dP (dZ over it), the two sums.  With 64 dims
+    // there is room for a second S, taken in turn, so that S of the next tile can
+    // be made before P of this one has been read.
+    static constexpr bool kAhead = kD == 64;
+    static constexpr uint32_t kDpCol = kAhead ? 256 : 128;
+    static constexpr uint32_t kAcc1Col = kDpCol + 128, kAcc2Col = kAcc1Col + kD;
+    // Streamed tiles in flight, in pairs.  X1(i + kPairs) takes the place of X1(i),
+    // free when dZ(i) has been formed: its rows' lse and delta, which come with
+    // X1, need kPairs places.
+    static constexpr uint32_t kPairs = kAhead ? 3 : 2, kSlots = 2 * kPairs;
     static constexpr uint32_t kStageAt = (2 + kSlots) * kTile;   // 32 rows x 32 dims of results per softmax warp
     static constexpr uint32_t kVecAt = kStageAt + kSoftmaxWarps * 2048;
-    static constexpr uint32_t kBarAt = kVecAt + 2 * kVecBytes;
+    static constexpr uint32_t kBarAt = kVecAt + kPairs * kVecBytes;
     static constexpr size_t kSmem = kBarAt + 1024;   // dynamic shared memory starts 1024-byte aligned (checked)
 };
 static_assert(Shape<128>::kSmem <= 232448 && Shape<64>::kSmem <= 232448, "shared memory budget");
 
-// The workspace: per query head and row (rounded up to tiles) lse in log2 (inf
-// for a row without keys) and the exact delta, then the tiles' spans.
+// The workspace: per query head and row (rounded up to tiles) minus lse in
+// log2 (-inf for a row without keys) and minus the exact delta, then the
+// tiles' spans.
 // With the dk dv kernel's sums split, also the parts: FP32 [splits][dv, dk]
 // [tokens][kv_heads][head_dim].
 struct Workspace {
-    float* lse2;
-    float* delta;
+    float* minus_lse2;
+    float* minus_delta;
     TileSpan* spans;
     float* parts;
     int64_t ld;         // rows per head
@@ -127,16 +134,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     using S = Shape<kD>;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* ring = smem + 2 * S::kTile;
-    float* vec = reinterpret_cast<float*>(smem + S::kVecAt);     // [2][lse2, delta][128] of the streamed rows
+    float* vec = reinterpret_cast<float*>(smem + S::kVecAt);     // [kPairs][lse2, delta][128] of the streamed rows
     float* exact_parts = vec;                                    // dq, instead: [4][128] quarters of exact deltas
     Item* items = reinterpret_cast<Item*>(smem + S::kBarAt);     // [2] the current and the next
     uint4* answer = reinterpret_cast<uint4*>(items + 2);
     uint64_t* full = reinterpret_cast<uint64_t*>(answer + 1);
-    uint64_t* empty = full + kSlots;
-    uint64_t* f_full = empty + kSlots;           // the item's own tiles loaded
+    uint64_t* empty = full + S::kSlots;
+    uint64_t* f_full = empty + S::kSlots;           // the item's own tiles loaded
     uint64_t* f_empty = f_full + 1;              // ... and their last scores done
-    uint64_t* s_full = f_empty + 1;
-    uint64_t* dp_full = s_full + 1;
+    uint64_t* s_full = f_empty + 1;              // [2], in turn: two S may be ahead of their softmax
+    uint64_t* dp_full = s_full + 2;
     uint64_t* p_full = dp_full + 1;
     uint64_t* dz_full = p_full + 1;
     uint64_t* acc_full = dz_full + 1;
@@ -153,13 +160,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31u;
     if (threadIdx.x == 0) {
-        for (uint32_t i = 0; i < kSlots; ++i) {
+        for (uint32_t i = 0; i < S::kSlots; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
         mbar_init(f_full, 1);
         mbar_init(f_empty, 1);
-        mbar_init(s_full, 1);
+        mbar_init(&s_full[0], 1);
+        mbar_init(&s_full[1], 1);
         mbar_init(dp_full, 1);
         mbar_init(p_full, kSoftmaxWarps);
         mbar_init(dz_full, kSoftmaxWarps);
@@ -224,13 +232,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tma_load_3d(ring + slot * S::kTile + c * kChunkBytes, x ? &map_x2 : &map_x1, &full[slot],
                                         (int32_t)c * 64, h, t * 128);
                         if (vectors) {
-                            float* to = vec + (n & 1u) * 256;
+                            float* to = vec + (n % S::kPairs) * 256;
                             const int64_t from = (int64_t)h * p.ws.ld + t * 128;
-                            bulk_load(to, p.ws.lse2 + from, 512, &full[slot]);
-                            bulk_load(to + 128, p.ws.delta + from, 512, &full[slot]);
+                            bulk_load(to, p.ws.minus_lse2 + from, 512, &full[slot]);
+                            bulk_load(to + 128, p.ws.minus_delta + from, 512, &full[slot]);
                         }
                         ++issued;
-                        if (++slot == kSlots) {
+                        if (++slot == S::kSlots) {
                             slot = 0;
                             phase ^= 1u;
                         }
@@ -254,9 +262,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             give_up(!ok);
             // every load has landed before the CTA exits
             if (own_loads) (void)mbar_wait(f_full, (own_loads - 1) & 1u, p.timeout_ns);
-            for (uint32_t back = 0; back < kSlots && back < issued; ++back) {
+            for (uint32_t back = 0; back < S::kSlots && back < issued; ++back) {
                 const uint32_t m = issued - 1 - back;
-                (void)mbar_wait(&full[m % kSlots], (m / kSlots) & 1u, p.timeout_ns);
+                (void)mbar_wait(&full[m % S::kSlots], (m / S::kSlots) & 1u, p.timeout_ns);
             }
         } else if (warp == 1) {
             // --------------------------------------------------- MMA issue
@@ -274,18 +282,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // places of X1(i), X2(i) for the products, of the next X1 for S and dP
             uint32_t n = 0, x1 = 0, x2 = 0, at = 0, at_phase = 0, own_tiles = 0;
+            uint32_t s_col = 0, p_col = 0;   // columns of the next S, of the P in hand
+            uint32_t s_count = 0;
             auto scores = [&](uint32_t x, bool last) {
                 const uint32_t slot = at;
                 (x ? x2 : x1) = slot;
                 await(full0 + 8 * slot, at_phase);
-                if (++at == kSlots) {
+                if (++at == S::kSlots) {
                     at = 0;
                     at_phase ^= 1u;
                 }
                 if (!ok) return;
-                mma_scores<kIdS, kD>(tmem + (x ? kDpCol : kSCol), f_lo + x * (S::kTile >> 4),
+                mma_scores<kIdS, kD>(tmem + (x ? S::kDpCol : s_col), f_lo + x * (S::kTile >> 4),
                                      xk_lo + slot * (S::kTile >> 4), elected);
-                tc_commit(x ? dp_full : s_full, elected);
+                if (x) tc_commit(dp_full, elected);
+                else tc_commit(&s_full[s_count++ & 1u], elected);
                 if (!kKeys && x == 1) tc_commit(&empty[slot], elected);   // dq: v is needed for dP alone
                 if (last) tc_commit(f_empty, elected);
             };
@@ -293,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 await(smem_u32(acc ? dz_full : p_full), n & 1u);
                 if (!ok) return;
                 // each 32 columns of S hold 32 rows' BF16 in their first 16
-                mma_sum<kIdAcc, 2, 32>(tmem + (acc ? kAcc2Col : kAcc1Col), tmem + (acc ? kDpCol : kSCol),
+                mma_sum<kIdAcc, 2, 32>(tmem + (acc ? S::kAcc2Col : S::kAcc1Col), tmem + (acc ? S::kDpCol : p_col),
                                        xn_lo + slot * (S::kTile >> 4), start ? 0u : 1u, elected);
                 if (kKeys || acc == 1) tc_commit(&empty[slot], elected);
             };
@@ -306,12 +317,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!valid) break;
                 if (total == 0) continue;
                 await(smem_u32(f_full), own_tiles++ & 1u);
+                if (S::kAhead) s_col = 128 * (n & 1u);
                 scores(0, false);
                 scores(1, total == 1);
                 for (int i = 0; i < total && ok; ++i, ++n) {
                     const uint32_t c1 = x1, c2 = x2;
-                    product(0, kKeys ? c2 : c1, i == 0);
-                    if (i + 1 < total) scores(0, false);
+                    p_col = s_col;
+                    if (S::kAhead) {
+                        s_col ^= 128;
+                        if (i + 1 < total) scores(0, false);
+                        product(0, kKeys ? c2 : c1, i == 0);
+                    } else {
+                        product(0, kKeys ? c2 : c1, i == 0);
+                        if (i + 1 < total) scores(0, false);
+                    }
                     product(1, c1, i == 0);
                     if (i + 1 < total) scores(1, i + 2 == total);
                 }
@@ -400,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t quarter = (warp - kFirstSoftmaxWarp) >> 2;         // columns 32 quarter ..
         const uint32_t row = (warp & 3u) * 32 + lane;                     // ... of this row
         const uint32_t lanes = tmem + (((warp & 3u) * 32u) << 16);
-        const uint32_t s_at = lanes + kSCol + 32 * quarter, dp_at = lanes + kDpCol + 32 * quarter;
+        const uint32_t dp_at = lanes + S::kDpCol + 32 * quarter;
         const bool biased = p.slopes != nullptr;
         const float c = p.sc.capped || biased ? 1.0f : p.sc.mult;
         uint32_t n = 0, results = 0;               // streamed tiles, items with a result so far
@@ -454,17 +473,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&item_empty[it & 1u]);
             if (!valid) break;
             const int64_t own = own0 + (int64_t)row;
-            float lse2 = INFINITY, delta = 0.0f;           // dq: of this row
+            float minus_lse2 = -INFINITY, delta = 0.0f;    // dq: of this row
             if constexpr (!kKeys) {
                 ok = warp_wait_or_abort(delta_full, it & 1u, p.timeout_ns, abort_flag);
                 if (!ok) break;
                 // a row without keys may hold anything
                 if (span.x < span.y) {
                     delta = row_delta[row];
-                    lse2 = lse * kLog2e;
+                    minus_lse2 = -lse * kLog2e;
                 }
             }
-            float exact = 0.0f;                            // dq: sum of P dP
+            uint64_t exact2 = 0;                           // dq: sum of P dP, in two halves
             for (int i = 0; i < total; ++i, ++n) {
                 const int x0 = t * 128;                    // first streamed row
                 const uint32_t n2 = 2 * n + 1;             // X2's place among the loads
@@ -473,14 +492,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (kKeys) ts = p.ws.spans[t];
                 const bool masked = kKeys ? (own0 < ts.all_lo || own0 + 128 > ts.all_hi)
                                           : (x0 < ts.all_lo || x0 + 128 > ts.all_hi);
-                const float* v_lse = vec + (n & 1u) * 256 + 32 * quarter;
+                const float* v_lse = vec + (n % S::kPairs) * 256 + 32 * quarter;
                 const float* v_delta = v_lse + 128;
-                ok = warp_wait_or_abort(s_full, n & 1u, p.timeout_ns, abort_flag);
+                ok = warp_wait_or_abort(&s_full[n & 1u], (n >> 1) & 1u, p.timeout_ns, abort_flag);
                 // (X1 is there, S was made of it; this makes its rows' vectors visible)
                 if (kKeys && ok)
-                    ok = warp_wait_or_abort(&full[(n2 - 1) % kSlots], ((n2 - 1) / kSlots) & 1u, p.timeout_ns, abort_flag);
+                    ok = warp_wait_or_abort(&full[(n2 - 1) % S::kSlots], ((n2 - 1) / S::kSlots) & 1u, p.timeout_ns, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
+                const uint32_t s_at = lanes + (S::kAhead ? 128 * (n & 1u) : 0u) + 32 * quarter;
                 float e[32], damp[32];
                 tmem_ld_32x32b_x32(s_at, reinterpret_cast<uint32_t*>(e));
                 tmem_ld_wait();
@@ -497,18 +517,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) e[j] = fmaf(-slope, fabsf(d - (float)j), e[j] * f);
                 }
-                if constexpr (kKeys) {
+                {
+                    const uint64_t c2 = pair(c, c), own2 = pair(minus_lse2, minus_lse2);
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
-                        const float4 l4 = *reinterpret_cast<const float4*>(v_lse + j);
-                        e[j] = ex2(fmaf(e[j], c, -l4.x));
-                        e[j + 1] = ex2(fmaf(e[j + 1], c, -l4.y));
-                        e[j + 2] = ex2(fmaf(e[j + 2], c, -l4.z));
-                        e[j + 3] = ex2(fmaf(e[j + 3], c, -l4.w));
+                        ulonglong2 l = make_ulonglong2(own2, own2);
+                        if constexpr (kKeys) l = *reinterpret_cast<const ulonglong2*>(v_lse + j);
+                        unpair(fma2(pair(e[j], e[j + 1]), c2, l.x), e[j], e[j + 1]);
+                        unpair(fma2(pair(e[j + 2], e[j + 3]), c2, l.y), e[j + 2], e[j + 3]);
+                        e[j] = ex2(e[j]);
+                        e[j + 1] = ex2(e[j + 1]);
+                        e[j + 2] = ex2(e[j + 2]);
+                        e[j + 3] = ex2(e[j + 3]);
                     }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) e[j] = ex2(fmaf(e[j], c, -lse2));
                 }
                 if (masked) {
                     if constexpr (kKeys) {
@@ -524,12 +545,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // rows of queries without keys may hold anything (their P
                         // and dZ are 0): they are zeroed for the products
                         if (ts.all_hi == 0) {
-                            ok = warp_wait_or_abort(&full[n2 % kSlots], (n2 / kSlots) & 1u, p.timeout_ns, abort_flag);
+                            ok = warp_wait_or_abort(&full[n2 % S::kSlots], (n2 / S::kSlots) & 1u, p.timeout_ns, abort_flag);
                             if (!ok) break;
                             if (quarter == (warp & 3u) && s.x >= s.y) {
                                 const uint32_t r = 32 * quarter + lane;
-                                zero_tile_row(ring + ((n2 - 1) % kSlots) * S::kTile, r, S::kChunks);
-                                zero_tile_row(ring + (n2 % kSlots) * S::kTile, r, S::kChunks);
+                                zero_tile_row(ring + ((n2 - 1) % S::kSlots) * S::kTile, r, S::kChunks);
+                                zero_tile_row(ring + (n2 % S::kSlots) * S::kTile, r, S::kChunks);
                             }
                             fence_proxy_async_smem();
                         }
@@ -542,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (quarter == 0 && (x0 < ts.lo || x0 + 128 > ts.hi)) {
                             const int key = x0 + (int)row;
                             if (key < ts.lo || key >= ts.hi)
-                                zero_tile_row(ring + ((n2 - 1) % kSlots) * S::kTile, row, S::kChunks);
+                                zero_tile_row(ring + ((n2 - 1) % S::kSlots) * S::kTile, row, S::kChunks);
                             fence_proxy_async_smem();
                         }
                     }
@@ -575,29 +596,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int j = 0; j < 16; ++j)
                             if (e[half + j] == 0.0f) g[j] = 0.0f;
                     }
-                    if constexpr (kKeys) {
+                    const uint64_t own2 = pair(-delta, -delta);
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const float4 d4 = *reinterpret_cast<const float4*>(v_delta + half + j);
-                            g[j] = e[half + j] * (g[j] - d4.x);
-                            g[j + 1] = e[half + j + 1] * (g[j + 1] - d4.y);
-                            g[j + 2] = e[half + j + 2] * (g[j + 2] - d4.z);
-                            g[j + 3] = e[half + j + 3] * (g[j + 3] - d4.w);
+                    for (int j = 0; j < 16; j += 4) {
+                        ulonglong2 d = make_ulonglong2(own2, own2);
+                        if constexpr (kKeys) d = *reinterpret_cast<const ulonglong2*>(v_delta + half + j);
+#pragma unroll
+                        for (int k = 0; k < 4; k += 2) {
+                            const uint64_t e2 = pair(e[half + j + k], e[half + j + k + 1]), g2 = pair(g[j + k], g[j + k + 1]);
+                            if constexpr (!kKeys) exact2 = fma2(e2, g2, exact2);
+                            uint64_t z = mul2(e2, add2(g2, k ? d.y : d.x));
+                            if (p.sc.capped) z = mul2(z, pair(damp[half + j + k], damp[half + j + k + 1]));
+                            unpair(z, g[j + k], g[j + k + 1]);
                         }
-                    } else {
-                        float sum[2] = {};
-#pragma unroll
-                        for (int j = 0; j < 16; j += 2) {
-                            sum[0] = fmaf(e[half + j], g[j], sum[0]);
-                            sum[1] = fmaf(e[half + j + 1], g[j + 1], sum[1]);
-                            g[j] = e[half + j] * (g[j] - delta);
-                            g[j + 1] = e[half + j + 1] * (g[j + 1] - delta);
-                        }
-                        exact += sum[0] + sum[1];
-                    }
-                    if (p.sc.capped) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) g[j] *= damp[half + j];
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) pk[half / 2 + j] = pack_bf16(g[2 * j], g[2 * j + 1]);
@@ -648,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (uint32_t u = quarter; u < 2 * (kD / 32); u += 4) {
                     const uint32_t k = u / (kD / 32), col = 32 * (u % (kD / 32));
                     uint32_t o[32];
-                    tmem_ld_32x32b_x32(lanes + (k ? kAcc2Col : kAcc1Col) + col, o);
+                    tmem_ld_32x32b_x32(lanes + (k ? S::kAcc2Col : S::kAcc1Col) + col, o);
                     tmem_ld_wait();
                     const float f = k ? p.scale : 1.0f;
 #pragma unroll
@@ -665,6 +676,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             } else {
+                float exact, odd;
+                unpair(exact2, exact, odd);
+                exact += odd;
                 exact_parts[quarter * 128 + row] = exact;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(exact_full);
@@ -675,8 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float turn = alive ? delta - exact : 0.0f;
                 if (quarter < kD / 32) {
                     uint32_t a1[32], a2[32];
-                    tmem_ld_32x32b_x32(lanes + kAcc1Col + 32 * quarter, a1);
-                    tmem_ld_32x32b_x32(lanes + kAcc2Col + 32 * quarter, a2);
+                    tmem_ld_32x32b_x32(lanes + S::kAcc1Col + 32 * quarter, a1);
+                    tmem_ld_32x32b_x32(lanes + S::kAcc2Col + 32 * quarter, a2);
                     tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
@@ -685,8 +699,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     store(&map_out1, 32 * quarter, a2);
                 }
                 if (quarter == 3) {
-                    p.ws.lse2[(int64_t)head * p.ws.ld + own] = lse2;
-                    p.ws.delta[(int64_t)head * p.ws.ld + own] = exact;
+                    p.ws.minus_lse2[(int64_t)head * p.ws.ld + own] = minus_lse2;
+                    p.ws.minus_delta[(int64_t)head * p.ws.ld + own] = -exact;
                 }
             }
         }
@@ -768,9 +782,9 @@ Workspace carve(float* base, int64_t tokens, int q_heads, int kv_heads, int head
     Workspace w;
     w.ld = (tokens + 127) / 128 * 128;
     w.part_size = tokens * kv_heads * head_dim;
-    w.lse2 = base;
-    w.delta = base + w.ld * q_heads;
-    w.spans = reinterpret_cast<TileSpan*>(w.delta + w.ld * q_heads);
+    w.minus_lse2 = base;
+    w.minus_delta = base + w.ld * q_heads;
+    w.spans = reinterpret_cast<TileSpan*>(w.minus_delta + w.ld * q_heads);
     w.parts = reinterpret_cast<float*>(w.spans + w.ld / 128);
     if (bytes)
         *bytes = (size_t)((w.ld * q_heads * 2 + w.ld / 32 + (splits > 1 ? 2 * splits * w.part_size : 0)) * 4);
