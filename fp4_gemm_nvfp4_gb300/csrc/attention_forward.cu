@@ -231,21 +231,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = ok && warp_wait_or_abort_addr(bar, parity, p.timeout_ns, abort_flag);
             };
             // the products of the step before
-            struct Due {
-                bool in = false, start = false, end = false;
-                uint32_t col = 0;
-            };
-            Due due[2];
-            uint32_t turn = 0;   // 2 * step mod 3
-            uint32_t s_count[2] = {0, 0};
-            auto product = [&](int x, const Due& d, uint32_t vl) {
+            bool due[2] = {false, false}, due_start[2] = {false, false}, due_end[2] = {false, false};
+            uint32_t due_col[2] = {0, 128}, turn = 0, s_count[2] = {0, 0};   // turn: 2 * step mod 3
+            auto product = [&](int x, bool start, bool end, uint32_t col, uint32_t vl) {
                 // O holds the last item's result until it has been read
-                if (d.start) await(smem_u32(&o_empty[x]), (o_items[x]++ & 1u) ^ 1u);
+                if (start) await(smem_u32(&o_empty[x]), (o_items[x]++ & 1u) ^ 1u);
                 await(smem_u32(&p_full[x]), p_phase[x]);
                 p_phase[x] ^= 1u;
                 tc_fence_after();
-                if (ok) mma_sum<kIdO, 8, 64>(tmem + S::kOutCol + kD * x, d.col, vl, d.start ? 0u : 1u, elected);
-                if (ok && d.end) tc_commit(&o_full[x], elected);
+                if (ok) mma_sum<kIdO, 8, 64>(tmem + S::kOutCol + kD * x, tmem + col, vl, start ? 0u : 1u, elected);
+                if (ok && end) tc_commit(&o_full[x], elected);
             };
             for (uint32_t it = 0;; ++it) {
                 await(smem_u32(&item_full[it & 1u]), (it >> 1) & 1u);
@@ -266,21 +261,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t kl = k_lo + slot * (2 * S::kTile >> 4), vl = v_lo + slot * (2 * S::kTile >> 4);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const Due before = due[x];
-                        if (!S::kAhead && before.in) product(x, before, vl);
-                        due[x].in = kt >= first[x] && kt < last[x];
-                        due[x].start = kt == first[x];
-                        due[x].end = kt + 1 == last[x];
-                        due[x].col = tmem + 128 * (S::kAhead ? (turn + x) % 3 : (uint32_t)x);
-                        if (due[x].in) {
-                            if (due[x].start) await(smem_u32(&q_full[x]), q_items[x]++ & 1u);
+                        const bool before = due[x], start = due_start[x], last_one = due_end[x];
+                        const uint32_t col = S::kAhead ? due_col[x] : 128u * x;
+                        if (!S::kAhead && before) product(x, start, last_one, col, vl);
+                        due[x] = kt >= first[x] && kt < last[x];
+                        due_start[x] = kt == first[x];
+                        due_end[x] = kt + 1 == last[x];
+                        if constexpr (S::kAhead) due_col[x] = 128 * ((turn + x) % 3);
+                        if (due[x]) {
+                            if (due_start[x]) await(smem_u32(&q_full[x]), q_items[x]++ & 1u);
                             tc_fence_after();
                             if (!ok) break;
-                            mma_scores<kIdS, kD>(due[x].col, q_lo + x * (S::kTile >> 4), kl, elected);
-                            tc_commit(&s_full[2 * x + (s_count[x]++ & 1u)], elected);
-                            if (due[x].end) tc_commit(&q_empty[x], elected);
+                            mma_scores<kIdS, kD>(tmem + (S::kAhead ? due_col[x] : 128u * x), q_lo + x * (S::kTile >> 4), kl,
+                                                 elected);
+                            tc_commit(S::kAhead ? &s_full[2 * x + (s_count[x]++ & 1u)] : &s_full[2 * x], elected);
+                            if (due_end[x]) tc_commit(&q_empty[x], elected);
                         }
-                        if (S::kAhead && before.in) product(x, before, vl);
+                        if (S::kAhead && before) product(x, start, last_one, col, vl);
                     }
                     turn = turn ? turn - 1 : 2;
                     if (!ok) break;
@@ -292,11 +289,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!ok) break;
             }
-            if (ok && (due[0].in || due[1].in)) {
+            if (ok && (due[0] || due[1])) {
                 await(full0 + 8 * slot, phase);
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
-                    if (ok && due[x].in) product(x, due[x], v_lo + slot * (2 * S::kTile >> 4));
+                    if (ok && due[x])
+                        product(x, due_start[x], due_end[x], S::kAhead ? due_col[x] : 128u * x, v_lo + slot * (2 * S::kTile >> 4));
             }
             give_up(!ok && elected);
             // every product is done before tensor memory is freed
@@ -395,7 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t s_at = lanes + 128 * (S::kAhead ? (2 * n + x) % 3 : x);
                 const uint32_t load = ++n;             // the value tile comes with the next stage
                 if (kt < first || kt >= last) continue;
-                ok = warp_wait_or_abort(&s_full[2 * x + (s_count & 1u)], (s_count >> 1) & 1u, p.timeout_ns, abort_flag);
+                ok = S::kAhead ? warp_wait_or_abort(&s_full[2 * x + (s_count & 1u)], (s_count >> 1) & 1u, p.timeout_ns, abort_flag)
+                               : warp_wait_or_abort(&s_full[2 * x], s_count & 1u, p.timeout_ns, abort_flag);
                 if (!ok) break;
                 ++s_count;
                 tc_fence_after();
