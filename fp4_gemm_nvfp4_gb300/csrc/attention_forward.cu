@@ -30,6 +30,8 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kFirstSoftmaxWarp = 4;
 constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kScoreCol = 0;     // two tiles of 128 columns: S, then P in its place
+constexpr uint32_t kOutCol = 256;     // two tiles of up to 128 columns
 constexpr float kRescale = 8.0f;
 
 template <int kD>
@@ -41,12 +43,6 @@ struct Shape {
     static constexpr uint32_t kStages = kD == 128 ? 2 : 4;
     static constexpr uint32_t kStageAt = (2 + 2 * kStages) * kTile;
     static constexpr uint32_t kBarAt = kStageAt + 8 * 4096;  // 32 rows x 64 dims of output per softmax warp
-    // Tensor memory: the places of S (and of P over it), 128 columns each, then
-    // O of the two tiles.  With 64 dims there is room for a third place, taken
-    // in turn, so that S of a tile's next step can be made before P of this one
-    // has been read.
-    static constexpr bool kAhead = kD == 64;
-    static constexpr uint32_t kOutCol = kAhead ? 384 : 256;
     static constexpr size_t kSmem = kBarAt + 1024;           // dynamic shared memory starts 1024-byte aligned (checked)
 };
 static_assert(Shape<128>::kSmem <= 232448 && Shape<64>::kSmem <= 232448, "shared memory budget");
@@ -93,8 +89,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* empty = full + S::kStages;
     uint64_t* q_full = empty + S::kStages;        // [2]
     uint64_t* q_empty = q_full + 2;              // [2] the item's scores done
-    uint64_t* s_full = q_empty + 2;              // [2][2] scores written: tile, its S in turn (two may be ahead)
-    uint64_t* p_full = s_full + 4;               // [2] scores read, P written
+    uint64_t* s_full = q_empty + 2;              // [2] scores written
+    uint64_t* p_full = s_full + 2;               // [2] scores read, P written
     uint64_t* o_full = p_full + 2;               // [2] the item's last product done
     uint64_t* o_empty = o_full + 2;              // [2] its result read
     uint64_t* item_full = o_empty + 2;           // [2]
@@ -114,8 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
             mbar_init(&q_empty[i], 1);
-            mbar_init(&s_full[2 * i], 1);
-            mbar_init(&s_full[2 * i + 1], 1);
+            mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
             mbar_init(&o_full[i], 1);
             mbar_init(&o_empty[i], 4);
@@ -214,8 +209,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == 1) {
             // --------------------------------------------------- MMA issue
             // Per step (a key tile) and query tile x: the product P V of the step
-            // before and S of this step, which, without a third place, overwrites P
-            // behind the product that reads it (MMAs of one thread run in order).
+            // before, then S of this step, which overwrites P behind the product
+            // that reads it (MMAs of one thread run in order).
             // The order of the two query tiles keeps their softmaxes half a step
             // apart, and an item's first scores go with the last item's last products.
             constexpr uint32_t kIdS = idesc_bf16(128, 128, false);
@@ -232,15 +227,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // the products of the step before
             bool due[2] = {false, false}, due_start[2] = {false, false}, due_end[2] = {false, false};
-            uint32_t due_col[2] = {0, 128}, turn = 0, s_count[2] = {0, 0};   // turn: 2 * step mod 3
-            auto product = [&](int x, bool start, bool end, uint32_t col, uint32_t vl) {
+            auto product = [&](int x, uint32_t vl) {
                 // O holds the last item's result until it has been read
-                if (start) await(smem_u32(&o_empty[x]), (o_items[x]++ & 1u) ^ 1u);
+                if (due_start[x]) await(smem_u32(&o_empty[x]), (o_items[x]++ & 1u) ^ 1u);
                 await(smem_u32(&p_full[x]), p_phase[x]);
                 p_phase[x] ^= 1u;
                 tc_fence_after();
-                if (ok) mma_sum<kIdO, 8, 64>(tmem + S::kOutCol + kD * x, tmem + col, vl, start ? 0u : 1u, elected);
-                if (ok && end) tc_commit(&o_full[x], elected);
+                if (ok)
+                    mma_sum<kIdO, 8, 64>(tmem + kOutCol + 128 * x, tmem + kScoreCol + 128 * x, vl,
+                                         due_start[x] ? 0u : 1u, elected);
+                if (ok && due_end[x]) tc_commit(&o_full[x], elected);
             };
             for (uint32_t it = 0;; ++it) {
                 await(smem_u32(&item_full[it & 1u]), (it >> 1) & 1u);
@@ -261,25 +257,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t kl = k_lo + slot * (2 * S::kTile >> 4), vl = v_lo + slot * (2 * S::kTile >> 4);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const bool before = due[x], start = due_start[x], last_one = due_end[x];
-                        const uint32_t col = S::kAhead ? due_col[x] : 128u * x;
-                        if (!S::kAhead && before) product(x, start, last_one, col, vl);
+                        if (due[x]) product(x, vl);
                         due[x] = kt >= first[x] && kt < last[x];
                         due_start[x] = kt == first[x];
                         due_end[x] = kt + 1 == last[x];
-                        if constexpr (S::kAhead) due_col[x] = 128 * ((turn + x) % 3);
                         if (due[x]) {
                             if (due_start[x]) await(smem_u32(&q_full[x]), q_items[x]++ & 1u);
                             tc_fence_after();
                             if (!ok) break;
-                            mma_scores<kIdS, kD>(tmem + (S::kAhead ? due_col[x] : 128u * x), q_lo + x * (S::kTile >> 4), kl,
-                                                 elected);
-                            tc_commit(S::kAhead ? &s_full[2 * x + (s_count[x]++ & 1u)] : &s_full[2 * x], elected);
+                            mma_scores<kIdS, kD>(tmem + kScoreCol + 128 * x, q_lo + x * (S::kTile >> 4), kl, elected);
+                            tc_commit(&s_full[x], elected);
                             if (due_end[x]) tc_commit(&q_empty[x], elected);
                         }
-                        if (S::kAhead && before) product(x, start, last_one, col, vl);
                     }
-                    turn = turn ? turn - 1 : 2;
                     if (!ok) break;
                     tc_commit(&empty[slot], elected);
                     if (++slot == S::kStages) {
@@ -293,8 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 await(full0 + 8 * slot, phase);
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
-                    if (ok && due[x])
-                        product(x, due_start[x], due_end[x], S::kAhead ? due_col[x] : 128u * x, v_lo + slot * (2 * S::kTile >> 4));
+                    if (ok && due[x]) product(x, v_lo + slot * (2 * S::kTile >> 4));
             }
             give_up(!ok && elected);
             // every product is done before tensor memory is freed
@@ -366,11 +355,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // --------------------------------------------------------- softmax
         const uint32_t x = (warp - kFirstSoftmaxWarp) >> 2, row = (warp & 3u) * 32 + lane;
         const uint32_t lanes = tmem + (((warp & 3u) * 32u) << 16);
-        const uint32_t o_at = lanes + S::kOutCol + kD * x;
+        const uint32_t s_at = lanes + kScoreCol + 128 * x, o_at = lanes + kOutCol + 128 * x;
         uint8_t* stage = smem + S::kStageAt + (warp - kFirstSoftmaxWarp) * 4096;
         const bool plain = !p.sc.capped && !p.slopes;
         const float c = plain ? p.sc.mult : 1.0f;      // scores in registers times c are in log2
-        uint32_t s_count = 0, o_phase = 0, n = 0;      // n: steps of the CTA so far
+        uint32_t s_phase = 0, o_phase = 0, n = 0;      // n: steps of the CTA so far
         bool ok = true;
         for (uint32_t it = 0;; ++it) {
             ok = warp_wait_or_abort(&item_full[it & 1u], (it >> 1) & 1u, p.timeout_ns, abort_flag);
@@ -390,13 +379,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = -INFINITY, l = 0.0f;             // maximum (log2) that P and O are scaled by; sum
             const int end = max(last, last2);
             for (int kt = min(first, first2); kt < end; ++kt) {
-                const uint32_t s_at = lanes + 128 * (S::kAhead ? (2 * n + x) % 3 : x);
                 const uint32_t load = ++n;             // the value tile comes with the next stage
                 if (kt < first || kt >= last) continue;
-                ok = S::kAhead ? warp_wait_or_abort(&s_full[2 * x + (s_count & 1u)], (s_count >> 1) & 1u, p.timeout_ns, abort_flag)
-                               : warp_wait_or_abort(&s_full[2 * x], s_count & 1u, p.timeout_ns, abort_flag);
+                ok = warp_wait_or_abort(&s_full[x], s_phase, p.timeout_ns, abort_flag);
                 if (!ok) break;
-                ++s_count;
+                s_phase ^= 1u;
                 tc_fence_after();
                 const int k0 = kt * 128;
                 float s[128];
