@@ -766,16 +766,15 @@ cudaError_t prepare_kernel() {
 
 // The dk dv kernel has an item per key tile and key head; where these are too
 // few for the SMs (few key heads, short sequences) each is split over its
-// streamed tiles, at the cost of FP32 parts written and summed.  Two items
-// per SM even out the items' lengths.
+// streamed tiles, at the cost of FP32 parts written and summed by one more
+// kernel: worth it from four streamed tiles per split.  Two items per SM even
+// out the items' lengths.
 int split_count(int64_t tokens, int q_heads, int kv_heads) {
     const int64_t tiles = (tokens + 127) / 128, items = tiles * kv_heads;
-    const int64_t want = 2 * (int64_t)device_sm_count();
-    if (2 * items > want) return 1;
-    const int64_t most = tiles * (q_heads / kv_heads);       // streamed tiles of the longest item
-    int64_t splits = want / items;
-    splits = splits < kMaxSplits ? splits : kMaxSplits;
-    return (int)(splits < most ? splits : most);
+    const int64_t want = 2 * (int64_t)device_sm_count() / items;
+    const int64_t most = tiles * (q_heads / kv_heads) / 4;   // of the longest item's streamed tiles
+    const int64_t splits = want < most ? want : most;
+    return (int)(splits < 1 ? 1 : (splits < kMaxSplits ? splits : kMaxSplits));
 }
 
 Workspace carve(float* base, int64_t tokens, int q_heads, int kv_heads, int head_dim, int splits, size_t* bytes) {

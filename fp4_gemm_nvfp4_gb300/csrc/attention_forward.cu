@@ -39,7 +39,8 @@ struct Shape {
     static constexpr uint32_t kChunks = kD / 64;
     static constexpr uint32_t kTile = kChunks * kChunkBytes;
     // A stage of the ring holds what one step of the MMA warp needs: the value
-    // tile of the step before, then the key tile of this one.
+    // tile of the step before, then the key tile of this one (an item's first
+    // stage has no value tile, its last no key tile).
     static constexpr uint32_t kStages = kD == 128 ? 2 : 4;
     static constexpr uint32_t kStageAt = (2 + 2 * kStages) * kTile;
     static constexpr uint32_t kBarAt = kStageAt + 8 * 4096;  // 32 rows x 64 dims of output per softmax warp
@@ -156,16 +157,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ok && !mbar_wait_or_abort(bar, parity, p.timeout_ns, abort_flag)) ok = false;
                 return ok;
             };
-            int v_head = 0, v_tile = -1;   // the value tile that goes with the next stage
-            auto stage = [&](bool with_key, int head, int kt) {
+            auto stage = [&](int head, int v_tile, int k_tile) {   // -1: none
                 if (!await(&empty[r.slot], r.phase ^ 1u)) return;
                 uint8_t* to = ring + r.slot * 2 * S::kTile;
-                mbar_arrive_expect_tx(&full[r.slot], (with_key ? S::kTile : 0u) + (v_tile >= 0 ? S::kTile : 0u));
+                mbar_arrive_expect_tx(&full[r.slot], (k_tile >= 0 ? S::kTile : 0u) + (v_tile >= 0 ? S::kTile : 0u));
                 for (uint32_t c = 0; c < S::kChunks; ++c) {
                     if (v_tile >= 0)
-                        tma_load_3d(to + c * kChunkBytes, &map_v, &full[r.slot], (int32_t)c * 64, v_head, v_tile * 128);
-                    if (with_key)
-                        tma_load_3d(to + S::kTile + c * kChunkBytes, &map_k, &full[r.slot], (int32_t)c * 64, head, kt * 128);
+                        tma_load_3d(to + c * kChunkBytes, &map_v, &full[r.slot], (int32_t)c * 64, head, v_tile * 128);
+                    if (k_tile >= 0)
+                        tma_load_3d(to + S::kTile + c * kChunkBytes, &map_k, &full[r.slot], (int32_t)c * 64, head, k_tile * 128);
                 }
                 ++issued;
                 if (++r.slot == S::kStages) {
@@ -187,15 +187,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tma_load_3d(smem + x * S::kTile + c * kChunkBytes, &map_q, &q_full[x], (int32_t)c * 64,
                                     item.head[x], item.tile[x] * 128);
                 }
-                const int end = max(item.last[0], item.last[1]);
-                for (int kt = min(item.first[0], item.first[1]); kt < end && ok; ++kt) {
-                    stage(true, item.kv_head, kt);
-                    v_head = item.kv_head;
-                    v_tile = kt;
-                }
-                mbar_arrive(loaded);
+                const int begin = min(item.first[0], item.first[1]), end = max(item.last[0], item.last[1]);
+                if (begin < end)
+                    for (int kt = begin; kt <= end && ok; ++kt)
+                        stage(item.kv_head, kt > begin ? kt - 1 : -1, kt < end ? kt : -1);
+                if (ok) mbar_arrive(loaded);
             }
-            if (ok && v_tile >= 0) stage(false, 0, 0);
             give_up(!ok);
             // every load has landed before the CTA exits (at once, unless a
             // wait ran out: then nothing else waits for them)
@@ -212,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // before, then S of this step, which overwrites P behind the product
             // that reads it (MMAs of one thread run in order).
             // The order of the two query tiles keeps their softmaxes half a step
-            // apart, and an item's first scores go with the last item's last products.
+            // apart.
             constexpr uint32_t kIdS = idesc_bf16(128, 128, false);
             constexpr uint32_t kIdO = idesc_bf16(128, kD, true);
             const uint32_t elected = elect_one();
@@ -251,8 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (lane == 0) mbar_arrive(&item_empty[it & 1u]);
                 if (!valid) break;
-                const int end = max(last[0], last[1]);
-                for (int kt = min(first[0], first[1]); kt < end && ok; ++kt) {
+                const int begin = min(first[0], first[1]), end = max(last[0], last[1]);
+                for (int kt = begin; begin < end && kt <= end && ok; ++kt) {
                     await(full0 + 8 * slot, phase);
                     const uint32_t kl = k_lo + slot * (2 * S::kTile >> 4), vl = v_lo + slot * (2 * S::kTile >> 4);
 #pragma unroll
@@ -278,12 +275,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (!ok) break;
-            }
-            if (ok && (due[0] || due[1])) {
-                await(full0 + 8 * slot, phase);
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    if (ok && due[x]) product(x, v_lo + slot * (2 * S::kTile >> 4));
             }
             give_up(!ok && elected);
             // every product is done before tensor memory is freed
@@ -359,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* stage = smem + S::kStageAt + (warp - kFirstSoftmaxWarp) * 4096;
         const bool plain = !p.sc.capped && !p.slopes;
         const float c = plain ? p.sc.mult : 1.0f;      // scores in registers times c are in log2
-        uint32_t s_phase = 0, o_phase = 0, n = 0;      // n: steps of the CTA so far
+        uint32_t s_phase = 0, o_phase = 0, n = 0;      // n: stages of the CTA so far
         bool ok = true;
         for (uint32_t it = 0;; ++it) {
             ok = warp_wait_or_abort(&item_full[it & 1u], (it >> 1) & 1u, p.timeout_ns, abort_flag);
@@ -472,6 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 unpair(add2(sum[0], sum[1]), l0, l1);
                 l = l0 + l1;
             }
+            if (min(first, first2) < end) ++n;         // the last value tile's stage
             // --------------------------------------------------- epilogue
             if (ok && first < last) {
                 ok = warp_wait_or_abort(&o_full[x], o_phase, p.timeout_ns, abort_flag);
