@@ -242,8 +242,7 @@ def nvfp4_qk_norm_rope(qkv, ld_qkv, tokens, q_heads, kv_heads, head_dim, q_weigh
                        table_rows, rotary_dim, interleaved, positions, q_out, k_out, stream):
     """RMS norm of every query and key head with the position rotation in the same pass."""
     return load().nvfp4_qk_norm_rope(qkv, ld_qkv, tokens, q_heads, kv_heads, head_dim, q_weight, k_weight, eps, cos,
-                                     sin, table_rows, rotary_dim, interleaved, positions, _ref(q_out), _ref(k_out),
-                                     stream)
+                                     sin, table_rows, rotary_dim, interleaved, positions, q_out, k_out, stream)
 
 
 def nvfp4_qk_norm_rope_backward_workspace_size(head_dim):
@@ -254,7 +253,7 @@ def nvfp4_qk_norm_rope_backward(dq, dk, qkv, ld_qkv, tokens, q_heads, kv_heads, 
                                 cos, sin, table_rows, rotary_dim, interleaved, positions, dqkv, ld_dqkv, dq_weight,
                                 dk_weight, workspace, workspace_bytes, stream):
     """Gradients of nvfp4_qk_norm_rope's input columns and weights."""
-    return load().nvfp4_qk_norm_rope_backward(_ref(dq), _ref(dk), qkv, ld_qkv, tokens, q_heads, kv_heads, head_dim,
+    return load().nvfp4_qk_norm_rope_backward(dq, dk, qkv, ld_qkv, tokens, q_heads, kv_heads, head_dim,
                                               q_weight, k_weight, eps, cos, sin, table_rows, rotary_dim, interleaved,
                                               positions, dqkv, ld_dqkv, dq_weight, dk_weight, workspace,
                                               workspace_bytes, stream)
@@ -266,7 +265,7 @@ def nvfp4_attention_spans(offsets, documents, prefix, causal, tokens, spans, str
 
 
 def nvfp4_attention(desc, q, k, v, out, lse, stream):
-    return load().nvfp4_attention(_ref(desc), _ref(q), _ref(k), _ref(v), _ref(out), lse, stream)
+    return load().nvfp4_attention(desc, q, k, v, out, lse, stream)
 
 
 def nvfp4_attention_backward_workspace_size(tokens, q_heads, kv_heads, head_dim):
@@ -274,8 +273,7 @@ def nvfp4_attention_backward_workspace_size(tokens, q_heads, kv_heads, head_dim)
 
 
 def nvfp4_attention_backward(desc, dout, q, k, v, out, lse, dq, dk, dv, workspace, workspace_bytes, stream):
-    return load().nvfp4_attention_backward(_ref(desc), _ref(dout), _ref(q), _ref(k), _ref(v), _ref(out), lse, _ref(dq),
-                                           _ref(dk), _ref(dv), workspace, workspace_bytes, stream)
+    return load().nvfp4_attention_backward(desc, dout, q, k, v, out, lse, dq, dk, dv, workspace, workspace_bytes, stream)
 
 
 def nvfp4_status_string(status):

@@ -287,22 +287,36 @@ def _heads(x: torch.Tensor, tokens: int, heads: int, dim: int, what: str) -> cap
     return capi.nvfp4_heads(x.data_ptr(), st if tokens > 1 else heads * dim, sh if heads > 1 else dim)
 
 
+def _new_heads(tokens: int, heads: int, dim: int, device) -> Tuple[torch.Tensor, capi.nvfp4_heads]:
+    x = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=device)
+    return x, capi.nvfp4_heads(x.data_ptr(), heads * dim, dim)
+
+
+def _check_float32(t: torch.Tensor, shape, what: str) -> None:
+    if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous float32 {list(shape)} expected, got {t.dtype} {list(t.shape)}")
+
+
 def _norm_rope_args(qkv, q_weight, k_weight, cos, sin, positions, q_heads, kv_heads, eps, interleaved):
-    if qkv.dtype != torch.bfloat16 or qkv.dim() != 2 or qkv.stride(1) != 1:
-        raise ValueError("qkv: a bfloat16 matrix with contiguous rows expected")
-    tokens, dim = qkv.shape[0], q_weight.numel()
-    if qkv.shape[1] < (q_heads + kv_heads) * dim:
-        raise ValueError(f"qkv: at least {(q_heads + kv_heads) * dim} columns expected, got {qkv.shape[1]}")
-    for name, t, shape in (("q_weight", q_weight, (dim,)), ("k_weight", k_weight, (dim,)), ("sin", sin, cos.shape)):
-        if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{name}: contiguous float32 {list(shape)} expected, got {t.dtype} {list(t.shape)}")
-    if cos.dtype != torch.float32 or cos.dim() != 2 or not cos.is_contiguous():
-        raise ValueError("cos: contiguous float32 [positions, rotary_dim / 2] expected")
+    if qkv.dtype != torch.bfloat16 or qkv.dim() != 2:
+        raise ValueError("qkv: a bfloat16 matrix expected")
+    tokens, columns = qkv.shape
+    ld, one = qkv.stride()
+    dim = q_weight.shape[-1] if q_weight.dim() else 0
+    if one != 1 or columns < (q_heads + kv_heads) * dim:
+        raise ValueError(f"qkv: contiguous rows of at least {(q_heads + kv_heads) * dim} columns expected")
+    _check_float32(q_weight, (dim,), "q_weight")
+    _check_float32(k_weight, (dim,), "k_weight")
+    if cos.dim() != 2:
+        raise ValueError("cos: [positions, rotary_dim / 2] expected")
+    rows, half = cos.shape
+    _check_float32(cos, (rows, half), "cos")
+    _check_float32(sin, (rows, half), "sin")
     if positions.dtype != torch.int32 or positions.shape != (tokens,) or not positions.is_contiguous():
         raise ValueError(f"positions: contiguous int32 [{tokens}] expected")
-    return (qkv.data_ptr(), qkv.stride(0) if tokens > 1 else qkv.shape[1], tokens, q_heads, kv_heads, dim,
-            q_weight.data_ptr(), k_weight.data_ptr(), eps, cos.data_ptr(), sin.data_ptr(), cos.shape[0],
-            2 * cos.shape[1], 1 if interleaved else 0, positions.data_ptr())
+    return (qkv.data_ptr(), ld if tokens > 1 else columns, tokens, q_heads, kv_heads, dim, q_weight.data_ptr(),
+            k_weight.data_ptr(), eps, cos.data_ptr(), sin.data_ptr(), rows, 2 * half, 1 if interleaved else 0,
+            positions.data_ptr())
 
 
 def qk_norm_rope(qkv: torch.Tensor, q_weight: torch.Tensor, k_weight: torch.Tensor, cos: torch.Tensor,
@@ -314,12 +328,16 @@ def qk_norm_rope(qkv: torch.Tensor, q_weight: torch.Tensor, k_weight: torch.Tens
     float32 [dim], the tables those of rope_tables."""
     args = _norm_rope_args(qkv, q_weight, k_weight, cos, sin, positions, q_heads, kv_heads, eps, interleaved)
     tokens, dim = args[2], args[5]
+    device = qkv.device
     if out_q is None:
-        out_q = torch.empty((tokens, q_heads, dim), dtype=torch.bfloat16, device=qkv.device)
+        out_q, hq = _new_heads(tokens, q_heads, dim, device)
+    else:
+        hq = _heads(out_q, tokens, q_heads, dim, "out_q")
     if out_k is None:
-        out_k = torch.empty((tokens, kv_heads, dim), dtype=torch.bfloat16, device=qkv.device)
-    status = capi.nvfp4_qk_norm_rope(*args, _heads(out_q, tokens, q_heads, dim, "out_q"),
-                                     _heads(out_k, tokens, kv_heads, dim, "out_k"), stream_handle(stream))
+        out_k, hk = _new_heads(tokens, kv_heads, dim, device)
+    else:
+        hk = _heads(out_k, tokens, kv_heads, dim, "out_k")
+    status = capi.nvfp4_qk_norm_rope(*args, hq, hk, stream_handle(stream))
     capi.check(status, "nvfp4_qk_norm_rope")
     return out_q, out_k
 
@@ -392,15 +410,18 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, spans: torch.Te
     Returns (out bf16 like q, lse float32 [q_heads, tokens])."""
     desc = _attention_desc(q, k, spans, scale, softcap, slopes)
     tokens, q_heads, kv_heads, dim = desc.tokens, desc.q_heads, desc.kv_heads, desc.head_dim
+    hq, hk = _heads(q, tokens, q_heads, dim, "q"), _heads(k, tokens, kv_heads, dim, "k")
+    hv = _heads(v, tokens, kv_heads, dim, "v")
+    device = q.device
     if out is None:
-        out = torch.empty((tokens, q_heads, dim), dtype=torch.bfloat16, device=q.device)
+        out, ho = _new_heads(tokens, q_heads, dim, device)
+    else:
+        ho = _heads(out, tokens, q_heads, dim, "out")
     if lse is None:
-        lse = torch.empty((q_heads, tokens), dtype=torch.float32, device=q.device)
-    elif lse.dtype != torch.float32 or lse.shape != (q_heads, tokens) or not lse.is_contiguous():
-        raise ValueError(f"lse: contiguous float32 [{q_heads}, {tokens}] expected")
-    status = capi.nvfp4_attention(desc, _heads(q, tokens, q_heads, dim, "q"), _heads(k, tokens, kv_heads, dim, "k"),
-                                  _heads(v, tokens, kv_heads, dim, "v"), _heads(out, tokens, q_heads, dim, "out"),
-                                  lse.data_ptr(), stream_handle(stream))
+        lse = torch.empty((q_heads, tokens), dtype=torch.float32, device=device)
+    else:
+        _check_float32(lse, (q_heads, tokens), "lse")
+    status = capi.nvfp4_attention(desc, hq, hk, hv, ho, lse.data_ptr(), stream_handle(stream))
     capi.check(status, "nvfp4_attention")
     return out, lse
 
@@ -415,25 +436,28 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     (nvfp4_attention_backward); dv may be a view of the QKV projection's output gradient."""
     desc = _attention_desc(q, k, spans, scale, softcap, slopes)
     tokens, q_heads, kv_heads, dim = desc.tokens, desc.q_heads, desc.kv_heads, desc.head_dim
-    if lse.dtype != torch.float32 or lse.shape != (q_heads, tokens) or not lse.is_contiguous():
-        raise ValueError(f"lse: contiguous float32 [{q_heads}, {tokens}] expected")
+    _check_float32(lse, (q_heads, tokens), "lse")
+    hdo, hq = _heads(dout, tokens, q_heads, dim, "dout"), _heads(q, tokens, q_heads, dim, "q")
+    hk, hv = _heads(k, tokens, kv_heads, dim, "k"), _heads(v, tokens, kv_heads, dim, "v")
+    ho = _heads(out, tokens, q_heads, dim, "out")
+    device = q.device
     if dq is None:
-        dq = torch.empty((tokens, q_heads, dim), dtype=torch.bfloat16, device=q.device)
-    if dk is None and dv is None:
-        dk, dv = torch.empty((2, tokens, kv_heads, dim), dtype=torch.bfloat16, device=q.device).unbind(0)
-    elif dk is None:
-        dk = torch.empty((tokens, kv_heads, dim), dtype=torch.bfloat16, device=q.device)
-    elif dv is None:
-        dv = torch.empty((tokens, kv_heads, dim), dtype=torch.bfloat16, device=q.device)
+        dq, hdq = _new_heads(tokens, q_heads, dim, device)
+    else:
+        hdq = _heads(dq, tokens, q_heads, dim, "dq")
+    if dk is None:
+        dk, hdk = _new_heads(tokens, kv_heads, dim, device)
+    else:
+        hdk = _heads(dk, tokens, kv_heads, dim, "dk")
+    if dv is None:
+        dv, hdv = _new_heads(tokens, kv_heads, dim, device)
+    else:
+        hdv = _heads(dv, tokens, kv_heads, dim, "dv")
     nbytes = capi.nvfp4_attention_backward_workspace_size(tokens, q_heads, kv_heads, dim)
     if workspace is None or workspace.numel() < nbytes:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    status = capi.nvfp4_attention_backward(
-        desc, _heads(dout, tokens, q_heads, dim, "dout"), _heads(q, tokens, q_heads, dim, "q"),
-        _heads(k, tokens, kv_heads, dim, "k"), _heads(v, tokens, kv_heads, dim, "v"),
-        _heads(out, tokens, q_heads, dim, "out"), lse.data_ptr(), _heads(dq, tokens, q_heads, dim, "dq"),
-        _heads(dk, tokens, kv_heads, dim, "dk"), _heads(dv, tokens, kv_heads, dim, "dv"), workspace.data_ptr(),
-        workspace.numel(), stream_handle(stream))
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    status = capi.nvfp4_attention_backward(desc, hdo, hq, hk, hv, ho, lse.data_ptr(), hdq, hdk, hdv,
+                                           workspace.data_ptr(), workspace.numel(), stream_handle(stream))
     capi.check(status, "nvfp4_attention_backward")
     return dq, dk, dv
 
