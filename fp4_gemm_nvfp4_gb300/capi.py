@@ -41,7 +41,7 @@ EXPORTED = ("nvfp4_scale_bytes", "nvfp4_quantize_workspace_size", "nvfp4_quantiz
             "nvfp4_qk_norm_rope", "nvfp4_qk_norm_rope_backward_workspace_size", "nvfp4_qk_norm_rope_backward",
             "nvfp4_attention_spans", "nvfp4_attention", "nvfp4_attention_backward_workspace_size",
             "nvfp4_attention_backward",
-            "nvfp4_testing_arm_gemm_timeout", "nvfp4_testing_bounds_violations",
+            "nvfp4_testing_arm_gemm_timeout", "nvfp4_testing_arm_attention_timeout", "nvfp4_testing_bounds_violations",
             "nvfp4_testing_bounds_shrink")
 
 
@@ -135,6 +135,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.nvfp4_device_error.argtypes, L.nvfp4_device_error.restype = [vp], i32
     L.nvfp4_testing_arm_gemm_timeout.argtypes = [ctypes.c_uint32]
     L.nvfp4_testing_arm_gemm_timeout.restype = i32
+    L.nvfp4_testing_arm_attention_timeout.argtypes = [c32, ctypes.c_uint32]
+    L.nvfp4_testing_arm_attention_timeout.restype = i32
     L.nvfp4_testing_bounds_violations.argtypes = [ctypes.POINTER(ctypes.c_uint64)]
     L.nvfp4_testing_bounds_violations.restype = i32
     L.nvfp4_testing_bounds_shrink.argtypes, L.nvfp4_testing_bounds_shrink.restype = [i64], i32
@@ -288,6 +290,12 @@ def nvfp4_testing_arm_gemm_timeout(wait_limit_us):
     """Test support (include/nvfp4_testing.h): the next GEMM launch withholds
     one barrier arrival and gives up on its waits after wait_limit_us."""
     return load().nvfp4_testing_arm_gemm_timeout(wait_limit_us)
+
+
+def nvfp4_testing_arm_attention_timeout(backward, wait_limit_us):
+    """Test support (include/nvfp4_testing.h): the next attention call's loads
+    never come and its waits give up after wait_limit_us."""
+    return load().nvfp4_testing_arm_attention_timeout(backward, wait_limit_us)
 
 
 def nvfp4_testing_bounds_violations():

@@ -684,6 +684,13 @@ nvfp4_status nvfp4_testing_arm_gemm_timeout(uint32_t wait_limit_us) {
     return NVFP4_OK;
 }
 
+nvfp4_status nvfp4_testing_arm_attention_timeout(int32_t backward, uint32_t wait_limit_us) {
+    if (wait_limit_us < 1000u || wait_limit_us > 2000000u) return NVFP4_ERR_INVALID_ARG;
+    if (backward) nvfp4::arm_attention_backward_fault((uint64_t)wait_limit_us * 1000u);
+    else nvfp4::arm_attention_forward_fault((uint64_t)wait_limit_us * 1000u);
+    return NVFP4_OK;
+}
+
 nvfp4_status nvfp4_testing_bounds_violations(uint64_t* count) {
 #ifdef NVFP4_BOUNDS_CHECK
     if (!count) return NVFP4_ERR_INVALID_ARG;

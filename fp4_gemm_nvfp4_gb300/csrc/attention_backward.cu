@@ -94,6 +94,7 @@ struct Params {
     int32_t head_dim;
     Workspace ws;
     uint64_t timeout_ns;
+    uint32_t withhold;               // test support: the loads of the first item never come
 };
 
 // One item: an owned tile, and the streamed tiles first .. first + count - 1
@@ -220,6 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Item item = items[it & 1u];
                 mbar_arrive(&item_empty[it & 1u]);
                 if (!item.valid) break;
+                if (p.withhold) await(drain, 0);   // (runs out)
                 // the streamed tiles need not wait for the owned ones' place:
                 // the first pair goes ahead
                 int h = item.head0 + item.from / max(item.count, 1), t = item.first + item.from % max(item.count, 1);
@@ -819,13 +821,15 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
     const int splits = split_count(a.tokens, a.q_heads, a.kv_heads);
     p.ws = carve(a.workspace, a.tokens, a.q_heads, a.kv_heads, a.head_dim, splits, nullptr);
     p.splits = 1;
-    p.timeout_ns = kAttentionTimeoutNs;
+    p.timeout_ns = attention_timeout(&p.withhold);
     if ((uint64_t)p.tiles * (uint64_t)a.q_heads > 0x7FFFFFFFull) return cudaErrorInvalidValue;
     p.heads = a.q_heads;
     attention_backward_kernel<kD, false><<<(unsigned)(p.tiles * a.q_heads), kThreads, Shape<kD>::kSmem, stream>>>(
         mq, mdo, mk, mv, mdq, mdq, p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    p.timeout_ns = kAttentionTimeoutNs;
+    p.withhold = 0;
     p.heads = a.kv_heads;
     p.dv = a.dv;
     p.dk = a.dk;
@@ -854,6 +858,8 @@ cudaError_t launch_attention_backward(const Attention& a, cudaStream_t stream) {
 }
 
 cudaError_t attention_backward_bounds_read_and_clear(uint64_t* n) { return bounds_read_and_clear_local(n); }
+
+void arm_attention_backward_fault(uint64_t timeout_ns) { g_attention_armed_ns.store(timeout_ns); }
 
 cudaError_t attention_backward_status_read_and_clear(unsigned int* status) {
     return attention_status_read_and_clear_local(status);

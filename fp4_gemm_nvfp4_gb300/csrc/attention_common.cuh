@@ -5,6 +5,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "bounds.cuh"
 #include "mma_common.cuh"
 
@@ -16,6 +18,16 @@ constexpr uint64_t kAttentionTimeoutNs = 2000000000ull;
 
 // Status word of this translation unit's kernels (kStatusTimeoutBit).
 static __device__ unsigned int g_attention_status = 0;
+
+// Wait limit of the next launch that leaves out one arrival (0: none armed).
+static std::atomic<uint64_t> g_attention_armed_ns{0};
+
+// The limit of a launch's waits, and whether it is the armed one.
+inline uint64_t attention_timeout(uint32_t* withhold) {
+    const uint64_t armed = g_attention_armed_ns.exchange(0);
+    *withhold = armed ? 1u : 0u;
+    return armed ? armed : kAttentionTimeoutNs;
+}
 
 inline cudaError_t attention_status_read_and_clear_local(unsigned int* status) {
     unsigned int v = 0;

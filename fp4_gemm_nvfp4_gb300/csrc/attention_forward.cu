@@ -60,6 +60,7 @@ struct Params {
     float* lse;
     Extent xlse;
     uint64_t timeout_ns;
+    uint32_t withhold;               // test support: the loads of the first item never come
 };
 
 // One item: two query tiles, the key tiles [first, last) each of them sees
@@ -177,6 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Item item = items[it & 1u];
                 mbar_arrive(&item_empty[it & 1u]);
                 if (!item.valid) break;
+                if (p.withhold) await(drain, 0);   // (runs out)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     if (item.first[x] >= item.last[x]) continue;
@@ -563,7 +565,7 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
     p.spans = a.spans;
     p.lse = a.lse;
     p.xlse = extent_of(a.lse, a.tokens * a.q_heads * 4);
-    p.timeout_ns = kAttentionTimeoutNs;
+    p.timeout_ns = attention_timeout(&p.withhold);
     const uint64_t grid = (uint64_t)p.tiles * p.items_per_tile;
     if (grid > 0x7FFFFFFFull) return cudaErrorInvalidValue;
     attention_forward_kernel<kD><<<(unsigned)grid, kThreads, Shape<kD>::kSmem, stream>>>(mq, mk, mv, mo, p);
@@ -575,6 +577,8 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
 cudaError_t launch_attention(const Attention& a, cudaStream_t stream) {
     return a.head_dim <= 64 ? launch<64>(a, stream) : launch<128>(a, stream);
 }
+
+void arm_attention_forward_fault(uint64_t timeout_ns) { g_attention_armed_ns.store(timeout_ns); }
 
 cudaError_t attention_forward_status_read_and_clear(unsigned int* status) {
     return attention_status_read_and_clear_local(status);

@@ -110,6 +110,11 @@ cudaError_t attention_backward_bounds_read_and_clear(uint64_t* n);
 // its leader CTA leaves out one scale-warp arrival, so one wait runs out.
 void arm_gemm_fault(uint64_t timeout_ns);
 
+// Test support: the next attention launch (the next backward call's first)
+// waits at most timeout_ns per barrier and its loads never come.
+void arm_attention_forward_fault(uint64_t timeout_ns);
+void arm_attention_backward_fault(uint64_t timeout_ns);
+
 cudaError_t launch_dequantize(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales, const float* sg,
                               int64_t rows, int64_t cols, void* y, int64_t ldy, bool out_fp32,
                               cudaStream_t stream);

@@ -42,6 +42,17 @@ extern "C" {
 NVFP4_API nvfp4_status nvfp4_testing_arm_gemm_timeout(uint32_t wait_limit_us);
 
 /*
+ * nvfp4_testing_arm_attention_timeout -- the same for attention: in the next
+ * nvfp4_attention call, or (backward != 0) in the first kernel of the next
+ * nvfp4_attention_backward call, no CTA loads its tiles, so every wait for
+ * them runs out after wait_limit_us (1000 .. 2000000); the kernel sets the
+ * status word's timeout bit, frees its tensor memory and returns.
+ * nvfp4_device_error then returns NVFP4_ERR_TIMEOUT (and clears the word);
+ * the forward call's outputs are not written.  Use a call of few tiles.
+ */
+NVFP4_API nvfp4_status nvfp4_testing_arm_attention_timeout(int32_t backward, uint32_t wait_limit_us);
+
+/*
  * nvfp4_testing_bounds_violations -- the number of stores the debug build's
  * bounds check skipped since the previous call (the count is then cleared).
  *  count  host pointer, receives the number.
