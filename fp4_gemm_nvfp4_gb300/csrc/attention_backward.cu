@@ -145,8 +145,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* f_empty = f_full + 1;              // ... and their last scores done
     uint64_t* s_full = f_empty + 1;              // [2], in turn: two S may be ahead of their softmax
     uint64_t* dp_full = s_full + 2;
+    // [2], in turn: with S one step ahead a warp may arrive for P(i + 1) while
+    // another has not yet for P(i)
     uint64_t* p_full = dp_full + 1;
-    uint64_t* dz_full = p_full + 1;
+    uint64_t* dz_full = p_full + 2;
     uint64_t* acc_full = dz_full + 1;
     uint64_t* item_full = acc_full + 1;          // [2]
     uint64_t* item_empty = item_full + 2;        // [2]
@@ -170,7 +172,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&s_full[0], 1);
         mbar_init(&s_full[1], 1);
         mbar_init(dp_full, 1);
-        mbar_init(p_full, kSoftmaxWarps);
+        mbar_init(&p_full[0], kSoftmaxWarps);
+        mbar_init(&p_full[1], kSoftmaxWarps);
         mbar_init(dz_full, kSoftmaxWarps);
         mbar_init(acc_full, 1);
         for (int i = 0; i < 2; ++i) {
@@ -303,7 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (last) tc_commit(f_empty, elected);
             };
             auto product = [&](uint32_t acc, uint32_t slot, bool start) {
-                await(smem_u32(acc ? dz_full : p_full), n & 1u);
+                if (acc) await(smem_u32(dz_full), n & 1u);
+                else await(smem_u32(&p_full[n & 1u]), (n >> 1) & 1u);
                 if (!ok) return;
                 // each 32 columns of S hold 32 rows' BF16 in their first 16
                 mma_sum<kIdAcc, 2, 32>(tmem + (acc ? S::kAcc2Col : S::kAcc1Col), tmem + (acc ? S::kDpCol : p_col),
@@ -582,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full);
+                if (lane == 0) mbar_arrive(&p_full[n & 1u]);
 
                 ok = warp_wait_or_abort(dp_full, n & 1u, p.timeout_ns, abort_flag);
                 if (!ok) break;
@@ -631,6 +635,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t next = it + 1;
                 ok = warp_wait_or_abort(&item_full[next & 1u], (next >> 1) & 1u, p.timeout_ns, abort_flag);
                 if (!ok) break;
+                // (once every warp has handed over its last P, and so has read this
+                // item's delta~; without streamed tiles none reads it)
+                if (total > 0) ok = warp_wait_or_abort(&p_full[(n - 1) & 1u], ((n - 1) >> 1) & 1u, p.timeout_ns, abort_flag);
+                if (!ok) break;
                 if (items[next & 1u].valid) prepare(items[next & 1u]);
             }
             // --------------------------------------------------- epilogue
@@ -678,16 +686,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             } else {
-                float exact, odd;
-                unpair(exact2, exact, odd);
-                exact += odd;
-                exact_parts[quarter * 128 + row] = exact;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(exact_full);
-                ok = warp_wait_or_abort(exact_full, it & 1u, p.timeout_ns, abort_flag);
-                if (!ok) break;
-                exact = alive ? (exact_parts[row] + exact_parts[128 + row]) + (exact_parts[256 + row] + exact_parts[384 + row])
-                              : 0.0f;
+                float exact = 0.0f;
+                if (total > 0) {
+                    float even, odd;
+                    unpair(exact2, even, odd);
+                    exact_parts[quarter * 128 + row] = even + odd;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(exact_full);
+                    ok = warp_wait_or_abort(exact_full, (results - 1) & 1u, p.timeout_ns, abort_flag);
+                    if (!ok) break;
+                    if (alive)
+                        exact = (exact_parts[row] + exact_parts[128 + row]) + (exact_parts[256 + row] + exact_parts[384 + row]);
+                }
                 const float turn = alive ? delta - exact : 0.0f;
                 if (quarter < kD / 32) {
                     uint32_t a1[32], a2[32];

@@ -287,6 +287,33 @@ def test_longer_sequences(T, HQ, HKV, D, softcap):
     _check(*_inputs(T, HQ, HKV, D, T), _causal(T), softcap=softcap)
 
 
+@pytest.mark.parametrize("HQ,HKV,D", [(40, 20, 64), (40, 20, 128), (36, 6, 40), (33, 33, 96)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_many_tiles_per_sm(HQ, HKV, D, causal):
+    """More tiles than SMs several times over, with documents from one token to
+    many tiles, whole tiles of padding among them: what one tile leaves behind
+    for the next on the same SM must not show, whatever their lengths.  Run
+    three times over changing inputs, the repeats equal bit for bit."""
+    lengths = [1, 3, 600, 1, 127, 130, 260, 40, 1, 1, 300, 5, 128, 128]
+    offsets = [0]
+    for n in lengths:
+        offsets.append(offsets[-1] + n)
+    T = offsets[-1] + 300
+    spans = ops.attention_spans(torch.tensor(offsets, dtype=torch.int32, device="cuda"), T, causal=causal)
+    first, other = _inputs(T, HQ, HKV, D, D), _inputs(T, HQ, HKV, D, D + 1)
+
+    def step(q, k, v, do):
+        o, lse = ops.attention(q, k, v, spans)
+        return (o, lse, *ops.attention_backward(do, q, k, v, o, lse, spans))
+
+    want = step(*first)
+    for _ in range(3):
+        step(*other)
+        again = step(*first)
+        assert all(torch.equal(a, b) for a, b in zip(again, want))
+    _check(*first, spans)
+
+
 def test_no_tokens():
     q = torch.empty((0, 4, 64), dtype=torch.bfloat16, device="cuda")
     k = torch.empty((0, 2, 64), dtype=torch.bfloat16, device="cuda")
