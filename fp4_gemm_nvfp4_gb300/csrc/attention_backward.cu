@@ -27,6 +27,8 @@
 // work.  Warps: 0 TMA loads, 1 MMA issue, 2 the next item, 4-19 softmax (a
 // lane one row, each group of four warps 32 of the columns).  As in the
 // forward pass a CTA goes on to blocks that have not started.
+#include <algorithm>
+
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -779,13 +781,16 @@ cudaError_t prepare_kernel() {
 // The dk dv kernel has an item per key tile and key head; where these are too
 // few for the SMs (few key heads, short sequences) each is split over its
 // streamed tiles, at the cost of FP32 parts written and summed by one more
-// kernel: worth it from four streamed tiles per split.  Two items per SM even
-// out the items' lengths.
+// kernel: worth it from eight streamed tiles per split while every split has
+// an SM, from sixteen where two share one (which evens out the items' lengths).
+// 1024 tokens, 24/12 heads of 128 (us): 55 unsplit, 74 in three; 2560 tokens, 16/4
+// heads: 168 unsplit, 118 in three.
 int split_count(int64_t tokens, int q_heads, int kv_heads) {
     const int64_t tiles = (tokens + 127) / 128, items = tiles * kv_heads;
-    const int64_t want = 2 * (int64_t)device_sm_count() / items;
-    const int64_t most = tiles * (q_heads / kv_heads) / 4;   // of the longest item's streamed tiles
-    const int64_t splits = want < most ? want : most;
+    const int64_t most = tiles * (q_heads / kv_heads);       // the longest item's streamed tiles
+    const int64_t one = std::min<int64_t>(device_sm_count() / items, most / 8), 
+                  two = std::min<int64_t>(2 * device_sm_count() / items, most / 16);
+    const int64_t splits = std::max(one, two);
     return (int)(splits < 1 ? 1 : (splits < kMaxSplits ? splits : kMaxSplits));
 }
 

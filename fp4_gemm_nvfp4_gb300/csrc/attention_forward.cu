@@ -44,7 +44,8 @@ struct Shape {
     static constexpr uint32_t kStages = kD == 128 ? 2 : 4;
     static constexpr uint32_t kStageAt = (2 + 2 * kStages) * kTile;
     static constexpr uint32_t kBarAt = kStageAt + 8 * 4096;  // 32 rows x 64 dims of output per softmax warp
-    static constexpr size_t kSmem = kBarAt + 1024;           // dynamic shared memory starts 1024-byte aligned (checked)
+    static constexpr uint32_t kJointAt = kBarAt + 1024;      // a split tile's second maxima and sums
+    static constexpr size_t kSmem = kJointAt + 1024;         // dynamic shared memory starts 1024-byte aligned (checked)
 };
 static_assert(Shape<128>::kSmem <= 232448 && Shape<64>::kSmem <= 232448, "shared memory budget");
 
@@ -66,6 +67,8 @@ struct Params {
 // One item: two query tiles, the key tiles [first, last) each of them sees
 // (first >= last: none) and their spans.  The key tiles from the lower first
 // to the higher last are loaded; a query tile passes over those not its own.
+// A split item is one query tile twice, which take every second key tile each
+// and are joined by the first's epilogue.
 struct Item {
     int valid, kv_head;
     int head[2], tile[2], first[2], last[2];
@@ -77,7 +80,8 @@ struct Ring {
     uint32_t slot = 0, phase = 0;
 };
 
-template <int kD>
+// kSplit: an item is one tile twice, with the key tiles in turn.
+template <int kD, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                              const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o,
@@ -95,7 +99,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* p_full = s_full + 2;               // [2] scores read, P written
     uint64_t* o_full = p_full + 2;               // [2] the item's last product done
     uint64_t* o_empty = o_full + 2;              // [2] its result read
-    uint64_t* item_full = o_empty + 2;           // [2]
+    uint64_t* joined = o_empty + 2;              // a split item's second maxima and sums written
+    uint64_t* item_full = joined + 1;            // [2]
     uint64_t* item_empty = item_full + 2;        // [2] read by loads, MMA and softmax warps
     uint64_t* loaded = item_empty + 2;           // the item's loads issued
     uint64_t* answered = loaded + 1;
@@ -119,6 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&item_full[i], 1);
             mbar_init(&item_empty[i], 10);
         }
+        mbar_init(joined, 4);
         mbar_init(loaded, 1);
         mbar_init(answered, 1);
         mbar_init(drain, 1);
@@ -254,20 +260,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int kt = begin; begin < end && kt <= end && ok; ++kt) {
                     await(full0 + 8 * slot, phase);
                     const uint32_t kl = k_lo + slot * (2 * S::kTile >> 4), vl = v_lo + slot * (2 * S::kTile >> 4);
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
+                    auto turn = [&](int x) {
                         if (due[x]) product(x, vl);
-                        due[x] = kt >= first[x] && kt < last[x];
+                        due[x] = kt >= first[x] && kt < last[x] && (!kSplit || ((kt - first[x]) & 1) == 0);
                         due_start[x] = kt == first[x];
-                        due_end[x] = kt + 1 == last[x];
-                        if (due[x]) {
-                            if (due_start[x]) await(smem_u32(&q_full[x]), q_items[x]++ & 1u);
-                            tc_fence_after();
-                            if (!ok) break;
-                            mma_scores<kIdS, kD>(tmem + kScoreCol + 128 * x, q_lo + x * (S::kTile >> 4), kl, elected);
-                            tc_commit(&s_full[x], elected);
-                            if (due_end[x]) tc_commit(&q_empty[x], elected);
-                        }
+                        due_end[x] = kSplit ? kt + 2 >= last[x] : kt + 1 == last[x];
+                        if (!due[x]) return;
+                        if (due_start[x]) await(smem_u32(&q_full[x]), q_items[x]++ & 1u);
+                        tc_fence_after();
+                        if (!ok) return;
+                        mma_scores<kIdS, kD>(tmem + kScoreCol + 128 * x, q_lo + x * (S::kTile >> 4), kl, elected);
+                        tc_commit(&s_full[x], elected);
+                        if (due_end[x]) tc_commit(&q_empty[x], elected);
+                    };
+                    // (split: the scores first, the other half's product may have to wait)
+                    if (kSplit && ((kt - begin) & 1)) {
+                        turn(1);
+                        if (ok) turn(0);
+                    } else {
+                        turn(0);
+                        if (ok) turn(1);
                     }
                     if (!ok) break;
                     tc_commit(&empty[slot], elected);
@@ -300,13 +312,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int n = (int)(block % p.items_per_tile), ti = p.tiles - 1 - (int)(block / p.items_per_tile);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        item.head[x] = p.pair_heads ? 2 * n + x : n;
-                        item.tile[x] = p.pair_heads ? ti : 2 * ti + x;
+                        item.head[x] = p.pair_heads ? 2 * n + x : n;   // (not both: pair_heads, split)
+                        item.tile[x] = p.pair_heads || kSplit ? ti : 2 * ti + x;
                     }
                     item.kv_head = item.head[0] / p.group;
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        if (x == 1 && p.pair_heads) {
+                        if (x == 1 && (p.pair_heads || kSplit)) {
                             item.span[1] = item.span[0];
                         } else {
                             TileSpan t{INT32_MAX, 0, 0, INT32_MAX};
@@ -317,9 +329,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             item.span[x] = t;
                         }
-                        const bool some = item.span[x].lo < item.span[x].hi;
-                        item.first[x] = some ? item.span[x].lo >> 7 : INT32_MAX;
-                        item.last[x] = some ? (item.span[x].hi + 127) >> 7 : 0;
+                        const int from = (item.span[x].lo >> 7) + (kSplit ? x : 0), to = (item.span[x].hi + 127) >> 7;
+                        const bool some = item.span[x].lo < item.span[x].hi && from < to;
+                        item.first[x] = some ? from : INT32_MAX;
+                        item.last[x] = some ? to : 0;
                     }
                 }
                 ok = warp_wait_or_abort(&item_empty[it & 1u], ((it >> 1) & 1u) ^ 1u, p.timeout_ns, abort_flag);
@@ -352,7 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* stage = smem + S::kStageAt + (warp - kFirstSoftmaxWarp) * 4096;
         const bool plain = !p.sc.capped && !p.slopes;
         const float c = plain ? p.sc.mult : 1.0f;      // scores in registers times c are in log2
-        uint32_t s_phase = 0, o_phase = 0, n = 0;      // n: stages of the CTA so far
+        float* joint = reinterpret_cast<float*>(smem + S::kJointAt);   // [2][128]
+        uint32_t s_phase = 0, o_phase = 0, join_phase = 0, n = 0;      // n: stages of the CTA so far
         bool ok = true;
         for (uint32_t it = 0;; ++it) {
             ok = warp_wait_or_abort(&item_full[it & 1u], (it >> 1) & 1u, p.timeout_ns, abort_flag);
@@ -373,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int end = max(last, last2);
             for (int kt = min(first, first2); kt < end; ++kt) {
                 const uint32_t load = ++n;             // the value tile comes with the next stage
-                if (kt < first || kt >= last) continue;
+                if (kt < first || kt >= last || (kSplit && ((kt - first) & 1))) continue;
                 ok = warp_wait_or_abort(&s_full[x], s_phase, p.timeout_ns, abort_flag);
                 if (!ok) break;
                 s_phase ^= 1u;
@@ -472,9 +486,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 o_phase ^= 1u;
             }
             if (!ok) break;
+            float f = 1.0f, f2 = 0.0f;
+            const bool join = kSplit && first2 < last2;
+            if (kSplit && x == 1) {
+                // (the first half has read the last item's before this one's O began)
+                if (first < last) {
+                    joint[row] = m;
+                    joint[128 + row] = l;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(joined);
+                }
+                continue;
+            }
+            if (join) {
+                ok = warp_wait_or_abort(&o_full[1], join_phase, p.timeout_ns, abort_flag) &&
+                     warp_wait_or_abort(joined, join_phase, p.timeout_ns, abort_flag);
+                if (!ok) break;
+                join_phase ^= 1u;
+                const float m2 = joint[row], l2 = joint[128 + row], top = fmaxf(m, m2);
+                f = m == -INFINITY ? 0.0f : ex2(m - top);
+                f2 = m2 == -INFINITY ? 0.0f : ex2(m2 - top);
+                m = top;
+                l = l * f + l2 * f2;
+            }
             tc_fence_after();
             const bool some = l > 0.0f;
-            const float f = some ? 1.0f / l : 0.0f;
+            const float over = some ? 1.0f / l : 0.0f;
+            f *= over;
+            f2 *= over;
+            const float g = join ? 1.0f : f;
             const int64_t row0 = token - lane;
             uint32_t pk[kD / 2];
 #pragma unroll
@@ -482,14 +522,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t o[32];
                 tmem_ld_32x32b_x32(o_at + 32 * h, o);
                 tmem_ld_wait();
+                if (join) {
+                    uint32_t o2[32];
+                    tmem_ld_32x32b_x32(o_at + 128 + 32 * h, o2);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        o[j] = __float_as_uint(fmaf(__uint_as_float(o2[j]), f2, __uint_as_float(o[j]) * f));
+                }
 #pragma unroll
                 for (int j = 0; j < 16; ++j)   // nothing summed: the columns may hold anything
-                    pk[16 * h + j] = some ? pack_bf16(__uint_as_float(o[2 * j]) * f, __uint_as_float(o[2 * j + 1]) * f) : 0u;
+                    pk[16 * h + j] = some ? pack_bf16(__uint_as_float(o[2 * j]) * g, __uint_as_float(o[2 * j + 1]) * g) : 0u;
             }
             if (first < last) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&o_empty[x]);
+                if (join && lane == 0) mbar_arrive(&o_empty[1]);
             }
 #pragma unroll
             for (int ch = 0; ch < (int)S::kChunks; ++ch) {
@@ -523,28 +572,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 // The warp groups trade registers against the launch's 168 per thread:
 // 128 * 80 + 256 * 208 = 63488 <= 384 * 168; a build that was given fewer is
 // not launched (setmaxnreg.inc would wait forever).
-template <int kD>
+template <int kD, bool kSplit>
 cudaError_t prepare_kernel() {
     static bool done[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (done[dev]) return cudaSuccess;
     cudaFuncAttributes f;
-    cudaError_t e = cudaFuncGetAttributes(&f, attention_forward_kernel<kD>);
+    cudaError_t e = cudaFuncGetAttributes(&f, attention_forward_kernel<kD, kSplit>);
     // the tiles' swizzle needs dynamic shared memory to start on 1024 bytes:
     // it does when there is no static shared memory before it
     if (e == cudaSuccess && (f.numRegs * kThreads < 128 * 80 + 256 * 208 || f.sharedSizeBytes != 0))
         e = cudaErrorInvalidConfiguration;
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(attention_forward_kernel<kD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(attention_forward_kernel<kD, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)Shape<kD>::kSmem);
     done[dev] = e == cudaSuccess;
     return e;
 }
 
-template <int kD>
+template <int kD, bool kSplit>
 cudaError_t launch(const Attention& a, cudaStream_t stream) {
-    cudaError_t e = prepare_kernel<kD>();
+    cudaError_t e = prepare_kernel<kD, kSplit>();
     if (e != cudaSuccess) return e;
     CUtensorMap mq, mk, mv, mo;
     if (!make_heads_map(&mq, a.q, a.tokens, a.q_heads, a.head_dim, 128) ||
@@ -556,9 +605,9 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
     p.tokens = a.tokens;
     p.group = a.q_heads / a.kv_heads;
     // two heads with the same keys have the same mask; an odd group has none to spare
-    p.pair_heads = p.group % 2 == 0 ? 1 : 0;
+    p.pair_heads = !kSplit && p.group % 2 == 0 ? 1 : 0;
     const int64_t t128 = (a.tokens + 127) / 128;
-    p.tiles = (int32_t)(p.pair_heads ? t128 : (t128 + 1) / 2);
+    p.tiles = (int32_t)(kSplit || p.pair_heads ? t128 : (t128 + 1) / 2);
     p.items_per_tile = (uint32_t)(p.pair_heads ? a.q_heads / 2 : a.q_heads);
     p.sc = make_scores(a.scale, a.softcap);
     p.slopes = a.slopes;
@@ -568,14 +617,29 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
     p.timeout_ns = attention_timeout(&p.withhold);
     const uint64_t grid = (uint64_t)p.tiles * p.items_per_tile;
     if (grid > 0x7FFFFFFFull) return cudaErrorInvalidValue;
-    attention_forward_kernel<kD><<<(unsigned)grid, kThreads, Shape<kD>::kSmem, stream>>>(mq, mk, mv, mo, p);
+    attention_forward_kernel<kD, kSplit><<<(unsigned)grid, kThreads, Shape<kD>::kSmem, stream>>>(mq, mk, mv, mo, p);
     return cudaGetLastError();
+}
+
+// Two tiles of 128 queries share their key tiles, which halves what comes
+// from L2.  Where there are too few pairs of tiles for the SMs, an item is one
+// tile whose key tiles the two halves of the CTA take in turn instead: twice
+// the items of half the length.  Below 9/8 of the SMs' number of pairs that is
+// as fast or faster (us, pairs and split: 2047 tokens, 5/1 heads of 96 with
+// cap and bias, 40 pairs: 73 and 42; 4096 tokens, 8/2 heads of 128, 128 pairs:
+// 55 and 42; 2560 tokens, 16/4 heads, 160 pairs: 39 and 39), from 192 slower
+// (2048 tokens, 24/12 heads: 33 and 41).
+template <int kD>
+cudaError_t launch_dim(const Attention& a, cudaStream_t stream) {
+    const int64_t t128 = (a.tokens + 127) / 128;
+    const int64_t pairs = (a.q_heads / a.kv_heads) % 2 == 0 ? t128 * (a.q_heads / 2) : (t128 + 1) / 2 * a.q_heads;
+    return 8 * pairs <= 9 * (int64_t)device_sm_count() ? launch<kD, true>(a, stream) : launch<kD, false>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_attention(const Attention& a, cudaStream_t stream) {
-    return a.head_dim <= 64 ? launch<64>(a, stream) : launch<128>(a, stream);
+    return a.head_dim <= 64 ? launch_dim<64>(a, stream) : launch_dim<128>(a, stream);
 }
 
 void arm_attention_forward_fault(uint64_t timeout_ns) { g_attention_armed_ns.store(timeout_ns); }
