@@ -654,10 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3u)) * 16)) =
-                        make_uint4(pack_bf16(__uint_as_float(v[8 * i]), __uint_as_float(v[8 * i + 1])),
-                                   pack_bf16(__uint_as_float(v[8 * i + 2]), __uint_as_float(v[8 * i + 3])),
-                                   pack_bf16(__uint_as_float(v[8 * i + 4]), __uint_as_float(v[8 * i + 5])),
-                                   pack_bf16(__uint_as_float(v[8 * i + 6]), __uint_as_float(v[8 * i + 7])));
+                        make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0 && own < p.tokens) {
@@ -684,6 +681,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (own < p.tokens && (int)col + j < p.head_dim)
                                 *reinterpret_cast<uint4*>(part + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                     } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] = pack_bf16(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1]));
                         store(k ? &map_out2 : &map_out1, col, o);
                     }
                 }
@@ -702,15 +701,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const float turn = alive ? delta - exact : 0.0f;
                 if (quarter < kD / 32) {
-                    uint32_t a1[32], a2[32];
-                    tmem_ld_32x32b_x32(lanes + S::kAcc1Col + 32 * quarter, a1);
-                    tmem_ld_32x32b_x32(lanes + S::kAcc2Col + 32 * quarter, a2);
-                    tmem_ld_wait();
+                    uint32_t o[16];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        a2[j] = total > 0 ? __float_as_uint(fmaf(turn, __uint_as_float(a1[j]), __uint_as_float(a2[j])) * p.scale)
-                                          : 0u;
-                    store(&map_out1, 32 * quarter, a2);
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t a1[16], a2[16];
+                        tmem_ld_32x32b_x16(lanes + S::kAcc1Col + 32 * quarter + 16 * half, a1);
+                        tmem_ld_32x32b_x16(lanes + S::kAcc2Col + 32 * quarter + 16 * half, a2);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            float v[2];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+                                v[k] = fmaf(turn, __uint_as_float(a1[2 * j + k]), __uint_as_float(a2[2 * j + k])) * p.scale;
+                            o[8 * half + j] = total > 0 ? pack_bf16(v[0], v[1]) : 0u;
+                        }
+                    }
+                    store(&map_out1, 32 * quarter, o);
                 }
                 if (quarter == 3) {
                     p.ws.minus_lse2[(int64_t)head * p.ws.ld + own] = minus_lse2;
