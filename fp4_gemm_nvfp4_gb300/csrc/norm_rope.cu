@@ -30,9 +30,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-// Vectors per lane group and unit, and blocks per SM: forward, backward.
-constexpr int kVectors[2] = {2, 2};
-constexpr int kBlocks[2] = {5, 3};
+// Blocks per SM: forward with 2 and 3 vectors per lane group and unit, backward.
+__host__ __device__ constexpr int blocks_per_sm(bool backward, int vectors) {
+    return backward ? 3 : vectors == 3 ? 4 : 5;
+}
 
 struct NormRopeParams {
     NormRope a;
@@ -89,10 +90,9 @@ __device__ __forceinline__ void rotate(float* v, const float* c, const float* s)
     }
 }
 
-template <int kLanes, bool kInterleaved, bool kBackward>
-__global__ void __launch_bounds__(kThreads, kBlocks[kBackward]) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+template <int kLanes, bool kInterleaved, bool kBackward, int kVectors>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(kBackward, kVectors)) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
     constexpr uint32_t kGroups = 32 / kLanes;
-    constexpr int kUnroll = kVectors[kBackward];
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
     const uint32_t l = lane % kLanes, grp = lane / kLanes;
     const uint32_t D = (uint32_t)p.a.head_dim, rot = (uint32_t)p.a.rotary_dim;
@@ -120,12 +120,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks[kBackward]) norm_rope_kernel
     const uint32_t step_tokens = step / chunks, step_chunks = step % chunks;
     uint32_t chunk = at % chunks;
     for (int64_t token = at / chunks; token < p.a.tokens;) {
-        const uint32_t h0 = chunk * (kGroups * kUnroll) + grp;
+        const uint32_t h0 = chunk * (kGroups * kVectors) + grp;
         const uint16_t* x = qkv + token * p.a.ld_qkv;
         uint16_t* yt = y.data + token * y.ld_token;
-        Piece xv[kUnroll], dyv[kUnroll];
+        Piece xv[kVectors], dyv[kVectors];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
+        for (int u = 0; u < kVectors; ++u) {
             const uint32_t h = h0 + u * kGroups;
             xv[u] = dyv[u] = Piece{make_uint2(0, 0), make_uint2(0, 0)};
             if (live && h < heads) {
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks[kBackward]) norm_rope_kernel
             s[0] = ss.x, s[1] = ss.y, s[2] = ss.z, s[3] = ss.w;
         }
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
+        for (int u = 0; u < kVectors; ++u) {
             const uint32_t h = h0 + u * kGroups;
             float v[8];
             unpack(xv[u], v);
@@ -234,14 +234,14 @@ __global__ void __launch_bounds__(1024) norm_weight_kernel(const float* __restri
     }
 }
 
-template <int kLanes, bool kInterleaved, bool kBackward>
+template <int kLanes, bool kInterleaved, bool kBackward, int kVectors>
 cudaError_t launch_one(NormRopeParams& p, cudaStream_t stream) {
-    constexpr uint32_t kPerUnit = 32 / kLanes * kVectors[kBackward];
+    constexpr uint32_t kPerUnit = 32 / kLanes * kVectors;
     p.chunks[0] = ((uint32_t)p.a.q_heads + kPerUnit - 1) / kPerUnit;
     p.chunks[1] = ((uint32_t)p.a.kv_heads + kPerUnit - 1) / kPerUnit;
     // as many blocks as stay resident, or one per kWarps units where there are
     // fewer; queries and keys share them by their vectors
-    int64_t most = (int64_t)device_sm_count() * kBlocks[kBackward];
+    int64_t most = (int64_t)device_sm_count() * blocks_per_sm(kBackward, kVectors);
     if (most > kNormRopeMaxBlocks) most = kNormRopeMaxBlocks;
     auto blocks_for = [&](int which, int64_t share) {
         const int64_t need = (p.a.tokens * p.chunks[which] + kWarps - 1) / kWarps;
@@ -251,7 +251,7 @@ cudaError_t launch_one(NormRopeParams& p, cudaStream_t stream) {
     q_share = q_share < 1 ? 1 : (q_share > most - 1 ? most - 1 : q_share);
     p.q_blocks = (uint32_t)blocks_for(0, q_share);
     const uint32_t blocks = p.q_blocks + (uint32_t)blocks_for(1, most - q_share);
-    norm_rope_kernel<kLanes, kInterleaved, kBackward><<<blocks, kThreads, 0, stream>>>(p);
+    norm_rope_kernel<kLanes, kInterleaved, kBackward, kVectors><<<blocks, kThreads, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (kBackward && e == cudaSuccess) {
         const uint32_t D = (uint32_t)p.a.head_dim;
@@ -262,14 +262,27 @@ cudaError_t launch_one(NormRopeParams& p, cudaStream_t stream) {
     return e;
 }
 
+// Three vectors per lane group where the heads fill them as well as they fill
+// two: 24/12 heads of 128, 16384 tokens (us) forward 53.2 for 55.6, backward
+// 84 for 89; 16/4 heads of 64, which leave a third of them empty, 28 for 24.
+template <int kLanes, bool kInterleaved, bool kBackward>
+cudaError_t launch_vectors(NormRopeParams& p, cudaStream_t stream) {
+    auto places = [&](int vectors) {
+        const int per = 32 / kLanes * vectors;
+        return ((p.a.q_heads + per - 1) / per + (p.a.kv_heads + per - 1) / per) * per;
+    };
+    return places(3) <= places(2) ? launch_one<kLanes, kInterleaved, kBackward, 3>(p, stream)
+                                  : launch_one<kLanes, kInterleaved, kBackward, 2>(p, stream);
+}
+
 template <bool kInterleaved, bool kBackward>
 cudaError_t launch_lanes(NormRopeParams& p, cudaStream_t stream) {
     const int pieces = p.a.head_dim / 8;   // 8 dims per lane
-    if (pieces > 8) return launch_one<16, kInterleaved, kBackward>(p, stream);
-    if (pieces > 4) return launch_one<8, kInterleaved, kBackward>(p, stream);
-    if (pieces > 2) return launch_one<4, kInterleaved, kBackward>(p, stream);
-    if (pieces > 1) return launch_one<2, kInterleaved, kBackward>(p, stream);
-    return launch_one<1, kInterleaved, kBackward>(p, stream);
+    if (pieces > 8) return launch_vectors<16, kInterleaved, kBackward>(p, stream);
+    if (pieces > 4) return launch_vectors<8, kInterleaved, kBackward>(p, stream);
+    if (pieces > 2) return launch_one<4, kInterleaved, kBackward, 2>(p, stream);
+    if (pieces > 1) return launch_one<2, kInterleaved, kBackward, 2>(p, stream);
+    return launch_one<1, kInterleaved, kBackward, 2>(p, stream);
 }
 
 }  // namespace
