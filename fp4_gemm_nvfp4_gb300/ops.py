@@ -360,13 +360,14 @@ def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor, qkv: torch.Tensor,
     nbytes = capi.nvfp4_qk_norm_rope_backward_workspace_size(dim)
     if workspace is None or workspace.numel() < nbytes:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=qkv.device)
-    dw = torch.empty((2, dim), dtype=torch.float32, device=qkv.device)
+    dq_weight = torch.empty(dim, dtype=torch.float32, device=qkv.device)
+    dk_weight = torch.empty(dim, dtype=torch.float32, device=qkv.device)
     status = capi.nvfp4_qk_norm_rope_backward(
         _heads(dq, tokens, q_heads, dim, "dq"), _heads(dk, tokens, kv_heads, dim, "dk"), *args, dqkv.data_ptr(),
-        dqkv.stride(0) if tokens > 1 else dqkv.shape[1], dw.data_ptr(), dw.data_ptr() + 4 * dim,
+        dqkv.stride(0) if tokens > 1 else dqkv.shape[1], dq_weight.data_ptr(), dk_weight.data_ptr(),
         workspace.data_ptr(), workspace.numel(), stream_handle(stream))
     capi.check(status, "nvfp4_qk_norm_rope_backward")
-    return dqkv, dw[0], dw[1]
+    return dqkv, dq_weight, dk_weight
 
 
 def attention_spans(offsets: torch.Tensor, tokens: int, *, causal: bool = True, prefix: Optional[torch.Tensor] = None,
