@@ -314,6 +314,49 @@ def test_many_tiles_per_sm(HQ, HKV, D, causal):
     _check(*first, spans)
 
 
+# Enough heads that there are more pairs of query tiles than SMs: an item is two
+# tiles then (two heads that share their keys, or two tiles of one head), where
+# the few heads of the tests above give one tile whose keys are split.
+MANY_HEADS = [(128, 64, 64), (128, 64, 128), (100, 100, 64), (100, 100, 96), (69, 23, 128)]
+
+
+@pytest.mark.parametrize("HQ,HKV,D", MANY_HEADS)
+@pytest.mark.parametrize("softcap,bias", [(0.0, False), (5.0, False), (0.0, True), (5.0, True)])
+def test_pairs_of_tiles(HQ, HKV, D, softcap, bias):
+    """Intervals that differ between the two tiles of an item, empty rows, ends
+    outside [0, tokens), an odd number of tiles."""
+    T = 700 if HQ == 69 else 330
+    g = torch.Generator().manual_seed(4)
+    rows = []
+    for i in range(T):
+        kind = int(torch.randint(0, 5, (1,), generator=g))
+        a, b = sorted(torch.randint(0, T + 1, (2,), generator=g).tolist())
+        rows.append([(0, 0), (a, b), (max(0, i - 40), i + 1), (i, T + 7), (-5, i // 2)][kind])
+    slopes = torch.rand(HQ, generator=_gen(5), device="cuda") * 0.2 if bias else None
+    _check(*_inputs(T, HQ, HKV, D, 14), _spans(rows), softcap=softcap, slopes=slopes)
+    _check(*_inputs(T, HQ, HKV, D, 15), _causal(T), softcap=softcap, slopes=slopes)
+
+
+@pytest.mark.parametrize("junk", [math.nan, -math.inf])
+@pytest.mark.parametrize("HQ,HKV,D", MANY_HEADS)
+def test_pairs_of_tiles_masked_places(junk, HQ, HKV, D):
+    T, first, end = 700, 150, 600
+    q, k, v, do = _inputs(T, HQ, HKV, D, 22)
+    pad = torch.ones(T, dtype=torch.bool, device="cuda")
+    pad[first:end] = False
+    clean = [x.clone() for x in (q, k, v, do)]
+    for x in (q, k, v, do):
+        x[pad] = junk
+    spans = ops.attention_spans(torch.tensor([first, 260, end], dtype=torch.int32, device="cuda"), T)
+    o, lse = ops.attention(q, k, v, spans)
+    o2, lse2 = ops.attention(*clean[:3], spans)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2) and torch.isfinite(o).all()
+    got = ops.attention_backward(do, q, k, v, o, lse, spans)
+    want = ops.attention_backward(clean[3], *clean[:3], o2, lse2, spans)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b) and torch.isfinite(a).all()
+
+
 def test_no_tokens():
     q = torch.empty((0, 4, 64), dtype=torch.bfloat16, device="cuda")
     k = torch.empty((0, 2, 64), dtype=torch.bfloat16, device="cuda")
