@@ -547,15 +547,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (masked) {
                     if constexpr (kKeys) {
-                        // each lane makes one query's mask over the warp's 32 keys,
-                        // which the lanes then take in turn
+                        // each lane makes one query's mask over the warp's 32 keys:
+                        // turned about, a key's over the 32 queries
                         const int2 s = span_of(p.spans, x0 + 32 * (int)quarter + (int)lane, p.tokens);
                         const int k0 = own0 + (int)(warp & 3u) * 32;
-                        const int lo = min(max(s.x - k0, 0), 32), hi = min(max(s.y - k0, 0), 32);
-                        const uint32_t bits = lo < hi ? (0xFFFFFFFFu >> (32 - (hi - lo))) << lo : 0u;
+                        const uint32_t in = transpose_bits(bits_between(s.x - k0, s.y - k0), lane);
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if (!((__shfl_sync(0xFFFFFFFFu, bits, j) >> lane) & 1u)) e[j] = 0.0f;
+                            if (!(in & (1u << j))) e[j] = 0.0f;
                         // rows of queries without keys may hold anything (their P
                         // and dZ are 0): they are zeroed for the products
                         if (ts.all_hi == 0) {
@@ -569,10 +568,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             fence_proxy_async_smem();
                         }
                     } else {
-                        const int lo = span.x - x0 - 32 * (int)quarter, hi = span.y - x0 - 32 * (int)quarter;
+                        const uint32_t in = bits_between(span.x - x0 - 32 * (int)quarter, span.y - x0 - 32 * (int)quarter);
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if (j < lo || j >= hi) e[j] = 0.0f;
+                            if (!(in & (1u << j))) e[j] = 0.0f;
                         // so may keys that no row of the tile reads
                         if (quarter == 0 && (x0 < ts.lo || x0 + 128 > ts.hi)) {
                             const int key = x0 + (int)row;

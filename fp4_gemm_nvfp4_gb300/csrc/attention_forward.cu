@@ -418,8 +418,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (k0 < all_lo || k0 + 128 > all_hi) {
                     const int lo = span.x - k0, hi = span.y - k0;
 #pragma unroll
-                    for (int j = 0; j < 128; ++j)
-                        if (j < lo || j >= hi) s[j] = -INFINITY;
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t in = bits_between(lo - 32 * i, hi - 32 * i);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (!(in & (1u << j))) s[32 * i + j] = -INFINITY;
+                    }
                     // value rows that no row of the CTA reads may hold anything
                     // (their P is 0): they are zeroed for the product
                     if (k0 < cta_lo || k0 + 128 > cta_hi) {
