@@ -207,6 +207,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish();
     }
     tc_fence_before();
+    wait_for_prior_grid();
+    let_next_grid_start();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
@@ -454,8 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < kTurns; ++j) {
                 const int64_t r = own0 + row8 + kRows * j;
                 const bool on = r < p.tokens && dim < p.head_dim;
-                op[j] = on ? ld_nc_v4(o + r * p.out.ld_token) : make_uint4(0, 0, 0, 0);
-                dp[j] = on ? ld_nc_v4(d + r * p.dout.ld_token) : make_uint4(0, 0, 0, 0);
+                op[j] = on ? *reinterpret_cast<const uint4*>(o + r * p.out.ld_token) : make_uint4(0, 0, 0, 0);
+                dp[j] = on ? *reinterpret_cast<const uint4*>(d + r * p.dout.ld_token) : make_uint4(0, 0, 0, 0);
             }
             span = span_of(p.spans, own0 + row, p.tokens);
             if (own0 + row < p.tokens) lse = p.lse[(int64_t)item.head * p.tokens + own0 + row];
@@ -743,6 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // dv and dk from their parts, summed in the order of the splits: a thread
 // takes 8 dims of one head vector.
 __global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ Params p) {
+    wait_for_prior_grid();
     const uint32_t pieces = (uint32_t)p.head_dim / 8;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= p.tokens * p.heads * pieces) return;
@@ -851,9 +854,8 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
     p.timeout_ns = attention_timeout(&p.withhold);
     if ((uint64_t)p.tiles * (uint64_t)a.q_heads > 0x7FFFFFFFull) return cudaErrorInvalidValue;
     p.heads = a.q_heads;
-    attention_backward_kernel<kD, false><<<(unsigned)(p.tiles * a.q_heads), kThreads, Shape<kD>::kSmem, stream>>>(
-        mq, mdo, mk, mv, mdq, mdq, p);
-    e = cudaGetLastError();
+    e = launch_early(attention_backward_kernel<kD, false>, dim3((unsigned)(p.tiles * a.q_heads)), dim3(kThreads),
+                     Shape<kD>::kSmem, stream, mq, mdo, mk, mv, mdq, mdq, p);
     if (e != cudaSuccess) return e;
     p.timeout_ns = kAttentionTimeoutNs;
     p.withhold = 0;
@@ -863,13 +865,11 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
     p.xdv = extent_heads(a.dv, a.tokens, a.kv_heads, a.head_dim);
     p.xdk = extent_heads(a.dk, a.tokens, a.kv_heads, a.head_dim);
     p.splits = splits;
-    attention_backward_kernel<kD, true><<<(unsigned)(p.tiles * a.kv_heads * splits), kThreads, Shape<kD>::kSmem, stream>>>(
-        mk, mv, mq, mdo, mdv, mdk, p);
-    e = cudaGetLastError();
+    e = launch_early(attention_backward_kernel<kD, true>, dim3((unsigned)(p.tiles * a.kv_heads * splits)),
+                     dim3(kThreads), Shape<kD>::kSmem, stream, mk, mv, mq, mdo, mdv, mdk, p);
     if (e != cudaSuccess || splits == 1) return e;
     const int64_t pieces = a.tokens * a.kv_heads * (a.head_dim / 8);
-    join_parts_kernel<<<dim3((unsigned)((pieces + 255) / 256), 2), 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_early(join_parts_kernel, dim3((unsigned)((pieces + 255) / 256), 2), dim3(256), 0, stream, p);
 }
 
 }  // namespace

@@ -151,6 +151,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish();
     }
     tc_fence_before();
+    wait_for_prior_grid();
+    let_next_grid_start();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
@@ -630,8 +632,8 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
     p.timeout_ns = attention_timeout(&p.withhold);
     const uint64_t grid = (uint64_t)p.tiles * p.items_per_tile;
     if (grid > 0x7FFFFFFFull) return cudaErrorInvalidValue;
-    attention_forward_kernel<kD, kSplit><<<(unsigned)grid, kThreads, Shape<kD>::kSmem, stream>>>(mq, mk, mv, mo, p);
-    return cudaGetLastError();
+    return launch_early(attention_forward_kernel<kD, kSplit>, dim3((unsigned)grid), dim3(kThreads), Shape<kD>::kSmem,
+                        stream, mq, mk, mv, mo, p);
 }
 
 // Two tiles of 128 queries share their key tiles, which halves what comes

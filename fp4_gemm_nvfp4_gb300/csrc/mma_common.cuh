@@ -216,4 +216,33 @@ __device__ __forceinline__ bool warp_wait_or_abort(uint64_t* bar, uint32_t parit
     return __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar, parity, timeout_ns, abort_flag));
 }
 
+// A kernel launched by launch_early may start, and make its barriers and
+// tensor memory, while the kernel before it on the stream still runs, as soon
+// as every block of that one has called let_next_grid_start or ended.
+// wait_for_prior_grid ends when that one is complete and its writes are
+// visible: nothing of global memory is touched before it, and nothing that
+// another kernel may have written is read by non-coherent loads.
+__device__ __forceinline__ void wait_for_prior_grid() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_grid_start() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                         const Args&... args) {
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace nvfp4

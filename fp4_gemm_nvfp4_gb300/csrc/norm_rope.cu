@@ -27,6 +27,7 @@
 #include "bounds.cuh"
 #include "device_common.cuh"
 #include "kernels.h"
+#include "mma_common.cuh"
 
 namespace nvfp4 {
 namespace {
@@ -95,6 +96,7 @@ __device__ __forceinline__ void rotate(float* v, const float* c, const float* s)
 
 template <int kLanes, bool kInterleaved, bool kBackward, int kVectors>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(kBackward, kVectors)) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+    if constexpr (kBackward) let_next_grid_start();
     constexpr uint32_t kGroups = 32 / kLanes;
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
     const uint32_t l = lane % kLanes, grp = lane / kLanes;
@@ -218,9 +220,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(kBackward, kVectors)) 
 
 // dw = the blocks' shares summed in a fixed order: 32 outputs per block, 32
 // slices of the blocks each, then the slices.
-__global__ void __launch_bounds__(1024) norm_weight_kernel(const float* __restrict__ partials, uint32_t q_blocks,
+__global__ void __launch_bounds__(1024) norm_weight_kernel(const float* partials, uint32_t q_blocks,
                                                            uint32_t blocks, uint32_t D, float* dq_weight,
                                                            float* dk_weight) {
+    wait_for_prior_grid();
     __shared__ float sums[32][33];
     const bool k = blockIdx.y != 0;
     const uint32_t i = blockIdx.x * 32 + threadIdx.x, end = k ? blocks : q_blocks;
@@ -258,9 +261,8 @@ cudaError_t launch_one(NormRopeParams& p, cudaStream_t stream) {
     cudaError_t e = cudaGetLastError();
     if (kBackward && e == cudaSuccess) {
         const uint32_t D = (uint32_t)p.a.head_dim;
-        norm_weight_kernel<<<dim3((D + 31) / 32, 2), dim3(32, 32), 0, stream>>>(p.a.partials, p.q_blocks, blocks, D,
-                                                                                 p.a.dq_weight, p.a.dk_weight);
-        e = cudaGetLastError();
+        e = launch_early(norm_weight_kernel, dim3((D + 31) / 32, 2), dim3(32, 32), 0, stream, p.a.partials, p.q_blocks,
+                         blocks, D, p.a.dq_weight, p.a.dk_weight);
     }
     return e;
 }
