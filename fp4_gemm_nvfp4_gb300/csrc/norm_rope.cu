@@ -56,9 +56,9 @@ struct Piece {
     uint2 a, b;
 };
 
-__device__ __forceinline__ uint2 ld_nc_v2(const void* p) {
+__device__ __forceinline__ uint2 ld_v2(const void* p) {
     uint2 r;
-    asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+    asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
     return r;
 }
 
@@ -96,7 +96,8 @@ __device__ __forceinline__ void rotate(float* v, const float* c, const float* s)
 
 template <int kLanes, bool kInterleaved, bool kBackward, int kVectors>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(kBackward, kVectors)) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
-    if constexpr (kBackward) let_next_grid_start();
+    wait_for_prior_grid();
+    let_next_grid_start();
     constexpr uint32_t kGroups = 32 / kLanes;
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
     const uint32_t l = lane % kLanes, grp = lane / kLanes;
@@ -135,10 +136,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(kBackward, kVectors)) 
             xv[u] = dyv[u] = Piece{make_uint2(0, 0), make_uint2(0, 0)};
             if (live && h < heads) {
                 const uint16_t* from = x + h * D;
-                xv[u] = Piece{ld_nc_v2(from + da), ld_nc_v2(from + db)};
+                xv[u] = Piece{ld_v2(from + da), ld_v2(from + db)};
                 if constexpr (kBackward) {
                     const uint16_t* dy = yt + (int64_t)h * y.ld_head;
-                    dyv[u] = Piece{ld_nc_v2(dy + da), ld_nc_v2(dy + db)};
+                    dyv[u] = Piece{ld_v2(dy + da), ld_v2(dy + db)};
                 }
             }
         }
@@ -257,8 +258,8 @@ cudaError_t launch_one(NormRopeParams& p, cudaStream_t stream) {
     q_share = q_share < 1 ? 1 : (q_share > most - 1 ? most - 1 : q_share);
     p.q_blocks = (uint32_t)blocks_for(0, q_share);
     const uint32_t blocks = p.q_blocks + (uint32_t)blocks_for(1, most - q_share);
-    norm_rope_kernel<kLanes, kInterleaved, kBackward, kVectors><<<blocks, kThreads, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_early(norm_rope_kernel<kLanes, kInterleaved, kBackward, kVectors>, dim3(blocks),
+                                 dim3(kThreads), 0, stream, p);
     if (kBackward && e == cudaSuccess) {
         const uint32_t D = (uint32_t)p.a.head_dim;
         e = launch_early(norm_weight_kernel, dim3((D + 31) / 32, 2), dim3(32, 32), 0, stream, p.a.partials, p.q_blocks,
