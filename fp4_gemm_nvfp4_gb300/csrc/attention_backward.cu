@@ -134,7 +134,7 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float t) {
 }
 
 // kKeys: the CTA owns keys (dk, dv), else queries (dq).
-template <int kD, bool kKeys>
+template <int kD, bool kKeys, bool kCapped>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_backward_kernel(const __grid_constant__ CUtensorMap map_f1, const __grid_constant__ CUtensorMap map_f2,
                               const __grid_constant__ CUtensorMap map_x1, const __grid_constant__ CUtensorMap map_x2,
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = tmem + (((warp & 3u) * 32u) << 16);
         const uint32_t dp_at = lanes + S::kDpCol + 32 * quarter;
         const bool biased = p.slopes != nullptr;
-        const float c = p.sc.capped || biased ? 1.0f : p.sc.mult;
+        const float c = kCapped || biased ? 1.0f : p.sc.mult;
         uint32_t n = 0, results = 0;               // streamed tiles, items with a result so far
         bool ok = true;
         // dq: an item's delta~ is formed before the epilogue of the item before, 8
@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float e[32], damp[32];
                 tmem_ld_32x32b_x32(s_at, reinterpret_cast<uint32_t*>(e));
                 tmem_ld_wait();
-                if (p.sc.capped) {
+                if (kCapped) {
                     cap_scores<32>(e, p.sc);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (biased) {
-                    const float f = p.sc.capped ? 1.0f : p.sc.mult, d = (float)((int)own - x0 - 32 * (int)quarter);
+                    const float f = kCapped ? 1.0f : p.sc.mult, d = (float)((int)own - x0 - 32 * (int)quarter);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) e[j] = fmaf(-slope, fabsf(d - (float)j), e[j] * f);
                 }
@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 uint32_t pk[16];
-                if (!kKeys && p.sc.capped) {
+                if (!kKeys && kCapped) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(e[2 * j] * damp[2 * j], e[2 * j + 1] * damp[2 * j + 1]);
                 } else {
@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const uint64_t e2 = pair(e[half + j + k], e[half + j + k + 1]), g2 = pair(g[j + k], g[j + k + 1]);
                             if constexpr (!kKeys) exact2 = fma2(e2, g2, exact2);
                             uint64_t z = mul2(e2, add2(g2, k ? d.y : d.x));
-                            if (p.sc.capped) z = mul2(z, pair(damp[half + j + k], damp[half + j + k + 1]));
+                            if (kCapped) z = mul2(z, pair(damp[half + j + k], damp[half + j + k + 1]));
                             unpair(z, g[j + k], g[j + k + 1]);
                         }
                     }
@@ -774,20 +774,20 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__
 
 // As in the forward pass: a build whose launch has too few registers for the
 // groups' shares is not launched.
-template <int kD, bool kKeys>
+template <int kD, bool kKeys, bool kCapped>
 cudaError_t prepare_kernel() {
     static bool done[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (done[dev]) return cudaSuccess;
     cudaFuncAttributes f;
-    cudaError_t e = cudaFuncGetAttributes(&f, attention_backward_kernel<kD, kKeys>);
+    cudaError_t e = cudaFuncGetAttributes(&f, attention_backward_kernel<kD, kKeys, kCapped>);
     // the tiles' swizzle needs dynamic shared memory to start on 1024 bytes:
     // it does when there is no static shared memory before it
     if (e == cudaSuccess && (f.numRegs * kThreads < 128 * kControlRegs + 512 * kSoftmaxRegs || f.sharedSizeBytes != 0))
         e = cudaErrorInvalidConfiguration;
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(attention_backward_kernel<kD, kKeys>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(attention_backward_kernel<kD, kKeys, kCapped>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)Shape<kD>::kSmem);
     done[dev] = e == cudaSuccess;
     return e;
@@ -822,10 +822,10 @@ Workspace carve(float* base, int64_t tokens, int q_heads, int kv_heads, int head
     return w;
 }
 
-template <int kD>
+template <int kD, bool kCapped>
 cudaError_t launch(const Attention& a, cudaStream_t stream) {
-    cudaError_t e = prepare_kernel<kD, false>();
-    if (e == cudaSuccess) e = prepare_kernel<kD, true>();
+    cudaError_t e = prepare_kernel<kD, false, kCapped>();
+    if (e == cudaSuccess) e = prepare_kernel<kD, true, kCapped>();
     if (e != cudaSuccess) return e;
     CUtensorMap mq, mk, mv, mdo, mdq, mdk, mdv;
     if (!make_heads_map(&mq, a.q, a.tokens, a.q_heads, a.head_dim, 128) ||
@@ -854,7 +854,7 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
     p.timeout_ns = attention_timeout(&p.withhold);
     if ((uint64_t)p.tiles * (uint64_t)a.q_heads > 0x7FFFFFFFull) return cudaErrorInvalidValue;
     p.heads = a.q_heads;
-    e = launch_early(attention_backward_kernel<kD, false>, dim3((unsigned)(p.tiles * a.q_heads)), dim3(kThreads),
+    e = launch_early(attention_backward_kernel<kD, false, kCapped>, dim3((unsigned)(p.tiles * a.q_heads)), dim3(kThreads),
                      Shape<kD>::kSmem, stream, mq, mdo, mk, mv, mdq, mdq, p);
     if (e != cudaSuccess) return e;
     p.timeout_ns = kAttentionTimeoutNs;
@@ -865,7 +865,7 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
     p.xdv = extent_heads(a.dv, a.tokens, a.kv_heads, a.head_dim);
     p.xdk = extent_heads(a.dk, a.tokens, a.kv_heads, a.head_dim);
     p.splits = splits;
-    e = launch_early(attention_backward_kernel<kD, true>, dim3((unsigned)(p.tiles * a.kv_heads * splits)),
+    e = launch_early(attention_backward_kernel<kD, true, kCapped>, dim3((unsigned)(p.tiles * a.kv_heads * splits)),
                      dim3(kThreads), Shape<kD>::kSmem, stream, mk, mv, mq, mdo, mdv, mdk, p);
     if (e != cudaSuccess || splits == 1) return e;
     const int64_t pieces = a.tokens * a.kv_heads * (a.head_dim / 8);
@@ -881,7 +881,8 @@ size_t attention_backward_workspace_bytes(int64_t tokens, int q_heads, int kv_he
 }
 
 cudaError_t launch_attention_backward(const Attention& a, cudaStream_t stream) {
-    return a.head_dim <= 64 ? launch<64>(a, stream) : launch<128>(a, stream);
+    if (a.softcap > 0.0f) return a.head_dim <= 64 ? launch<64, true>(a, stream) : launch<128, true>(a, stream);
+    return a.head_dim <= 64 ? launch<64, false>(a, stream) : launch<128, false>(a, stream);
 }
 
 cudaError_t attention_backward_bounds_read_and_clear(uint64_t* n) { return bounds_read_and_clear_local(n); }

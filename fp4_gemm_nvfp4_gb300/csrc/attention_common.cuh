@@ -70,11 +70,13 @@ inline cudaError_t attention_status_read_and_clear_local(unsigned int* status) {
 // Chebyshev points: relative error 3e-8.
 constexpr float kSmallCap = 0.75f;
 constexpr int kCapTerms = 6;
+// ... and on [0, 0.375^2]: 6e-8.
+constexpr float kTinyCap = 0.375f;
+constexpr int kTinyTerms = 4;
 
 struct Scores {
-    float mult, cap_log2, over_cap, kappa, small;   // kappa = scale / cap, small = kSmallCap / kappa
-    float poly[kCapTerms];                          // times cap_log2
-    int capped;
+    float mult, cap_log2, over_cap, kappa, small, tiny;   // kappa = scale / cap, small = kSmallCap / kappa, ...
+    float poly[kCapTerms], tiny_poly[kTinyTerms];         // times cap_log2
 };
 
 inline Scores make_scores(float scale, float softcap) {
@@ -85,14 +87,16 @@ inline Scores make_scores(float scale, float softcap) {
     }
     const double c[kCapTerms] = {0.9999999704657849,    -0.33332954098406786, 0.1332533884815183,
                                  -0.053341115329099964, 0.019576216425263346, -0.004711522234826275};
+    const double t[kTinyTerms] = {0.9999999402412297, -0.33331971067426597, 0.13284431227543994, -0.04826890785276893};
     const double cap_log2 = (double)softcap * (double)kLog2e, kappa = (double)scale / softcap;
     s.mult = (float)(2.0 * (double)kLog2e * kappa);
     s.cap_log2 = (float)cap_log2;
     s.over_cap = (float)(1.0 / cap_log2);
     s.kappa = (float)kappa;
     s.small = (float)(kSmallCap / kappa);
+    s.tiny = (float)(kTinyCap / kappa);
+    for (int i = 0; i < kTinyTerms; ++i) s.tiny_poly[i] = (float)(cap_log2 * t[i]);
     for (int i = 0; i < kCapTerms; ++i) s.poly[i] = (float)(cap_log2 * c[i]);
-    s.capped = 1;
     return s;
 }
 
@@ -122,26 +126,33 @@ __device__ __forceinline__ void cap_inverse_x4(float* v, float mult) {
     v[3] = rcd * d[2];
 }
 
+template <int kN, int kTerms>
+__device__ __forceinline__ void cap_polynomial(float* s, float kappa, const float* poly) {
+    const uint64_t kappa2 = pair(kappa, kappa);
+    uint64_t c[kTerms];
+#pragma unroll
+    for (int i = 0; i < kTerms; ++i) c[i] = pair(poly[i], poly[i]);
+#pragma unroll
+    for (int j = 0; j < kN; j += 2) {
+        const uint64_t u = mul2(pair(s[j], s[j + 1]), kappa2), w = mul2(u, u);
+        uint64_t r = c[kTerms - 1];
+#pragma unroll
+        for (int i = kTerms - 2; i >= 0; --i) r = fma2(r, w, c[i]);
+        unpair(mul2(r, u), s[j], s[j + 1]);
+    }
+}
+
 // kN products of a lane's row to capped scores; a warp whose products are all
-// small takes the polynomial alone.
+// small takes a polynomial alone, the shorter one where it can.
 template <int kN>
 __device__ __forceinline__ void cap_scores(float* s, const Scores& sc) {
     float top = 0.0f;
 #pragma unroll
     for (int j = 0; j < kN; j += 2) top = max3(top, fabsf(s[j]), fabsf(s[j + 1]));
-    if (!__any_sync(0xFFFFFFFFu, top > sc.small)) {
-        const uint64_t kappa = pair(sc.kappa, sc.kappa);
-        uint64_t c[kCapTerms];
-#pragma unroll
-        for (int i = 0; i < kCapTerms; ++i) c[i] = pair(sc.poly[i], sc.poly[i]);
-#pragma unroll
-        for (int j = 0; j < kN; j += 2) {
-            const uint64_t u = mul2(pair(s[j], s[j + 1]), kappa), w = mul2(u, u);
-            uint64_t r = c[kCapTerms - 1];
-#pragma unroll
-            for (int i = kCapTerms - 2; i >= 0; --i) r = fma2(r, w, c[i]);
-            unpair(mul2(r, u), s[j], s[j + 1]);
-        }
+    if (!__any_sync(0xFFFFFFFFu, top > sc.tiny)) {
+        cap_polynomial<kN, kTinyTerms>(s, sc.kappa, sc.tiny_poly);
+    } else if (!__any_sync(0xFFFFFFFFu, top > sc.small)) {
+        cap_polynomial<kN, kCapTerms>(s, sc.kappa, sc.poly);
     } else {
 #pragma unroll
         for (int j = 0; j < kN; j += 4) {

@@ -89,8 +89,9 @@ struct Ring {
     uint32_t slot = 0, phase = 0;
 };
 
-// kSplit: an item is one tile twice, with the key tiles in turn.
-template <int kD, bool kSplit>
+// kSplit: an item is one tile twice, with the key tiles in turn.  kCapped: the
+// cap's code in the same kernel would cost the scores without one 2 %.
+template <int kD, bool kSplit, bool kCapped>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                              const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o,
@@ -374,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = tmem + (((warp & 3u) * 32u) << 16);
         const uint32_t s_at = lanes + kScoreCol + 128 * x, o_at = lanes + kOutCol + 128 * x;
         uint8_t* stage = smem + S::kStageAt + (warp - kFirstSoftmaxWarp) * 4096;
-        const bool plain = !p.sc.capped && !p.slopes;
+        const bool plain = !kCapped && !p.slopes;
         const float c = plain ? p.sc.mult : 1.0f;      // scores in registers times c are in log2
         float* joint = reinterpret_cast<float*>(smem + S::kJointAt);   // [2][128]
         uint32_t s_phase = 0, o_phase = 0, join_phase = 0, n = 0;      // n: stages of the CTA so far
@@ -411,9 +412,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(s_at + 32 * i, r + 32 * i);
                     tmem_ld_wait();
                 }
-                if (p.sc.capped) cap_scores<128>(s, p.sc);
+                if (kCapped) cap_scores<128>(s, p.sc);
                 if (p.slopes) {
-                    const float f = p.sc.capped ? 1.0f : p.sc.mult, d = (float)((int)token - k0);
+                    const float f = kCapped ? 1.0f : p.sc.mult, d = (float)((int)token - k0);
 #pragma unroll
                     for (int j = 0; j < 128; ++j) s[j] = fmaf(-slope, fabsf(d - (float)j), s[j] * f);
                 }
@@ -587,28 +588,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 // The warp groups trade registers against the launch's 168 per thread:
 // 128 * 80 + 256 * 208 = 63488 <= 384 * 168; a build that was given fewer is
 // not launched (setmaxnreg.inc would wait forever).
-template <int kD, bool kSplit>
+template <int kD, bool kSplit, bool kCapped>
 cudaError_t prepare_kernel() {
     static bool done[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (done[dev]) return cudaSuccess;
     cudaFuncAttributes f;
-    cudaError_t e = cudaFuncGetAttributes(&f, attention_forward_kernel<kD, kSplit>);
+    cudaError_t e = cudaFuncGetAttributes(&f, attention_forward_kernel<kD, kSplit, kCapped>);
     // the tiles' swizzle needs dynamic shared memory to start on 1024 bytes:
     // it does when there is no static shared memory before it
     if (e == cudaSuccess && (f.numRegs * kThreads < 128 * 80 + 256 * 208 || f.sharedSizeBytes != 0))
         e = cudaErrorInvalidConfiguration;
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(attention_forward_kernel<kD, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(attention_forward_kernel<kD, kSplit, kCapped>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)Shape<kD>::kSmem);
     done[dev] = e == cudaSuccess;
     return e;
 }
 
-template <int kD, bool kSplit>
+template <int kD, bool kSplit, bool kCapped>
 cudaError_t launch(const Attention& a, cudaStream_t stream) {
-    cudaError_t e = prepare_kernel<kD, kSplit>();
+    cudaError_t e = prepare_kernel<kD, kSplit, kCapped>();
     if (e != cudaSuccess) return e;
     CUtensorMap mq, mk, mv, mo;
     if (!make_heads_map(&mq, a.q, a.tokens, a.q_heads, a.head_dim, 128) ||
@@ -632,7 +633,7 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
     p.timeout_ns = attention_timeout(&p.withhold);
     const uint64_t grid = (uint64_t)p.tiles * p.items_per_tile;
     if (grid > 0x7FFFFFFFull) return cudaErrorInvalidValue;
-    return launch_early(attention_forward_kernel<kD, kSplit>, dim3((unsigned)grid), dim3(kThreads), Shape<kD>::kSmem,
+    return launch_early(attention_forward_kernel<kD, kSplit, kCapped>, dim3((unsigned)grid), dim3(kThreads), Shape<kD>::kSmem,
                         stream, mq, mk, mv, mo, p);
 }
 
@@ -644,17 +645,19 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
 // cap and bias, 40 pairs: 73 and 42; 4096 tokens, 8/2 heads of 128, 128 pairs:
 // 55 and 42; 2560 tokens, 16/4 heads, 160 pairs: 39 and 39), from 192 slower
 // (2048 tokens, 24/12 heads: 33 and 41).
-template <int kD>
+template <int kD, bool kCapped>
 cudaError_t launch_dim(const Attention& a, cudaStream_t stream) {
     const int64_t t128 = (a.tokens + 127) / 128;
     const int64_t pairs = (a.q_heads / a.kv_heads) % 2 == 0 ? t128 * (a.q_heads / 2) : (t128 + 1) / 2 * a.q_heads;
-    return 8 * pairs <= 9 * (int64_t)device_sm_count() ? launch<kD, true>(a, stream) : launch<kD, false>(a, stream);
+    return 8 * pairs <= 9 * (int64_t)device_sm_count() ? launch<kD, true, kCapped>(a, stream)
+                                                    : launch<kD, false, kCapped>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_attention(const Attention& a, cudaStream_t stream) {
-    return a.head_dim <= 64 ? launch_dim<64>(a, stream) : launch_dim<128>(a, stream);
+    if (a.softcap > 0.0f) return a.head_dim <= 64 ? launch_dim<64, true>(a, stream) : launch_dim<128, true>(a, stream);
+    return a.head_dim <= 64 ? launch_dim<64, false>(a, stream) : launch_dim<128, false>(a, stream);
 }
 
 void arm_attention_forward_fault(uint64_t timeout_ns) { g_attention_armed_ns.store(timeout_ns); }
