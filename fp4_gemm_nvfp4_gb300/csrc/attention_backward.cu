@@ -134,13 +134,14 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float t) {
 }
 
 // kKeys: the CTA owns keys (dk, dv), else queries (dq).
-template <int kD, bool kKeys, bool kCapped>
+template <int kD, bool kKeys, int kForm>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_backward_kernel(const __grid_constant__ CUtensorMap map_f1, const __grid_constant__ CUtensorMap map_f2,
                               const __grid_constant__ CUtensorMap map_x1, const __grid_constant__ CUtensorMap map_x2,
                               const __grid_constant__ CUtensorMap map_out1,
                               const __grid_constant__ CUtensorMap map_out2, const __grid_constant__ Params p) {
     using S = Shape<kD>;
+    constexpr bool kCapped = (kForm & kCapBit) != 0, kBiased = (kForm & kBiasBit) != 0;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* ring = smem + 2 * S::kTile;
     float* vec = reinterpret_cast<float*>(smem + S::kVecAt);     // [kPairs][lse2, delta][128] of the streamed rows
@@ -436,8 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t row = (warp & 3u) * 32 + lane;                     // ... of this row
         const uint32_t lanes = tmem + (((warp & 3u) * 32u) << 16);
         const uint32_t dp_at = lanes + S::kDpCol + 32 * quarter;
-        const bool biased = p.slopes != nullptr;
-        const float c = kCapped || biased ? 1.0f : p.sc.mult;
+        const float c = kCapped || kBiased ? 1.0f : p.sc.mult;
         uint32_t n = 0, results = 0;               // streamed tiles, items with a result so far
         bool ok = true;
         // dq: an item's delta~ is formed before the epilogue of the item before, 8
@@ -503,8 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < total; ++i, ++n) {
                 const int x0 = t * 128;                    // first streamed row
                 const uint32_t n2 = 2 * n + 1;             // X2's place among the loads
-                float slope = 0.0f;
-                if (biased) slope = p.slopes[kKeys ? h : head] * kLog2e;
+                const float slope = kBiased ? p.slopes[kKeys ? h : head] * kLog2e : 0.0f;
                 if constexpr (kKeys) ts = p.ws.spans[t];
                 const bool masked = kKeys ? (own0 < ts.all_lo || own0 + 128 > ts.all_hi)
                                           : (x0 < ts.all_lo || x0 + 128 > ts.all_hi);
@@ -528,11 +527,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         damp[j] = fmaf(-th, th, 1.0f);
                     }
                 }
-                if (biased) {
-                    const float f = kCapped ? 1.0f : p.sc.mult, d = (float)((int)own - x0 - 32 * (int)quarter);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) e[j] = fmaf(-slope, fabsf(d - (float)j), e[j] * f);
-                }
+                if (kBiased)
+                    add_bias<32, kCapped>(e, p.sc.mult, slope, (float)((int)own - x0 - 32 * (int)quarter), own0 - x0);
                 {
                     const uint64_t c2 = pair(c, c), own2 = pair(minus_lse2, minus_lse2);
 #pragma unroll
@@ -774,20 +770,20 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__
 
 // As in the forward pass: a build whose launch has too few registers for the
 // groups' shares is not launched.
-template <int kD, bool kKeys, bool kCapped>
+template <int kD, bool kKeys, int kForm>
 cudaError_t prepare_kernel() {
     static bool done[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (done[dev]) return cudaSuccess;
     cudaFuncAttributes f;
-    cudaError_t e = cudaFuncGetAttributes(&f, attention_backward_kernel<kD, kKeys, kCapped>);
+    cudaError_t e = cudaFuncGetAttributes(&f, attention_backward_kernel<kD, kKeys, kForm>);
     // the tiles' swizzle needs dynamic shared memory to start on 1024 bytes:
     // it does when there is no static shared memory before it
     if (e == cudaSuccess && (f.numRegs * kThreads < 128 * kControlRegs + 512 * kSoftmaxRegs || f.sharedSizeBytes != 0))
         e = cudaErrorInvalidConfiguration;
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(attention_backward_kernel<kD, kKeys, kCapped>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(attention_backward_kernel<kD, kKeys, kForm>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)Shape<kD>::kSmem);
     done[dev] = e == cudaSuccess;
     return e;
@@ -822,10 +818,10 @@ Workspace carve(float* base, int64_t tokens, int q_heads, int kv_heads, int head
     return w;
 }
 
-template <int kD, bool kCapped>
+template <int kD, int kForm>
 cudaError_t launch(const Attention& a, cudaStream_t stream) {
-    cudaError_t e = prepare_kernel<kD, false, kCapped>();
-    if (e == cudaSuccess) e = prepare_kernel<kD, true, kCapped>();
+    cudaError_t e = prepare_kernel<kD, false, kForm>();
+    if (e == cudaSuccess) e = prepare_kernel<kD, true, kForm>();
     if (e != cudaSuccess) return e;
     CUtensorMap mq, mk, mv, mdo, mdq, mdk, mdv;
     if (!make_heads_map(&mq, a.q, a.tokens, a.q_heads, a.head_dim, 128) ||
@@ -854,7 +850,7 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
     p.timeout_ns = attention_timeout(&p.withhold);
     if ((uint64_t)p.tiles * (uint64_t)a.q_heads > 0x7FFFFFFFull) return cudaErrorInvalidValue;
     p.heads = a.q_heads;
-    e = launch_early(attention_backward_kernel<kD, false, kCapped>, dim3((unsigned)(p.tiles * a.q_heads)), dim3(kThreads),
+    e = launch_early(attention_backward_kernel<kD, false, kForm>, dim3((unsigned)(p.tiles * a.q_heads)), dim3(kThreads),
                      Shape<kD>::kSmem, stream, mq, mdo, mk, mv, mdq, mdq, p);
     if (e != cudaSuccess) return e;
     p.timeout_ns = kAttentionTimeoutNs;
@@ -865,7 +861,7 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
     p.xdv = extent_heads(a.dv, a.tokens, a.kv_heads, a.head_dim);
     p.xdk = extent_heads(a.dk, a.tokens, a.kv_heads, a.head_dim);
     p.splits = splits;
-    e = launch_early(attention_backward_kernel<kD, true, kCapped>, dim3((unsigned)(p.tiles * a.kv_heads * splits)),
+    e = launch_early(attention_backward_kernel<kD, true, kForm>, dim3((unsigned)(p.tiles * a.kv_heads * splits)),
                      dim3(kThreads), Shape<kD>::kSmem, stream, mk, mv, mq, mdo, mdv, mdk, p);
     if (e != cudaSuccess || splits == 1) return e;
     const int64_t pieces = a.tokens * a.kv_heads * (a.head_dim / 8);
@@ -881,8 +877,11 @@ size_t attention_backward_workspace_bytes(int64_t tokens, int q_heads, int kv_he
 }
 
 cudaError_t launch_attention_backward(const Attention& a, cudaStream_t stream) {
-    if (a.softcap > 0.0f) return a.head_dim <= 64 ? launch<64, true>(a, stream) : launch<128, true>(a, stream);
-    return a.head_dim <= 64 ? launch<64, false>(a, stream) : launch<128, false>(a, stream);
+    auto launch_form = [&](auto form) {
+        return a.head_dim <= 64 ? launch<64, decltype(form)::value>(a, stream)
+                                : launch<128, decltype(form)::value>(a, stream);
+    };
+    return with_form(a.softcap, a.slopes, launch_form);
 }
 
 cudaError_t attention_backward_bounds_read_and_clear(uint64_t* n) { return bounds_read_and_clear_local(n); }

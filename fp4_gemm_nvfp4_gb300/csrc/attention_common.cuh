@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "bounds.cuh"
 #include "mma_common.cuh"
@@ -56,6 +57,18 @@ inline cudaError_t attention_status_read_and_clear_local(unsigned int* status) {
     if (e == cudaSuccess && v) e = cudaMemcpyToSymbol(g_attention_status, &zero, sizeof zero);
     *status |= v;
     return e;
+}
+
+// What a kernel's scores are made of, as a template argument: code that another
+// form needs costs every form (the cap's 1 % forward, 12 % backward with 64 dims).
+constexpr int kCapBit = 1, kBiasBit = 2;
+template <typename F>
+cudaError_t with_form(float softcap, const float* slopes, F&& launch) {
+    const bool capped = softcap > 0.0f;
+    if (capped && slopes) return launch(std::integral_constant<int, kCapBit | kBiasBit>{});
+    if (capped) return launch(std::integral_constant<int, kCapBit>{});
+    if (slopes) return launch(std::integral_constant<int, kBiasBit>{});
+    return launch(std::integral_constant<int, 0>{});
 }
 
 // How a product q.k becomes a score in units of log2 (exp becomes ex2), with
@@ -124,6 +137,36 @@ __device__ __forceinline__ void cap_inverse_x4(float* v, float mult) {
     v[1] = rab * d[0];
     v[2] = rcd * d[3];
     v[3] = rcd * d[2];
+}
+
+// s f - slope |d - j| over kN columns j of a lane's row; apart is the distance
+// of the tiles' first rows and columns.  Off the diagonal the distance has one
+// sign for the whole tile, and the bias takes two packed operations per pair
+// (a constant of its own for every pair would take two moves more).  Capped
+// scores (f = 1) are as well off with the one form (8192 tokens, 16/4 heads of
+// 128: 336 us, 350 with both).
+template <int kN, bool kCapped>
+__device__ __forceinline__ void add_bias(float* s, float f, float slope, float d, int apart) {
+    if (kCapped || apart == 0) {
+#pragma unroll
+        for (int j = 0; j < kN; ++j) s[j] = fmaf(-slope, fabsf(d - (float)j), kCapped ? s[j] : s[j] * f);
+    } else {
+        const float g = apart > 0 ? slope : -slope, at = -g * d;
+        const uint64_t f2 = pair(f, f);
+        uint64_t step[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) step[i] = pair(g * (float)(2 * i), g * (float)(2 * i + 1));
+#pragma unroll
+        for (int j = 0; j < kN; j += 8) {
+            const float base = fmaf(g, (float)j, at);
+            const uint64_t base2 = pair(base, base);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int k = j + 2 * i;
+                unpair(fma2(pair(s[k], s[k + 1]), f2, add2(step[i], base2)), s[k], s[k + 1]);
+            }
+        }
+    }
 }
 
 template <int kN, int kTerms>

@@ -89,14 +89,15 @@ struct Ring {
     uint32_t slot = 0, phase = 0;
 };
 
-// kSplit: an item is one tile twice, with the key tiles in turn.  kCapped: the
-// cap's code in the same kernel would cost the scores without one 2 %.
-template <int kD, bool kSplit, bool kCapped>
+// kSplit: an item is one tile twice, with the key tiles in turn.  kForm: what
+// the scores are made of.
+template <int kD, bool kSplit, int kForm>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                              const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o,
                              const __grid_constant__ Params p) {
     using S = Shape<kD>;
+    constexpr bool kCapped = (kForm & kCapBit) != 0, kBiased = (kForm & kBiasBit) != 0;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* ring = smem + 2 * S::kTile;
     Item* items = reinterpret_cast<Item*>(smem + S::kBarAt);     // [2] the current and the next
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = tmem + (((warp & 3u) * 32u) << 16);
         const uint32_t s_at = lanes + kScoreCol + 128 * x, o_at = lanes + kOutCol + 128 * x;
         uint8_t* stage = smem + S::kStageAt + (warp - kFirstSoftmaxWarp) * 4096;
-        const bool plain = !kCapped && !p.slopes;
+        constexpr bool plain = !kCapped && !kBiased;
         const float c = plain ? p.sc.mult : 1.0f;      // scores in registers times c are in log2
         float* joint = reinterpret_cast<float*>(smem + S::kJointAt);   // [2][128]
         uint32_t s_phase = 0, o_phase = 0, join_phase = 0, n = 0;      // n: stages of the CTA so far
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!valid) break;
             const int64_t token = (int64_t)tile * 128 + row;
             const int2 span = span_of(p.spans, token, p.tokens);
-            const float slope = p.slopes ? p.slopes[head] * kLog2e : 0.0f;
+            const float slope = kBiased ? p.slopes[head] * kLog2e : 0.0f;
             float m = -INFINITY, l = 0.0f;             // maximum (log2) that P and O are scaled by; sum
             const int end = max(last, last2);
             for (int kt = min(first, first2); kt < end; ++kt) {
@@ -413,11 +414,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld_wait();
                 }
                 if (kCapped) cap_scores<128>(s, p.sc);
-                if (p.slopes) {
-                    const float f = kCapped ? 1.0f : p.sc.mult, d = (float)((int)token - k0);
-#pragma unroll
-                    for (int j = 0; j < 128; ++j) s[j] = fmaf(-slope, fabsf(d - (float)j), s[j] * f);
-                }
+                if (kBiased)
+                    add_bias<128, kCapped>(s, p.sc.mult, slope, (float)((int)token - k0), tile * 128 - k0);
                 if (k0 < all_lo || k0 + 128 > all_hi) {
                     const int lo = span.x - k0, hi = span.y - k0;
 #pragma unroll
@@ -588,28 +586,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 // The warp groups trade registers against the launch's 168 per thread:
 // 128 * 80 + 256 * 208 = 63488 <= 384 * 168; a build that was given fewer is
 // not launched (setmaxnreg.inc would wait forever).
-template <int kD, bool kSplit, bool kCapped>
+template <int kD, bool kSplit, int kForm>
 cudaError_t prepare_kernel() {
     static bool done[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (done[dev]) return cudaSuccess;
     cudaFuncAttributes f;
-    cudaError_t e = cudaFuncGetAttributes(&f, attention_forward_kernel<kD, kSplit, kCapped>);
+    cudaError_t e = cudaFuncGetAttributes(&f, attention_forward_kernel<kD, kSplit, kForm>);
     // the tiles' swizzle needs dynamic shared memory to start on 1024 bytes:
     // it does when there is no static shared memory before it
     if (e == cudaSuccess && (f.numRegs * kThreads < 128 * 80 + 256 * 208 || f.sharedSizeBytes != 0))
         e = cudaErrorInvalidConfiguration;
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(attention_forward_kernel<kD, kSplit, kCapped>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(attention_forward_kernel<kD, kSplit, kForm>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)Shape<kD>::kSmem);
     done[dev] = e == cudaSuccess;
     return e;
 }
 
-template <int kD, bool kSplit, bool kCapped>
+template <int kD, bool kSplit, int kForm>
 cudaError_t launch(const Attention& a, cudaStream_t stream) {
-    cudaError_t e = prepare_kernel<kD, kSplit, kCapped>();
+    cudaError_t e = prepare_kernel<kD, kSplit, kForm>();
     if (e != cudaSuccess) return e;
     CUtensorMap mq, mk, mv, mo;
     if (!make_heads_map(&mq, a.q, a.tokens, a.q_heads, a.head_dim, 128) ||
@@ -633,7 +631,7 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
     p.timeout_ns = attention_timeout(&p.withhold);
     const uint64_t grid = (uint64_t)p.tiles * p.items_per_tile;
     if (grid > 0x7FFFFFFFull) return cudaErrorInvalidValue;
-    return launch_early(attention_forward_kernel<kD, kSplit, kCapped>, dim3((unsigned)grid), dim3(kThreads), Shape<kD>::kSmem,
+    return launch_early(attention_forward_kernel<kD, kSplit, kForm>, dim3((unsigned)grid), dim3(kThreads), Shape<kD>::kSmem,
                         stream, mq, mk, mv, mo, p);
 }
 
@@ -645,19 +643,22 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
 // cap and bias, 40 pairs: 73 and 42; 4096 tokens, 8/2 heads of 128, 128 pairs:
 // 55 and 42; 2560 tokens, 16/4 heads, 160 pairs: 39 and 39), from 192 slower
 // (2048 tokens, 24/12 heads: 33 and 41).
-template <int kD, bool kCapped>
+template <int kD, int kForm>
 cudaError_t launch_dim(const Attention& a, cudaStream_t stream) {
     const int64_t t128 = (a.tokens + 127) / 128;
     const int64_t pairs = (a.q_heads / a.kv_heads) % 2 == 0 ? t128 * (a.q_heads / 2) : (t128 + 1) / 2 * a.q_heads;
-    return 8 * pairs <= 9 * (int64_t)device_sm_count() ? launch<kD, true, kCapped>(a, stream)
-                                                    : launch<kD, false, kCapped>(a, stream);
+    return 8 * pairs <= 9 * (int64_t)device_sm_count() ? launch<kD, true, kForm>(a, stream)
+                                                    : launch<kD, false, kForm>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_attention(const Attention& a, cudaStream_t stream) {
-    if (a.softcap > 0.0f) return a.head_dim <= 64 ? launch_dim<64, true>(a, stream) : launch_dim<128, true>(a, stream);
-    return a.head_dim <= 64 ? launch_dim<64, false>(a, stream) : launch_dim<128, false>(a, stream);
+    auto launch_form = [&](auto form) {
+        return a.head_dim <= 64 ? launch_dim<64, decltype(form)::value>(a, stream)
+                                : launch_dim<128, decltype(form)::value>(a, stream);
+    };
+    return with_form(a.softcap, a.slopes, launch_form);
 }
 
 void arm_attention_forward_fault(uint64_t timeout_ns) { g_attention_armed_ns.store(timeout_ns); }
