@@ -28,11 +28,12 @@
 // forward pass a CTA goes on to blocks that have not started.
 //
 // Eight products are made where five are counted (S and dP twice, P' k): 8192
-// causal tokens, 24/12 heads of 128: dq 512 us + dk dv 485 us, 1025 TFLOP/s
-// of the five, 1640 of the eight (83 % of a BF16 library GEMM); 32768 tokens
-// 1040.  4 x 2048 tokens: 168 + 145 us (the masked tiles, and 4 us from each
-// dq tile's last scores to the next one's first, most of it reading its out
-// and dout beside the TMA loads).  64 dims: 770 us.
+// causal tokens, 24/12 heads of 128: 957 us (dq and dk dv about half each),
+// 1075 TFLOP/s of the five, 1720 of the eight (87 % of a BF16 library GEMM).
+// 4 x 2048 tokens: 297 us (the masked tiles, and 4 us from each dq tile's last
+// scores to the next one's first, most of it reading its out and dout beside
+// the TMA loads).  64 dims: 665 us.  16/4 heads: 655-675 us, 900 with a cap of
+// 30, 719 with the bias, 954 with both.
 #include <algorithm>
 
 #include <cuda.h>

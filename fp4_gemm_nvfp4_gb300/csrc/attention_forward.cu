@@ -21,12 +21,12 @@
 // and the FP32 sums hold as precisely, and the factor cancels in O / sum.
 //
 // Bound by the tensor cores' wait for the softmax: 8192 causal tokens, 24/12
-// heads of 128: 257 us, 1600 TFLOP/s of the pairs' work (81 % of a BF16
-// library GEMM); 32768 tokens 1670 TFLOP/s.  4 x 2048 tokens: 88 us, 1170
-// TFLOP/s (the masked tiles, and 1.8 us from each item's last scores to the
-// next one's first).  64 dims: 223-235 us (the same softmax for half the
-// products).  A cap of 30, 16/4 heads: 293 us, 935 TFLOP/s (the cap's 9 FMAs
-// and more per score).
+// heads of 128: 248 us, 1660 TFLOP/s of the pairs' work (84 % of a BF16
+// library GEMM); 32768 tokens 1690 TFLOP/s.  4 x 2048 tokens: 81 us, 1275
+// TFLOP/s (the masked tiles, and 1.5 us from each item's last scores to the
+// next one's first).  64 dims: 213-225 us (the same softmax for half the
+// products).  16/4 heads: 168 us, 250 with a cap of 30 (the polynomial and its
+// check, 5 operations per score), 248 with the bias, 340 with both.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
