@@ -292,6 +292,11 @@ def _new_heads(tokens: int, heads: int, dim: int, device) -> Tuple[torch.Tensor,
     return x, capi.nvfp4_heads(x.data_ptr(), heads * dim, dim)
 
 
+def _check_on_gpu(on_gpu: bool) -> None:
+    if not on_gpu:
+        raise ValueError("CUDA tensors expected, got one on the host")
+
+
 def _check_float32(t: torch.Tensor, shape, what: str) -> None:
     if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what}: contiguous float32 {list(shape)} expected, got {t.dtype} {list(t.shape)}")
@@ -337,6 +342,8 @@ def qk_norm_rope(qkv: torch.Tensor, q_weight: torch.Tensor, k_weight: torch.Tens
         out_k, hk = _new_heads(tokens, kv_heads, dim, device)
     else:
         hk = _heads(out_k, tokens, kv_heads, dim, "out_k")
+    _check_on_gpu(qkv.is_cuda and q_weight.is_cuda and k_weight.is_cuda and cos.is_cuda and sin.is_cuda and
+                  positions.is_cuda and out_q.is_cuda and out_k.is_cuda)
     status = capi.nvfp4_qk_norm_rope(*args, hq, hk, stream_handle(stream))
     capi.check(status, "nvfp4_qk_norm_rope")
     return out_q, out_k
@@ -362,6 +369,8 @@ def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor, qkv: torch.Tensor,
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=qkv.device)
     dq_weight = torch.empty(dim, dtype=torch.float32, device=qkv.device)
     dk_weight = torch.empty(dim, dtype=torch.float32, device=qkv.device)
+    _check_on_gpu(dq.is_cuda and dk.is_cuda and qkv.is_cuda and q_weight.is_cuda and k_weight.is_cuda and
+                  cos.is_cuda and sin.is_cuda and positions.is_cuda and dqkv.is_cuda and workspace.is_cuda)
     status = capi.nvfp4_qk_norm_rope_backward(
         _heads(dq, tokens, q_heads, dim, "dq"), _heads(dk, tokens, kv_heads, dim, "dk"), *args, dqkv.data_ptr(),
         dqkv.stride(0) if tokens > 1 else dqkv.shape[1], dq_weight.data_ptr(), dk_weight.data_ptr(),
@@ -384,6 +393,7 @@ def attention_spans(offsets: torch.Tensor, tokens: int, *, causal: bool = True, 
         out = torch.empty((tokens, 2), dtype=torch.int32, device=offsets.device)
     elif out.dtype != torch.int32 or out.shape != (tokens, 2) or not out.is_contiguous():
         raise ValueError(f"out: contiguous int32 [{tokens}, 2] expected")
+    _check_on_gpu(offsets.is_cuda and (prefix is None or prefix.is_cuda) and out.is_cuda)
     status = capi.nvfp4_attention_spans(offsets.data_ptr(), documents, None if prefix is None else prefix.data_ptr(),
                                         1 if causal else 0, tokens, out.data_ptr(), stream_handle(stream))
     capi.check(status, "nvfp4_attention_spans")
@@ -422,6 +432,8 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, spans: torch.Te
         lse = torch.empty((q_heads, tokens), dtype=torch.float32, device=device)
     else:
         _check_float32(lse, (q_heads, tokens), "lse")
+    _check_on_gpu(q.is_cuda and k.is_cuda and v.is_cuda and spans.is_cuda and (slopes is None or slopes.is_cuda) and
+                  out.is_cuda and lse.is_cuda)
     status = capi.nvfp4_attention(desc, hq, hk, hv, ho, lse.data_ptr(), stream_handle(stream))
     capi.check(status, "nvfp4_attention")
     return out, lse
@@ -457,6 +469,9 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     nbytes = capi.nvfp4_attention_backward_workspace_size(tokens, q_heads, kv_heads, dim)
     if workspace is None or workspace.numel() < nbytes:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    _check_on_gpu(dout.is_cuda and q.is_cuda and k.is_cuda and v.is_cuda and out.is_cuda and lse.is_cuda and
+                  spans.is_cuda and (slopes is None or slopes.is_cuda) and dq.is_cuda and dk.is_cuda and
+                  dv.is_cuda and workspace.is_cuda)
     status = capi.nvfp4_attention_backward(desc, hdo, hq, hk, hv, ho, lse.data_ptr(), hdq, hdk, hdv,
                                            workspace.data_ptr(), workspace.numel(), stream_handle(stream))
     capi.check(status, "nvfp4_attention_backward")

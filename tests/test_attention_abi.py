@@ -190,6 +190,22 @@ def test_python_refusals():
         ops.attention_spans(torch.zeros(3, dtype=torch.int32), 8, prefix=torch.zeros(3, dtype=torch.int32))
 
 
+def test_python_host_tensors():
+    """Tensors that are right but for their place are refused before a kernel reads them."""
+    bf = torch.bfloat16
+    q, k = torch.zeros((8, 4, 64), dtype=bf), torch.zeros((8, 2, 64), dtype=bf)
+    spans, lse = torch.zeros((8, 2), dtype=torch.int32), torch.zeros((4, 8))
+    w, table, pos = torch.ones(64), torch.zeros((10, 32)), torch.zeros(8, dtype=torch.int32)
+    qkv = torch.zeros((8, 8 * 64), dtype=bf)
+    for call in (lambda: ops.attention(q, k, k, spans),
+                 lambda: ops.attention_backward(q, q, k, k, q, lse, spans),
+                 lambda: ops.attention_spans(torch.zeros(3, dtype=torch.int32), 8),
+                 lambda: ops.qk_norm_rope(qkv, w, w, table, table, pos, q_heads=4, kv_heads=2),
+                 lambda: ops.qk_norm_rope_backward(q, k, qkv, w, w, table, table, pos)):
+        with pytest.raises(ValueError, match="host"):
+            call()
+
+
 def test_rope_tables():
     cos, sin = ops.rope_tables(50, 32, base=100.0, device="cpu")
     assert cos.shape == sin.shape == (50, 16)
