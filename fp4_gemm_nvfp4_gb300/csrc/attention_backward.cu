@@ -795,12 +795,12 @@ cudaError_t prepare_kernel() {
 // streamed tiles, at the cost of FP32 parts written and summed by one more
 // kernel: worth it from eight streamed tiles per split while every split has
 // an SM, from sixteen where two share one (which evens out the items' lengths).
-// 1024 tokens, 24/12 heads of 128 (us): 55 unsplit, 74 in three; 2560 tokens, 16/4
-// heads: 168 unsplit, 118 in three.
+// Both kernels, 1024 tokens, 24/12 heads of 128 (us): 45.5 unsplit, 63 in three;
+// 2560 tokens, 16/4 heads: 150 unsplit, 98 in three.
 int split_count(int64_t tokens, int q_heads, int kv_heads) {
     const int64_t tiles = (tokens + 127) / 128, items = tiles * kv_heads;
     const int64_t most = tiles * (q_heads / kv_heads);       // the longest item's streamed tiles
-    const int64_t one = std::min<int64_t>(device_sm_count() / items, most / 8), 
+    const int64_t one = std::min<int64_t>(device_sm_count() / items, most / 8),
                   two = std::min<int64_t>(2 * device_sm_count() / items, most / 16);
     const int64_t splits = std::max(one, two);
     return (int)(splits < 1 ? 1 : (splits < kMaxSplits ? splits : kMaxSplits));

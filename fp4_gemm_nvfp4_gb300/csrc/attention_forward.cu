@@ -638,16 +638,17 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
 // Two tiles of 128 queries share their key tiles, which halves what comes
 // from L2.  Where there are too few pairs of tiles for the SMs, an item is one
 // tile whose key tiles the two halves of the CTA take in turn instead: twice
-// the items of half the length.  Below 9/8 of the SMs' number of pairs that is
-// as fast or faster (us, pairs and split: 2047 tokens, 5/1 heads of 96 with
-// cap and bias, 40 pairs: 73 and 42; 4096 tokens, 8/2 heads of 128, 128 pairs:
-// 55 and 42; 2560 tokens, 16/4 heads, 160 pairs: 39 and 39), from 192 slower
-// (2048 tokens, 24/12 heads: 33 and 41).
+// the items of half the length.  Up to 6/5 of the SMs' number of pairs that is
+// faster (us, pairs and split: 2047 tokens, 5/1 heads of 96 with cap and bias,
+// 40 pairs: 52 and 33; 4096 tokens, 8/2 heads of 128, 128 pairs: 49 and 35; 5000
+// tokens, 9/3 heads of 80, 180 pairs: 61 and 57.5; but documents of 300, 5/1
+// heads of 64, 160 pairs: 18.6 and 21.7), from 192 slower (2048 tokens, 24/12
+// heads of 128: 28.6 and 33.7).
 template <int kD, int kForm>
 cudaError_t launch_dim(const Attention& a, cudaStream_t stream) {
     const int64_t t128 = (a.tokens + 127) / 128;
     const int64_t pairs = (a.q_heads / a.kv_heads) % 2 == 0 ? t128 * (a.q_heads / 2) : (t128 + 1) / 2 * a.q_heads;
-    return 8 * pairs <= 9 * (int64_t)device_sm_count() ? launch<kD, true, kForm>(a, stream)
+    return 5 * pairs <= 6 * (int64_t)device_sm_count() ? launch<kD, true, kForm>(a, stream)
                                                     : launch<kD, false, kForm>(a, stream);
 }
 

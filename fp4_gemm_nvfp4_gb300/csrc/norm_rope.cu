@@ -269,8 +269,9 @@ cudaError_t launch_one(NormRopeParams& p, cudaStream_t stream) {
 }
 
 // Three vectors per lane group where the heads fill them as well as they fill
-// two: 24/12 heads of 128, 16384 tokens (us) forward 53.2 for 55.6, backward
-// 84 for 89; 16/4 heads of 64, which leave a third of them empty, 28 for 24.
+// two: 24/12 heads of 128, 16384 tokens (us, launched one after the other)
+// forward 53.2 for 55.6, backward 84 for 89; 16/4 heads of 64, which leave a third
+// of the places empty, 28 for 24.
 template <int kLanes, bool kInterleaved, bool kBackward>
 cudaError_t launch_vectors(NormRopeParams& p, cudaStream_t stream) {
     auto places = [&](int vectors) {
