@@ -314,6 +314,49 @@ def test_many_tiles_per_sm(HQ, HKV, D, causal):
     _check(*first, spans)
 
 
+@pytest.mark.parametrize("T,HQ,HKV,D", [(1, 4, 2, 64), (150, 8, 2, 64), (700, 8, 4, 128), (2100, 24, 12, 128)])
+def test_calls_in_a_row_over_the_same_buffers(T, HQ, HKV, D):
+    """Kernels start under the tail of the one before: every call reads what the
+    call before wrote, and overwrites what the one before that read.  The last
+    step's results equal those of steps with the device idle between the calls."""
+    g = _gen(31)
+    qkvs = [_bf16(g, T, (HQ + 2 * HKV) * D) for _ in range(3)]
+    douts = [_bf16(g, T, HQ, D, std=0.02) for _ in range(3)]
+    wq, wk = (torch.rand(D, generator=g, device="cuda") + 0.5 for _ in range(2))
+    cos, sin = ops.rope_tables(T, D)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    spans = ops.attention_spans(torch.tensor([0, T // 3, T], dtype=torch.int32, device="cuda"), T)
+    new = lambda *shape: torch.empty(shape, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    q, k, o, lse = new(T, HQ, D), new(T, HKV, D), new(T, HQ, D), torch.empty((HQ, T), device="cuda")
+    dq, dk, dqkv = new(T, HQ, D), new(T, HKV, D), new(T, (HQ + 2 * HKV) * D)
+    size = capi.nvfp4_attention_backward_workspace_size(T, HQ, HKV, D)
+    size = max(size, capi.nvfp4_qk_norm_rope_backward_workspace_size(D))
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+
+    def step(i, idle):
+        wait = torch.cuda.synchronize if idle else (lambda: None)
+        qkv, do = qkvs[i % 3], douts[i % 3]
+        v = qkv.view(T, HQ + 2 * HKV, D)[:, HQ + HKV:]
+        wait()
+        ops.qk_norm_rope(qkv, wq, wk, cos, sin, pos, q_heads=HQ, kv_heads=HKV, out_q=q, out_k=k)
+        wait()
+        ops.attention(q, k, v, spans, out=o, lse=lse)
+        wait()
+        ops.attention_backward(do, q, k, v, o, lse, spans, dq=dq, dk=dk,
+                               dv=dqkv.view(T, HQ + 2 * HKV, D)[:, HQ + HKV:], workspace=ws)
+        wait()
+        dw = ops.qk_norm_rope_backward(dq, dk, qkv, wq, wk, cos, sin, pos, dqkv=dqkv, workspace=ws)[1:]
+        wait()
+        return [x.clone() for x in (q, k, o, lse, dq, dk, dqkv, *dw)]
+
+    want = [step(i, True) for i in range(3)]
+    for steps in (2, 3, 4, 12):
+        for i in range(steps):
+            got = step(i, False)
+        for a, b in zip(got, want[(steps - 1) % 3]):
+            assert torch.equal(a, b)
+
+
 # Enough heads that there are more pairs of query tiles than SMs: an item is two
 # tiles then (two heads that share their keys, or two tiles of one head), where
 # the few heads of the tests above give one tile whose keys are split.
