@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t in = transpose_bits(bits_between(s.x - k0, s.y - k0), lane);
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if (!(in & (1u << j))) e[j] = 0.0f;
+                            if (!(in & (1u << j))) e[j] = damp[j] = 0.0f;   // (damp of NaN is NaN)
                         // rows of queries without keys may hold anything (their P
                         // and dZ are 0): they are zeroed for the products
                         if (ts.all_hi == 0) {
@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t in = bits_between(span.x - x0 - 32 * (int)quarter, span.y - x0 - 32 * (int)quarter);
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if (!(in & (1u << j))) e[j] = 0.0f;
+                            if (!(in & (1u << j))) e[j] = damp[j] = 0.0f;   // (damp of NaN is NaN)
                         // so may keys that no row of the tile reads
                         if (quarter == 0 && (x0 < ts.lo || x0 + 128 > ts.hi)) {
                             const int key = x0 + (int)row;
