@@ -70,7 +70,10 @@ struct Shape {
     static constexpr uint32_t kStageAt = (2 + kSlots) * kTile;   // 32 rows x 32 dims of results per softmax warp
     static constexpr uint32_t kVecAt = kStageAt + kSoftmaxWarps * 2048;
     static constexpr uint32_t kBarAt = kVecAt + kPairs * kVecBytes;
-    static constexpr size_t kSmem = kBarAt + 1024;   // dynamic shared memory starts 1024-byte aligned (checked)
+    // dq: looks for unseen keys so far (a byte per softmax warp); keys that some
+    // row sees, [2][quarter][warp]; the rows' deltas
+    static constexpr uint32_t kLooksAt = kBarAt + (kAhead ? 432 : 368), kSeenAt = kLooksAt + 16, kDeltaAt = kSeenAt + 128;
+    static constexpr size_t kSmem = kDeltaAt + 512;  // dynamic shared memory starts 1024-byte aligned (checked)
 };
 static_assert(Shape<128>::kSmem <= 232448 && Shape<64>::kSmem <= 232448, "shared memory budget");
 
@@ -112,9 +115,12 @@ struct Params {
 struct Item {
     int valid, head, tile, split;
     int head0, first, count, from, total;
-    TileSpan span;   // dq
-    int pad[3];
+    TileSpan span;   // dq; lo > hi: between the keys that some row sees there may be others
+    int pad;
 };
+template <int kD>
+constexpr bool kBarsFit = 2 * sizeof(Item) + 16 + 8 * (2 * Shape<kD>::kSlots + 20) + 8 <= Shape<kD>::kLooksAt - Shape<kD>::kBarAt;
+static_assert(2 * sizeof(Item) % 16 == 0 && kBarsFit<64> && kBarsFit<128>, "items, answer and barriers before kLooksAt");
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -167,9 +173,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* exact_full = delta_full + 1;       // ... the quarters of the exact ones
     uint64_t* answered = exact_full + 1;
     uint64_t* drain = answered + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* seen_full = drain + 1;             // dq: [2], in turn: the keys that the rows see written
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(seen_full + 2);
     volatile uint32_t* abort_flag = tmem_slot + 1;
-    float* row_delta = reinterpret_cast<float*>(smem + S::kBarAt + 512);   // dq: [128]
+    float* row_delta = reinterpret_cast<float*>(smem + S::kDeltaAt);
 
     const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31u;
     if (threadIdx.x == 0) {
@@ -195,7 +202,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(exact_full, kSoftmaxWarps);
         mbar_init(answered, 1);
         mbar_init(drain, 1);
+        mbar_init(&seen_full[0], kSoftmaxWarps);
+        mbar_init(&seen_full[1], kSoftmaxWarps);
         *abort_flag = 0u;
+        *reinterpret_cast<uint4*>(smem + S::kLooksAt) = make_uint4(0, 0, 0, 0);
         fence_barrier_init();
     }
     if (warp == 0 && lane == 0) {
@@ -394,13 +404,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         item.from = min(item.split * per, all);
                         item.total = min(per, all - item.from);
                     } else {
-                        TileSpan t{INT32_MAX, 0, 0, INT32_MAX};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int64_t q = own0 + 32 * j + (int)lane;
-                            t = join_spans(t, warp_span(span_of(p.spans, q, p.tokens), q < p.tokens));
-                        }
+                        int2 before = make_int2(0, 0);
+                        bool gaps = false;
+                        const TileSpan t = tile_span(p.spans, own0, p.tokens, lane, before, gaps);
                         item.span = t;
+                        if (gaps) item.span.lo = 1, item.span.hi = 0;
                         if (t.lo < t.hi) {
                             item.first = t.lo >> 7;
                             item.count = ((t.hi + 127) >> 7) - item.first;
@@ -572,10 +580,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int j = 0; j < 32; ++j)
                             if (!(in & (1u << j))) e[j] = damp[j] = 0.0f;   // (damp of NaN is NaN)
                         // so may keys that no row of the tile reads
-                        if (quarter == 0 && (x0 < ts.lo || x0 + 128 > ts.hi)) {
-                            const int key = x0 + (int)row;
-                            if (key < ts.lo || key >= ts.hi)
-                                zero_tile_row(ring + ((n2 - 1) % S::kSlots) * S::kTile, row, S::kChunks);
+                        if (x0 < ts.lo || x0 + 128 > ts.hi) {
+                            if (__builtin_expect(ts.lo > ts.hi, 0)) {
+                                // what each warp's rows see of its 32 keys, for the warp of
+                                // the four that zeroes the others.  (It has read them before
+                                // the S after the next can be made: two places in turn.)
+                                uint8_t* looks = smem + S::kLooksAt + (warp - kFirstSoftmaxWarp);
+                                const uint32_t look = *looks;
+                                uint32_t* seen = reinterpret_cast<uint32_t*>(smem + S::kSeenAt) + 16 * (look & 1u) + 4 * quarter;
+                                const uint32_t word = __reduce_or_sync(0xFFFFFFFFu, in);
+                                __syncwarp();
+                                if (lane == 0) {
+                                    *looks = (uint8_t)(look + 1);
+                                    seen[warp & 3u] = word;
+                                    mbar_arrive(&seen_full[look & 1u]);
+                                }
+                                if (quarter == (warp & 3u)) {
+                                    ok = warp_wait_or_abort(&seen_full[look & 1u], (look >> 1) & 1u, p.timeout_ns, abort_flag);
+                                    if (!ok) break;
+                                    const uint4 w = *reinterpret_cast<const uint4*>(seen);
+                                    if (!(((w.x | w.y | w.z | w.w) >> lane) & 1u))
+                                        zero_tile_row(ring + ((n2 - 1) % S::kSlots) * S::kTile, 32 * quarter + lane, S::kChunks);
+                                }
+                            } else if (quarter == 0) {
+                                const int key = x0 + (int)row;
+                                if (key < ts.lo || key >= ts.hi)
+                                    zero_tile_row(ring + ((n2 - 1) % S::kSlots) * S::kTile, row, S::kChunks);
+                            }
                             fence_proxy_async_smem();
                         }
                     }

@@ -245,6 +245,38 @@ __device__ __forceinline__ TileSpan join_spans(TileSpan a, const TileSpan& b) {
     return a;
 }
 
+// Whether a key between some of 32 rows' intervals (one row per lane) may be
+// one that no row sees.  Where every interval touches that of the row with
+// keys before it, all of them together are one interval, as under any mask of
+// packed documents; else what the rows see has to be found key by key.
+// before: the interval of the last row with keys so far (none: empty), kept up to date.
+__device__ __forceinline__ bool may_have_gaps(int2 s, uint32_t lane, int2& before) {
+    const bool some = s.x < s.y;
+    const uint32_t rows = __ballot_sync(0xFFFFFFFFu, some), above = rows & ((1u << lane) - 1u);
+    const int from = above ? 31 - __clz(above) : 0, last = rows ? 31 - __clz(rows) : 0;
+    int2 b = make_int2(__shfl_sync(0xFFFFFFFFu, s.x, from), __shfl_sync(0xFFFFFFFFu, s.y, from));
+    if (!above) b = before;
+    const int2 end = make_int2(__shfl_sync(0xFFFFFFFFu, s.x, last), __shfl_sync(0xFFFFFFFFu, s.y, last));
+    if (rows) before = end;
+    return __any_sync(0xFFFFFFFFu, some && b.x < b.y && (s.x > b.y || s.y < b.x));
+}
+
+// The TileSpan of the tile from row0 on, by a whole warp; gaps is set where
+// its rows, or they and the rows before them, may leave keys unseen.  All
+// loads come first: one after the other they cost the next item 1 us.
+__device__ __forceinline__ TileSpan tile_span(const int32_t* spans, int64_t row0, int64_t tokens, uint32_t lane,
+                                              int2& before, bool& gaps) {
+    int2 s[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = span_of(spans, row0 + 32 * j + (int)lane, tokens);
+    TileSpan t{INT32_MAX, 0, 0, INT32_MAX};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) t = join_spans(t, warp_span(s[j], row0 + 32 * j + (int)lane < tokens));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) gaps |= may_have_gaps(s[j], lane, before);
+    return t;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);

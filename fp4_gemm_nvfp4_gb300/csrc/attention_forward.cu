@@ -54,6 +54,8 @@ struct Shape {
     static constexpr uint32_t kStageAt = (2 + 2 * kStages) * kTile;
     static constexpr uint32_t kBarAt = kStageAt + 8 * 4096;  // 32 rows x 64 dims of output per softmax warp
     static constexpr uint32_t kJointAt = kBarAt + 1024;      // a split tile's second maxima and sums
+    static constexpr uint32_t kLooksAt = kBarAt + 864;       // looks for unseen keys so far, per softmax warp
+    static constexpr uint32_t kSeenAt = kBarAt + 896;        // keys that some row of a tile sees: [2][4 words of 32][warp]
     static constexpr size_t kSmem = kJointAt + 1024;         // dynamic shared memory starts 1024-byte aligned (checked)
 };
 static_assert(Shape<128>::kSmem <= 232448 && Shape<64>::kSmem <= 232448, "shared memory budget");
@@ -82,12 +84,67 @@ struct Item {
     int valid, kv_head;
     int head[2], tile[2], first[2], last[2];
     TileSpan span[2];
-    int pad[2];
+    int lo, hi;       // the keys that some row sees; lo > hi: there may be others between them
 };
+static_assert(2 * sizeof(Item) + 16 + 8 * (2 * Shape<64>::kStages + 22) + 8 <= 864, "barriers before kLooksAt");
 
 struct Ring {
     uint32_t slot = 0, phase = 0;
 };
+
+// Value rows that no row of the CTA reads may hold anything (their P is 0):
+// they are zeroed for the product, key k0 + row by each thread of tile x.
+// cta_lo, cta_hi: the item's lo, hi; span: the keys this row sees; token2: this
+// row's of a neighbouring tile with the same value tile.  False: a wait ran out.
+template <int kD>
+__device__ __forceinline__ bool zero_unseen(const int32_t* spans, int64_t tokens, int64_t token2, int2 span, int k0,
+                                            int cta_lo, int cta_hi, uint32_t warp, uint32_t lane, uint32_t x, uint32_t load,
+                                            uint8_t* smem, uint64_t* full, uint64_t* seen_full, uint64_t timeout_ns,
+                                            const volatile uint32_t* abort_flag) {
+    using S = Shape<kD>;
+    const uint32_t row = (warp & 3u) * 32 + lane, slot = load % S::kStages;
+    const int key = k0 + (int)row;
+    bool unseen = key < cta_lo || key >= cta_hi;
+    if (__builtin_expect(cta_lo > cta_hi, 0)) {
+        // what this warp's rows see, then the tile's four warps together (all have
+        // read it when the next scores are there).  What only this needs is
+        // kept in shared memory: registers are short.
+        const int2 span2 = span_of(spans, token2, tokens);
+        uint32_t* looks = reinterpret_cast<uint32_t*>(smem + S::kLooksAt) + (warp - kFirstSoftmaxWarp);
+        const uint32_t look = *looks;
+        uint32_t* seen = reinterpret_cast<uint32_t*>(smem + S::kSeenAt) + 16 * x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t word = __reduce_or_sync(
+                0xFFFFFFFFu, bits_between(span.x - k0 - 32 * i, span.y - k0 - 32 * i) |
+                                 bits_between(span2.x - k0 - 32 * i, span2.y - k0 - 32 * i));
+            if (lane == 0) seen[4 * i + (warp & 3u)] = word;
+        }
+        __syncwarp();
+        if (lane == 0) {
+            *looks = look + 1;
+            mbar_arrive(&seen_full[x]);
+        }
+        if (!warp_wait_or_abort(&seen_full[x], look & 1u, timeout_ns, abort_flag)) return false;
+        const uint4 w = *reinterpret_cast<const uint4*>(seen + 4 * (warp & 3u));
+        unseen = !(((w.x | w.y | w.z | w.w) >> lane) & 1u);
+    }
+    if (!warp_wait_or_abort(&full[slot], (load / S::kStages) & 1u, timeout_ns, abort_flag)) return false;
+    if (unseen) zero_tile_row(smem + (2 + 2 * slot) * S::kTile, row, S::kChunks);
+    fence_proxy_async_smem();
+    return true;
+}
+// Its code within a capped kernel's softmax loop costs that loop registers,
+// a call from the others' loops does (8192 tokens, us, within and called: 16/4
+// heads with a cap 263 and 249, 24/12 heads without 248 and 257).
+template <int kD>
+__device__ __noinline__ bool zero_unseen_apart(const int32_t* spans, int64_t tokens, int64_t token2, int2 span, int k0,
+                                               int cta_lo, int cta_hi, uint32_t x, uint32_t load, uint8_t* smem,
+                                               uint64_t* full, uint64_t* seen_full, uint64_t timeout_ns,
+                                               const volatile uint32_t* abort_flag) {
+    return zero_unseen<kD>(spans, tokens, token2, span, k0, cta_lo, cta_hi, threadIdx.x >> 5, threadIdx.x & 31u, x, load,
+                           smem, full, seen_full, timeout_ns, abort_flag);
+}
 
 // kSplit: an item is one tile twice, with the key tiles in turn.  kForm: what
 // the scores are made of.
@@ -116,7 +173,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* loaded = item_empty + 2;           // the item's loads issued
     uint64_t* answered = loaded + 1;
     uint64_t* drain = answered + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* seen_full = drain + 1;             // [2] the keys that a tile's rows see written
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(seen_full + 2);
     volatile uint32_t* abort_flag = tmem_slot + 1;
 
     const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31u;
@@ -132,6 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&p_full[i], 4);
             mbar_init(&o_full[i], 1);
             mbar_init(&o_empty[i], 4);
+            mbar_init(&seen_full[i], 4);
             mbar_init(&item_full[i], 1);
             mbar_init(&item_empty[i], 10);
         }
@@ -140,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(answered, 1);
         mbar_init(drain, 1);
         *abort_flag = 0u;
+        for (int i = 0; i < 8; ++i) reinterpret_cast<uint32_t*>(smem + S::kLooksAt)[i] = 0u;
         fence_barrier_init();
     }
     if (warp == 0 && lane == 0) {
@@ -329,24 +389,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                         item.tile[x] = p.pair_heads || kSplit ? ti : 2 * ti + x;
                     }
                     item.kv_head = item.head[0] / p.group;
+                    int2 before = make_int2(0, 0);
+                    bool gaps = false;
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         if (x == 1 && (p.pair_heads || kSplit)) {
                             item.span[1] = item.span[0];
                         } else {
-                            TileSpan t{INT32_MAX, 0, 0, INT32_MAX};
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const int64_t token = (int64_t)item.tile[x] * 128 + 32 * j + lane;
-                                t = join_spans(t, warp_span(span_of(p.spans, token, p.tokens), token < p.tokens));
-                            }
-                            item.span[x] = t;
+                            item.span[x] = tile_span(p.spans, (int64_t)item.tile[x] * 128, p.tokens, lane, before, gaps);
                         }
                         const int from = (item.span[x].lo >> 7) + (kSplit ? x : 0), to = (item.span[x].hi + 127) >> 7;
                         const bool some = item.span[x].lo < item.span[x].hi && from < to;
                         item.first[x] = some ? from : INT32_MAX;
                         item.last[x] = some ? to : 0;
                     }
+                    item.lo = gaps ? 1 : min(item.span[0].lo, item.span[1].lo);
+                    item.hi = gaps ? 0 : max(item.span[0].hi, item.span[1].hi);
                 }
                 ok = warp_wait_or_abort(&item_empty[it & 1u], ((it >> 1) & 1u) ^ 1u, p.timeout_ns, abort_flag);
                 if (!ok) break;
@@ -388,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool valid = item.valid != 0;
             const int first = item.first[x], last = item.last[x], first2 = item.first[x ^ 1u], last2 = item.last[x ^ 1u];
             const int all_lo = item.span[x].all_lo, all_hi = item.span[x].all_hi;
-            const int cta_lo = min(item.span[0].lo, item.span[1].lo), cta_hi = max(item.span[0].hi, item.span[1].hi);
+            const int cta_lo = item.lo, cta_hi = item.hi;
             const int head = item.head[x], tile = item.tile[x];
             __syncwarp();
             if (lane == 0) mbar_arrive(&item_empty[it & 1u]);
@@ -424,16 +482,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (!(in & (1u << j))) s[32 * i + j] = -INFINITY;
-                    }
-                    // value rows that no row of the CTA reads may hold anything
-                    // (their P is 0): they are zeroed for the product
-                    if (k0 < cta_lo || k0 + 128 > cta_hi) {
-                        const uint32_t slot = load % S::kStages;
-                        ok = warp_wait_or_abort(&full[slot], (load / S::kStages) & 1u, p.timeout_ns, abort_flag);
-                        if (!ok) break;
-                        const int key = k0 + (int)row;
-                        if (key < cta_lo || key >= cta_hi) zero_tile_row(ring + slot * 2 * S::kTile, row, S::kChunks);
-                        fence_proxy_async_smem();
                     }
                 }
                 float mx[4] = {max3(s[0], s[1], s[2]), max3(s[3], s[4], s[5]), max3(s[6], s[7], s[8]), s[9]};
@@ -484,6 +532,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pk[i] = pack_bf16(e0, e1);
                     }
                     tmem_st_32x32b_x32(s_at + 32 * h, pk);
+                }
+                if (k0 < cta_lo || k0 + 128 > cta_hi) {
+                    const int tile2 = kSplit || p.pair_heads ? tile : tile ^ 1;
+                    const int64_t token2 = (int64_t)tile2 * 128 + row;
+                    if constexpr (kCapped)
+                        ok = zero_unseen_apart<kD>(p.spans, p.tokens, token2, span, k0, cta_lo, cta_hi, x, load, smem, full,
+                                                   seen_full, p.timeout_ns, abort_flag);
+                    else
+                        ok = zero_unseen<kD>(p.spans, p.tokens, token2, span, k0, cta_lo, cta_hi, warp, lane, x, load, smem,
+                                             full, seen_full, p.timeout_ns, abort_flag);
+                    if (!ok) break;
                 }
                 tmem_st_wait();
                 tc_fence_before();

@@ -481,9 +481,9 @@ NVFP4_API nvfp4_status nvfp4_qk_norm_rope_backward(const nvfp4_heads *dq, const 
  * (nvfp4_attention_spans writes the common ones); a row whose interval is
  * empty gets out = 0, lse = -inf and gradients 0.  Intervals are cut to
  * [0, tokens).  Work is spent only on 128 x 128 tiles that some interval
- * reaches.  Inputs are finite; the rows of keys and values that no interval of a
- * tile of 128 queries reaches, and of queries with an empty interval, may
- * hold anything.
+ * reaches.  Inputs are finite; the rows of keys and values that no interval
+ * reaches, and of q, out and dout with an empty interval, may hold anything
+ * (NaN, infinities): padding need not be cleared, wherever it lies.
  */
 typedef struct {
     int64_t        tokens;

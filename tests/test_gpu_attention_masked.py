@@ -83,3 +83,39 @@ def test_caps_and_biases_of_padded_ends(heads, softcap, bias, junk, causal):
     T, first, end = 333, 19, 290
     off = torch.tensor([first, 100, end], dtype=torch.int32, device="cuda")
     _junk_changes_nothing(T, heads, ops.attention_spans(off, T, causal=causal), junk, 21, softcap, bias)
+
+
+def _padded(T, lengths, causal):
+    """Sequences with padding after each: (tokens, padding) in turn."""
+    rows, n = [(0, 0)] * T, 0
+    while n < T:
+        for keep, pad in lengths:
+            for i in range(n, min(n + keep, T)):
+                rows[i] = (n, i + 1 if causal else min(n + keep, T))
+            n += keep + pad
+    return torch.tensor(rows, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("junk", JUNK)
+@pytest.mark.parametrize("softcap,bias", [(0.0, False), *FORMS[:3]])
+@pytest.mark.parametrize("heads", SPLIT + PAIRS)
+def test_padding_between_sequences(heads, softcap, bias, junk):
+    """Each sequence padded: the padding lies between keys that rows of the same
+    tiles see, within a tile and across the two tiles of an item."""
+    for T, lengths in ((333, [(40, 10)]), (520, [(100, 50), (106, 1)]), (470, [(3, 1), (1, 2), (200, 133)])):
+        for causal in (True, False):
+            _junk_changes_nothing(T, heads, _padded(T, lengths, causal), junk, T, softcap, bias)
+
+
+@pytest.mark.parametrize("heads", SPLIT + PAIRS)
+def test_scattered_intervals(heads):
+    """Rows of one tile that see keys far apart, in no order, whole tiles of unseen keys between."""
+    T = 700
+    g = torch.Generator().manual_seed(heads[2])
+    rows = []
+    for i in range(T):
+        a = int(torch.randint(0, 3, (1,), generator=g)) * 300 + int(torch.randint(0, 40, (1,), generator=g))
+        rows.append([(a, a + int(torch.randint(1, 50, (1,), generator=g))), (0, 0)][i % 7 == 3])
+    spans = torch.tensor(rows, dtype=torch.int32, device="cuda")
+    for junk in JUNK:
+        _junk_changes_nothing(T, heads, spans, junk, 5)
