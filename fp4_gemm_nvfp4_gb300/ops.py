@@ -4,6 +4,10 @@ PyTorch provides the device memory and the stream; every step of the
 quantize / GEMM / dequantize path runs in the library's CUDA kernels.  These
 helpers only allocate the caller-owned buffers the ABI expects and marshal
 pointers.
+
+With `stream` a call runs on that stream.  Its results are allocated on the
+current one: the two are ordered by the caller, as for any tensor used on a
+stream other than its own.
 """
 from dataclasses import dataclass
 from typing import Optional, Tuple
@@ -57,6 +61,18 @@ def stream_handle(stream: Optional[torch.cuda.Stream] = None) -> int:
     # torch.cuda.current_stream().cuda_stream without the Stream object, which
     # costs as much as a kernel launch
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _scratch(given: Optional[torch.Tensor], nbytes: int, device, stream) -> torch.Tensor:
+    """The scratch a call was given, or one of its own.  That is dropped when the call returns, so it comes
+    from the pool of the stream its kernels run on: from the current stream's it could be handed to that
+    stream's next tensor while they still use it."""
+    if given is not None and given.numel() >= nbytes:
+        return given
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 class Workspace:
@@ -207,8 +223,7 @@ def gemm_lora(a: NVFP4Operand, b: NVFP4Operand, u: torch.Tensor, v: torch.Tensor
     if out is None:
         out = torch.empty((a.rows, b.rows), dtype=out_dtype, device=a.codes.device)
     nbytes = capi.nvfp4_gemm_lora_workspace_size(a.rows, r)
-    if scratch is None or scratch.numel() < nbytes:
-        scratch = torch.empty(nbytes, dtype=torch.uint8, device=a.codes.device)
+    scratch = _scratch(scratch, nbytes, a.codes.device, stream)
     dt = capi.NVFP4_OUT_FP32 if out.dtype == torch.float32 else capi.NVFP4_OUT_BF16
     status = capi.nvfp4_gemm_lora(a.struct(), b.struct(), out.data_ptr(), out.stride(0), dt, u.data_ptr(),
                                   u.stride(0), v.data_ptr(), v.stride(0), r, float(beta), scratch.data_ptr(),
@@ -240,9 +255,7 @@ def newton_schulz_step(x: torch.Tensor, a: float, b: float, c: float, rht_mask: 
     m, n = x.shape
     if out is None:
         out = torch.empty_like(x)
-    nbytes = capi.nvfp4_newton_schulz_workspace_size(m, n)
-    if workspace is None or workspace.numel() < nbytes:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    workspace = _scratch(workspace, capi.nvfp4_newton_schulz_workspace_size(m, n), x.device, stream)
     status = capi.nvfp4_newton_schulz_step(x.data_ptr(), m, n, x.stride(0), float(a), float(b), float(c),
                                            rht_mask, out.data_ptr(), out.stride(0), workspace.data_ptr(),
                                            workspace.numel(), stream_handle(stream))
@@ -364,9 +377,7 @@ def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor, qkv: torch.Tensor,
     elif (dqkv.dtype != torch.bfloat16 or dqkv.dim() != 2 or dqkv.shape[0] != tokens or dqkv.stride(1) != 1 or
           dqkv.shape[1] < (q_heads + kv_heads) * dim):
         raise ValueError(f"dqkv: bfloat16 [{tokens}, >= {(q_heads + kv_heads) * dim}] expected")
-    nbytes = capi.nvfp4_qk_norm_rope_backward_workspace_size(dim)
-    if workspace is None or workspace.numel() < nbytes:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=qkv.device)
+    workspace = _scratch(workspace, capi.nvfp4_qk_norm_rope_backward_workspace_size(dim), qkv.device, stream)
     dq_weight = torch.empty(dim, dtype=torch.float32, device=qkv.device)
     dk_weight = torch.empty(dim, dtype=torch.float32, device=qkv.device)
     _check_on_gpu(dq.is_cuda and dk.is_cuda and qkv.is_cuda and q_weight.is_cuda and k_weight.is_cuda and
@@ -466,9 +477,8 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
         dv, hdv = _new_heads(tokens, kv_heads, dim, device)
     else:
         hdv = _heads(dv, tokens, kv_heads, dim, "dv")
-    nbytes = capi.nvfp4_attention_backward_workspace_size(tokens, q_heads, kv_heads, dim)
-    if workspace is None or workspace.numel() < nbytes:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    workspace = _scratch(workspace, capi.nvfp4_attention_backward_workspace_size(tokens, q_heads, kv_heads, dim),
+                         device, stream)
     _check_on_gpu(dout.is_cuda and q.is_cuda and k.is_cuda and v.is_cuda and out.is_cuda and lse.is_cuda and
                   spans.is_cuda and (slopes is None or slopes.is_cuda) and dq.is_cuda and dk.is_cuda and
                   dv.is_cuda and workspace.is_cuda)
