@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l = l * f + l2 * f2;
             }
             tc_fence_after();
-            const bool some = l > 0.0f;
+            const bool some = !(l == 0.0f);            // (a NaN is no empty row: it reaches out and lse)
             const float over = some ? 1.0f / l : 0.0f;
             f *= over;
             f2 *= over;

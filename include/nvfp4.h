@@ -483,7 +483,11 @@ NVFP4_API nvfp4_status nvfp4_qk_norm_rope_backward(const nvfp4_heads *dq, const 
  * [0, tokens).  Work is spent only on 128 x 128 tiles that some interval
  * reaches.  Inputs are finite; the rows of keys and values that no interval
  * reaches, and of q, out and dout with an empty interval, may hold anything
- * (NaN, infinities): padding need not be cleared, wherever it lies.
+ * (NaN, infinities): padding need not be cleared, wherever it lies.  A row
+ * that sees a NaN, or whose scores overflow, gets NaN in out and lse.  Scores
+ * are FP32 and P is formed from their difference to a maximum or to lse: from
+ * a size of 2^24 on, where FP32 steps by 1, P has no digits left, and rows with
+ * scores beyond 2^30 may be NaN or 0.
  */
 typedef struct {
     int64_t        tokens;

@@ -119,3 +119,47 @@ def test_scattered_intervals(heads):
     spans = torch.tensor(rows, dtype=torch.int32, device="cuda")
     for junk in JUNK:
         _junk_changes_nothing(T, heads, spans, junk, 5)
+
+
+@pytest.mark.parametrize("softcap,bias", [(0.0, False), *FORMS[:3]])
+@pytest.mark.parametrize("heads", SPLIT + PAIRS)
+def test_nan_in_a_seen_place_reaches_its_rows(heads, softcap, bias):
+    """A row that sees a NaN has NaN as its result, not that of a row without
+    keys; the other rows keep theirs."""
+    HQ, HKV, D = heads
+    T, key, row = 400, 150, 260
+    q, k, v, _ = _inputs(T, HQ, HKV, D, 8)
+    form = dict(softcap=softcap, slopes=torch.linspace(0.0, 0.4, HQ, device="cuda") if bias else None)
+    spans = ops.attention_spans(torch.tensor([0, 70, 333], dtype=torch.int32, device="cuda"), T)
+    want, want_lse = ops.attention(q, k, v, spans, **form)
+    sees = torch.zeros(T, dtype=torch.bool, device="cuda")
+    sees[key:333] = True                             # causal, one document from 70 to 333
+    bad = k.clone()
+    bad[key, :, D // 2] = math.nan
+    o, lse = ops.attention(q, bad, v, spans, **form)
+    assert torch.isnan(o[sees]).all() and torch.isnan(lse[:, sees]).all()
+    assert torch.equal(o[~sees], want[~sees]) and torch.equal(lse[:, ~sees], want_lse[:, ~sees])
+    sees[:] = False
+    sees[row] = True
+    bad = q.clone()
+    bad[row, :, 3] = math.nan
+    o, lse = ops.attention(bad, k, v, spans, **form)
+    assert torch.isnan(o[row]).all() and torch.isnan(lse[:, row]).all()
+    assert torch.equal(o[~sees], want[~sees]) and torch.equal(lse[:, ~sees], want_lse[:, ~sees])
+    sees[key:333] = True
+    bad = v.clone()
+    bad[key, :, 5] = math.nan
+    o, lse = ops.attention(q, k, bad, spans, **form)
+    assert torch.isnan(o[key:333, :, 5]).all() and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("heads", SPLIT + PAIRS)
+def test_a_product_that_overflows_is_not_an_empty_row(heads):
+    HQ, HKV, D = heads
+    T = 300
+    q, k, v, _ = _inputs(T, HQ, HKV, D, 9)
+    q[200], k[40] = 1e30, 1e30
+    o, lse = ops.attention(q, k, v, ops.attention_spans(torch.tensor([0, T], dtype=torch.int32, device="cuda"), T))
+    assert torch.isnan(o[200]).all() and torch.isnan(lse[:, 200]).all()
+    # (the rows between see a score of 1e30, of which FP32 holds no digit that exp could use)
+    assert torch.isfinite(o[:40]).all() and torch.isfinite(lse[:, :40]).all()
