@@ -41,7 +41,8 @@ EXPORTED = ("nvfp4_scale_bytes", "nvfp4_quantize_workspace_size", "nvfp4_quantiz
             "nvfp4_qk_norm_rope", "nvfp4_qk_norm_rope_backward_workspace_size", "nvfp4_qk_norm_rope_backward",
             "nvfp4_attention_spans", "nvfp4_attention", "nvfp4_attention_backward_workspace_size",
             "nvfp4_attention_backward",
-            "nvfp4_testing_arm_gemm_timeout", "nvfp4_testing_arm_attention_timeout", "nvfp4_testing_bounds_violations",
+            "nvfp4_testing_arm_gemm_timeout", "nvfp4_testing_arm_attention_timeout",
+            "nvfp4_testing_attention_wait_limit_us", "nvfp4_testing_bounds_violations",
             "nvfp4_testing_bounds_shrink")
 
 
@@ -137,6 +138,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.nvfp4_testing_arm_gemm_timeout.restype = i32
     L.nvfp4_testing_arm_attention_timeout.argtypes = [c32, ctypes.c_uint32]
     L.nvfp4_testing_arm_attention_timeout.restype = i32
+    L.nvfp4_testing_attention_wait_limit_us.argtypes = [c32, i64, c32, c32]
+    L.nvfp4_testing_attention_wait_limit_us.restype = ctypes.c_uint64
     L.nvfp4_testing_bounds_violations.argtypes = [ctypes.POINTER(ctypes.c_uint64)]
     L.nvfp4_testing_bounds_violations.restype = i32
     L.nvfp4_testing_bounds_shrink.argtypes, L.nvfp4_testing_bounds_shrink.restype = [i64], i32
@@ -296,6 +299,11 @@ def nvfp4_testing_arm_attention_timeout(backward, wait_limit_us):
     """Test support (include/nvfp4_testing.h): the next attention call's loads
     never come and its waits give up after wait_limit_us."""
     return load().nvfp4_testing_arm_attention_timeout(backward, wait_limit_us)
+
+
+def nvfp4_testing_attention_wait_limit_us(backward, tokens, q_heads, kv_heads):
+    """Test support (include/nvfp4_testing.h): the limit of one wait of such a call."""
+    return load().nvfp4_testing_attention_wait_limit_us(backward, tokens, q_heads, kv_heads)
 
 
 def nvfp4_testing_bounds_violations():

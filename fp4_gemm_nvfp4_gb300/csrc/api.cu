@@ -691,6 +691,11 @@ nvfp4_status nvfp4_testing_arm_attention_timeout(int32_t backward, uint32_t wait
     return NVFP4_OK;
 }
 
+uint64_t nvfp4_testing_attention_wait_limit_us(int32_t backward, int64_t tokens, int32_t q_heads, int32_t kv_heads) {
+    if (check_head_shape(tokens, q_heads, kv_heads, 8) != NVFP4_OK) return 0;
+    return nvfp4::attention_wait_limit_ns(backward != 0, tokens, q_heads, kv_heads) / 1000u;
+}
+
 nvfp4_status nvfp4_testing_bounds_violations(uint64_t* count) {
 #ifdef NVFP4_BOUNDS_CHECK
     if (!count) return NVFP4_ERR_INVALID_ARG;

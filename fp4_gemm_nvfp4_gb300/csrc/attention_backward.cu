@@ -879,13 +879,14 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
     const int splits = split_count(a.tokens, a.q_heads, a.kv_heads);
     p.ws = carve(a.workspace, a.tokens, a.q_heads, a.kv_heads, a.head_dim, splits, nullptr);
     p.splits = 1;
-    p.timeout_ns = attention_timeout(&p.withhold);
+    const uint64_t limit_ns = attention_wait_limit_ns(true, a.tokens, a.q_heads, a.kv_heads);
+    p.timeout_ns = attention_timeout(limit_ns, &p.withhold);
     if ((uint64_t)p.tiles * (uint64_t)a.q_heads > 0x7FFFFFFFull) return cudaErrorInvalidValue;
     p.heads = a.q_heads;
     e = launch_early(attention_backward_kernel<kD, false, kForm>, dim3((unsigned)(p.tiles * a.q_heads)), dim3(kThreads),
                      Shape<kD>::kSmem, stream, mq, mdo, mk, mv, mdq, mdq, p);
     if (e != cudaSuccess) return e;
-    p.timeout_ns = kAttentionTimeoutNs;
+    p.timeout_ns = limit_ns;
     p.withhold = 0;
     p.heads = a.kv_heads;
     p.dv = a.dv;

@@ -15,7 +15,6 @@ namespace nvfp4 {
 
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.693147180559945309f;
-constexpr uint64_t kAttentionTimeoutNs = 2000000000ull;
 
 // Status word of this translation unit's kernels (kStatusTimeoutBit).
 static __device__ unsigned int g_attention_status = 0;
@@ -43,11 +42,11 @@ __device__ __forceinline__ uint32_t transpose_bits(uint32_t x, uint32_t lane) {
     return x;
 }
 
-// The limit of a launch's waits, and whether it is the armed one.
-inline uint64_t attention_timeout(uint32_t* withhold) {
+// The limit of a launch's waits, or the armed one.
+inline uint64_t attention_timeout(uint64_t limit_ns, uint32_t* withhold) {
     const uint64_t armed = g_attention_armed_ns.exchange(0);
     *withhold = armed ? 1u : 0u;
-    return armed ? armed : kAttentionTimeoutNs;
+    return armed ? armed : limit_ns;
 }
 
 inline cudaError_t attention_status_read_and_clear_local(unsigned int* status) {

@@ -687,7 +687,7 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
     p.spans = a.spans;
     p.lse = a.lse;
     p.xlse = extent_of(a.lse, a.tokens * a.q_heads * 4);
-    p.timeout_ns = attention_timeout(&p.withhold);
+    p.timeout_ns = attention_timeout(attention_wait_limit_ns(false, a.tokens, a.q_heads, a.kv_heads), &p.withhold);
     const uint64_t grid = (uint64_t)p.tiles * p.items_per_tile;
     if (grid > 0x7FFFFFFFull) return cudaErrorInvalidValue;
     return launch_early(attention_forward_kernel<kD, kSplit, kForm>, dim3((unsigned)grid), dim3(kThreads), Shape<kD>::kSmem,

@@ -158,6 +158,14 @@ struct Attention {
     HeadsView dout, dq, dk, dv;  // backward only
     float* workspace;            // backward only
 };
+// The limit of each of a call's waits: 2 s, and 10 us for every streamed tile of
+// its longest item (a tile takes about 1 us).  Some waits last for a whole
+// item: the next item's for the loads of this one, and where two query tiles
+// share an item, one's for the other's.
+inline uint64_t attention_wait_limit_ns(bool backward, int64_t tokens, int q_heads, int kv_heads) {
+    const uint64_t tiles = (uint64_t)(tokens + 127) / 128;
+    return 2000000000ull + 10000ull * tiles * (uint64_t)(backward ? q_heads / kv_heads : 1);
+}
 cudaError_t launch_attention_spans(const int32_t* offsets, int64_t documents, const int32_t* prefix, bool causal,
                                    int64_t tokens, int32_t* spans, cudaStream_t stream);
 cudaError_t launch_attention(const Attention& a, cudaStream_t stream);

@@ -53,6 +53,14 @@ NVFP4_API nvfp4_status nvfp4_testing_arm_gemm_timeout(uint32_t wait_limit_us);
 NVFP4_API nvfp4_status nvfp4_testing_arm_attention_timeout(int32_t backward, uint32_t wait_limit_us);
 
 /*
+ * nvfp4_testing_attention_wait_limit_us -- the microseconds after which a wait
+ * of an nvfp4_attention (nvfp4_attention_backward) call of this shape gives up
+ * when nothing is armed; 0 for a shape that is refused.
+ */
+NVFP4_API uint64_t nvfp4_testing_attention_wait_limit_us(int32_t backward, int64_t tokens, int32_t q_heads,
+                                                         int32_t kv_heads);
+
+/*
  * nvfp4_testing_bounds_violations -- the number of stores the debug build's
  * bounds check skipped since the previous call (the count is then cleared).
  *  count  host pointer, receives the number.
