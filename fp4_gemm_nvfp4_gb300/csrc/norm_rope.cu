@@ -106,6 +106,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(kBackward, kVectors)) 
     const uint32_t da = !kInterleaved && turned ? 4 * l : 8 * l;                  // first of the lane's dims
     const uint32_t db = !kInterleaved && turned ? rot / 2 + 4 * l : 8 * l + 4;    // ... of its other four
     const float inv_d = 1.0f / (float)D;
+    // x of a place without a head, whose dy is 0: ones backward, where zeros
+    // would make its share of dw 0 * inf with eps = 0
+    const uint32_t blank = kBackward && live ? 0x3F803F80u : 0u;
     const bool is_q = blockIdx.x < p.q_blocks;
     const uint32_t block = is_q ? blockIdx.x : blockIdx.x - p.q_blocks;
     const uint32_t blocks = is_q ? p.q_blocks : gridDim.x - p.q_blocks;
@@ -133,7 +136,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(kBackward, kVectors)) 
 #pragma unroll
         for (int u = 0; u < kVectors; ++u) {
             const uint32_t h = h0 + u * kGroups;
-            xv[u] = dyv[u] = Piece{make_uint2(0, 0), make_uint2(0, 0)};
+            xv[u] = Piece{make_uint2(blank, blank), make_uint2(blank, blank)};
+            dyv[u] = Piece{make_uint2(0, 0), make_uint2(0, 0)};
             if (live && h < heads) {
                 const uint16_t* from = x + h * D;
                 xv[u] = Piece{ld_v2(from + da), ld_v2(from + db)};
