@@ -321,8 +321,9 @@ def _norm_rope_args(qkv, q_weight, k_weight, cos, sin, positions, q_heads, kv_he
     tokens, columns = qkv.shape
     ld, one = qkv.stride()
     dim = q_weight.shape[-1] if q_weight.dim() else 0
-    if one != 1 or columns < (q_heads + kv_heads) * dim:
-        raise ValueError(f"qkv: contiguous rows of at least {(q_heads + kv_heads) * dim} columns expected")
+    need = (q_heads + kv_heads) * dim
+    if one != 1 or columns < need:
+        raise ValueError(f"qkv: contiguous rows of at least {need} columns expected")
     _check_float32(q_weight, (dim,), "q_weight")
     _check_float32(k_weight, (dim,), "k_weight")
     if cos.dim() != 2:
@@ -332,7 +333,8 @@ def _norm_rope_args(qkv, q_weight, k_weight, cos, sin, positions, q_heads, kv_he
     _check_float32(sin, (rows, half), "sin")
     if positions.dtype != torch.int32 or positions.shape != (tokens,) or not positions.is_contiguous():
         raise ValueError(f"positions: contiguous int32 [{tokens}] expected")
-    return (qkv.data_ptr(), ld if tokens > 1 else columns, tokens, q_heads, kv_heads, dim, q_weight.data_ptr(),
+    # (the stride of one row says nothing)
+    return (qkv.data_ptr(), ld if tokens > 1 else need, tokens, q_heads, kv_heads, dim, q_weight.data_ptr(),
             k_weight.data_ptr(), eps, cos.data_ptr(), sin.data_ptr(), rows, 2 * half, 1 if interleaved else 0,
             positions.data_ptr())
 
@@ -372,11 +374,12 @@ def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor, qkv: torch.Tensor,
     q_heads, kv_heads = dq.shape[1], dk.shape[1]
     args = _norm_rope_args(qkv, q_weight, k_weight, cos, sin, positions, q_heads, kv_heads, eps, interleaved)
     tokens, dim = args[2], args[5]
+    need = (q_heads + kv_heads) * dim
     if dqkv is None:
-        dqkv = torch.empty((tokens, (q_heads + kv_heads) * dim), dtype=torch.bfloat16, device=qkv.device)
+        dqkv = torch.empty((tokens, need), dtype=torch.bfloat16, device=qkv.device)
     elif (dqkv.dtype != torch.bfloat16 or dqkv.dim() != 2 or dqkv.shape[0] != tokens or dqkv.stride(1) != 1 or
-          dqkv.shape[1] < (q_heads + kv_heads) * dim):
-        raise ValueError(f"dqkv: bfloat16 [{tokens}, >= {(q_heads + kv_heads) * dim}] expected")
+          dqkv.shape[1] < need):
+        raise ValueError(f"dqkv: bfloat16 [{tokens}, >= {need}] expected")
     workspace = _scratch(workspace, capi.nvfp4_qk_norm_rope_backward_workspace_size(dim), qkv.device, stream)
     dq_weight = torch.empty(dim, dtype=torch.float32, device=qkv.device)
     dk_weight = torch.empty(dim, dtype=torch.float32, device=qkv.device)
@@ -384,7 +387,7 @@ def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor, qkv: torch.Tensor,
                   cos.is_cuda and sin.is_cuda and positions.is_cuda and dqkv.is_cuda and workspace.is_cuda)
     status = capi.nvfp4_qk_norm_rope_backward(
         _heads(dq, tokens, q_heads, dim, "dq"), _heads(dk, tokens, kv_heads, dim, "dk"), *args, dqkv.data_ptr(),
-        dqkv.stride(0) if tokens > 1 else dqkv.shape[1], dq_weight.data_ptr(), dk_weight.data_ptr(),
+        dqkv.stride(0) if tokens > 1 else need, dq_weight.data_ptr(), dk_weight.data_ptr(),
         workspace.data_ptr(), workspace.numel(), stream_handle(stream))
     capi.check(status, "nvfp4_qk_norm_rope_backward")
     return dqkv, dq_weight, dk_weight
