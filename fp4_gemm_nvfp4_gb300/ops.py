@@ -68,6 +68,8 @@ def _scratch(given: Optional[torch.Tensor], nbytes: int, device, stream) -> torc
     from the pool of the stream its kernels run on: from the current stream's it could be handed to that
     stream's next tensor while they still use it."""
     if given is not None and given.numel() >= nbytes:
+        if not given.is_contiguous():
+            raise ValueError("scratch: a contiguous tensor expected")
         return given
     if stream is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)

@@ -46,3 +46,25 @@ def test_row_stride_of_few_tokens(calls, tokens, columns):
     assert ld[3] == ld[4] and calls[2][2] == calls[2][17]
     if tokens > 1:
         assert ld == [width] * 5
+
+
+@pytest.mark.parametrize("name", ["strided", "expanded"])
+def test_scratch_with_holes_is_refused(calls, name, monkeypatch):
+    """A scratch tensor's element count is its size only if it has no holes and no
+    repeats: the kernels write that many bytes from its first on."""
+    def scratch(n):
+        return torch.zeros(2 * n, dtype=torch.uint8)[::2] if name == "strided" else torch.zeros(1, dtype=torch.uint8).expand(n)
+
+    for entry in ("nvfp4_attention_backward", "nvfp4_gemm_lora", "nvfp4_newton_schulz_step"):
+        monkeypatch.setattr(capi, entry, lambda *args: calls.append(args) or capi.NVFP4_OK)
+    qkv, *rest = _args(2, NEED, NEED)
+    q, k = (torch.zeros((2, h, D), dtype=torch.bfloat16) for h in (HQ, HKV))
+    a, u, x = ops.alloc_operand(128, 256, "cpu"), torch.zeros((128, 64), dtype=torch.bfloat16), torch.zeros((128, 256), dtype=torch.bfloat16)
+    ws = scratch(1 << 20)
+    for call in (lambda: ops.qk_norm_rope_backward(q, k, qkv, *rest, workspace=ws),
+                 lambda: ops.attention_backward(q, q, k, k, q, torch.zeros((HQ, 2)), torch.zeros((2, 2), dtype=torch.int32), workspace=ws),
+                 lambda: ops.gemm_lora(a, a, u, u, 1.0, scratch=ws),
+                 lambda: ops.newton_schulz_step(x, 1.0, 1.0, 1.0, 0, workspace=ws)):
+        with pytest.raises(ValueError, match="contiguous"):
+            call()
+    assert not calls
