@@ -180,7 +180,8 @@ nvfp4_status check_attention(const nvfp4_attention_desc* d, const nvfp4_heads* q
     nvfp4_status s;
     if ((s = check_head_shape(d->tokens, d->q_heads, d->kv_heads, d->head_dim)) != NVFP4_OK) return s;
     if (d->q_heads % d->kv_heads != 0) return NVFP4_ERR_SHAPE;
-    if (!std::isfinite(d->scale) || !(d->scale > 0.0f) || !std::isfinite(d->softcap) || d->softcap < 0.0f)
+    // (from 2^127 on scale log2 e, in which the scores are held, may overflow)
+    if (!(d->scale > 0.0f) || !(d->scale < 0x1p127f) || !std::isfinite(d->softcap) || d->softcap < 0.0f)
         return NVFP4_ERR_INVALID_ARG;
     *a = nvfp4::Attention{};
     a->tokens = d->tokens;
@@ -188,7 +189,9 @@ nvfp4_status check_attention(const nvfp4_attention_desc* d, const nvfp4_heads* q
     a->kv_heads = d->kv_heads;
     a->head_dim = d->head_dim;
     a->scale = d->scale;
-    a->softcap = d->softcap;
+    // a cap above 2^64 changes no score that FP32 holds a digit of exp's argument of
+    // (2^24), and near the type's end its constants would overflow
+    a->softcap = d->softcap > 0x1p64f ? 0.0f : d->softcap;
     a->slopes = d->slopes;
     a->spans = d->spans;
     if (d->tokens == 0) return NVFP4_OK;

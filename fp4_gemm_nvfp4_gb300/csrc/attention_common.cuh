@@ -91,7 +91,10 @@ struct Scores {
     float poly[kCapTerms], tiny_poly[kTinyTerms];         // times cap_log2
 };
 
+// Tiny caps and large ratios are held to 2^-96 and 2^96, where every constant is
+// a normal number: no score changes by more than 2^-96 (unless its product is below that).
 inline Scores make_scores(float scale, float softcap) {
+    constexpr double kTiniest = 0x1p-96, kSteepest = 0x1p96;
     Scores s{};
     if (!(softcap > 0.0f)) {
         s.mult = scale * kLog2e;
@@ -100,7 +103,8 @@ inline Scores make_scores(float scale, float softcap) {
     const double c[kCapTerms] = {0.9999999704657849,    -0.33332954098406786, 0.1332533884815183,
                                  -0.053341115329099964, 0.019576216425263346, -0.004711522234826275};
     const double t[kTinyTerms] = {0.9999999402412297, -0.33331971067426597, 0.13284431227543994, -0.04826890785276893};
-    const double cap_log2 = (double)softcap * (double)kLog2e, kappa = (double)scale / softcap;
+    const double cap = softcap > kTiniest ? softcap : kTiniest, ratio = (double)scale / softcap;
+    const double cap_log2 = cap * (double)kLog2e, kappa = ratio < kSteepest ? ratio : kSteepest;
     s.mult = (float)(2.0 * (double)kLog2e * kappa);
     s.cap_log2 = (float)cap_log2;
     s.over_cap = (float)(1.0 / cap_log2);

@@ -520,7 +520,7 @@ NVFP4_API nvfp4_status nvfp4_attention_spans(const int32_t *offsets, int64_t doc
  * out's own rounding), the result once more to BF16.
  * Requirements: head_dim as for nvfp4_qk_norm_rope, q_heads a multiple of
  * kv_heads, tokens < 2^31 - 256 [SHAPE]; data 16-byte aligned, strides positive
- * multiples of 8 [ALIGNMENT]; finite scale > 0 and softcap >= 0
+ * multiples of 8 [ALIGNMENT]; 0 < scale < 2^127, finite softcap >= 0
  * [INVALID_ARG].  tokens = 0 enqueues nothing.
  */
 NVFP4_API nvfp4_status nvfp4_attention(const nvfp4_attention_desc *desc, const nvfp4_heads *q, const nvfp4_heads *k,
