@@ -735,10 +735,7 @@ nvfp4_status nvfp4_device_error(nvfp4_stream_t stream) {
     const ApiRange range("nvfp4_device_error");
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return NVFP4_ERR_CUDA;
     unsigned int status = 0;
-    if (nvfp4::gemm_read_and_clear_status(&status) != cudaSuccess ||
-        nvfp4::attention_forward_status_read_and_clear(&status) != cudaSuccess ||
-        nvfp4::attention_backward_status_read_and_clear(&status) != cudaSuccess)
-        return NVFP4_ERR_CUDA;
+    if (nvfp4::read_and_clear_status(&status) != cudaSuccess) return NVFP4_ERR_CUDA;
     return (status & nvfp4::kStatusTimeoutBit) ? NVFP4_ERR_TIMEOUT : NVFP4_OK;
 }
 

@@ -105,6 +105,7 @@ struct Params {
     Extent xdv, xdk;
     int32_t head_dim;
     Workspace ws;
+    unsigned int* status;            // the status word
     uint64_t timeout_ns;
     uint32_t withhold;               // test support: the loads of the first item never come
 };
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto give_up = [&](bool one) {
         if (one) {
             *abort_flag = 1u;
-            atomicOr(&g_attention_status, kStatusTimeoutBit);
+            atomicOr(p.status, kStatusTimeoutBit);
         }
     };
 
@@ -879,6 +880,8 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
     const int splits = split_count(a.tokens, a.q_heads, a.kv_heads);
     p.ws = carve(a.workspace, a.tokens, a.q_heads, a.kv_heads, a.head_dim, splits, nullptr);
     p.splits = 1;
+    p.status = status_word();
+    if (!p.status) return cudaErrorInvalidDevice;
     const uint64_t limit_ns = attention_wait_limit_ns(true, a.tokens, a.q_heads, a.kv_heads);
     p.timeout_ns = attention_timeout(limit_ns, &p.withhold);
     if ((uint64_t)p.tiles * (uint64_t)a.q_heads > 0x7FFFFFFFull) return cudaErrorInvalidValue;
@@ -920,9 +923,5 @@ cudaError_t launch_attention_backward(const Attention& a, cudaStream_t stream) {
 cudaError_t attention_backward_bounds_read_and_clear(uint64_t* n) { return bounds_read_and_clear_local(n); }
 
 void arm_attention_backward_fault(uint64_t timeout_ns) { g_attention_armed_ns.store(timeout_ns); }
-
-cudaError_t attention_backward_status_read_and_clear(unsigned int* status) {
-    return attention_status_read_and_clear_local(status);
-}
 
 }  // namespace nvfp4

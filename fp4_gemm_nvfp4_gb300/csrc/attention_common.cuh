@@ -16,9 +16,6 @@ namespace nvfp4 {
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.693147180559945309f;
 
-// Status word of this translation unit's kernels (kStatusTimeoutBit).
-static __device__ unsigned int g_attention_status = 0;
-
 // Wait limit of the next launch that leaves out one arrival (0: none armed).
 static std::atomic<uint64_t> g_attention_armed_ns{0};
 
@@ -47,15 +44,6 @@ inline uint64_t attention_timeout(uint64_t limit_ns, uint32_t* withhold) {
     const uint64_t armed = g_attention_armed_ns.exchange(0);
     *withhold = armed ? 1u : 0u;
     return armed ? armed : limit_ns;
-}
-
-inline cudaError_t attention_status_read_and_clear_local(unsigned int* status) {
-    unsigned int v = 0;
-    const unsigned int zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&v, g_attention_status, sizeof v);
-    if (e == cudaSuccess && v) e = cudaMemcpyToSymbol(g_attention_status, &zero, sizeof zero);
-    *status |= v;
-    return e;
 }
 
 // What a kernel's scores are made of, as a template argument: code that another

@@ -71,6 +71,7 @@ struct Params {
     const int32_t* spans;
     float* lse;
     Extent xlse;
+    unsigned int* status;            // the status word
     uint64_t timeout_ns;
     uint32_t withhold;               // test support: the loads of the first item never come
 };
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto give_up = [&](bool one) {
         if (one) {
             *abort_flag = 1u;
-            atomicOr(&g_attention_status, kStatusTimeoutBit);
+            atomicOr(p.status, kStatusTimeoutBit);
         }
     };
 
@@ -687,6 +688,8 @@ cudaError_t launch(const Attention& a, cudaStream_t stream) {
     p.spans = a.spans;
     p.lse = a.lse;
     p.xlse = extent_of(a.lse, a.tokens * a.q_heads * 4);
+    p.status = status_word();
+    if (!p.status) return cudaErrorInvalidDevice;
     p.timeout_ns = attention_timeout(attention_wait_limit_ns(false, a.tokens, a.q_heads, a.kv_heads), &p.withhold);
     const uint64_t grid = (uint64_t)p.tiles * p.items_per_tile;
     if (grid > 0x7FFFFFFFull) return cudaErrorInvalidValue;
@@ -723,9 +726,6 @@ cudaError_t launch_attention(const Attention& a, cudaStream_t stream) {
 
 void arm_attention_forward_fault(uint64_t timeout_ns) { g_attention_armed_ns.store(timeout_ns); }
 
-cudaError_t attention_forward_status_read_and_clear(unsigned int* status) {
-    return attention_status_read_and_clear_local(status);
-}
 cudaError_t attention_forward_bounds_read_and_clear(uint64_t* n) { return bounds_read_and_clear_local(n); }
 
 }  // namespace nvfp4

@@ -49,7 +49,8 @@
 
 namespace nvfp4 {
 
-static __device__ unsigned int g_gemm_status = 0;
+// The library's status word (kStatusTimeoutBit): kernels of other files get its address.
+static __device__ unsigned int g_status = 0;
 
 // Wait limit of the next GEMM launch that withholds one arrival (0: none
 // armed); set by arm_gemm_fault, consumed by launch_gemm.
@@ -261,7 +262,7 @@ __device__ __forceinline__ void mma_bf16_pair_stage(uint32_t d_tmem, uint32_t a_
 
 __device__ __forceinline__ void record_timeout(volatile uint32_t* abort_flag) {
     *abort_flag = 1u;
-    atomicOr(&g_gemm_status, kStatusTimeoutBit);
+    atomicOr(&g_status, kStatusTimeoutBit);
 }
 
 // Named barrier over the scale warps (id 2); id 0 and the cluster barrier
@@ -1203,11 +1204,24 @@ cudaError_t launch_gemm(const GemmOperand& a, const GemmOperand& b, void* d, int
 
 void arm_gemm_fault(uint64_t timeout_ns) { g_armed_fault_ns.store(timeout_ns); }
 
-cudaError_t gemm_read_and_clear_status(unsigned int* status) {
+unsigned int* status_word() {
+    static std::atomic<unsigned int*> words[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+    unsigned int* word = words[dev].load(std::memory_order_relaxed);
+    void* p = nullptr;
+    if (!word && cudaGetSymbolAddress(&p, g_status) == cudaSuccess) {
+        word = static_cast<unsigned int*>(p);
+        words[dev].store(word, std::memory_order_relaxed);
+    }
+    return word;
+}
+
+cudaError_t read_and_clear_status(unsigned int* status) {
     unsigned int v = 0, zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&v, g_gemm_status, sizeof v);
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_status, sizeof v);
     if (e != cudaSuccess) return e;
-    if (v) e = cudaMemcpyToSymbol(g_gemm_status, &zero, sizeof zero);
+    if (v) e = cudaMemcpyToSymbol(g_status, &zero, sizeof zero);
     *status = v;
     return e;
 }

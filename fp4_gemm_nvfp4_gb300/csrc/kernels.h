@@ -88,12 +88,12 @@ cudaError_t launch_gemm(const GemmOperand& a, const GemmOperand& b, void* d, int
                         cudaStream_t stream, const LowRank* lora = nullptr, float* amax_out = nullptr,
                         uint32_t rht_mask = 0, const Axpby* axpby = nullptr);
 
-// Read and clear the GEMM kernels' device status word (synchronous).
-cudaError_t gemm_read_and_clear_status(unsigned int* status);
+// The device address of the current device's status word (null on an error),
+// which the kernels with bounded waits set bits of.
+unsigned int* status_word();
 
-// As gemm_read_and_clear_status, for the attention kernels: or-ed into *status.
-cudaError_t attention_forward_status_read_and_clear(unsigned int* status);
-cudaError_t attention_backward_status_read_and_clear(unsigned int* status);
+// Read and clear the status word (synchronous).
+cudaError_t read_and_clear_status(unsigned int* status);
 
 // Add the stores that the debug build's bounds check skipped in one source
 // file's kernels to *n and clear that count (synchronous; in the regular
