@@ -23,17 +23,23 @@
 // itself in rows that one key dominates.  The dq kernel therefore also sums
 // the exact delta = sum_j P dP in FP32; with P' = P (1 - tanh^2) its acc1
 // turns dq for the difference, dq = scale (acc2 + (delta~ - delta) acc1), and
-// the dk dv kernel uses the exact delta.  That product is one of eight.  Warps: 0 TMA loads, 1 MMA issue, 2 the next item, 4-19 softmax (a
+// the dk dv kernel uses the exact delta.  That product is one of eight.
+//
+// P, P' and dZ are rounded to BF16 because the tensor cores take them so beside
+// BF16 tiles: each term of a gradient is off by at most 2^-8 of itself; scores,
+// delta and every sum are FP32.
+//
+// Warps: 0 TMA loads, 1 MMA issue, 2 the next item, 4-19 softmax (a
 // lane one row, each group of four warps 32 of the columns).  As in the
 // forward pass a CTA goes on to blocks that have not started.
 //
 // Eight products are made where five are counted (S and dP twice, P' k): 8192
-// causal tokens, 24/12 heads of 128: 957 us (dq and dk dv about half each),
-// 1075 TFLOP/s of the five, 1720 of the eight (87 % of a BF16 library GEMM).
-// 4 x 2048 tokens: 297 us (the masked tiles, and 4 us from each dq tile's last
+// causal tokens, 24/12 heads of 128: 943-957 us (dq and dk dv about half each),
+// 1080 TFLOP/s of the five, 1730 of the eight (88 % of a BF16 library GEMM).
+// 4 x 2048 tokens: 301 us (the masked tiles, and 4 us from each dq tile's last
 // scores to the next one's first, most of it reading its out and dout beside
-// the TMA loads).  64 dims: 665 us.  16/4 heads: 655-675 us, 900 with a cap of
-// 30, 719 with the bias, 954 with both.
+// the TMA loads).  64 dims: 670 us.  16/4 heads: 655-675 us, 909 with a cap of
+// 30, 725 with the bias, 963 with both.
 #include <algorithm>
 
 #include <cuda.h>

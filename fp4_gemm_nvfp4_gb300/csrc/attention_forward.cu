@@ -20,13 +20,20 @@
 // log2) since it was last scaled: until then P is at most 2^8, which BF16
 // and the FP32 sums hold as precisely, and the factor cancels in O / sum.
 //
+// P is rounded to BF16 because the tensor cores take it so beside a BF16 V:
+// each term of O is off by at most 2^-8 of itself, as out's own rounding, and
+// the row's sum is that of the unrounded P in FP32.
+//
 // Bound by the tensor cores' wait for the softmax: 8192 causal tokens, 24/12
-// heads of 128: 248 us, 1660 TFLOP/s of the pairs' work (84 % of a BF16
-// library GEMM); 32768 tokens 1690 TFLOP/s.  4 x 2048 tokens: 81 us, 1275
+// heads of 128: 247 us, 1670 TFLOP/s of the pairs' work (85 % of a BF16
+// library GEMM); 32768 tokens 1690 TFLOP/s.  4 x 2048 tokens: 82 us, 1260
 // TFLOP/s (the masked tiles, and 1.5 us from each item's last scores to the
-// next one's first).  64 dims: 213-225 us (the same softmax for half the
-// products).  16/4 heads: 168 us, 250 with a cap of 30 (the polynomial and its
-// check, 5 operations per score), 248 with the bias, 340 with both.
+// next one's first).  64 dims: 205-227 us; half the products with the same
+// softmax, but S a step ahead, which would hide the wait for it, gained nothing:
+// what bounds it is not settled.  Head sizes between the tiles' are multiplied
+// as 64 or 128 dims (80 takes 60 % more products than it has, 96 a third).
+// 16/4 heads: 168 us, 250 with a cap of 30 (the polynomial and its check, 5
+// operations per score, and the running maximum), 250 with the bias, 341 with both.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -18,7 +18,7 @@
 // takes units of queries or of keys only: one weight, and one sum of its
 // gradient, in registers.  Both passes are bound by HBM: 4 bytes per element
 // forward, 6 backward; 24/12 heads of 128, 16384 tokens, calls in a row:
-// 51 us (5.90 TB/s, 88 % of a copy) and 80 us (5.67 TB/s), 8192 tokens 27.5 us.  Loading the
+// 51 us (5.90 TB/s, 88 % of a copy) and 81 us (5.62 TB/s), 8192 tokens 27.6 us.  Loading the
 // next unit ahead of a unit's arithmetic (56 to 80 us: the registers cost
 // blocks) and packed FP32 arithmetic (no change) were tried.
 #include <cuda_bf16.h>

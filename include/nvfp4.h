@@ -455,7 +455,9 @@ NVFP4_API nvfp4_status nvfp4_qk_norm_rope(const void *qkv, int64_t ld_qkv, int64
  *  dqkv         BF16 [tokens][ld_dqkv]: the first (q_heads + kv_heads) *
  *               head_dim columns are written, what follows keeps its values
  *               (nvfp4_attention_backward writes dv there).  May be qkv.
- *  dq_weight, dk_weight  FP32 [head_dim], overwritten (0 for no tokens).
+ *  dq_weight, dk_weight  FP32 [head_dim], overwritten (0 for no tokens).  Every
+ *               token takes part: a NaN in padding reaches them, also where its
+ *               dq and dk are 0.
  *  workspace    nvfp4_qk_norm_rope_backward_workspace_size(head_dim) bytes,
  *               16-byte aligned.
  * The sums run in a fixed order: equal inputs give equal bits.
@@ -480,14 +482,15 @@ NVFP4_API nvfp4_status nvfp4_qk_norm_rope_backward(const nvfp4_heads *dq, const 
  * document, prefix and window masks and padding are all such intervals
  * (nvfp4_attention_spans writes the common ones); a row whose interval is
  * empty gets out = 0, lse = -inf and gradients 0.  Intervals are cut to
- * [0, tokens).  Work is spent only on 128 x 128 tiles that some interval
- * reaches.  Inputs are finite; the rows of keys and values that no interval
- * reaches, and of q, out and dout with an empty interval, may hold anything
- * (NaN, infinities): padding need not be cleared, wherever it lies.  A row
- * that sees a NaN, or whose scores overflow, gets NaN in out and lse.  Scores
- * are FP32 and P is formed from their difference to a maximum or to lse: from
- * a size of 2^24 on, where FP32 steps by 1, P has no digits left, and rows with
- * scores beyond 2^30 may be NaN or 0.
+ * [0, tokens).  Work is spent only on tiles of 128 x 128 between the first and
+ * the last that intervals of their rows (backward: their columns too) reach.
+ * Inputs are finite; the rows of keys and values that no interval reaches, and
+ * of q, out and dout with an empty interval, may hold anything (NaN,
+ * infinities): padding need not be cleared, wherever it lies.  A row with a NaN
+ * in its q or in a key that it sees, or whose scores overflow, gets NaN in out
+ * and lse.  Scores are FP32 and P is formed from their difference to a maximum
+ * or to lse: from a size of 2^24 on, where FP32 steps by 1, P has no digits
+ * left, and rows with scores beyond 2^30 may be NaN or 0.
  */
 typedef struct {
     int64_t        tokens;
