@@ -31,6 +31,9 @@ NVFP4_OUT_BF16 = 0
 NVFP4_OUT_FP32 = 1
 NVFP4_ROWWISE = 1
 NVFP4_COLWISE = 2
+NVFP4_GATE_NONE = 0
+NVFP4_GATE_CHANNEL = 1
+NVFP4_GATE_TOKEN = 2
 
 EXPORTED = ("nvfp4_scale_bytes", "nvfp4_quantize_workspace_size", "nvfp4_quantize",
             "nvfp4_rht_quantize", "nvfp4_gemm", "nvfp4_dequantize", "nvfp4_status_string",
@@ -41,6 +44,8 @@ EXPORTED = ("nvfp4_scale_bytes", "nvfp4_quantize_workspace_size", "nvfp4_quantiz
             "nvfp4_qk_norm_rope", "nvfp4_qk_norm_rope_backward_workspace_size", "nvfp4_qk_norm_rope_backward",
             "nvfp4_attention_spans", "nvfp4_attention", "nvfp4_attention_backward_workspace_size",
             "nvfp4_attention_backward",
+            "nvfp4_checkpoint_encode", "nvfp4_checkpoint_decode", "nvfp4_block_norm",
+            "nvfp4_block_norm_backward_workspace_size", "nvfp4_block_norm_backward",
             "nvfp4_testing_arm_gemm_timeout", "nvfp4_testing_arm_attention_timeout",
             "nvfp4_testing_attention_wait_limit_us", "nvfp4_testing_bounds_violations",
             "nvfp4_testing_bounds_shrink")
@@ -61,6 +66,18 @@ class nvfp4_attention_desc(ctypes.Structure):
     _fields_ = [("tokens", ctypes.c_int64), ("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
                 ("slopes", ctypes.c_void_p), ("spans", ctypes.c_void_p)]
+
+
+class nvfp4_checkpoint(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int64), ("scales", ctypes.c_void_p),
+                ("ld_scales", ctypes.c_int64)]
+
+
+class nvfp4_block_norm_desc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("width", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("residual_scale", ctypes.c_float), ("residual_dtype", ctypes.c_int32),
+                ("post_weight", ctypes.c_void_p), ("pre_weight", ctypes.c_void_p), ("gate_kind", ctypes.c_int32),
+                ("gate", ctypes.c_void_p), ("ld_gate", ctypes.c_int64)]
 
 
 class NVFP4Error(RuntimeError):
@@ -130,6 +147,16 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.nvfp4_attention_backward_workspace_size.restype = sz
     L.nvfp4_attention_backward.argtypes = [dp, hp, hp, hp, hp, hp, vp, hp, hp, hp, vp, sz, vp]
     L.nvfp4_attention_backward.restype = i32
+    kp, np_ = ctypes.POINTER(nvfp4_checkpoint), ctypes.POINTER(nvfp4_block_norm_desc)
+    L.nvfp4_checkpoint_encode.argtypes, L.nvfp4_checkpoint_encode.restype = [vp, i64, i64, i64, kp, vp], i32
+    L.nvfp4_checkpoint_decode.argtypes, L.nvfp4_checkpoint_decode.restype = [kp, i64, i64, vp, i64, i32, vp], i32
+    L.nvfp4_block_norm.argtypes = [np_, vp, i64, vp, i64, vp, i64, vp, i64, kp, vp]
+    L.nvfp4_block_norm.restype = i32
+    L.nvfp4_block_norm_backward_workspace_size.argtypes = [c32]
+    L.nvfp4_block_norm_backward_workspace_size.restype = sz
+    L.nvfp4_block_norm_backward.argtypes = [np_, vp, i64, vp, i64, vp, i64, kp, vp, i64, vp, i64, vp, vp, vp, i64, vp,
+                                            sz, vp]
+    L.nvfp4_block_norm_backward.restype = i32
     L.nvfp4_dequantize.argtypes = [tp, vp, i64, i32, vp]
     L.nvfp4_dequantize.restype = i32
     L.nvfp4_status_string.argtypes, L.nvfp4_status_string.restype = [i32], ctypes.c_char_p
@@ -279,6 +306,37 @@ def nvfp4_attention_backward_workspace_size(tokens, q_heads, kv_heads, head_dim)
 
 def nvfp4_attention_backward(desc, dout, q, k, v, out, lse, dq, dk, dv, workspace, workspace_bytes, stream):
     return load().nvfp4_attention_backward(desc, dout, q, k, v, out, lse, dq, dk, dv, workspace, workspace_bytes, stream)
+
+
+def nvfp4_checkpoint_encode(x, rows, cols, ld_x, out, stream):
+    """A BF16 matrix to the 8-bit form kept for the backward pass."""
+    return load().nvfp4_checkpoint_encode(x, rows, cols, ld_x, _ref(out), stream)
+
+
+def nvfp4_checkpoint_decode(in_, rows, cols, y, ldy, out_dtype, stream):
+    """The values of an 8-bit matrix as BF16 or FP32."""
+    return load().nvfp4_checkpoint_decode(_ref(in_), rows, cols, y, ldy, out_dtype, stream)
+
+
+def nvfp4_block_norm(desc, residual, ld_residual, branch, ld_branch, residual_out, ld_residual_out, normed, ld_normed,
+                     branch_kept, stream):
+    """The norms after and before a block with its gate and the residual's scale."""
+    return load().nvfp4_block_norm(_ref(desc), residual, ld_residual, branch, ld_branch, residual_out, ld_residual_out,
+                                   normed, ld_normed, _ref(branch_kept), stream)
+
+
+def nvfp4_block_norm_backward_workspace_size(width):
+    return load().nvfp4_block_norm_backward_workspace_size(width)
+
+
+def nvfp4_block_norm_backward(desc, dresidual_out, ld_dresidual_out, dnormed, ld_dnormed, residual_out,
+                              ld_residual_out, branch, dresidual, ld_dresidual, dbranch, ld_dbranch, dpost_weight,
+                              dpre_weight, dgate, ld_dgate, workspace, workspace_bytes, stream):
+    """Gradients of nvfp4_block_norm's inputs, weights and gate."""
+    return load().nvfp4_block_norm_backward(_ref(desc), dresidual_out, ld_dresidual_out, dnormed, ld_dnormed,
+                                            residual_out, ld_residual_out, _ref(branch), dresidual, ld_dresidual,
+                                            dbranch, ld_dbranch, dpost_weight, dpre_weight, dgate, ld_dgate, workspace,
+                                            workspace_bytes, stream)
 
 
 def nvfp4_status_string(status):

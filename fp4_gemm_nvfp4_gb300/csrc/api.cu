@@ -173,6 +173,67 @@ nvfp4_status check_norm_rope(const nvfp4::NormRope& a) {
     return NVFP4_OK;
 }
 
+// A matrix of `esz`-byte elements whose rows start on 16-byte boundaries.
+nvfp4_status check_rows(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t esz) {
+    if (!p) return NVFP4_ERR_INVALID_ARG;
+    if (ld < cols) return NVFP4_ERR_SHAPE;
+    if (rows > 0 && ld > (int64_t(1) << 50) / rows) return NVFP4_ERR_UNSUPPORTED;   // (past any address)
+    if (!aligned16(p) || ld * esz % 16 != 0) return NVFP4_ERR_ALIGNMENT;
+    return NVFP4_OK;
+}
+
+// A matrix kept for the backward pass, in the 8-bit form only if only_8bit.
+nvfp4_status check_checkpoint(const nvfp4_checkpoint* t, int64_t rows, int64_t cols, bool only_8bit) {
+    if (!t || (only_8bit && !t->scales)) return NVFP4_ERR_INVALID_ARG;
+    nvfp4_status s;
+    if ((s = check_rows(t->data, rows, cols, t->ld, t->scales ? 1 : 2)) != NVFP4_OK) return s;
+    if (t->scales && (s = check_rows(t->scales, rows, ceil_div(cols, 32), t->ld_scales, 1)) != NVFP4_OK) return s;
+    return NVFP4_OK;
+}
+
+nvfp4::CheckpointView to_checkpoint(const nvfp4_checkpoint* t) {
+    return nvfp4::CheckpointView{t->data, t->ld, t->scales, t->ld_scales};
+}
+
+nvfp4_status check_checkpoint_shape(int64_t rows, int64_t cols) {
+    if (rows < 0 || cols < 0 || cols % 8 != 0) return NVFP4_ERR_SHAPE;
+    if (cols > (int64_t(1) << 24) || rows >= (int64_t(1) << 40)) return NVFP4_ERR_UNSUPPORTED;
+    if (rows * ceil_div(cols, 32) >= (int64_t(1) << 40)) return NVFP4_ERR_UNSUPPORTED;
+    return NVFP4_OK;
+}
+
+// The arguments the two calls of the norms around a block share; *a gets them.
+nvfp4_status check_block_norm(const nvfp4_block_norm_desc* d, nvfp4::BlockNorm* a) {
+    if (!d) return NVFP4_ERR_INVALID_ARG;
+    if (d->tokens < 0 || d->tokens >= kMaxTokens || d->width < 8 || d->width % 8 != 0) return NVFP4_ERR_SHAPE;
+    if (d->width > nvfp4::kBlockNormMaxWidth) return NVFP4_ERR_UNSUPPORTED;
+    if (!std::isfinite(d->eps) || d->eps < 0.0f || !std::isfinite(d->residual_scale)) return NVFP4_ERR_INVALID_ARG;
+    if (d->residual_dtype != NVFP4_OUT_BF16 && d->residual_dtype != NVFP4_OUT_FP32) return NVFP4_ERR_INVALID_ARG;
+    if (d->gate_kind != NVFP4_GATE_NONE && d->gate_kind != NVFP4_GATE_CHANNEL && d->gate_kind != NVFP4_GATE_TOKEN)
+        return NVFP4_ERR_INVALID_ARG;
+    if (!aligned16(d->post_weight) || !aligned16(d->pre_weight)) return NVFP4_ERR_ALIGNMENT;
+    *a = nvfp4::BlockNorm{};
+    a->tokens = d->tokens;
+    a->width = d->width;
+    a->eps = d->eps;
+    a->scale = d->residual_scale;
+    a->fp32 = d->residual_dtype == NVFP4_OUT_FP32;
+    a->post = d->post_weight;
+    a->pre = d->pre_weight;
+    a->gate_kind = d->gate_kind;
+    if (d->gate_kind == NVFP4_GATE_CHANNEL) {
+        if (!d->gate) return NVFP4_ERR_INVALID_ARG;
+        if (!aligned16(d->gate)) return NVFP4_ERR_ALIGNMENT;
+        a->gate = d->gate;
+    } else if (d->gate_kind == NVFP4_GATE_TOKEN && d->tokens > 0) {
+        nvfp4_status s;
+        if ((s = check_rows(d->gate, d->tokens, d->width, d->ld_gate, 2)) != NVFP4_OK) return s;
+        a->gate = d->gate;
+        a->ld_gate = d->ld_gate;
+    }
+    return NVFP4_OK;
+}
+
 // The arguments the two attention entry points share; *a gets the shape.
 nvfp4_status check_attention(const nvfp4_attention_desc* d, const nvfp4_heads* q, const nvfp4_heads* k,
                              const nvfp4_heads* v, const nvfp4_heads* out, const float* lse, nvfp4::Attention* a) {
@@ -667,6 +728,143 @@ nvfp4_status nvfp4_attention_backward(const nvfp4_attention_desc* desc, const nv
                : NVFP4_ERR_CUDA;
 }
 
+nvfp4_status nvfp4_checkpoint_encode(const void* x, int64_t rows, int64_t cols, int64_t ld_x,
+                                     const nvfp4_checkpoint* out, nvfp4_stream_t stream) {
+    const ApiRange range("nvfp4_checkpoint_encode");
+    nvfp4_status s;
+    if ((s = check_checkpoint_shape(rows, cols)) != NVFP4_OK) return s;
+    if (rows == 0 || cols == 0) return NVFP4_OK;
+    if ((s = check_rows(x, rows, cols, ld_x, 2)) != NVFP4_OK) return s;
+    if ((s = check_checkpoint(out, rows, cols, true)) != NVFP4_OK) return s;
+    return nvfp4::launch_checkpoint_encode(static_cast<const uint16_t*>(x), ld_x, rows, cols, to_checkpoint(out),
+                                           reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? NVFP4_OK
+               : NVFP4_ERR_CUDA;
+}
+
+nvfp4_status nvfp4_checkpoint_decode(const nvfp4_checkpoint* in, int64_t rows, int64_t cols, void* y, int64_t ldy,
+                                     nvfp4_dtype out_dtype, nvfp4_stream_t stream) {
+    const ApiRange range("nvfp4_checkpoint_decode");
+    if (out_dtype != NVFP4_OUT_BF16 && out_dtype != NVFP4_OUT_FP32) return NVFP4_ERR_INVALID_ARG;
+    nvfp4_status s;
+    if ((s = check_checkpoint_shape(rows, cols)) != NVFP4_OK) return s;
+    if (rows == 0 || cols == 0) return NVFP4_OK;
+    if ((s = check_checkpoint(in, rows, cols, true)) != NVFP4_OK) return s;
+    if ((s = check_rows(y, rows, cols, ldy, out_dtype == NVFP4_OUT_FP32 ? 4 : 2)) != NVFP4_OK) return s;
+    return nvfp4::launch_checkpoint_decode(to_checkpoint(in), rows, cols, y, ldy, out_dtype == NVFP4_OUT_FP32,
+                                           reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? NVFP4_OK
+               : NVFP4_ERR_CUDA;
+}
+
+nvfp4_status nvfp4_block_norm(const nvfp4_block_norm_desc* desc, const void* residual, int64_t ld_residual,
+                              const void* branch, int64_t ld_branch, void* residual_out, int64_t ld_residual_out,
+                              void* normed, int64_t ld_normed, const nvfp4_checkpoint* branch_kept,
+                              nvfp4_stream_t stream) {
+    const ApiRange range("nvfp4_block_norm");
+    nvfp4::BlockNorm a;
+    nvfp4_status s;
+    if ((s = check_block_norm(desc, &a)) != NVFP4_OK) return s;
+    if (a.tokens == 0) return NVFP4_OK;
+    const int64_t T = a.tokens, H = a.width, esz = a.fp32 ? 4 : 2;
+    if (!branch && (a.post || a.gate_kind != NVFP4_GATE_NONE || branch_kept)) return NVFP4_ERR_INVALID_ARG;
+    if ((normed != nullptr) != (a.pre != nullptr) || (!normed && !residual_out)) return NVFP4_ERR_INVALID_ARG;
+    if ((s = check_rows(residual, T, H, ld_residual, esz)) != NVFP4_OK) return s;
+    if (branch && (s = check_rows(branch, T, H, ld_branch, 2)) != NVFP4_OK) return s;
+    if (residual_out && (s = check_rows(residual_out, T, H, ld_residual_out, esz)) != NVFP4_OK) return s;
+    if (residual_out == residual && ld_residual_out != ld_residual) return NVFP4_ERR_INVALID_ARG;
+    if (normed && (s = check_rows(normed, T, H, ld_normed, 2)) != NVFP4_OK) return s;
+    if (branch_kept && (s = check_checkpoint(branch_kept, T, H, true)) != NVFP4_OK) return s;
+    a.residual = residual;
+    a.ld_residual = ld_residual;
+    a.branch = static_cast<const uint16_t*>(branch);
+    a.ld_branch = ld_branch;
+    if (branch_kept) a.kept = to_checkpoint(branch_kept);
+    a.residual_out = residual_out;
+    a.ld_residual_out = ld_residual_out;
+    a.normed = static_cast<uint16_t*>(normed);
+    a.ld_normed = ld_normed;
+    return nvfp4::launch_block_norm(a, false, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? NVFP4_OK
+                                                                                                     : NVFP4_ERR_CUDA;
+}
+
+size_t nvfp4_block_norm_backward_workspace_size(int32_t width) {
+    if (width <= 0 || width > nvfp4::kBlockNormMaxWidth) return 0;
+    return (size_t)nvfp4::kBlockNormMaxBlocks * 2 * (size_t)width * sizeof(float);
+}
+
+nvfp4_status nvfp4_block_norm_backward(const nvfp4_block_norm_desc* desc, const void* dresidual_out,
+                                       int64_t ld_dresidual_out, const void* dnormed, int64_t ld_dnormed,
+                                       const void* residual_out, int64_t ld_residual_out,
+                                       const nvfp4_checkpoint* branch, void* dresidual, int64_t ld_dresidual,
+                                       void* dbranch, int64_t ld_dbranch, float* dpost_weight, float* dpre_weight,
+                                       void* dgate, int64_t ld_dgate, void* workspace, size_t workspace_bytes,
+                                       nvfp4_stream_t stream) {
+    const ApiRange range("nvfp4_block_norm_backward");
+    nvfp4::BlockNorm a;
+    nvfp4_status s;
+    if ((s = check_block_norm(desc, &a)) != NVFP4_OK) return s;
+    const int64_t T = a.tokens, H = a.width, esz = a.fp32 ? 4 : 2;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if ((dpost_weight != nullptr) != (a.post != nullptr) || (dpre_weight != nullptr) != (a.pre != nullptr))
+        return NVFP4_ERR_INVALID_ARG;
+    if (((reinterpret_cast<uintptr_t>(dpost_weight) | reinterpret_cast<uintptr_t>(dpre_weight)) & 3u) != 0)
+        return NVFP4_ERR_ALIGNMENT;
+    const bool channel = a.gate_kind == NVFP4_GATE_CHANNEL;
+    if (channel) {
+        if (!dgate) return NVFP4_ERR_INVALID_ARG;
+        if ((reinterpret_cast<uintptr_t>(dgate) & 3u) != 0) return NVFP4_ERR_ALIGNMENT;
+    }
+    if (T == 0) {   // empty sums
+        for (void* sum : {static_cast<void*>(dpost_weight), static_cast<void*>(dpre_weight), channel ? dgate : nullptr})
+            if (sum && cudaMemsetAsync(sum, 0, (size_t)H * sizeof(float), st) != cudaSuccess) return NVFP4_ERR_CUDA;
+        return NVFP4_OK;
+    }
+    if (!branch && (a.post || a.gate_kind != NVFP4_GATE_NONE)) return NVFP4_ERR_INVALID_ARG;
+    if ((dbranch != nullptr) != (branch != nullptr) || (dnormed != nullptr) != (a.pre != nullptr) ||
+        (residual_out == nullptr && a.pre) || (!dresidual_out && !dnormed))
+        return NVFP4_ERR_INVALID_ARG;
+    if (dresidual_out && (s = check_rows(dresidual_out, T, H, ld_dresidual_out, esz)) != NVFP4_OK) return s;
+    if ((s = check_rows(dresidual, T, H, ld_dresidual, esz)) != NVFP4_OK) return s;
+    if (dresidual == dresidual_out && ld_dresidual != ld_dresidual_out) return NVFP4_ERR_INVALID_ARG;
+    if (a.pre) {
+        if ((s = check_rows(dnormed, T, H, ld_dnormed, 2)) != NVFP4_OK) return s;
+        if ((s = check_rows(residual_out, T, H, ld_residual_out, esz)) != NVFP4_OK) return s;
+        a.dnormed = static_cast<const uint16_t*>(dnormed);
+        a.ld_dnormed = ld_dnormed;
+        a.residual = residual_out;
+        a.ld_residual = ld_residual_out;
+    }
+    if (branch) {
+        if ((s = check_checkpoint(branch, T, H, false)) != NVFP4_OK) return s;
+        if ((s = check_rows(dbranch, T, H, ld_dbranch, 2)) != NVFP4_OK) return s;
+        if (branch->scales) {
+            a.kept = to_checkpoint(branch);
+        } else {
+            a.branch = static_cast<const uint16_t*>(branch->data);
+            a.ld_branch = branch->ld;
+        }
+        a.dbranch = static_cast<uint16_t*>(dbranch);
+        a.ld_dbranch = ld_dbranch;
+    }
+    if (a.gate_kind == NVFP4_GATE_TOKEN && (s = check_rows(dgate, T, H, ld_dgate, 2)) != NVFP4_OK) return s;
+    a.dgate = a.gate_kind == NVFP4_GATE_NONE ? nullptr : dgate;
+    a.ld_dgate = ld_dgate;
+    a.dresidual = dresidual_out;
+    a.ld_dresidual = ld_dresidual_out;
+    a.dresidual_out = dresidual;
+    a.ld_dresidual_out = ld_dresidual;
+    a.dpost = dpost_weight;
+    a.dpre = dpre_weight;
+    if (dpost_weight || dpre_weight || channel) {
+        if (!workspace || !aligned16(workspace) ||
+            workspace_bytes < nvfp4_block_norm_backward_workspace_size(desc->width))
+            return NVFP4_ERR_WORKSPACE;
+        a.partials = static_cast<float*>(workspace);
+    }
+    return nvfp4::launch_block_norm(a, true, st) == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+}
+
 const char* nvfp4_status_string(nvfp4_status status) {
     switch (status) {
         case NVFP4_OK: return "NVFP4_OK";
@@ -710,7 +908,9 @@ nvfp4_status nvfp4_testing_bounds_violations(uint64_t* count) {
         nvfp4::norm_rope_bounds_read_and_clear(&n) != cudaSuccess ||
         nvfp4::attention_spans_bounds_read_and_clear(&n) != cudaSuccess ||
         nvfp4::attention_forward_bounds_read_and_clear(&n) != cudaSuccess ||
-        nvfp4::attention_backward_bounds_read_and_clear(&n) != cudaSuccess)
+        nvfp4::attention_backward_bounds_read_and_clear(&n) != cudaSuccess ||
+        nvfp4::checkpoint_bounds_read_and_clear(&n) != cudaSuccess ||
+        nvfp4::block_norm_bounds_read_and_clear(&n) != cudaSuccess)
         return NVFP4_ERR_CUDA;
     *count = n;
     return NVFP4_OK;

@@ -105,6 +105,8 @@ cudaError_t norm_rope_bounds_read_and_clear(uint64_t* n);
 cudaError_t attention_spans_bounds_read_and_clear(uint64_t* n);
 cudaError_t attention_forward_bounds_read_and_clear(uint64_t* n);
 cudaError_t attention_backward_bounds_read_and_clear(uint64_t* n);
+cudaError_t checkpoint_bounds_read_and_clear(uint64_t* n);
+cudaError_t block_norm_bounds_read_and_clear(uint64_t* n);
 
 // Test support: the next GEMM launch waits at most timeout_ns per barrier and
 // its leader CTA leaves out one scale-warp arrival, so one wait runs out.
@@ -145,6 +147,58 @@ struct NormRope {
     float *dq_weight, *dk_weight, *partials;
 };
 cudaError_t launch_norm_rope(const NormRope& a, bool backward, cudaStream_t stream);
+
+// A matrix kept for the backward pass: BF16 (scales null, ld in elements) or
+// E4M3 codes with one power-of-two scale byte per 1x32 block (ld in bytes).
+struct CheckpointView {
+    void* data;
+    int64_t ld;
+    uint8_t* scales;
+    int64_t ld_scales;
+};
+cudaError_t launch_checkpoint_encode(const uint16_t* x, int64_t ld_x, int64_t rows, int64_t cols,
+                                     const CheckpointView& out, cudaStream_t stream);
+cudaError_t launch_checkpoint_decode(const CheckpointView& in, int64_t rows, int64_t cols, void* y, int64_t ld_y,
+                                     bool out_fp32, cudaStream_t stream);
+
+// The norms after and before a block (block_norm.cu).  Leading dimensions in
+// elements; optional parts are null.
+enum GateKind { kGateNone = 0, kGateChannel = 1, kGateToken = 2 };
+constexpr int kBlockNormMaxWidth = 8192;
+constexpr int kBlockNormMaxBlocks = 1024;  // partial sums of the weights' gradients: 2 * width floats each
+struct BlockNorm {
+    int64_t tokens;
+    int width;
+    float eps, scale;
+    bool fp32;                   // the residual and its gradients
+    const float *post, *pre;     // [width]
+    int gate_kind;
+    const void* gate;            // FP32 [width] or BF16 [tokens][ld_gate]
+    int64_t ld_gate;
+    const void* residual;        // forward: the input; backward: the forward pass's output
+    int64_t ld_residual;
+    const uint16_t* branch;
+    int64_t ld_branch;
+    CheckpointView kept;         // forward: the branch's 8-bit output; backward: the branch in 8 bits
+    // forward
+    void* residual_out;
+    int64_t ld_residual_out;
+    uint16_t* normed;
+    int64_t ld_normed;
+    // backward
+    const void* dresidual;       // of residual_out
+    int64_t ld_dresidual;
+    const uint16_t* dnormed;
+    int64_t ld_dnormed;
+    void* dresidual_out;         // of the residual input
+    int64_t ld_dresidual_out;
+    uint16_t* dbranch;
+    int64_t ld_dbranch;
+    void* dgate;                 // as gate
+    int64_t ld_dgate;
+    float *dpost, *dpre, *partials;
+};
+cudaError_t launch_block_norm(const BlockNorm& a, bool backward, cudaStream_t stream);
 
 // Attention whose mask is one key interval per query row (attention_*.cu).
 struct Attention {

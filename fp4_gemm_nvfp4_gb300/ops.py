@@ -10,7 +10,7 @@ current one: the two are ordered by the caller, as for any tensor used on a
 stream other than its own.
 """
 from dataclasses import dataclass
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple, Union
 
 import torch
 
@@ -491,6 +491,242 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
                                            workspace.data_ptr(), workspace.numel(), stream_handle(stream))
     capi.check(status, "nvfp4_attention_backward")
     return dq, dk, dv
+
+
+@dataclass
+class Checkpoint:
+    """A matrix kept for the backward pass (see nvfp4_checkpoint): BF16, or with `scales` E4M3 codes and a
+    power-of-two scale byte per 1x32 block."""
+    data: torch.Tensor                # bfloat16 [rows, cols], or uint8 [rows, >= cols]
+    scales: Optional[torch.Tensor]    # uint8 [rows, >= cols / 32], or None
+    rows: int
+    cols: int
+
+    def struct(self) -> capi.nvfp4_checkpoint:
+        data, scales, rows, cols = self.data, self.scales, self.rows, self.cols
+        if scales is None:
+            return capi.nvfp4_checkpoint(data.data_ptr(), _leading(data, rows, cols, torch.bfloat16, "data"), None, 0)
+        return capi.nvfp4_checkpoint(data.data_ptr(), _leading(data, rows, cols, torch.uint8, "data"),
+                                     scales.data_ptr(),
+                                     _leading(scales, rows, (cols + 31) // 32, torch.uint8, "scales"))
+
+    def nbytes(self) -> int:
+        return self.data.numel() * self.data.element_size() + (0 if self.scales is None else self.scales.numel())
+
+
+def _leading(x: torch.Tensor, rows: int, cols: int, dtype, what: str) -> int:
+    """The leading dimension of a matrix with at least `cols` contiguous columns."""
+    if x.dtype != dtype or x.dim() != 2 or x.shape[0] != rows or x.shape[1] < cols:
+        raise ValueError(f"{what}: {dtype} [{rows}, {cols}] expected, got {x.dtype} {list(x.shape)}")
+    ld, one = x.stride()
+    if one != 1 and x.shape[1] > 1:
+        raise ValueError(f"{what}: the columns must be contiguous")
+    # the stride of one row says nothing
+    return ld if rows > 1 else (cols + 15) // 16 * 16
+
+
+def _matrix(x: torch.Tensor, rows: int, cols: int, dtype, what: str) -> Tuple[int, int]:
+    """Address and leading dimension of a [rows, cols] matrix."""
+    if x.shape != (rows, cols):
+        raise ValueError(f"{what}: [{rows}, {cols}] expected, got {list(x.shape)}")
+    return x.data_ptr(), _leading(x, rows, cols, dtype, what)
+
+
+def _check_here(*tensors: Optional[torch.Tensor]) -> None:
+    """Every tensor on the current device, where the kernels run."""
+    for t in tensors:
+        if t is not None:
+            _check_on_gpu(t.is_cuda)
+            if t.get_device() != torch._C._cuda_getDevice():
+                raise ValueError(f"tensors on the current device expected, got one on {t.device}")
+
+
+def alloc_checkpoint(rows: int, cols: int, kind: str = "e4m3", device="cuda") -> Checkpoint:
+    """A checkpoint's memory: kind "e4m3" (8 bits) or "bf16"."""
+    if kind == "bf16":
+        return Checkpoint(torch.empty((rows, _round_up(cols, 8)), dtype=torch.bfloat16, device=device), None, rows, cols)
+    if kind != "e4m3":
+        raise ValueError(f'"bf16" or "e4m3" expected, got {kind!r}')
+    return Checkpoint(torch.empty((rows, _round_up(cols, 16)), dtype=torch.uint8, device=device),
+                      torch.empty((rows, _round_up((cols + 31) // 32, 16)), dtype=torch.uint8, device=device), rows, cols)
+
+
+def checkpoint_encode(x: torch.Tensor, out: Optional[Checkpoint] = None, stream=None) -> Checkpoint:
+    """A bf16 matrix in 8 bits (nvfp4_checkpoint_encode)."""
+    if x.dim() != 2:
+        raise ValueError("x: a matrix expected")
+    rows, cols = x.shape
+    ptr, ld = _matrix(x, rows, cols, torch.bfloat16, "x")
+    if out is None:
+        out = alloc_checkpoint(rows, cols, device=x.device)
+    elif (out.rows, out.cols) != (rows, cols) or out.scales is None:
+        raise ValueError(f"out: an 8-bit checkpoint of [{rows}, {cols}] expected")
+    _check_here(x, out.data, out.scales)
+    capi.check(capi.nvfp4_checkpoint_encode(ptr, rows, cols, ld, out.struct(), stream_handle(stream)),
+               "nvfp4_checkpoint_encode")
+    return out
+
+
+def checkpoint_decode(kept: Checkpoint, out_dtype=torch.bfloat16, out: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+    """The matrix that an 8-bit checkpoint stands for, bf16 (exact) or float32 (nvfp4_checkpoint_decode)."""
+    rows, cols = kept.rows, kept.cols
+    if kept.scales is None:
+        raise ValueError("kept: an 8-bit checkpoint expected")
+    if out is None:
+        out = torch.empty((rows, cols), dtype=out_dtype, device=kept.data.device)
+    elif out.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"out: bfloat16 or float32 expected, got {out.dtype}")
+    ptr, ld = _matrix(out, rows, cols, out.dtype, "out")
+    _check_here(kept.data, kept.scales, out)
+    dt = capi.NVFP4_OUT_FP32 if out.dtype == torch.float32 else capi.NVFP4_OUT_BF16
+    capi.check(capi.nvfp4_checkpoint_decode(kept.struct(), rows, cols, ptr, ld, dt, stream_handle(stream)),
+               "nvfp4_checkpoint_decode")
+    return out
+
+
+def _block_norm_desc(tokens, width, dtype, post_weight, pre_weight, gate, residual_scale, eps
+                     ) -> capi.nvfp4_block_norm_desc:
+    if dtype == torch.bfloat16:
+        kind = capi.NVFP4_OUT_BF16
+    elif dtype == torch.float32:
+        kind = capi.NVFP4_OUT_FP32
+    else:
+        raise ValueError(f"residual: bfloat16 or float32 expected, got {dtype}")
+    for w, what in ((post_weight, "post_weight"), (pre_weight, "pre_weight")):
+        if w is not None:
+            _check_float32(w, (width,), what)
+    gate_kind, gate_ptr, ld_gate = capi.NVFP4_GATE_NONE, None, 0
+    if gate is not None:
+        if gate.dim() == 1:
+            _check_float32(gate, (width,), "gate")
+            gate_kind, gate_ptr = capi.NVFP4_GATE_CHANNEL, gate.data_ptr()
+        else:
+            gate_kind = capi.NVFP4_GATE_TOKEN
+            gate_ptr, ld_gate = _matrix(gate, tokens, width, torch.bfloat16, "gate")
+    return capi.nvfp4_block_norm_desc(tokens, width, eps, residual_scale, kind,
+                                      None if post_weight is None else post_weight.data_ptr(),
+                                      None if pre_weight is None else pre_weight.data_ptr(), gate_kind, gate_ptr,
+                                      ld_gate)
+
+
+def block_norm(residual: torch.Tensor, branch: Optional[torch.Tensor] = None, *,
+               pre_weight: Optional[torch.Tensor] = None, post_weight: Optional[torch.Tensor] = None,
+               gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0, eps: float = 1e-6,
+               keep: Optional[str] = None, out: Optional[torch.Tensor] = None, normed: Optional[torch.Tensor] = None,
+               stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor], Optional[Checkpoint]]:
+    """The norms after and before a block with its gate and the residual's scale (nvfp4_block_norm):
+    residual_out = residual_scale * residual + gate * norm(branch) * post_weight, normed = norm(residual_out) *
+    pre_weight.  residual: bf16 or float32 [tokens, width]; branch: the block's bf16 output, not normed without
+    post_weight; gate: float32 [width] or bf16 [tokens, width].
+    Returns (residual_out, normed or None without pre_weight, kept): keep="e4m3" keeps the branch in 8 bits for
+    block_norm_backward, "bf16" as it is.  Without a branch and with residual_scale 1, residual_out is `residual`
+    itself unless `out` is given."""
+    if residual.dim() != 2:
+        raise ValueError("residual: a matrix expected")
+    tokens, width = residual.shape
+    desc = _block_norm_desc(tokens, width, residual.dtype, post_weight, pre_weight, gate, residual_scale, eps)
+    r, ld_r = _matrix(residual, tokens, width, residual.dtype, "residual")
+    b = ld_b = n = ld_n = o = ld_o = 0
+    kept = None
+    if branch is not None:
+        b, ld_b = _matrix(branch, tokens, width, torch.bfloat16, "branch")
+        if keep == "bf16":
+            kept = Checkpoint(branch, None, tokens, width)
+        elif keep is not None:
+            kept = alloc_checkpoint(tokens, width, keep, residual.device)
+    elif keep is not None:
+        raise ValueError("keep: there is no branch to keep")
+    if pre_weight is not None:
+        if normed is None:
+            normed = torch.empty((tokens, width), dtype=torch.bfloat16, device=residual.device)
+        n, ld_n = _matrix(normed, tokens, width, torch.bfloat16, "normed")
+    elif normed is not None:
+        raise ValueError("normed: no pre_weight given")
+    if out is None and branch is None and residual_scale == 1.0:
+        if pre_weight is None:
+            raise ValueError("neither a branch nor a pre_weight: there is nothing to compute")
+        out = residual
+    else:
+        if out is None:
+            out = torch.empty((tokens, width), dtype=residual.dtype, device=residual.device)
+        o, ld_o = _matrix(out, tokens, width, residual.dtype, "out")
+    _check_here(residual, branch, post_weight, pre_weight, gate, out, normed)
+    status = capi.nvfp4_block_norm(desc, r, ld_r, b, ld_b, o, ld_o, n, ld_n,
+                                   None if kept is None or kept.scales is None else kept.struct(),
+                                   stream_handle(stream))
+    capi.check(status, "nvfp4_block_norm")
+    return out, normed, kept
+
+
+class BlockNormGradients(NamedTuple):
+    """What block_norm_backward returns; None for what the forward call did not have."""
+    dresidual: torch.Tensor
+    dbranch: Optional[torch.Tensor]
+    dpost_weight: Optional[torch.Tensor]
+    dpre_weight: Optional[torch.Tensor]
+    dgate: Optional[torch.Tensor]
+
+
+def block_norm_backward(dresidual_out: Optional[torch.Tensor], dnormed: Optional[torch.Tensor],
+                        residual_out: torch.Tensor, branch: Union[torch.Tensor, Checkpoint, None] = None, *,
+                        pre_weight: Optional[torch.Tensor] = None, post_weight: Optional[torch.Tensor] = None,
+                        gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0, eps: float = 1e-6,
+                        dresidual: Optional[torch.Tensor] = None, dbranch: Optional[torch.Tensor] = None,
+                        dgate: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None
+                        ) -> BlockNormGradients:
+    """Gradients of block_norm (nvfp4_block_norm_backward) from those of its outputs, the residual_out that it
+    returned and the branch or what was kept of it.  dresidual_out None: nothing reaches the residual stream but
+    through normed."""
+    if residual_out.dim() != 2:
+        raise ValueError("residual_out: a matrix expected")
+    tokens, width = residual_out.shape
+    kind, device = residual_out.dtype, residual_out.device
+    desc = _block_norm_desc(tokens, width, kind, post_weight, pre_weight, gate, residual_scale, eps)
+    do = ld_do = dn = ld_dn = db = ld_db = 0
+    if dresidual_out is not None:
+        do, ld_do = _matrix(dresidual_out, tokens, width, kind, "dresidual_out")
+    if dnormed is not None:
+        dn, ld_dn = _matrix(dnormed, tokens, width, torch.bfloat16, "dnormed")
+    ro, ld_ro = _matrix(residual_out, tokens, width, kind, "residual_out")
+    if dresidual is None:
+        dresidual = torch.empty((tokens, width), dtype=kind, device=device)
+    dr, ld_dr = _matrix(dresidual, tokens, width, kind, "dresidual")
+    kept = data = scales = None
+    if branch is not None:
+        if not isinstance(branch, Checkpoint):
+            branch = Checkpoint(branch, None, tokens, width)
+        if (branch.rows, branch.cols) != (tokens, width):
+            raise ValueError(f"branch: [{tokens}, {width}] expected, got [{branch.rows}, {branch.cols}]")
+        kept, data, scales = branch.struct(), branch.data, branch.scales
+        if dbranch is None:
+            dbranch = torch.empty((tokens, width), dtype=torch.bfloat16, device=device)
+        db, ld_db = _matrix(dbranch, tokens, width, torch.bfloat16, "dbranch")
+    elif dbranch is not None:
+        raise ValueError("dbranch: there is no branch")
+    dpost = None if post_weight is None else torch.empty(width, dtype=torch.float32, device=device)
+    dpre = None if pre_weight is None else torch.empty(width, dtype=torch.float32, device=device)
+    dg = ld_dg = 0
+    if desc.gate_kind == capi.NVFP4_GATE_CHANNEL:
+        if dgate is None:
+            dgate = torch.empty(width, dtype=torch.float32, device=device)
+        _check_float32(dgate, (width,), "dgate")
+        dg = dgate.data_ptr()
+    elif desc.gate_kind == capi.NVFP4_GATE_TOKEN:
+        if dgate is None:
+            dgate = torch.empty((tokens, width), dtype=torch.bfloat16, device=device)
+        dg, ld_dg = _matrix(dgate, tokens, width, torch.bfloat16, "dgate")
+    elif dgate is not None:
+        raise ValueError("dgate: there is no gate")
+    workspace = _scratch(workspace, capi.nvfp4_block_norm_backward_workspace_size(width), device, stream)
+    _check_here(dresidual_out, dnormed, residual_out, data, scales, post_weight, pre_weight, gate, dresidual, dbranch,
+                dgate, workspace)
+    status = capi.nvfp4_block_norm_backward(
+        desc, do, ld_do, dn, ld_dn, ro, ld_ro, kept, dr, ld_dr, db, ld_db, None if dpost is None else dpost.data_ptr(),
+        None if dpre is None else dpre.data_ptr(), dg, ld_dg, workspace.data_ptr(), workspace.numel(),
+        stream_handle(stream))
+    capi.check(status, "nvfp4_block_norm_backward")
+    return BlockNormGradients(dresidual, dbranch, dpost, dpre, dgate)
 
 
 def device_error(stream=None) -> int:

@@ -547,6 +547,115 @@ NVFP4_API nvfp4_status nvfp4_attention_backward(const nvfp4_attention_desc *desc
                                                 const nvfp4_heads *dk, const nvfp4_heads *dv, void *workspace,
                                                 size_t workspace_bytes, nvfp4_stream_t stream);
 
+/*
+ * ---- Activations kept for the backward pass ---------------------------------
+ *
+ * A matrix [rows][cols] kept from the forward for the backward pass, either
+ * as the caller chooses: BF16 as it is, or in 8 bits, half the memory.
+ *   scales == NULL: data is BF16 [rows][ld], ld in elements.
+ *   else:           data holds E4M3 codes [rows][ld], ld in bytes, and
+ *     scales[r * ld_scales + c / 32] the byte b of the 1x32 block of (r, c):
+ *     value = e4m3(code) * 2^(b - 127), b the smallest byte >= 10 that takes
+ *     the block's largest finite magnitude to at most 448.  Codes are rounded
+ *     to nearest even: an error of at most 2^-4 of the value, or 2^(b - 137)
+ *     where that is more.  Magnitudes past 1.9375 * 2^127 are kept as 1.875 *
+ *     2^127.  Infinities and NaN are kept as NaN and leave their block's scale
+ *     as it is without them.
+ * data and scales 16-byte aligned, rows a multiple of 16 bytes apart; only the
+ * cols values (and ceil(cols / 32) scale bytes) of a row are written or used.
+ */
+typedef struct {
+    void    *data;
+    int64_t  ld;
+    uint8_t *scales;
+    int64_t  ld_scales;
+} nvfp4_checkpoint;
+
+/*
+ * nvfp4_checkpoint_encode -- BF16 x [rows][ld_x] to 8 bits.
+ * nvfp4_checkpoint_decode -- the kept values of `in` (8 bits) as BF16 (exact) or
+ * FP32, y [rows][ldy].
+ * Requirements: cols % 8 == 0 [SHAPE], cols <= 2^24 and rows * ceil(cols / 32)
+ * < 2^40 [UNSUPPORTED]; x and y 16-byte aligned with rows a multiple of 16 bytes
+ * apart [ALIGNMENT]; leading dimensions that hold a row [SHAPE].  No rows or no
+ * columns enqueue nothing.
+ */
+NVFP4_API nvfp4_status nvfp4_checkpoint_encode(const void *x, int64_t rows, int64_t cols, int64_t ld_x,
+                                               const nvfp4_checkpoint *out, nvfp4_stream_t stream);
+NVFP4_API nvfp4_status nvfp4_checkpoint_decode(const nvfp4_checkpoint *in, int64_t rows, int64_t cols, void *y,
+                                               int64_t ldy, nvfp4_dtype out_dtype, nvfp4_stream_t stream);
+
+/*
+ * ---- Around a block ---------------------------------------------------------
+ *
+ * What the two norm calls share.  Per token, over `width` columns:
+ *   a = y / sqrt(mean(y^2) + eps),  h = a post   (h = y if post_weight is NULL)
+ *   r' = residual_scale r + gate h               (r' = residual_scale r without a branch y)
+ *   n  = r' / sqrt(mean(r'^2) + eps) pre         (if pre_weight)
+ * y is the block's output (nvfp4_gemm's), r the residual stream and n the next
+ * block's input; the model's first norm has no branch.  Binary32 throughout; n
+ * is the norm of r' as stored, rounded once if the residual is BF16.
+ */
+typedef enum { NVFP4_GATE_NONE = 0, NVFP4_GATE_CHANNEL = 1, NVFP4_GATE_TOKEN = 2 } nvfp4_gate;
+typedef struct {
+    int64_t      tokens;
+    int32_t      width;            /* a multiple of 8, 8 to 8192 */
+    float        eps;              /* >= 0 */
+    float        residual_scale;   /* finite */
+    nvfp4_dtype  residual_dtype;   /* of the residual and its gradients */
+    const float *post_weight;      /* device FP32 [width], or NULL */
+    const float *pre_weight;       /* device FP32 [width], or NULL */
+    nvfp4_gate   gate_kind;
+    const void  *gate;             /* device: FP32 [width] (CHANNEL) or BF16 [tokens][ld_gate] (TOKEN) */
+    int64_t      ld_gate;
+} nvfp4_block_norm_desc;
+
+/*
+ * nvfp4_block_norm -- the forward pass.
+ *  residual     [tokens][ld_residual] of residual_dtype.
+ *  branch       BF16 [tokens][ld_branch], or NULL (then no post_weight, gate or
+ *               branch_kept).
+ *  residual_out r', [tokens][ld_residual_out]; may be `residual` with its
+ *               leading dimension; NULL: not wanted (n alone).
+ *  normed       n, BF16 [tokens][ld_normed]; NULL exactly if pre_weight is.
+ *  branch_kept  8-bit copy of the branch for the backward pass, or NULL.
+ * Requirements: width as above, leading dimensions >= width [SHAPE]; every
+ * pointer 16-byte aligned, rows a multiple of 16 bytes apart [ALIGNMENT]; finite
+ * eps >= 0 and residual_scale [INVALID_ARG].  tokens = 0 enqueues nothing.
+ * A NaN or infinity stays in its token's row.
+ */
+NVFP4_API nvfp4_status nvfp4_block_norm(const nvfp4_block_norm_desc *desc, const void *residual, int64_t ld_residual,
+                                        const void *branch, int64_t ld_branch, void *residual_out,
+                                        int64_t ld_residual_out, void *normed, int64_t ld_normed,
+                                        const nvfp4_checkpoint *branch_kept, nvfp4_stream_t stream);
+
+/*
+ * nvfp4_block_norm_backward -- the gradients of nvfp4_block_norm's inputs.
+ *  dresidual_out  of r', residual_dtype; NULL: zero (the stream ends here).
+ *  dnormed      of n, BF16; NULL exactly if pre_weight is.
+ *  residual_out the r' that the forward pass stored; NULL if pre_weight is.
+ *  branch       y as kept, BF16 or 8 bits (whose values then stand for y
+ *               throughout); NULL without a branch.
+ *  dresidual    of r, residual_dtype; may be dresidual_out with its leading dimension.
+ *  dbranch      of y, BF16; NULL exactly if branch is.
+ *  dpost_weight, dpre_weight  FP32 [width], overwritten (0 for no tokens);
+ *               NULL exactly if the weight is.
+ *  dgate        as gate: FP32 [width] or BF16 [tokens][ld_dgate]; NULL exactly
+ *               if there is no gate.
+ *  workspace    nvfp4_block_norm_backward_workspace_size(width) bytes, 16-byte
+ *               aligned.
+ * The weights' gradients sum over every token, padding included; sums run in a
+ * fixed order: equal inputs give equal bits.
+ */
+NVFP4_API size_t nvfp4_block_norm_backward_workspace_size(int32_t width);
+NVFP4_API nvfp4_status nvfp4_block_norm_backward(const nvfp4_block_norm_desc *desc, const void *dresidual_out,
+                                                 int64_t ld_dresidual_out, const void *dnormed, int64_t ld_dnormed,
+                                                 const void *residual_out, int64_t ld_residual_out,
+                                                 const nvfp4_checkpoint *branch, void *dresidual, int64_t ld_dresidual,
+                                                 void *dbranch, int64_t ld_dbranch, float *dpost_weight,
+                                                 float *dpre_weight, void *dgate, int64_t ld_dgate, void *workspace,
+                                                 size_t workspace_bytes, nvfp4_stream_t stream);
+
 /* Human-readable name of a status. */
 NVFP4_API const char *nvfp4_status_string(nvfp4_status status);
 
