@@ -20,7 +20,7 @@ OUT_DIR_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_DEBUG = os.path.join(OUT_DIR_DEBUG, "libnvfp4_debug.so")
 SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "dequantize.cu", "quantize_noalloc.cu", "norm_rope.cu",
            "attention_spans.cu", "attention_forward.cu", "attention_backward.cu", "checkpoint.cu", "block_norm.cu"]
-HEADERS = ["device_common.cuh", "kernels.h", "bounds.cuh", "mma_common.cuh", "attention_common.cuh", "checkpoint.cuh"]
+HEADERS = ["device_common.cuh", "kernels.h", "bounds.cuh", "mma_common.cuh", "attention_common.cuh", "checkpoint.cuh", "gemm_gated.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "-Xcompiler", "-fvisibility=hidden", "-I", os.path.join(ROOT, "include")]

@@ -34,6 +34,8 @@ NVFP4_COLWISE = 2
 NVFP4_GATE_NONE = 0
 NVFP4_GATE_CHANNEL = 1
 NVFP4_GATE_TOKEN = 2
+NVFP4_ACT_SILU = 0
+NVFP4_ACT_GELU = 1
 
 EXPORTED = ("nvfp4_scale_bytes", "nvfp4_quantize_workspace_size", "nvfp4_quantize",
             "nvfp4_rht_quantize", "nvfp4_gemm", "nvfp4_dequantize", "nvfp4_status_string",
@@ -46,6 +48,7 @@ EXPORTED = ("nvfp4_scale_bytes", "nvfp4_quantize_workspace_size", "nvfp4_quantiz
             "nvfp4_attention_backward",
             "nvfp4_checkpoint_encode", "nvfp4_checkpoint_decode", "nvfp4_block_norm",
             "nvfp4_block_norm_backward_workspace_size", "nvfp4_block_norm_backward",
+            "nvfp4_gemm_gated", "nvfp4_gemm_gated_backward",
             "nvfp4_testing_arm_gemm_timeout", "nvfp4_testing_arm_attention_timeout",
             "nvfp4_testing_attention_wait_limit_us", "nvfp4_testing_bounds_violations",
             "nvfp4_testing_bounds_shrink")
@@ -157,6 +160,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.nvfp4_block_norm_backward.argtypes = [np_, vp, i64, vp, i64, vp, i64, kp, vp, i64, vp, i64, vp, vp, vp, i64, vp,
                                             sz, vp]
     L.nvfp4_block_norm_backward.restype = i32
+    L.nvfp4_gemm_gated.argtypes, L.nvfp4_gemm_gated.restype = [tp, tp, tp, i32, vp, i64, kp, kp, vp, u16, vp], i32
+    L.nvfp4_gemm_gated_backward.argtypes = [tp, tp, i32, kp, kp, vp, i64, vp, i64, vp, u16, vp]
+    L.nvfp4_gemm_gated_backward.restype = i32
     L.nvfp4_dequantize.argtypes = [tp, vp, i64, i32, vp]
     L.nvfp4_dequantize.restype = i32
     L.nvfp4_status_string.argtypes, L.nvfp4_status_string.restype = [i32], ctypes.c_char_p
@@ -337,6 +343,19 @@ def nvfp4_block_norm_backward(desc, dresidual_out, ld_dresidual_out, dnormed, ld
                                             residual_out, ld_residual_out, _ref(branch), dresidual, ld_dresidual,
                                             dbranch, ld_dbranch, dpost_weight, dpre_weight, dgate, ld_dgate, workspace,
                                             workspace_bytes, stream)
+
+
+def nvfp4_gemm_gated(A, B_gate, B_up, activation, H, ldh, gate, up, amax_out, rht_sign_mask, stream):
+    """H = act(A B_gate^T) * (A B_up^T), gate and up kept if wanted."""
+    return load().nvfp4_gemm_gated(_ref(A), _ref(B_gate), _ref(B_up), activation, H, ldh, _ref(gate), _ref(up),
+                                   amax_out, rht_sign_mask, stream)
+
+
+def nvfp4_gemm_gated_backward(A, B, activation, gate, up, dgate, ld_dgate, dup, ld_dup, amax_out, rht_sign_mask,
+                              stream):
+    """Gradients of gate and up from the down projection's Dgrad operands."""
+    return load().nvfp4_gemm_gated_backward(_ref(A), _ref(B), activation, _ref(gate), _ref(up), dgate, ld_dgate, dup,
+                                            ld_dup, amax_out, rht_sign_mask, stream)
 
 
 def nvfp4_status_string(status):

@@ -865,6 +865,92 @@ nvfp4_status nvfp4_block_norm_backward(const nvfp4_block_norm_desc* desc, const 
     return nvfp4::launch_block_norm(a, true, st) == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
+namespace {
+
+// An operand that may have no rows (and then no buffers).
+nvfp4_status check_operand_or_empty(const nvfp4_tensor* t) {
+    if (!t) return NVFP4_ERR_INVALID_ARG;
+    if (t->rows != 0) return check_operand(t);
+    return t->cols >= 0 && t->cols % 16 == 0 ? NVFP4_OK : NVFP4_ERR_SHAPE;
+}
+
+// The arguments the two calls of a gated block share: A [M][K], B [N][K].
+nvfp4_status check_gated(const nvfp4_tensor* A, const nvfp4_tensor* B, nvfp4_activation activation,
+                         const float* amax_out) {
+    nvfp4_status s;
+    if (activation != NVFP4_ACT_SILU && activation != NVFP4_ACT_GELU) return NVFP4_ERR_INVALID_ARG;
+    if ((s = check_operand_or_empty(A)) != NVFP4_OK) return s;
+    if ((s = check_operand_or_empty(B)) != NVFP4_OK) return s;
+    if (A->cols != B->cols || B->rows % 16 != 0) return NVFP4_ERR_SHAPE;
+    if (amax_out && A->rows % 16 != 0) return NVFP4_ERR_SHAPE;   // 16-row blocks of the rotated amax
+    if ((reinterpret_cast<uintptr_t>(amax_out) & 3u) != 0) return NVFP4_ERR_ALIGNMENT;
+    if (A->cols == 0) return NVFP4_ERR_UNSUPPORTED;
+    if (ceil_div(A->rows, 128) * ceil_div(B->rows, 128) >= (int64_t(1) << 32)) return NVFP4_ERR_UNSUPPORTED;
+    return NVFP4_OK;
+}
+
+// Gate and up as kept, of one kind.
+nvfp4_status check_kept(const nvfp4_checkpoint* gate, const nvfp4_checkpoint* up, int64_t rows, int64_t cols) {
+    nvfp4_status s;
+    if ((s = check_checkpoint(gate, rows, cols, false)) != NVFP4_OK) return s;
+    if ((s = check_checkpoint(up, rows, cols, false)) != NVFP4_OK) return s;
+    return (gate->scales != nullptr) == (up->scales != nullptr) ? NVFP4_OK : NVFP4_ERR_INVALID_ARG;
+}
+
+nvfp4_status empty_product(float* amax_out, cudaStream_t st) {
+    if (!amax_out) return NVFP4_OK;
+    return cudaMemsetAsync(amax_out, 0, 2 * sizeof(float), st) == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+}
+
+}  // namespace
+
+nvfp4_status nvfp4_gemm_gated(const nvfp4_tensor* A, const nvfp4_tensor* B_gate, const nvfp4_tensor* B_up,
+                              nvfp4_activation activation, void* H, int64_t ldh, const nvfp4_checkpoint* gate,
+                              const nvfp4_checkpoint* up, float* amax_out, uint16_t rht_sign_mask,
+                              nvfp4_stream_t stream) {
+    const ApiRange range("nvfp4_gemm_gated");
+    nvfp4_status s;
+    if ((s = check_gated(A, B_gate, activation, amax_out)) != NVFP4_OK) return s;
+    if ((s = check_operand_or_empty(B_up)) != NVFP4_OK) return s;
+    if (B_up->rows != B_gate->rows || B_up->cols != B_gate->cols) return NVFP4_ERR_SHAPE;
+    if ((gate != nullptr) != (up != nullptr)) return NVFP4_ERR_INVALID_ARG;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t M = A->rows, N = B_gate->rows;
+    if (M == 0 || N == 0) return empty_product(amax_out, st);
+    if ((s = check_rows(H, M, N, ldh, 2)) != NVFP4_OK) return s;
+    nvfp4::CheckpointView g{}, u{};
+    if (gate) {
+        if ((s = check_kept(gate, up, M, N)) != NVFP4_OK) return s;
+        g = to_checkpoint(gate);
+        u = to_checkpoint(up);
+    }
+    return nvfp4::launch_gemm_gated(to_operand(A), to_operand(B_gate), to_operand(B_up), activation == NVFP4_ACT_GELU,
+                                    H, ldh, gate ? &g : nullptr, gate ? &u : nullptr, amax_out, rht_sign_mask,
+                                    st) == cudaSuccess
+               ? NVFP4_OK
+               : NVFP4_ERR_CUDA;
+}
+
+nvfp4_status nvfp4_gemm_gated_backward(const nvfp4_tensor* A, const nvfp4_tensor* B, nvfp4_activation activation,
+                                       const nvfp4_checkpoint* gate, const nvfp4_checkpoint* up, void* dgate,
+                                       int64_t ld_dgate, void* dup, int64_t ld_dup, float* amax_out,
+                                       uint16_t rht_sign_mask, nvfp4_stream_t stream) {
+    const ApiRange range("nvfp4_gemm_gated_backward");
+    nvfp4_status s;
+    if ((s = check_gated(A, B, activation, amax_out)) != NVFP4_OK) return s;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t M = A->rows, N = B->rows;
+    if (M == 0 || N == 0) return empty_product(amax_out, st);
+    if ((s = check_kept(gate, up, M, N)) != NVFP4_OK) return s;
+    if ((s = check_rows(dgate, M, N, ld_dgate, 2)) != NVFP4_OK) return s;
+    if ((s = check_rows(dup, M, N, ld_dup, 2)) != NVFP4_OK) return s;
+    return nvfp4::launch_gemm_gated_backward(to_operand(A), to_operand(B), activation == NVFP4_ACT_GELU,
+                                             to_checkpoint(gate), to_checkpoint(up), dgate, ld_dgate, dup, ld_dup,
+                                             amax_out, rht_sign_mask, st) == cudaSuccess
+               ? NVFP4_OK
+               : NVFP4_ERR_CUDA;
+}
+
 const char* nvfp4_status_string(nvfp4_status status) {
     switch (status) {
         case NVFP4_OK: return "NVFP4_OK";

@@ -42,10 +42,13 @@
 
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 
 #include "bounds.cuh"
+#include "checkpoint.cuh"
 #include "device_common.cuh"
 #include "kernels.h"
+#include "mma_common.cuh"
 
 namespace nvfp4 {
 
@@ -64,14 +67,13 @@ constexpr int kCtaM = 128;                       // rows of A (and accumulator l
 constexpr int kBN = 256;                         // output columns per tile
 constexpr int kCtaN = 128;                       // rows of B per CTA
 constexpr int kBKBytes = 128;                    // 256 fp4 of K per row per stage
-constexpr int kStages = 5;
 constexpr int kKStepsPerStage = 4;               // K = 64 per MMA
 constexpr uint32_t kABytes = kCtaM * kBKBytes;   // 16 KiB
 constexpr uint32_t kBBytes = kCtaN * kBKBytes;   // 16 KiB
 constexpr uint32_t kSFABytes = kKStepsPerStage * 512;
 constexpr uint32_t kSFBBytes = 2 * kKStepsPerStage * 512;
 constexpr uint32_t kStageBytes = kABytes + kBBytes + kSFABytes + kSFBBytes;
-constexpr uint32_t kStagingBytes = kNumEpiWarpsStaging * 4096;   // 32 rows x 64 BF16 columns per epilogue warp
+constexpr uint32_t kSliceBytes = 4096;           // 32 rows x 64 BF16 columns: an epilogue warp's piece
 constexpr int kProdAWarp = 0;
 constexpr int kMmaWarp = 1;
 constexpr int kProdBWarp = 2;
@@ -89,11 +91,26 @@ constexpr uint32_t kAccCol = 0;                   // 256 FP32 accumulator column
 constexpr uint32_t kSfCol0 = 256;                 // then the per-stage scale columns
 constexpr uint32_t kSfColsPerStage = 4 * kKStepsPerStage + 8 * kKStepsPerStage;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
-constexpr size_t kSmemBytes = (size_t)kStages * kStageBytes + kStagingBytes + 1024 /*align*/ + 256 /*barriers*/;
+
+// Epilogue variants: the plain product; the product plus the output's two
+// tensor amaxes (p.amax_out); alpha times the product plus beta C (p.c); the
+// gated pair of products and its backward pass (gemm_gated.cuh).
+enum EpiMode { kEpiPlain = 0, kEpiAmax = 1, kEpiC = 2, kEpiGated = 3, kEpiGatedBack = 4 };
+
+// The gated backward pass reads two matrices through its slices and writes two
+// back: two slices per epilogue warp, paid for with a stage of operands.
+__host__ __device__ constexpr int stages_of(int mode) { return mode == kEpiGatedBack ? 4 : 5; }
+__host__ __device__ constexpr uint32_t slices_of(int mode) { return mode == kEpiGatedBack ? 2 : 1; }
+__host__ __device__ constexpr uint32_t staging_of(int mode) {
+    return kNumEpiWarpsStaging * slices_of(mode) * kSliceBytes;
+}
+__host__ __device__ constexpr size_t smem_of(int mode) {
+    return (size_t)stages_of(mode) * kStageBytes + staging_of(mode) + 1024 /*align*/ + 256 /*barriers*/;
+}
 
 static_assert(kStageBytes % 1024 == 0, "stages must keep 1024-byte alignment for the 128B swizzle");
-static_assert(kSfCol0 + kStages * kSfColsPerStage <= kTmemCols, "tensor memory budget");
-static_assert(kSmemBytes <= 232448, "shared memory budget");
+static_assert(kSfCol0 + stages_of(kEpiPlain) * kSfColsPerStage <= kTmemCols, "tensor memory budget");
+static_assert(smem_of(kEpiPlain) <= 232448 && smem_of(kEpiGatedBack) <= 232448, "shared memory budget");
 
 struct Params {
     uint32_t M, N;
@@ -122,6 +139,26 @@ struct Params {
     uint64_t timeout_ns;         // limit of every mbarrier wait
     uint32_t withhold;           // test support: the leader's first scale-warp arrival is left out
     Extent xd;                   // the bytes of D the epilogue's direct stores may write
+    // the gated pair (gemm_gated.cuh)
+    int gelu;                    // the gate's activation: SiLU or GELU
+    int kept;                    // gate and up: 0 not kept, 1 BF16, 2 in 8 bits
+    const float* sgu;            // B's second operand's tensor scale (forward)
+    uint8_t *gate_scales, *up_scales;
+    int64_t ld_gate_scales, ld_up_scales;
+    uint32_t scale_blocks;       // 1x32 blocks of a row
+    Extent x_gate_scales, x_up_scales;
+};
+
+// Tensor maps that only some modes have: gate and up as kept.
+template <int kMode>
+struct ExtraMaps {};
+template <>
+struct ExtraMaps<kEpiGated> {
+    CUtensorMap gate, up;
+};
+template <>
+struct ExtraMaps<kEpiGatedBack> {
+    CUtensorMap gate, up;
 };
 
 // 32 consecutive values of C's row `row` from column n0 (zeros past M or N):
@@ -358,20 +395,21 @@ __device__ __forceinline__ void store_round_tail(const Params& p, const uint8_t*
     }
 }
 
-// Epilogue variants: the plain product; the product plus the output's two
-// tensor amaxes (p.amax_out); alpha times the product plus beta C (p.c).
-enum EpiMode { kEpiPlain = 0, kEpiAmax = 1, kEpiC = 2 };
+#include "gemm_gated.cuh"
 
 template <int kMode>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_nvf4_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_constant__ CUtensorMap tma_b,
                      const __grid_constant__ CUtensorMap tma_sfa, const __grid_constant__ CUtensorMap tma_sfb,
                      const __grid_constant__ CUtensorMap tma_d, const __grid_constant__ CUtensorMap tma_u,
-                     const __grid_constant__ CUtensorMap tma_v, const Params p) {
+                     const __grid_constant__ CUtensorMap tma_v, const Params p,
+                     const __grid_constant__ ExtraMaps<kMode> extra) {
+    constexpr int kStages = stages_of(kMode);
+    constexpr bool kGated = kMode == kEpiGated, kGatedBack = kMode == kEpiGatedBack;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* staging = smem + kStages * kStageBytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(staging + kStagingBytes);   // leader: tiles + scale warps
+    uint64_t* full = reinterpret_cast<uint64_t*>(staging + staging_of(kMode));   // leader: tiles + scale warps
     uint64_t* sf_full = full + kStages;          // local: this CTA's scale bytes
     uint64_t* empty = sf_full + kStages;         // local: released by the leader's commit
     uint64_t* acc_full = empty + kStages;        // local: released by the leader's commit
@@ -380,6 +418,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile uint32_t* abort_flag = tmem_slot + 1;
     volatile uint32_t* sf_ok = tmem_slot + 4;    // [2]: scales-landed verdicts, by stage-count parity
+    uint64_t* loaded = reinterpret_cast<uint64_t*>(tmem_slot + 6);   // gated backward: an epilogue warp's gate and up
 
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
     const uint32_t rank = cluster_ctarank();
@@ -393,16 +432,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         mbar_init(acc_full, 1);
         mbar_init(acc_empty, 2 * kNumEpiWarps);
         mbar_init(drain, 1);
+        if constexpr (kGatedBack) {
+            for (int w = 0; w < kNumEpiWarps; ++w) mbar_init(&loaded[w], 1);
+        }
         *abort_flag = 0u;
         fence_barrier_init();
     }
     if (warp == kProdAWarp && lane == 0) {
         prefetch_tmap(&tma_a);
-        if (p.lora_stages) prefetch_tmap(&tma_u);
+        if (p.lora_stages || kGated || kGatedBack) prefetch_tmap(&tma_u);
     }
     if (warp == kProdBWarp && lane == 0) {
         prefetch_tmap(&tma_b);
-        if (p.lora_stages) prefetch_tmap(&tma_v);
+        if (p.lora_stages || kGated) prefetch_tmap(&tma_v);
     }
     if (warp == kProdSfWarp && lane == 0) {
         prefetch_tmap(&tma_sfa);
@@ -454,8 +496,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             tma_load_2d_pair(st, &tma_a, leader_full, (int32_t)(ks * kBKBytes),
                                              (int32_t)(mt * kPairM + rank * kCtaM));
                         } else if (warp == kProdBWarp) {
-                            tma_load_2d_pair(st + kABytes, &tma_b, leader_full, (int32_t)(ks * kBKBytes),
-                                             (int32_t)(nt * kBN + rank * kCtaN));
+                            // gated: the leader's half of the tile is the gate's
+                            // rows, its peer's the up projection's (in tma_u)
+                            tma_load_2d_pair(st + kABytes, kGated && rank ? &tma_u : &tma_b, leader_full,
+                                             (int32_t)(ks * kBKBytes),
+                                             (int32_t)(kGated ? nt * kCtaN : nt * kBN + rank * kCtaN));
                         } else {
                             // scale boxes: 4 groups of 512 bytes per 128-row tile;
                             // groups past K and row tiles past M / N read as zero
@@ -463,8 +508,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             mbar_arrive_expect_tx(&sf_full[stage], kSFABytes + kSFBBytes);
                             tma_load_3d(sfa_s, &tma_sfa, &sf_full[stage], 0, (int32_t)(ks * kKStepsPerStage),
                                         (int32_t)(2 * mt + rank));
-                            tma_load_3d(sfa_s + kSFABytes, &tma_sfb, &sf_full[stage], 0,
-                                        (int32_t)(ks * kKStepsPerStage), (int32_t)(2 * nt));
+                            if constexpr (kGated) {
+                                tma_load_3d(sfa_s + kSFABytes, &tma_sfb, &sf_full[stage], 0,
+                                            (int32_t)(ks * kKStepsPerStage), (int32_t)nt);
+                                tma_load_3d(sfa_s + kSFABytes + kSFBBytes / 2, &tma_v, &sf_full[stage], 0,
+                                            (int32_t)(ks * kKStepsPerStage), (int32_t)nt);
+                            } else {
+                                tma_load_3d(sfa_s + kSFABytes, &tma_sfb, &sf_full[stage], 0,
+                                            (int32_t)(ks * kKStepsPerStage), (int32_t)(2 * nt));
+                            }
                         }
                         if (++stage == kStages) {
                             stage = 0;
@@ -688,6 +740,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t q = warp & 3u;                          // TMEM lane quadrant
         const uint32_t half = (warp - kFirstEpiWarp) >> 2;     // 128-column half of the tile
         const float alpha = __fmul_rn(__fmul_rn(*p.sga, *p.sgb), p.alpha);
+        uint8_t* const own_slice = staging + (half * 4 + q) * (slices_of(kMode) * kSliceBytes);
+        GatedWarp gated{&loaded[half * 4 + q]};   // (of the gated modes)
         constexpr bool kAmax = kMode == kEpiAmax;
         constexpr bool has_c = kMode == kEpiC;
         const uint32_t leader_acc_empty = map_to_cta(smem_u32(acc_empty), 0);
@@ -704,6 +758,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tile_coords(tile, p, mt, nt);
             if constexpr (has_c)
                 prefetch_c_row(p, mt * kPairM + rank * kCtaM + row_local, nt * kBN + half * 128);
+            if constexpr (kGatedBack)
+                gated_backward_load(p, extra, gated, own_slice, lane, mt * kPairM + rank * kCtaM + q * 32,
+                                    nt * kBN + half * 128);
             // One thread per warp waits for the accumulator, suspended in the
             // barrier's try_wait (no issue slots taken from the MMA issuer);
             // each warp wakes on the barrier itself, not behind a named
@@ -721,7 +778,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t row = row0 + row_local;
             const uint32_t nbase = nt * kBN + half * 128;
             const uint32_t taddr = tmem + ((q * 32u) << 16) + kAccCol + half * 128;
-            if (has_c && p.c_staged) {
+            if constexpr (kGated) {
+                // (the accumulator's first 128 columns are the gate's)
+                uint32_t v[4][32];
+                const uint32_t at = tmem + ((q * 32u) << 16) + kAccCol + half * 64;
+                tmem_ld_32x32b_x32(at, v[0]);
+                tmem_ld_32x32b_x32(at + 32, v[1]);
+                tmem_ld_32x32b_x32(at + 128, v[2]);
+                tmem_ld_32x32b_x32(at + 160, v[3]);
+                tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(leader_acc_empty);
+                gated_epilogue(p, extra, &tma_d, own_slice, lane, row0 + q * 32, nt * kCtaN + half * 64, v, alpha,
+                               __fmul_rn(*p.sga, *p.sgu), amax_plain, amax_rht);
+            } else if constexpr (kGatedBack) {
+                uint32_t v[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(taddr + c * 32, v[c]);
+                tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(leader_acc_empty);
+                if (!gated_backward_epilogue(p, extra, gated, &tma_d, &tma_u, own_slice, lane, row0 + q * 32, nbase, v,
+                                             alpha, abort_flag, amax_plain, amax_rht))
+                    break;
+            } else if (has_c && p.c_staged) {
                 // C through this warp's 4 KiB slice: each round the lanes copy
                 // the round's 32 rows of C into the slice (the output map's
                 // box and swizzle), every lane replaces its row's values by
@@ -923,8 +1005,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             ++tiles_done;
         }
+        if constexpr (kGatedBack) gated_backward_drain(p, gated, lane);
         if (p.tma_store && lane == 0) bulk_wait_all();
-        if constexpr (kAmax) {
+        if (kAmax || ((kGated || kGatedBack) && p.amax_out)) {
             amax_plain = warp_max(amax_plain);
             amax_rht = warp_max(amax_rht);
             if (lane == 0) {
@@ -1035,14 +1118,14 @@ cudaError_t launch_lora_prescale(const void* u, int64_t ldu, int64_t rows, int64
 bool register_split_ok() {
     static int ok = -1;
     if (ok < 0) {
-        cudaFuncAttributes f0, f1;
-        cudaFuncAttributes f2;
-        ok = (cudaFuncGetAttributes(&f0, gemm_nvf4_kernel<kEpiPlain>) == cudaSuccess &&
-              cudaFuncGetAttributes(&f1, gemm_nvf4_kernel<kEpiAmax>) == cudaSuccess &&
-              cudaFuncGetAttributes(&f2, gemm_nvf4_kernel<kEpiC>) == cudaSuccess &&
-              f0.numRegs * kThreads >= 128 * (64 + 72) + 256 * 184 &&
-              f1.numRegs * kThreads >= 128 * (64 + 72) + 256 * 184 &&
-              f2.numRegs * kThreads >= 128 * (64 + 72) + 256 * 184)
+        cudaFuncAttributes f;
+        auto split = [&](auto* kernel) {
+            return cudaFuncGetAttributes(&f, kernel) == cudaSuccess &&
+                   f.numRegs * kThreads >= 128 * (64 + 72) + 256 * 184;
+        };
+        ok = (split(gemm_nvf4_kernel<kEpiPlain>) && split(gemm_nvf4_kernel<kEpiAmax>) &&
+              split(gemm_nvf4_kernel<kEpiC>) && split(gemm_nvf4_kernel<kEpiGated>) &&
+              split(gemm_nvf4_kernel<kEpiGatedBack>))
                  ? 1
                  : 0;
     }
@@ -1058,7 +1141,7 @@ int max_active_pairs() {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2 * (unsigned)(device_sm_count() / 2), 1, 1);
         cfg.blockDim = dim3(kThreads, 1, 1);
-        cfg.dynamicSmemBytes = kSmemBytes;
+        cfg.dynamicSmemBytes = smem_of(kEpiPlain);
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
         attr.val.clusterDim.x = 2;
@@ -1102,55 +1185,160 @@ int device_sm_count() {
     return counts[dev];
 }
 
-cudaError_t launch_gemm(const GemmOperand& a, const GemmOperand& b, void* d, int64_t ldd, bool out_fp32,
-                        cudaStream_t stream, const LowRank* lora, float* amax_out, uint32_t rht_mask,
-                        const Axpby* axpby) {
+namespace {
+
+// The kernels' shared memory, once per device, and the register split.
+cudaError_t prepare_gemm() {
     static bool attr_set[64];
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-        cudaError_t e =
-            cudaFuncSetAttribute(gemm_nvf4_kernel<kEpiPlain>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)kSmemBytes);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(gemm_nvf4_kernel<kEpiAmax>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)kSmemBytes);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(gemm_nvf4_kernel<kEpiC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)kSmemBytes);
+        cudaError_t e = cudaSuccess;
+        auto allow = [&](auto* kernel, int mode) {
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(mode));
+        };
+        allow(gemm_nvf4_kernel<kEpiPlain>, kEpiPlain);
+        allow(gemm_nvf4_kernel<kEpiAmax>, kEpiAmax);
+        allow(gemm_nvf4_kernel<kEpiC>, kEpiC);
+        allow(gemm_nvf4_kernel<kEpiGated>, kEpiGated);
+        allow(gemm_nvf4_kernel<kEpiGatedBack>, kEpiGatedBack);
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
-    if (!register_split_ok()) return cudaErrorInvalidConfiguration;
-    CUtensorMap ma, mb, msa, msb, md;
-    if (!make_codes_map(&ma, a, kCtaM) || !make_codes_map(&mb, b, kCtaN) || !make_scale_map(&msa, a, 1) ||
-        !make_scale_map(&msb, b, 2))
-        return cudaErrorInvalidValue;
+    return register_split_ok() ? cudaSuccess : cudaErrorInvalidConfiguration;
+}
+
+// The sizes, scales and wait limit of a product of a with columns of b, in
+// tiles of `bn` columns.
+Params gemm_params(const GemmOperand& a, const GemmOperand& b, uint32_t bn) {
     Params p{};
     p.M = (uint32_t)a.rows;
     p.N = (uint32_t)b.rows;
     p.m_tiles = (uint32_t)((a.rows + kPairM - 1) / kPairM);
-    p.n_tiles = (uint32_t)((b.rows + kBN - 1) / kBN);
+    p.n_tiles = (uint32_t)((b.rows + bn - 1) / bn);
     p.ksteps = (uint32_t)((a.cols + 63) / 64);
     p.kstages = (p.ksteps + kKStepsPerStage - 1) / kKStepsPerStage;
     p.last_nk = p.ksteps - (p.kstages - 1) * kKStepsPerStage;
-    p.n_fast = b.rows <= a.rows ? 1 : 0;   // B is the smaller operand: keep it in L2
+    p.n_fast = b.rows * (kBN / bn) <= a.rows ? 1 : 0;   // B is the smaller operand: keep it in L2
     p.sga = a.sg;
     p.sgb = b.sg;
+    p.alpha = 1.0f;
+    p.timeout_ns = kTimeoutNs;
+    // a fault armed by the test support entry point applies to this launch only
+    const uint64_t armed = g_armed_fault_ns.exchange(0);
+    if (armed) {
+        p.timeout_ns = armed;
+        p.withhold = 1;
+    }
+    return p;
+}
+
+// amax_out of a call, cleared on its stream, and the RHT's signs.
+cudaError_t set_amax(Params& p, float* amax_out, uint32_t rht_mask, cudaStream_t stream) {
+    p.amax_out = amax_out;
+    for (int i = 0; i < 16; ++i) p.rht_sgn[i] = ((rht_mask >> i) & 1u) ? 0x80008000u : 0u;
+    return cudaMemsetAsync(amax_out, 0, 2 * sizeof(float), stream);
+}
+
+int gemm_grid(const Params& p) {
+    const uint32_t tiles = p.m_tiles * p.n_tiles;
+    const uint32_t pairs = (uint32_t)max_active_pairs();
+    return 2 * (int)(tiles < pairs ? tiles : pairs);
+}
+
+// 2-D map over a matrix kept for the backward pass: 64 columns by 32 rows per
+// box, BF16 (128-byte swizzle) or 8-bit codes (64-byte swizzle).
+bool make_checkpoint_map(CUtensorMap* map, const CheckpointView& t, int64_t rows, int64_t cols) {
+    if (!t.scales) return make_output_map(map, t.data, rows, cols, t.ld, false);
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)t.ld};
+    const cuuint32_t box[2] = {64, 32};
+    const cuuint32_t elem[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, t.data, dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Gate and up as kept, of the call's M x N.
+bool set_checkpoints(Params& p, CUtensorMap* gate_map, CUtensorMap* up_map, const CheckpointView& gate,
+                     const CheckpointView& up) {
+    p.kept = gate.scales ? 2 : 1;
+    p.scale_blocks = (p.N + 31) / 32;
+    p.gate_scales = gate.scales;
+    p.up_scales = up.scales;
+    p.ld_gate_scales = gate.ld_scales;
+    p.ld_up_scales = up.ld_scales;
+    if (gate.scales) {
+        p.x_gate_scales = extent_rows(gate.scales, p.M, gate.ld_scales, p.scale_blocks);
+        p.x_up_scales = extent_rows(up.scales, p.M, up.ld_scales, p.scale_blocks);
+    }
+    return make_checkpoint_map(gate_map, gate, p.M, p.N) && make_checkpoint_map(up_map, up, p.M, p.N);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_gated(const GemmOperand& a, const GemmOperand& gate, const GemmOperand& up, bool gelu, void* h,
+                              int64_t ldh, const CheckpointView* gate_kept, const CheckpointView* up_kept,
+                              float* amax_out, uint32_t rht_mask, cudaStream_t stream) {
+    cudaError_t e = prepare_gemm();
+    if (e != cudaSuccess) return e;
+    CUtensorMap ma, mg, mu, msa, msg, msu, mh;
+    ExtraMaps<kEpiGated> extra;
+    Params p = gemm_params(a, gate, kCtaN);
+    if (!make_codes_map(&ma, a, kCtaM) || !make_codes_map(&mg, gate, kCtaN) || !make_codes_map(&mu, up, kCtaN) ||
+        !make_scale_map(&msa, a, 1) || !make_scale_map(&msg, gate, 1) || !make_scale_map(&msu, up, 1) ||
+        !make_output_map(&mh, h, a.rows, gate.rows, ldh, false))
+        return cudaErrorInvalidValue;
+    extra.gate = extra.up = mh;   // (not read unless they are kept)
+    if (gate_kept && !set_checkpoints(p, &extra.gate, &extra.up, *gate_kept, *up_kept)) return cudaErrorInvalidValue;
+    p.gelu = gelu ? 1 : 0;
+    p.sgu = up.sg;
+    p.tma_store = 1;
+    if (amax_out && (e = set_amax(p, amax_out, rht_mask, stream)) != cudaSuccess) return e;
+    gemm_nvf4_kernel<kEpiGated>
+        <<<gemm_grid(p), kThreads, smem_of(kEpiGated), stream>>>(ma, mg, msa, msg, mh, mu, msu, p, extra);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_gemm_gated_backward(const GemmOperand& a, const GemmOperand& b, bool gelu,
+                                       const CheckpointView& gate, const CheckpointView& up, void* dgate,
+                                       int64_t ld_dgate, void* dup, int64_t ld_dup, float* amax_out, uint32_t rht_mask,
+                                       cudaStream_t stream) {
+    cudaError_t e = prepare_gemm();
+    if (e != cudaSuccess) return e;
+    CUtensorMap ma, mb, msa, msb, mg, mu;
+    ExtraMaps<kEpiGatedBack> extra;
+    Params p = gemm_params(a, b, kBN);
+    if (!make_codes_map(&ma, a, kCtaM) || !make_codes_map(&mb, b, kCtaN) || !make_scale_map(&msa, a, 1) ||
+        !make_scale_map(&msb, b, 2) || !make_output_map(&mg, dgate, a.rows, b.rows, ld_dgate, false) ||
+        !make_output_map(&mu, dup, a.rows, b.rows, ld_dup, false) ||
+        !set_checkpoints(p, &extra.gate, &extra.up, gate, up))
+        return cudaErrorInvalidValue;
+    p.gelu = gelu ? 1 : 0;
+    p.tma_store = 1;
+    if (amax_out && (e = set_amax(p, amax_out, rht_mask, stream)) != cudaSuccess) return e;
+    gemm_nvf4_kernel<kEpiGatedBack>
+        <<<gemm_grid(p), kThreads, smem_of(kEpiGatedBack), stream>>>(ma, mb, msa, msb, mg, mu, mb, p, extra);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_gemm(const GemmOperand& a, const GemmOperand& b, void* d, int64_t ldd, bool out_fp32,
+                        cudaStream_t stream, const LowRank* lora, float* amax_out, uint32_t rht_mask,
+                        const Axpby* axpby) {
+    cudaError_t e = prepare_gemm();
+    if (e != cudaSuccess) return e;
+    CUtensorMap ma, mb, msa, msb, md;
+    if (!make_codes_map(&ma, a, kCtaM) || !make_codes_map(&mb, b, kCtaN) || !make_scale_map(&msa, a, 1) ||
+        !make_scale_map(&msb, b, 2))
+        return cudaErrorInvalidValue;
+    Params p = gemm_params(a, b, kBN);
     p.d = d;
     p.ldd = ldd;
     p.out_fp32 = out_fp32 ? 1 : 0;
     p.xd = extent_rows(d, a.rows, ldd * (out_fp32 ? 4 : 2), b.rows * (out_fp32 ? 4 : 2));
-    p.alpha = 1.0f;
-    p.timeout_ns = kTimeoutNs;
-    {
-        // a fault armed by the test support entry point applies to this launch only
-        const uint64_t armed = g_armed_fault_ns.exchange(0);
-        if (armed) {
-            p.timeout_ns = armed;
-            p.withhold = 1;
-        }
-    }
     const int64_t esz = out_fp32 ? 4 : 2;
     if (axpby) {
         // the C term goes with the plain product only
@@ -1172,10 +1360,7 @@ cudaError_t launch_gemm(const GemmOperand& a, const GemmOperand& b, void* d, int
     if (amax_out) {
         // the amax is taken in the BF16 TMA-store epilogue
         if (out_fp32 || !p.tma_store) return cudaErrorInvalidValue;
-        const cudaError_t e = cudaMemsetAsync(amax_out, 0, 2 * sizeof(float), stream);
-        if (e != cudaSuccess) return e;
-        p.amax_out = amax_out;
-        for (int i = 0; i < 16; ++i) p.rht_sgn[i] = ((rht_mask >> i) & 1u) ? 0x80008000u : 0u;
+        if ((e = set_amax(p, amax_out, rht_mask, stream)) != cudaSuccess) return e;
     }
     CUtensorMap mu = ma, mv = ma;  // low-rank operands (unused by the kernel otherwise; any valid map)
     p.c_staged = (p.c && p.c_vec && p.tma_store) ? 1 : 0;
@@ -1186,19 +1371,16 @@ cudaError_t launch_gemm(const GemmOperand& a, const GemmOperand& b, void* d, int
         p.lora_stages = (uint32_t)(lora->r / 64);
         // U' = U * (beta / (s_gA s_gB)), so that the epilogue's factor
         // s_gA s_gB leaves beta * U V^T
-        const cudaError_t e = launch_lora_prescale(lora->u, lora->ldu, a.rows, lora->r, lora->beta, a.sg, b.sg,
-                                                   lora->u_scaled, stream);
+        e = launch_lora_prescale(lora->u, lora->ldu, a.rows, lora->r, lora->beta, a.sg, b.sg, lora->u_scaled, stream);
         if (e != cudaSuccess) return e;
     }
-    const uint32_t tiles = p.m_tiles * p.n_tiles;
-    const uint32_t pairs = (uint32_t)max_active_pairs();
-    const int grid = 2 * (int)(tiles < pairs ? tiles : pairs);
+    const int grid = gemm_grid(p);
     if (p.amax_out)
-        gemm_nvf4_kernel<kEpiAmax><<<grid, kThreads, kSmemBytes, stream>>>(ma, mb, msa, msb, md, mu, mv, p);
+        gemm_nvf4_kernel<kEpiAmax><<<grid, kThreads, smem_of(kEpiAmax), stream>>>(ma, mb, msa, msb, md, mu, mv, p, {});
     else if (p.c)
-        gemm_nvf4_kernel<kEpiC><<<grid, kThreads, kSmemBytes, stream>>>(ma, mb, msa, msb, md, mu, mv, p);
+        gemm_nvf4_kernel<kEpiC><<<grid, kThreads, smem_of(kEpiC), stream>>>(ma, mb, msa, msb, md, mu, mv, p, {});
     else
-        gemm_nvf4_kernel<kEpiPlain><<<grid, kThreads, kSmemBytes, stream>>>(ma, mb, msa, msb, md, mu, mv, p);
+        gemm_nvf4_kernel<kEpiPlain><<<grid, kThreads, smem_of(kEpiPlain), stream>>>(ma, mb, msa, msb, md, mu, mv, p, {});
     return cudaGetLastError();
 }
 

@@ -161,6 +161,19 @@ cudaError_t launch_checkpoint_encode(const uint16_t* x, int64_t ld_x, int64_t ro
 cudaError_t launch_checkpoint_decode(const CheckpointView& in, int64_t rows, int64_t cols, void* y, int64_t ld_y,
                                      bool out_fp32, cudaStream_t stream);
 
+// The gated pair of products of a feed-forward block and its backward pass
+// (gemm.cu, gemm_gated.cuh): h = act(A gate^T) (A up^T), gate and up kept in
+// gate_kept and up_kept if given (both BF16 or both in 8 bits); dgate and dup
+// from dh = A B^T and the kept ones.  amax_out as for launch_gemm: of h, or of
+// dgate and dup together.
+cudaError_t launch_gemm_gated(const GemmOperand& a, const GemmOperand& gate, const GemmOperand& up, bool gelu, void* h,
+                              int64_t ldh, const CheckpointView* gate_kept, const CheckpointView* up_kept,
+                              float* amax_out, uint32_t rht_mask, cudaStream_t stream);
+cudaError_t launch_gemm_gated_backward(const GemmOperand& a, const GemmOperand& b, bool gelu,
+                                       const CheckpointView& gate, const CheckpointView& up, void* dgate,
+                                       int64_t ld_dgate, void* dup, int64_t ld_dup, float* amax_out, uint32_t rht_mask,
+                                       cudaStream_t stream);
+
 // The norms after and before a block (block_norm.cu).  Leading dimensions in
 // elements; optional parts are null.
 enum GateKind { kGateNone = 0, kGateChannel = 1, kGateToken = 2 };

@@ -585,6 +585,82 @@ def checkpoint_decode(kept: Checkpoint, out_dtype=torch.bfloat16, out: Optional[
     return out
 
 
+_ACTIVATIONS = {"silu": capi.NVFP4_ACT_SILU, "gelu": capi.NVFP4_ACT_GELU}
+
+
+def _activation(name: str) -> int:
+    if name not in _ACTIVATIONS:
+        raise ValueError(f"activation: one of {sorted(_ACTIVATIONS)} expected, got {name!r}")
+    return _ACTIVATIONS[name]
+
+
+def _check_amax(amax: Optional[torch.Tensor], rht_mask: Optional[int]) -> None:
+    if (amax is None) != (rht_mask is None):
+        raise ValueError("amax and rht_mask go together")
+    if amax is not None and (amax.dtype != torch.float32 or amax.numel() < 2 or not amax.is_contiguous()):
+        raise ValueError("amax: contiguous float32 [2] expected")
+
+
+def operand_rows(q: NVFP4Operand, start: int, stop: int) -> NVFP4Operand:
+    """Rows start .. stop - 1 of an operand, a view (start a multiple of 128, where its scales' tiles begin):
+    the gate's and the up projection's halves of weights quantized as one matrix."""
+    if not 0 <= start <= stop <= q.rows or start % 128 != 0:
+        raise ValueError(f"rows {start}..{stop} of {q.rows}: a start at a multiple of 128 expected")
+    first = start // 128 * ((q.cols + 63) // 64) * 512
+    return NVFP4Operand(q.codes[start:stop], q.scales[first:], q.amax, q.global_scale, stop - start, q.cols)
+
+
+def gemm_gated(a: NVFP4Operand, b_gate: NVFP4Operand, b_up: NVFP4Operand, *, activation: str = "silu",
+               keep: Optional[str] = None, out: Optional[torch.Tensor] = None, amax: Optional[torch.Tensor] = None,
+               rht_mask: Optional[int] = None, stream=None
+               ) -> Tuple[torch.Tensor, Optional[Checkpoint], Optional[Checkpoint]]:
+    """H = act(A * B_gate^T) * (A * B_up^T), bf16 [a.rows, b_gate.rows] (nvfp4_gemm_gated): a gated feed-forward
+    block's projections, activation ("silu" or "gelu", its tanh form) and product in one kernel.
+    keep "bf16" or "e4m3" (8 bits) keeps gate and up for gemm_gated_backward.  amax (float32 [2]) takes H's two
+    amaxes for quantize_row_col_rht_amax with rht_mask.  Returns (H, gate, up), the latter None without keep."""
+    act = _activation(activation)
+    _check_amax(amax, rht_mask)
+    rows, cols, device = a.rows, b_gate.rows, a.codes.device
+    if out is None:
+        out = torch.empty((rows, cols), dtype=torch.bfloat16, device=device)
+    ptr, ld = _matrix(out, rows, cols, torch.bfloat16, "out")
+    gate = up = None
+    if keep is not None:
+        gate, up = alloc_checkpoint(rows, cols, keep, device), alloc_checkpoint(rows, cols, keep, device)
+    _check_here(a.codes, b_gate.codes, b_up.codes, out, amax)
+    status = capi.nvfp4_gemm_gated(a.struct(), b_gate.struct(), b_up.struct(), act, ptr, ld,
+                                   None if gate is None else gate.struct(), None if up is None else up.struct(),
+                                   None if amax is None else amax.data_ptr(), rht_mask or 0, stream_handle(stream))
+    capi.check(status, "nvfp4_gemm_gated")
+    return out, gate, up
+
+
+def gemm_gated_backward(dy: NVFP4Operand, w_down: NVFP4Operand, gate: Union[torch.Tensor, Checkpoint],
+                        up: Union[torch.Tensor, Checkpoint], *, activation: str = "silu",
+                        out: Optional[torch.Tensor] = None, amax: Optional[torch.Tensor] = None,
+                        rht_mask: Optional[int] = None, stream=None) -> torch.Tensor:
+    """The gradients of gate and up, bf16 [dy.rows, 2 * w_down.rows] with gate's in the first half of the columns
+    (nvfp4_gemm_gated_backward): dH = dY * W_down^T with the down projection's col-wise operand, then
+    dgate = dH * up * act'(gate) and dup = dH * act(gate) in the epilogue.  gate and up as gemm_gated kept them.
+    amax takes the result's two amaxes."""
+    act = _activation(activation)
+    _check_amax(amax, rht_mask)
+    rows, cols = dy.rows, w_down.rows
+    gate, up = (x if isinstance(x, Checkpoint) else Checkpoint(x, None, rows, cols) for x in (gate, up))
+    for x, what in ((gate, "gate"), (up, "up")):
+        if (x.rows, x.cols) != (rows, cols):
+            raise ValueError(f"{what}: [{rows}, {cols}] expected, got [{x.rows}, {x.cols}]")
+    if out is None:
+        out = torch.empty((rows, 2 * cols), dtype=torch.bfloat16, device=dy.codes.device)
+    ptr, ld = _matrix(out, rows, 2 * cols, torch.bfloat16, "out")
+    _check_here(dy.codes, w_down.codes, gate.data, up.data, gate.scales, up.scales, out, amax)
+    status = capi.nvfp4_gemm_gated_backward(dy.struct(), w_down.struct(), act, gate.struct(), up.struct(), ptr, ld,
+                                            ptr + 2 * cols, ld, None if amax is None else amax.data_ptr(),
+                                            rht_mask or 0, stream_handle(stream))
+    capi.check(status, "nvfp4_gemm_gated_backward")
+    return out
+
+
 def _block_norm_desc(tokens, width, dtype, post_weight, pre_weight, gate, residual_scale, eps
                      ) -> capi.nvfp4_block_norm_desc:
     if dtype == torch.bfloat16:

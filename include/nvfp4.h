@@ -656,6 +656,54 @@ NVFP4_API nvfp4_status nvfp4_block_norm_backward(const nvfp4_block_norm_desc *de
                                                  float *dpre_weight, void *dgate, int64_t ld_dgate, void *workspace,
                                                  size_t workspace_bytes, nvfp4_stream_t stream);
 
+/*
+ * ---- A gated feed-forward block ----------------------------------------------
+ *
+ * nvfp4_gemm_gated -- both projections of a gated feed-forward block [FS: a
+ * SwiGLU transformer, hidden 3072, FFN 9216], the activation and the product in
+ * one kernel:
+ *   g = A B_gate^T,  u = A B_up^T  (decoded products, as nvfp4_gemm's),
+ *   H = act(g) * u
+ *  A            [M][K] operand;  B_gate, B_up  [N][K] operands (each with its own
+ *               scales; two row ranges of one operand are two operands with the
+ *               same global_scale, the second at a multiple of 128 rows).
+ *  activation   SILU: g / (1 + e^-g);  GELU: its tanh form,
+ *               g / (1 + e^-2z), z = sqrt(2/pi) (g + 0.044715 g^3).
+ *  H            BF16 [M][ldh]: the down projection's input.
+ *  gate, up     where g and u are kept for the backward pass, both BF16 or both
+ *               8-bit (nvfp4_checkpoint); both NULL: not kept.
+ *  amax_out     NULL, or H's two tensor amaxes as nvfp4_gemm_amax writes them
+ *               (for nvfp4_quantize_row_col_rht_amax), with rht_sign_mask.
+ * FP32 from the accumulators to one rounding of each output.
+ * Requirements: K % 16 == 0 and N % 16 == 0, with amax_out M % 16 == 0 [SHAPE];
+ * operands as for nvfp4_gemm; H 16-byte aligned, ldh % 8 == 0 and >= N; K = 0 is
+ * UNSUPPORTED.  M = 0 or N = 0 enqueues nothing but amax_out = 0.
+ */
+typedef enum { NVFP4_ACT_SILU = 0, NVFP4_ACT_GELU = 1 } nvfp4_activation;
+NVFP4_API nvfp4_status nvfp4_gemm_gated(const nvfp4_tensor *A, const nvfp4_tensor *B_gate, const nvfp4_tensor *B_up,
+                                        nvfp4_activation activation, void *H, int64_t ldh,
+                                        const nvfp4_checkpoint *gate, const nvfp4_checkpoint *up, float *amax_out,
+                                        uint16_t rht_sign_mask, nvfp4_stream_t stream);
+
+/*
+ * nvfp4_gemm_gated_backward -- the down projection's Dgrad with the gradient of
+ * the activation and the product in its epilogue: dH = A B^T (A the output
+ * gradient's ROWWISE operand [M][K], B the down projection's COLWISE one
+ * [N][K]) is not written, but
+ *   dgate = dH u act'(g),  dup = dH act(g)
+ * from the gate and up that nvfp4_gemm_gated kept (8-bit: the values they stand
+ * for).  dgate and dup, BF16 [M][N], are usually the two halves of one
+ * [M][2 N] matrix, whose quantization feeds the up projections' Dgrad and Wgrad.
+ *  amax_out     NULL, or the two amaxes of dgate and dup together.
+ * Requirements as nvfp4_gemm_gated's; dgate and dup 16-byte aligned, leading
+ * dimensions multiples of 8 and >= N.  Outputs may not overlap inputs.
+ */
+NVFP4_API nvfp4_status nvfp4_gemm_gated_backward(const nvfp4_tensor *A, const nvfp4_tensor *B,
+                                                 nvfp4_activation activation, const nvfp4_checkpoint *gate,
+                                                 const nvfp4_checkpoint *up, void *dgate, int64_t ld_dgate, void *dup,
+                                                 int64_t ld_dup, float *amax_out, uint16_t rht_sign_mask,
+                                                 nvfp4_stream_t stream);
+
 /* Human-readable name of a status. */
 NVFP4_API const char *nvfp4_status_string(nvfp4_status status);
 

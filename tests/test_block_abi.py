@@ -164,3 +164,78 @@ def test_wrappers_refuse():
                  lambda: ops.block_norm_backward(x, x, x, x, pre_weight=w, dgate=w)):
         with pytest.raises(ValueError):
             call()
+
+
+def operand(rows=64, cols=64, **kw):
+    args = dict(codes=A16, scales=A16, amax=None, sg=A16, rows=rows, cols=cols, ld=(cols // 2 + 15) // 16 * 16)
+    args.update(kw)
+    return capi.nvfp4_tensor(*args.values())
+
+
+def gated(**kw):
+    args = dict(A=operand(), B=operand(), B_up=operand(), act=0, H=A16, ldh=64, gate=kept(), up=kept(), amax=A16, mask=0,
+                stream=None)
+    args.update(kw)
+    return capi.nvfp4_gemm_gated(*args.values())
+
+
+def gated_backward(**kw):
+    args = dict(A=operand(), B=operand(), act=0, gate=kept(), up=kept(), dgate=A16, ld_dgate=128, dup=A16 + 128,
+                ld_dup=128, amax=A16, mask=0, stream=None)
+    args.update(kw)
+    return capi.nvfp4_gemm_gated_backward(*args.values())
+
+
+@pytest.mark.parametrize("call,matrices", [(gated, (("H", "ldh"),)),
+                                           (gated_backward, (("dgate", "ld_dgate"), ("dup", "ld_dup")))])
+def test_gated_refusals(call, matrices):
+    for bad in (-1, 2):
+        assert call(act=bad) == E.NVFP4_ERR_INVALID_ARG
+    assert call(A=None) == E.NVFP4_ERR_INVALID_ARG and call(B=None) == E.NVFP4_ERR_INVALID_ARG
+    assert call(A=operand(cols=128)) == E.NVFP4_ERR_SHAPE
+    assert call(A=operand(rows=63)) == E.NVFP4_ERR_SHAPE                  # the rotated amax's 16-row blocks
+    assert call(amax=A16 + 2) == E.NVFP4_ERR_ALIGNMENT
+    for n in (8, 60):
+        assert call(B=operand(rows=n), **({"B_up": operand(rows=n)} if call is gated else {})) == E.NVFP4_ERR_SHAPE
+    empty = {"A": operand(cols=0), "B": operand(cols=0)}
+    assert call(**empty, **({"B_up": operand(cols=0)} if call is gated else {})) == E.NVFP4_ERR_UNSUPPORTED
+    for name, ld in matrices:
+        assert call(**{name: None}) == E.NVFP4_ERR_INVALID_ARG
+        assert call(**{name: A16 + 8}) == E.NVFP4_ERR_ALIGNMENT
+        assert call(**{ld: 68}) == E.NVFP4_ERR_ALIGNMENT
+        assert call(**{ld: 56}) == E.NVFP4_ERR_SHAPE
+    for name in ("gate", "up"):
+        assert call(**{name: None}) == E.NVFP4_ERR_INVALID_ARG
+        assert call(**{name: kept(data=None)}) == E.NVFP4_ERR_INVALID_ARG
+        assert call(**{name: kept(data=A16 + 8)}) == E.NVFP4_ERR_ALIGNMENT
+        assert call(**{name: kept(ld=48)}) == E.NVFP4_ERR_SHAPE
+        assert call(**{name: kept(ld_scales=8)}) == E.NVFP4_ERR_ALIGNMENT
+        assert call(**{name: kept(scales=None)}) == E.NVFP4_ERR_INVALID_ARG   # one kind for both
+    assert call(A=operand(rows=0), amax=None) == E.NVFP4_OK
+
+
+def test_gated_operands_differ():
+    assert gated(B_up=None) == E.NVFP4_ERR_INVALID_ARG
+    assert gated(B_up=operand(rows=80)) == E.NVFP4_ERR_SHAPE
+    assert gated(B_up=operand(cols=128)) == E.NVFP4_ERR_SHAPE
+
+
+def test_gated_wrappers_refuse():
+    q = ops.alloc_operand(64, 64, "cpu")
+    x = torch.zeros(64, 64, dtype=torch.bfloat16)
+    wide = torch.zeros(64, 128, dtype=torch.bfloat16)
+    for call in (lambda: ops.gemm_gated(q, q, q),                                     # on the host
+                 lambda: ops.gemm_gated(q, q, q, activation="relu"),
+                 lambda: ops.gemm_gated(q, q, q, keep="int8"),
+                 lambda: ops.gemm_gated(q, q, q, out=wide),
+                 lambda: ops.gemm_gated(q, q, q, amax=torch.zeros(2)),
+                 lambda: ops.gemm_gated(q, q, q, rht_mask=1),
+                 lambda: ops.gemm_gated(q, q, q, amax=torch.zeros(1), rht_mask=1),
+                 lambda: ops.gemm_gated_backward(q, q, x, x),
+                 lambda: ops.gemm_gated_backward(q, q, x, x, out=x),
+                 lambda: ops.gemm_gated_backward(q, q, x, x.float()),
+                 lambda: ops.gemm_gated_backward(q, q, ops.Checkpoint(x, None, 64, 32), x),
+                 lambda: ops.operand_rows(q, 64, 64),
+                 lambda: ops.operand_rows(q, 0, 65)):
+        with pytest.raises(ValueError):
+            call()
