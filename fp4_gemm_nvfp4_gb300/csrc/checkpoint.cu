@@ -17,7 +17,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kAhead = 4;
-constexpr int kBlocksPerSm = 8;
+constexpr int kBlocksPerSm = 6;
 
 struct Params {
     const void* in;
@@ -92,22 +92,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) encode_kernel(const __
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const float v[8] = {bf16lo(w[i].x), bf16hi(w[i].x), bf16lo(w[i].y), bf16hi(w[i].y),
-                                bf16lo(w[i].z), bf16hi(w[i].z), bf16lo(w[i].w), bf16hi(w[i].w)};
-            uint32_t m = 0;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) m = max(m, finite_magnitude(v[k]));
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-            const uint32_t b = checkpoint_scale(m);
-            const float inv = checkpoint_inverse(b);
+            bool special;
+            const uint32_t b = bf16_scale(w[i], special);
             if (here[i].row < p.rows) {
                 if (here[i].block * 32u + part * 8u < p.cols)
                     store_out(reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + here[i].row * p.ld_out +
                                                        here[i].block * 32u + part * 8u),
-                              make_uint2(e4m3_codes_x4(v[0], v[1], v[2], v[3], inv),
-                                         e4m3_codes_x4(v[4], v[5], v[6], v[7], inv)),
-                              p.x_out);
+                              bf16_codes(w[i], b, special), p.x_out);
                 if (part == 0)
                     store_out(p.scales + here[i].row * p.ld_scales + here[i].block, (uint8_t)b, p.x_scales);
             }

@@ -43,22 +43,78 @@ __device__ __forceinline__ uint32_t checkpoint_scale(uint32_t amax_bits) {
 __device__ __forceinline__ float checkpoint_factor(uint32_t b) { return __uint_as_float(b << 23); }
 __device__ __forceinline__ float checkpoint_inverse(uint32_t b) { return __uint_as_float((254u - b) << 23); }
 
-// One value in units of its block's scale.  The conversion saturates an
-// infinity to 448; a product with 0 makes it NaN.
-__device__ __forceinline__ float checkpoint_scaled(float x, float inv) {
-    float v = x * (finite_magnitude(x) == 0u ? 0.0f : inv);
-    if (inv == 0x1p-120f && fabsf(v) > 240.0f) v = copysignf(240.0f, v);   // the type's end
-    return v;
-}
-
-// Four values, times inv, as four codes, the first in the lowest byte.
-__device__ __forceinline__ uint32_t e4m3_codes_x4(float a, float b, float c, float d, float inv) {
+// Four values as four codes, the first in the lowest byte.
+__device__ __forceinline__ uint32_t e4m3_codes_x4(float a, float b, float c, float d) {
     uint16_t lo, hi;
-    a = checkpoint_scaled(a, inv), b = checkpoint_scaled(b, inv);
-    c = checkpoint_scaled(c, inv), d = checkpoint_scaled(d, inv);
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
     return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
+// One value in units of its block's scale where the block is not an ordinary
+// one: the conversion would saturate an infinity to 448, so that it is made a
+// NaN, and at the type's end codes stop at 240.
+__device__ __forceinline__ float checkpoint_scaled(float x, float inv) {
+    float v = x * (finite_magnitude(x) == 0u ? 0.0f : inv);
+    if (inv == 0x1p-120f && fabsf(v) > 240.0f) v = copysignf(240.0f, v);
+    return v;
+}
+// Whether a block with this largest magnitude, infinities and NaN counted, is
+// not an ordinary one.
+constexpr uint32_t kOrdinaryBelow = 0x7F000000u;   // 2^127
+
+// Eight BF16 values, of which four lanes have a 1x32 block: its scale byte (all
+// four lanes).  Magnitudes order like their bits, two at a time.  `special` is
+// set where a block of the warp is not an ordinary one.
+__device__ __forceinline__ uint32_t bf16_scale(const uint4& w, bool& special) {
+    constexpr uint32_t kMagnitudes = 0x7FFF7FFFu;
+    uint32_t m = __vmaxu2(__vmaxu2(w.x & kMagnitudes, w.y & kMagnitudes), __vmaxu2(w.z & kMagnitudes, w.w & kMagnitudes));
+    m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    m = max(m & 0xFFFF0000u, m << 16);
+    special = __any_sync(0xFFFFFFFFu, m >= kOrdinaryBelow);
+    if (special) {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = max(m, max(finite_magnitude(bf16lo(u[i])), finite_magnitude(bf16hi(u[i]))));
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    }
+    return checkpoint_scale(m);
+}
+// ... and a lane's codes.
+__device__ __forceinline__ uint2 bf16_codes(const uint4& w, uint32_t b, bool special) {
+    float v[8] = {bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y), bf16lo(w.z), bf16hi(w.z), bf16lo(w.w), bf16hi(w.w)};
+    const float inv = checkpoint_inverse(b);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = special ? checkpoint_scaled(v[k], inv) : v[k] * inv;
+    return make_uint2(e4m3_codes_x4(v[0], v[1], v[2], v[3]), e4m3_codes_x4(v[4], v[5], v[6], v[7]));
+}
+
+// 32 FP32 values as the codes of one block; returns its scale byte.  v is used up.
+__device__ __forceinline__ uint32_t fp32_codes(uint32_t* v, uint32_t* codes) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(__uint_as_float(v[i]))));
+    uint32_t bits = __float_as_uint(m) & 0x7FFFFFFFu;
+    uint32_t b = checkpoint_scale(bits);
+    float f = checkpoint_inverse(b);
+    if (bits >= kOrdinaryBelow) {
+        bits = 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) bits = max(bits, finite_magnitude(__uint_as_float(v[i])));
+        b = checkpoint_scale(bits);
+        f = 1.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            v[i] = __float_as_uint(checkpoint_scaled(__uint_as_float(v[i]), checkpoint_inverse(b)));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        codes[i] = e4m3_codes_x4(__uint_as_float(v[4 * i]) * f, __uint_as_float(v[4 * i + 1]) * f,
+                                 __uint_as_float(v[4 * i + 2]) * f, __uint_as_float(v[4 * i + 3]) * f);
+    return b;
 }
 
 // Four codes, times factor.

@@ -42,20 +42,6 @@ __device__ __forceinline__ float gate_slope(float g, float s) {
     return fmaf(s, r, s);
 }
 
-// 8-bit codes of 32 values and their scale byte.
-__device__ __forceinline__ uint32_t encode_32(const uint32_t* v, float alpha, uint32_t* codes) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) m = max(m, finite_magnitude(__uint_as_float(v[i]) * alpha));
-    const uint32_t b = checkpoint_scale(m);
-    const float inv = checkpoint_inverse(b);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        codes[i] = e4m3_codes_x4(__uint_as_float(v[4 * i]) * alpha, __uint_as_float(v[4 * i + 1]) * alpha,
-                                 __uint_as_float(v[4 * i + 2]) * alpha, __uint_as_float(v[4 * i + 3]) * alpha, inv);
-    return b;
-}
-
 // The place of a lane's 16-byte piece i in a slice of 128-byte rows, and in a
 // half slice of 64-byte rows.
 __device__ __forceinline__ uint4* piece128(uint8_t* slice, uint32_t lane, int i) {
@@ -81,12 +67,18 @@ __device__ __forceinline__ void slice_free(uint32_t lane) {
     __syncwarp();
 }
 
-// Forward: columns x .. x + 63 of rows y .. y + 31; v: gate (2 x 32), up.
+// Forward: columns x .. x + 63 of rows y .. y + 31; v: gate (2 x 32), up, used up.
 __device__ __forceinline__ void gated_epilogue(const Params& p, const ExtraMaps<kEpiGated>& extra,
                                                const CUtensorMap* h_map, uint8_t* slice, uint32_t lane, uint32_t y,
                                                uint32_t x, uint32_t (&v)[4][32], float alpha_gate, float alpha_up,
                                                float& amax_plain, float& amax_rht) {
     const bool inside = y < p.M && x < p.N;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j][i] = __float_as_uint(__uint_as_float(v[j][i]) * (j < 2 ? alpha_gate : alpha_up));
+    }
     slice_free(lane);
     auto product = [&](auto gelu) {
 #pragma unroll
@@ -95,8 +87,8 @@ __device__ __forceinline__ void gated_epilogue(const Params& p, const ExtraMaps<
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const int c = 8 * (i & 3) + k;
-                const float g = __uint_as_float(v[i >> 2][c]) * alpha_gate;
-                h[k] = g * gate_sigmoid<decltype(gelu)::value>(g) * (__uint_as_float(v[2 + (i >> 2)][c]) * alpha_up);
+                const float g = __uint_as_float(v[i >> 2][c]);
+                h[k] = g * gate_sigmoid<decltype(gelu)::value>(g) * __uint_as_float(v[2 + (i >> 2)][c]);
             }
             *piece128(slice, lane, i) = make_uint4(pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3]), pack_bf16(h[4], h[5]),
                                                    pack_bf16(h[6], h[7]));
@@ -114,15 +106,13 @@ __device__ __forceinline__ void gated_epilogue(const Params& p, const ExtraMaps<
     if (p.kept == 1) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const float alpha = t ? alpha_up : alpha_gate;
             slice_free(lane);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const uint32_t* a = &v[2 * t + (i >> 2)][8 * (i & 3)];
                 uint32_t w[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    w[k] = pack_bf16(__uint_as_float(a[2 * k]) * alpha, __uint_as_float(a[2 * k + 1]) * alpha);
+                for (int k = 0; k < 4; ++k) w[k] = pack_bf16(__uint_as_float(a[2 * k]), __uint_as_float(a[2 * k + 1]));
                 *piece128(slice, lane, i) = make_uint4(w[0], w[1], w[2], w[3]);
             }
             fence_proxy_async_smem();
@@ -136,12 +126,11 @@ __device__ __forceinline__ void gated_epilogue(const Params& p, const ExtraMaps<
         slice_free(lane);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const float alpha = t ? alpha_up : alpha_gate;
             uint32_t b[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 uint32_t codes[8];
-                b[j] = encode_32(v[2 * t + j], alpha, codes);
+                b[j] = fp32_codes(v[2 * t + j], codes);
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     *piece64(slice + t * (kSliceBytes / 2), lane, 2 * j + i) =
