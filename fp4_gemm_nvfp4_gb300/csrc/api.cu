@@ -790,7 +790,7 @@ nvfp4_status nvfp4_block_norm(const nvfp4_block_norm_desc* desc, const void* res
 
 size_t nvfp4_block_norm_backward_workspace_size(int32_t width) {
     if (width <= 0 || width > nvfp4::kBlockNormMaxWidth) return 0;
-    return (size_t)nvfp4::kBlockNormMaxBlocks * 2 * (size_t)width * sizeof(float);
+    return (size_t)nvfp4::block_norm_max_blocks(width) * 2 * (size_t)width * sizeof(float);
 }
 
 nvfp4_status nvfp4_block_norm_backward(const nvfp4_block_norm_desc* desc, const void* dresidual_out,

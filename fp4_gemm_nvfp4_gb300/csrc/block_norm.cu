@@ -19,13 +19,13 @@
 // each output; the weights' gradients are summed in a fixed order (thread,
 // then blocks), so equal inputs give equal bits.
 //
-// A row is spread over `row_warps` warps, 8 columns per lane and vector, kV
-// vectors per lane, so that a thread meets the same columns in every row: the
-// weights and the columns' sums stay in registers, and what it needs of the
-// next rows it copies to its own places in shared memory ahead of time
-// (cp.async; no other thread reads them, so no barrier stands between).  Rows
-// narrower than a block share it.  Bound by HBM: forward 8 bytes per element
-// (BF16 residual), backward 12.
+// A block takes one row at a time, 8 columns per lane and vector, kV vectors
+// per lane, so that a thread meets the same columns in every row: the weights
+// and the columns' sums stay in registers, and what it needs of the next rows
+// it copies to its own places in shared memory ahead of time (cp.async; no
+// other thread reads them, so no barrier stands between).  Columns are worked
+// on in packed pairs.  Bound by HBM: forward 8 bytes per element (BF16
+// residual), backward 12, where the instructions of a row leave it.
 #include <cuda_runtime.h>
 
 #include "bounds.cuh"
@@ -39,45 +39,103 @@ namespace {
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kMostAhead = 4;
 
-// Threads of the largest block with one and two vectors per lane, and how many
-// such blocks an SM's registers are to hold (which bounds a thread's).
-__host__ __device__ constexpr int most_threads(int vectors) { return vectors == 1 ? 384 : 512; }
-__host__ __device__ constexpr int blocks_at_most_threads(bool backward, int vectors) {
-    return vectors == 2 ? 1 : backward ? 2 : 3;
+// Kernels by the width they serve, and how many blocks of the largest size an
+// SM's registers are to hold (which bounds a thread's).  Up to 256 columns a row
+// is one warp's.  Up to 3072 the forward pass has one vector per lane and three
+// blocks of 12 warps (16384 x 3072: 70 us; two vectors and four blocks of 6 warps
+// 76, three vectors and five of 4 warps 74); the backward pass, which needs 146
+// registers per thread, two vectors and two blocks of 6 warps (115 us; three
+// vectors 115, but 10 % more where more is read; with one vector and 80
+// registers 132, with 96 registers, which spill, 136).
+enum WidthClass { kNarrow, kMedium, kWide };
+__host__ __device__ constexpr int vectors_of(int w, bool backward) {
+    return w == kWide || (w == kMedium && backward) ? 2 : 1;
+}
+__host__ __device__ constexpr int most_threads(int w, bool backward) {
+    return w == kNarrow ? 32 : w == kMedium ? 384 / vectors_of(w, backward) : 512;
+}
+__host__ __device__ constexpr int blocks_of(int w, bool backward) {
+    return w == kNarrow ? 24 : w == kMedium ? (backward ? 2 : 3) : 1;
 }
 
 struct Params {
     BlockNorm a;
-    uint32_t row_warps;          // warps of a row
-    uint32_t rows;               // rows a block takes at once
+    uint32_t warps;              // of a row
     uint32_t ahead;              // rows a thread has in shared memory, 1 to kMostAhead
     Extent x_residual, x_normed, x_codes, x_scales, x_branch, x_gate;
 };
 
-__device__ __forceinline__ void bf16_values(const uint4& w, float* v) {
-    v[0] = bf16lo(w.x), v[1] = bf16hi(w.x), v[2] = bf16lo(w.y), v[3] = bf16hi(w.y);
-    v[4] = bf16lo(w.z), v[5] = bf16hi(w.z), v[6] = bf16lo(w.w), v[7] = bf16hi(w.w);
+// Eight columns as packed pairs.
+struct Eight {
+    uint64_t p[4];
+};
+__device__ __forceinline__ uint64_t both(float x) { return pair(x, x); }
+__device__ __forceinline__ Eight zeros() { return Eight{{0, 0, 0, 0}}; }
+__device__ __forceinline__ Eight mul8(const Eight& a, const Eight& b) {
+    return Eight{{mul2(a.p[0], b.p[0]), mul2(a.p[1], b.p[1]), mul2(a.p[2], b.p[2]), mul2(a.p[3], b.p[3])}};
+}
+__device__ __forceinline__ Eight mul8(const Eight& a, uint64_t b) {
+    return Eight{{mul2(a.p[0], b), mul2(a.p[1], b), mul2(a.p[2], b), mul2(a.p[3], b)}};
+}
+__device__ __forceinline__ Eight fma8(const Eight& a, const Eight& b, const Eight& c) {
+    return Eight{{fma2(a.p[0], b.p[0], c.p[0]), fma2(a.p[1], b.p[1], c.p[1]), fma2(a.p[2], b.p[2], c.p[2]),
+                  fma2(a.p[3], b.p[3], c.p[3])}};
+}
+__device__ __forceinline__ Eight fma8(const Eight& a, uint64_t b, const Eight& c) {
+    return Eight{{fma2(a.p[0], b, c.p[0]), fma2(a.p[1], b, c.p[1]), fma2(a.p[2], b, c.p[2]), fma2(a.p[3], b, c.p[3])}};
+}
+// s plus the products, in the two halves of a pair.
+__device__ __forceinline__ uint64_t dot8(const Eight& a, const Eight& b, uint64_t s) {
+    return fma2(a.p[3], b.p[3], fma2(a.p[2], b.p[2], fma2(a.p[1], b.p[1], fma2(a.p[0], b.p[0], s))));
+}
+__device__ __forceinline__ float halves(uint64_t s) {
+    float lo, hi;
+    unpair(s, lo, hi);
+    return lo + hi;
 }
 
-__device__ __forceinline__ void fp32_values(const float* p, float* v) {
+__device__ __forceinline__ Eight bf16_values(const uint4& w) {
+    return Eight{{pair(bf16lo(w.x), bf16hi(w.x)), pair(bf16lo(w.y), bf16hi(w.y)), pair(bf16lo(w.z), bf16hi(w.z)),
+                  pair(bf16lo(w.w), bf16hi(w.w))}};
+}
+__device__ __forceinline__ Eight fp32_values(const float* p) {
     const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    return Eight{{pair(a.x, a.y), pair(a.z, a.w), pair(b.x, b.y), pair(b.z, b.w)}};
 }
-
-__device__ __forceinline__ uint4 pack8(const float* v) {
-    return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+__device__ __forceinline__ Eight fp32_values(const uint4& a, const uint4& b) {
+    return Eight{{(uint64_t)a.y << 32 | a.x, (uint64_t)a.w << 32 | a.z, (uint64_t)b.y << 32 | b.x,
+                  (uint64_t)b.w << 32 | b.z}};
 }
-
-template <bool kFp32>
-__device__ __forceinline__ void store8(void* base, int64_t at, const float* v, const Extent& e) {
-    uint8_t* p = static_cast<uint8_t*>(base) + at * (kFp32 ? 4 : 2);
-    if constexpr (kFp32) {
-        store_out(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]), e);
-        store_out(reinterpret_cast<float4*>(p) + 1, make_float4(v[4], v[5], v[6], v[7]), e);
-    } else {
-        store_out(reinterpret_cast<uint4*>(p), pack8(v), e);
+__device__ __forceinline__ uint32_t pack_pair(uint64_t p) {
+    float lo, hi;
+    unpair(p, lo, hi);
+    return pack_bf16(lo, hi);
+}
+__device__ __forceinline__ uint4 pack8(const Eight& v) {
+    return make_uint4(pack_pair(v.p[0]), pack_pair(v.p[1]), pack_pair(v.p[2]), pack_pair(v.p[3]));
+}
+__device__ __forceinline__ void store_fp32(float* p, const Eight& v, const Extent& e) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float4 f;
+        unpair(v.p[2 * i], f.x, f.y);
+        unpair(v.p[2 * i + 1], f.z, f.w);
+        store_out(reinterpret_cast<float4*>(p) + i, f, e);
     }
+}
+template <bool kFp32>
+__device__ __forceinline__ void store8(void* row, uint32_t c, const Eight& v, const Extent& e) {
+    if constexpr (kFp32)
+        store_fp32(static_cast<float*>(row) + c, v, e);
+    else
+        store_out(reinterpret_cast<uint4*>(static_cast<uint16_t*>(row) + c), pack8(v), e);
+}
+
+// Row r of a matrix with ld bytes between rows.  (The row is the block's, so
+// that the product is the uniform datapath's; pointers kept and advanced row
+// by row took 5 to 14 % more instructions.)
+__device__ __forceinline__ uint8_t* row_of(const void* base, uint32_t r, int64_t ld) {
+    return static_cast<uint8_t*>(const_cast<void*>(base)) + (uint64_t)r * (uint64_t)ld;
 }
 
 // A thread's pieces of the rows ahead: slots of 16 bytes, slot by slot over
@@ -119,21 +177,15 @@ __device__ __forceinline__ void oldest_landed(uint32_t ahead) {
 
 template <bool kFp32, int kV>
 __device__ __forceinline__ void copy_residual(const Ring<kV>& ring, uint32_t stage, uint32_t slot, int i,
-                                              const void* base, int64_t at) {
-    const uint8_t* from = static_cast<const uint8_t*>(base) + at * (kFp32 ? 4 : 2);
+                                              const uint8_t* row, uint32_t c) {
+    const uint8_t* from = row + c * (kFp32 ? 4u : 2u);
     copy16(ring.at(stage, slot, i), from);
     if constexpr (kFp32) copy16(ring.at(stage, slot + 1, i), from + 16);
 }
 template <bool kFp32, int kV>
-__device__ __forceinline__ void read_residual(const Ring<kV>& ring, uint32_t stage, uint32_t slot, int i, float* v) {
-    const uint4 w = ring.read(stage, slot, i);
-    if constexpr (kFp32) {
-        const uint4 u = ring.read(stage, slot + 1, i);
-        v[0] = __uint_as_float(w.x), v[1] = __uint_as_float(w.y), v[2] = __uint_as_float(w.z), v[3] = __uint_as_float(w.w);
-        v[4] = __uint_as_float(u.x), v[5] = __uint_as_float(u.y), v[6] = __uint_as_float(u.z), v[7] = __uint_as_float(u.w);
-    } else {
-        bf16_values(w, v);
-    }
+__device__ __forceinline__ Eight read_residual(const Ring<kV>& ring, uint32_t stage, uint32_t slot, int i) {
+    if constexpr (kFp32) return fp32_values(ring.read(stage, slot, i), ring.read(stage, slot + 1, i));
+    else return bf16_values(ring.read(stage, slot, i));
 }
 
 // Slots of a row: forward residual, branch, gate; backward r', dr', dn, branch,
@@ -151,141 +203,129 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // A sum over the row's warps: `slot` is this use's own place in shared memory
 // (uses alternate, so that one barrier per use is enough).
-__device__ __forceinline__ float row_sum(float v, float* slot, uint32_t warp, uint32_t first, uint32_t row_warps) {
+__device__ __forceinline__ float row_sum(float v, float* slot, uint32_t warps) {
     v = warp_sum(v);
-    if (row_warps == 1) return v;
-    if ((threadIdx.x & 31u) == 0) slot[warp] = v;
+    if (warps == 1) return v;
+    const uint32_t lane = threadIdx.x & 31u;
+    if (lane == 0) slot[threadIdx.x >> 5] = v;
     __syncthreads();
-    const uint32_t l = threadIdx.x & 31u;
-    return warp_sum(l < row_warps ? slot[first + l] : 0.0f);
+    return warp_sum(lane < warps ? slot[lane] : 0.0f);
 }
 
 // What a branch value is multiplied with besides 1 / rms and a token's gate.
-__device__ __forceinline__ void branch_factors(const BlockNorm& a, uint32_t c, float* v) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = 1.0f;
-    if (a.post) fp32_values(a.post + c, v);
-    if (a.gate_kind == kGateChannel) {
-        float g[8];
-        fp32_values(static_cast<const float*>(a.gate) + c, g);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] *= g[k];
-    }
+__device__ __forceinline__ Eight branch_factors(const BlockNorm& a, uint32_t c) {
+    const uint64_t one = both(1.0f);
+    Eight v{{one, one, one, one}};
+    if (a.post) v = fp32_values(a.post + c);
+    if (a.gate_kind == kGateChannel) v = mul8(v, fp32_values(static_cast<const float*>(a.gate) + c));
+    return v;
 }
 
-template <bool kFp32, int kV>
-__global__ void __launch_bounds__(most_threads(kV), blocks_at_most_threads(false, kV)) forward_kernel(const __grid_constant__ Params p) {
+template <bool kFp32, int kClass>
+__global__ void __launch_bounds__(most_threads(kClass, false), blocks_of(kClass, false))
+    forward_kernel(const __grid_constant__ Params p) {
     wait_for_prior_grid();
     let_next_grid_start();
     __shared__ float sums[4][32];
     extern __shared__ __align__(16) uint8_t smem[];
     constexpr uint32_t kR = kFp32 ? 2 : 1, kBranch = kR, kGate = kR + 1;
-    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
-    const uint32_t mine = warp / p.row_warps, first = mine * p.row_warps;
-    const uint32_t l = (warp - first) * 32u + lane, lanes = p.row_warps * 32u;
-    const uint32_t H = (uint32_t)p.a.width;
+    constexpr int kV = vectors_of(kClass, false);
+    const uint32_t lane = threadIdx.x & 31u, H = (uint32_t)p.a.width;
     const float inv_h = 1.0f / (float)H;
-    const bool token = p.a.gate_kind == kGateToken;
+    const bool token = p.a.gate_kind == kGateToken, has_post = p.a.post != nullptr, has_branch = p.a.branch != nullptr;
     const Ring<kV> ring(smem, row_slots(kFp32, false, token));
-    const int64_t step = (int64_t)gridDim.x * p.rows;
-    const int64_t row0 = (int64_t)blockIdx.x * p.rows + mine;
-    auto load = [&](int64_t row, uint32_t stage) {
+    auto column = [&](int i) { return (threadIdx.x + i * blockDim.x) * 8u; };
+    auto load = [&](uint32_t row, uint32_t stage) {
         if (row < p.a.tokens) {
 #pragma unroll
             for (int i = 0; i < kV; ++i) {
-                const uint32_t c = (l + i * lanes) * 8u;
+                const uint32_t c = column(i);
                 if (c >= H) continue;
-                copy_residual<kFp32>(ring, stage, 0, i, p.a.residual, row * p.a.ld_residual + c);
-                if (p.a.branch) copy16(ring.at(stage, kBranch, i), p.a.branch + row * p.a.ld_branch + c);
-                if (token)
-                    copy16(ring.at(stage, kGate, i), static_cast<const uint16_t*>(p.a.gate) + row * p.a.ld_gate + c);
+                copy_residual<kFp32>(ring, stage, 0, i, row_of(p.a.residual, row, p.a.ld_residual), c);
+                if (has_branch)
+                    copy16(ring.at(stage, kBranch, i), row_of(p.a.branch, row, p.a.ld_branch) + 2u * c);
+                if (token) copy16(ring.at(stage, kGate, i), row_of(p.a.gate, row, p.a.ld_gate) + 2u * c);
             }
         }
         copies_issued();
     };
-    for (uint32_t s = 0; s < p.ahead; ++s) load(row0 + s * step, s);
-    float factor[kV][8] = {}, pre[kV][8] = {};
+    for (uint32_t s = 0; s < p.ahead; ++s) load(blockIdx.x + s * gridDim.x, s);
+    Eight factor[kV], pre[kV];
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
-        const uint32_t c = (l + i * lanes) * 8u;
-        if (c < H) {
-            branch_factors(p.a, c, factor[i]);
-            if (p.a.pre) fp32_values(p.a.pre + c, pre[i]);
+        factor[i] = pre[i] = zeros();
+        if (column(i) < H) {
+            factor[i] = branch_factors(p.a, column(i));
+            if (p.a.pre) pre[i] = fp32_values(p.a.pre + column(i));
         }
     }
+    const uint64_t scale = both(p.a.scale);
     uint32_t turn = 0, stage = 0;
-    // (the rows of a block begin and end together: its barriers are met by all)
-    for (int64_t row = row0; row - mine < p.a.tokens; row += step) {
-        const bool live = row < p.a.tokens;
+    for (uint32_t row = blockIdx.x; row < p.a.tokens; row += gridDim.x) {
         oldest_landed(p.ahead);
-        float rp = 1.0f, sum = 0.0f;
-        if (p.a.post) {
+        uint64_t rp = both(1.0f);
+        if (has_post) {
+            uint64_t s = 0;
 #pragma unroll
             for (int i = 0; i < kV; ++i) {
-                if (live && (l + i * lanes) * 8u < H) {
-                    float v[8];
-                    bf16_values(ring.read(stage, kBranch, i), v);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) sum = fmaf(v[k], v[k], sum);
+                if (column(i) < H) {
+                    const Eight y = bf16_values(ring.read(stage, kBranch, i));
+                    s = dot8(y, y, s);
                 }
             }
-            sum = row_sum(sum, sums[2 * (turn & 1u)], warp, first, p.row_warps);
-            rp = rsqrtf(fmaf(sum, inv_h, p.a.eps));
+            const float sum = row_sum(halves(s), sums[2 * (turn & 1u)], p.warps);
+            rp = both(rsqrtf(fmaf(sum, inv_h, p.a.eps)));
         }
-        float out[kV][8];
-        sum = 0.0f;
+        if (p.a.kept.data) {
+            uint8_t* codes = row_of(p.a.kept.data, row, p.a.kept.ld);
+            uint8_t* scales = row_of(p.a.kept.scales, row, p.a.kept.ld_scales);
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const uint32_t c = (l + i * lanes) * 8u;
-            const bool here = live && c < H;
-            float(&v)[8] = out[i];
-            uint4 y = make_uint4(0, 0, 0, 0);
-            if (here && p.a.branch) y = ring.read(stage, kBranch, i);
-            if (p.a.kept.data) {
+            for (int i = 0; i < kV; ++i) {
                 // (a block of 32 columns is four lanes of one vector)
+                const uint32_t c = column(i);
+                const uint4 y = c < H ? ring.read(stage, kBranch, i) : make_uint4(0, 0, 0, 0);
                 bool special;
                 const uint32_t b = bf16_scale(y, special);
-                if (here) {
-                    store_out(reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.a.kept.data) + row * p.a.kept.ld + c),
-                              bf16_codes(y, b, special), p.x_codes);
-                    if ((lane & 3u) == 0)
-                        store_out(p.a.kept.scales + row * p.a.kept.ld_scales + c / 32u, (uint8_t)b, p.x_scales);
+                if (c < H) {
+                    store_out(reinterpret_cast<uint2*>(codes + c), bf16_codes(y, b, special), p.x_codes);
+                    if ((lane & 3u) == 0) store_out(scales + c / 32u, (uint8_t)b, p.x_scales);
                 }
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = 0.0f;
-            if (here) {
-                float h[8];
-                read_residual<kFp32>(ring, stage, 0, i, v);
-                bf16_values(y, h);
-                if (token) {
-                    float g[8];
-                    bf16_values(ring.read(stage, kGate, i), g);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) h[k] *= g[k];
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = fmaf(h[k], rp * factor[i][k], p.a.scale * v[k]);
-                if (p.a.residual_out) store8<kFp32>(p.a.residual_out, row * p.a.ld_residual_out + c, v, p.x_residual);
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                if constexpr (!kFp32) v[k] = __bfloat162float(__float2bfloat16_rn(v[k]));
-                sum = fmaf(v[k], v[k], sum);
             }
         }
-        load(row + p.ahead * step, stage);
+        Eight out[kV];
+        uint8_t* residual_out = row_of(p.a.residual_out, row, p.a.ld_residual_out);
+        uint64_t s = 0;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            const uint32_t c = column(i);
+            out[i] = zeros();
+            if (c >= H) continue;
+            Eight v = mul8(read_residual<kFp32>(ring, stage, 0, i), scale);
+            if (has_branch) {
+                Eight f = mul8(factor[i], rp);
+                if (token) f = mul8(f, bf16_values(ring.read(stage, kGate, i)));
+                v = fma8(bf16_values(ring.read(stage, kBranch, i)), f, v);
+            }
+            if constexpr (kFp32) {
+                if (p.a.residual_out) store8<true>(residual_out, c, v, p.x_residual);
+            } else {
+                const uint4 w = pack8(v);
+                if (p.a.residual_out)
+                    store_out(reinterpret_cast<uint4*>(residual_out + 2u * c), w, p.x_residual);
+                v = bf16_values(w);   // n is the norm of what is stored
+            }
+            out[i] = v;
+            s = dot8(v, v, s);
+        }
+        load(row + p.ahead * gridDim.x, stage);
         if (p.a.pre) {
-            sum = row_sum(sum, sums[2 * (turn & 1u) + 1], warp, first, p.row_warps);
-            const float rq = rsqrtf(fmaf(sum, inv_h, p.a.eps));
+            const float sum = row_sum(halves(s), sums[2 * (turn & 1u) + 1], p.warps);
+            const uint64_t rq = both(rsqrtf(fmaf(sum, inv_h, p.a.eps)));
+            uint8_t* normed = row_of(p.a.normed, row, p.a.ld_normed);
 #pragma unroll
             for (int i = 0; i < kV; ++i) {
-                const uint32_t c = (l + i * lanes) * 8u;
-                if (live && c < H) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) out[i][k] *= rq * pre[i][k];
-                    store_out(reinterpret_cast<uint4*>(p.a.normed + row * p.a.ld_normed + c), pack8(out[i]), p.x_normed);
-                }
+                if (column(i) < H)
+                    store8<false>(normed, column(i), mul8(out[i], mul8(pre[i], rq)), p.x_normed);
             }
         }
         ++turn;
@@ -294,7 +334,7 @@ __global__ void __launch_bounds__(most_threads(kV), blocks_at_most_threads(false
 }
 
 // The row's sums of the backward pass (and two that make them eight).
-enum { kSumY2, kSumX2, kSumGx, kSumRy, kSumGy, kSumXy, kSums = 8 };
+enum { kSumY2, kSumX2, kSumGx, kSumRy, kSumGy, kSumXy, kUsedSums, kSums = 8 };
 
 // Sums of eight values over a warp with nine exchanges: at each of the first
 // three a lane hands half of its values on and keeps the other half's sums, so
@@ -314,200 +354,163 @@ __device__ __forceinline__ float warp_sums(float (&s)[kSums], uint32_t lane) {
     return t + __shfl_xor_sync(kAll, t, 16);
 }
 
-template <bool kFp32, int kV>
-__global__ void __launch_bounds__(most_threads(kV), blocks_at_most_threads(true, kV)) backward_kernel(const __grid_constant__ Params p) {
+template <bool kFp32, int kClass>
+__global__ void __launch_bounds__(most_threads(kClass, true), blocks_of(kClass, true))
+    backward_kernel(const __grid_constant__ Params p) {
     wait_for_prior_grid();
     let_next_grid_start();
     __shared__ float sums[2][16][kSums];
     extern __shared__ __align__(16) uint8_t smem[];
     constexpr uint32_t kR = kFp32 ? 2 : 1, kDr = kR, kDn = 2 * kR, kBranch = kDn + 1, kGate = kDn + 2;
-    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
-    const uint32_t mine = warp / p.row_warps, first = mine * p.row_warps;
-    const uint32_t l = (warp - first) * 32u + lane, lanes = p.row_warps * 32u;
-    const uint32_t H = (uint32_t)p.a.width;
+    constexpr int kV = vectors_of(kClass, true);
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u, H = (uint32_t)p.a.width;
     const float inv_h = 1.0f / (float)H;
     const bool token = p.a.gate_kind == kGateToken, has_pre = p.a.pre != nullptr, has_post = p.a.post != nullptr;
-    const bool coded = p.a.kept.data != nullptr, has_dr = p.a.dresidual != nullptr;
+    const bool coded = p.a.kept.data != nullptr, has_dr = p.a.dresidual != nullptr, has_branch = p.a.dbranch != nullptr;
     const Ring<kV> ring(smem, row_slots(kFp32, true, token));
-    const int64_t step = (int64_t)gridDim.x * p.rows;
-    const int64_t row0 = (int64_t)blockIdx.x * p.rows + mine;
-    auto load = [&](int64_t row, uint32_t stage) {
+    auto column = [&](int i) { return (threadIdx.x + i * blockDim.x) * 8u; };
+    auto load = [&](uint32_t row, uint32_t stage) {
         if (row < p.a.tokens) {
 #pragma unroll
             for (int i = 0; i < kV; ++i) {
-                const uint32_t c = (l + i * lanes) * 8u;
+                const uint32_t c = column(i);
                 if (c >= H) continue;
                 if (has_pre) {
-                    copy_residual<kFp32>(ring, stage, 0, i, p.a.residual, row * p.a.ld_residual + c);
-                    copy16(ring.at(stage, kDn, i), p.a.dnormed + row * p.a.ld_dnormed + c);
+                    copy_residual<kFp32>(ring, stage, 0, i, row_of(p.a.residual, row, p.a.ld_residual), c);
+                    copy16(ring.at(stage, kDn, i), row_of(p.a.dnormed, row, p.a.ld_dnormed) + 2u * c);
                 }
-                if (has_dr) copy_residual<kFp32>(ring, stage, kDr, i, p.a.dresidual, row * p.a.ld_dresidual + c);
+                if (has_dr)
+                    copy_residual<kFp32>(ring, stage, kDr, i, row_of(p.a.dresidual, row, p.a.ld_dresidual), c);
                 if (coded) {
                     uint8_t* to = ring.at(stage, kBranch, i);
-                    copy8(to, static_cast<const uint8_t*>(p.a.kept.data) + row * p.a.kept.ld + c);
+                    copy8(to, row_of(p.a.kept.data, row, p.a.kept.ld) + c);
                     // the aligned word around the block's scale, of it what lies in the row
                     const uint32_t word = (c / 32u) & ~3u, rest = (H + 31u) / 32u - word;
-                    copy4(to + 8, p.a.kept.scales + row * p.a.kept.ld_scales + word, rest < 4u ? rest : 4u);
-                } else if (p.a.branch) {
-                    copy16(ring.at(stage, kBranch, i), p.a.branch + row * p.a.ld_branch + c);
+                    copy4(to + 8, row_of(p.a.kept.scales, row, p.a.kept.ld_scales) + word, rest < 4u ? rest : 4u);
+                } else if (has_branch) {
+                    copy16(ring.at(stage, kBranch, i), row_of(p.a.branch, row, p.a.ld_branch) + 2u * c);
                 }
-                if (token)
-                    copy16(ring.at(stage, kGate, i), static_cast<const uint16_t*>(p.a.gate) + row * p.a.ld_gate + c);
+                if (token) copy16(ring.at(stage, kGate, i), row_of(p.a.gate, row, p.a.ld_gate) + 2u * c);
             }
         }
         copies_issued();
     };
-    for (uint32_t s = 0; s < p.ahead; ++s) load(row0 + s * step, s);
-    float factor[kV][8] = {}, pre[kV][8] = {};
+    for (uint32_t s = 0; s < p.ahead; ++s) load(blockIdx.x + s * gridDim.x, s);
+    Eight factor[kV], pre[kV], dpre[kV], dpost[kV];
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
-        const uint32_t c = (l + i * lanes) * 8u;
-        if (c < H) {
-            branch_factors(p.a, c, factor[i]);
-            if (has_pre) fp32_values(p.a.pre + c, pre[i]);
+        factor[i] = pre[i] = dpre[i] = dpost[i] = zeros();
+        if (column(i) < H) {
+            factor[i] = branch_factors(p.a, column(i));
+            if (has_pre) pre[i] = fp32_values(p.a.pre + column(i));
         }
     }
-    auto branch_values = [&](uint32_t stage, int i, uint32_t c, float* v) {
+    auto branch_values = [&](uint32_t stage, int i) {
         const uint4 w = ring.read(stage, kBranch, i);
-        if (coded) {
-            const float f = checkpoint_factor((w.z >> (8u * ((c / 32u) & 3u))) & 0xFFu);
-            e4m3_values_x4(w.x, f, v);
-            e4m3_values_x4(w.y, f, v + 4);
-        } else {
-            bf16_values(w, v);
-        }
+        if (!coded) return bf16_values(w);
+        const float f = checkpoint_factor((w.z >> (8u * ((column(i) / 32u) & 3u))) & 0xFFu);
+        float v[8];
+        e4m3_values_x4(w.x, f, v);
+        e4m3_values_x4(w.y, f, v + 4);
+        return Eight{{pair(v[0], v[1]), pair(v[2], v[3]), pair(v[4], v[5]), pair(v[6], v[7])}};
     };
-    float dpre[kV][8] = {}, dpost[kV][8] = {};
+    const uint64_t scale = both(p.a.scale);
     uint32_t turn = 0, stage = 0;
-    for (int64_t row = row0; row - mine < p.a.tokens; row += step) {
-        const bool live = row < p.a.tokens;
+    for (uint32_t row = blockIdx.x; row < p.a.tokens; row += gridDim.x) {
         oldest_landed(p.ahead);
-        float s[kSums] = {};
+        uint64_t part[kUsedSums] = {};
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-            const uint32_t c = (l + i * lanes) * 8u;
-            if (!live || c >= H) continue;
-            float vx[8] = {}, g[8] = {};
+            if (column(i) >= H) continue;
+            Eight x = zeros(), g = zeros();
             if (has_pre) {
-                read_residual<kFp32>(ring, stage, 0, i, vx);
-                bf16_values(ring.read(stage, kDn, i), g);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    g[k] *= pre[i][k];
-                    s[kSumX2] = fmaf(vx[k], vx[k], s[kSumX2]);
-                    s[kSumGx] = fmaf(g[k], vx[k], s[kSumGx]);
-                }
+                x = read_residual<kFp32>(ring, stage, 0, i);
+                g = mul8(bf16_values(ring.read(stage, kDn, i)), pre[i]);
+                part[kSumX2] = dot8(x, x, part[kSumX2]);
+                part[kSumGx] = dot8(g, x, part[kSumGx]);
             }
             if (has_post) {
-                float vr[8] = {}, vy[8], gt[8];
-                if (has_dr) read_residual<kFp32>(ring, stage, kDr, i, vr);
-                branch_values(stage, i, c, vy);
-                if (token) bf16_values(ring.read(stage, kGate, i), gt);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    s[kSumY2] = fmaf(vy[k], vy[k], s[kSumY2]);
-                    float cy = factor[i][k] * vy[k];
-                    if (token) cy *= gt[k];
-                    s[kSumRy] = fmaf(vr[k], cy, s[kSumRy]);
-                    s[kSumGy] = fmaf(g[k], cy, s[kSumGy]);
-                    s[kSumXy] = fmaf(vx[k], cy, s[kSumXy]);
-                }
+                const Eight y = branch_values(stage, i);
+                part[kSumY2] = dot8(y, y, part[kSumY2]);
+                Eight cy = mul8(factor[i], y);
+                if (token) cy = mul8(cy, bf16_values(ring.read(stage, kGate, i)));
+                if (has_dr) part[kSumRy] = dot8(read_residual<kFp32>(ring, stage, kDr, i), cy, part[kSumRy]);
+                part[kSumGy] = dot8(g, cy, part[kSumGy]);
+                part[kSumXy] = dot8(x, cy, part[kSumXy]);
             }
         }
+        float rq = 0.0f, along = 0.0f, rp = 1.0f, mean = 0.0f;
         if (has_pre || has_post) {
+            float s[kSums] = {};
+#pragma unroll
+            for (int j = 0; j < kUsedSums; ++j) s[j] = halves(part[j]);
             float t = warp_sums(s, lane);
-            if (p.row_warps > 1) {
+            if (p.warps > 1) {
                 float(*slot)[kSums] = sums[turn & 1u];
                 if (lane < kSums) slot[warp][lane] = t;
                 __syncthreads();
                 t = 0.0f;
-                for (uint32_t w = lane >> 3; w < p.row_warps; w += 4) t += slot[first + w][lane & 7u];
+#pragma unroll
+                for (uint32_t w = 0; w < 16; w += 4)
+                    if (w + (lane >> 3) < p.warps) t += slot[w + (lane >> 3)][lane & 7u];
                 t += __shfl_xor_sync(kAll, t, 8);
                 t += __shfl_xor_sync(kAll, t, 16);
             }
 #pragma unroll
-            for (int j = 0; j < 6; ++j) s[j] = __shfl_sync(kAll, t, j);
+            for (int j = 0; j < kUsedSums; ++j) s[j] = __shfl_sync(kAll, t, j);
+            if (has_pre) {
+                rq = rsqrtf(fmaf(s[kSumX2], inv_h, p.a.eps));
+                along = rq * rq * (s[kSumGx] * inv_h) * rq;
+            }
+            if (has_post) {
+                rp = rsqrtf(fmaf(s[kSumY2], inv_h, p.a.eps));
+                mean = rp * rp * (fmaf(rq, s[kSumGy], s[kSumRy]) - along * s[kSumXy]) * inv_h;
+            }
         }
         ++turn;
-        float rq = 0.0f, along = 0.0f, rp = 1.0f, mean = 0.0f;
-        if (has_pre) {
-            rq = rsqrtf(fmaf(s[kSumX2], inv_h, p.a.eps));
-            along = rq * rq * (s[kSumGx] * inv_h) * rq;
-        }
-        if (has_post) {
-            rp = rsqrtf(fmaf(s[kSumY2], inv_h, p.a.eps));
-            mean = rp * rp * (fmaf(rq, s[kSumGy], s[kSumRy]) - along * s[kSumXy]) * inv_h;
-        }
+        const uint64_t rq2 = both(rq), less = both(-along), rp2 = both(rp), less_mean = both(-mean);
+        uint8_t* dresidual_out = row_of(p.a.dresidual_out, row, p.a.ld_dresidual_out);
+        uint8_t* dbranch = row_of(p.a.dbranch, row, p.a.ld_dbranch);
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-            const uint32_t c = (l + i * lanes) * 8u;
-            if (!live || c >= H) continue;
-            float d[8] = {};
-            if (has_dr) read_residual<kFp32>(ring, stage, kDr, i, d);
+            const uint32_t c = column(i);
+            if (c >= H) continue;
+            Eight d = has_dr ? read_residual<kFp32>(ring, stage, kDr, i) : zeros();
             if (has_pre) {
-                float vx[8], dn[8];
-                read_residual<kFp32>(ring, stage, 0, i, vx);
-                bf16_values(ring.read(stage, kDn, i), dn);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    dpre[i][k] = fmaf(dn[k], vx[k] * rq, dpre[i][k]);
-                    d[k] = fmaf(-along, vx[k], fmaf(rq, dn[k] * pre[i][k], d[k]));
-                }
+                const Eight x = read_residual<kFp32>(ring, stage, 0, i), dn = bf16_values(ring.read(stage, kDn, i));
+                const Eight dnr = mul8(dn, rq2);
+                dpre[i] = fma8(dnr, x, dpre[i]);
+                d = fma8(x, less, fma8(dnr, pre[i], d));
             }
-            float to[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) to[k] = p.a.scale * d[k];
-            store8<kFp32>(p.a.dresidual_out, row * p.a.ld_dresidual_out + c, to, p.x_residual);
-            if (!p.a.dbranch) continue;
-            float vy[8];
-            branch_values(stage, i, c, vy);
+            store8<kFp32>(dresidual_out, c, mul8(d, scale), p.x_residual);
+            if (!has_branch) continue;
+            const Eight y = branch_values(stage, i), a = mul8(y, rp2);
             if (token) {
                 // the gate's own gradient; then d stands for d gate
-                float gt[8];
-                bf16_values(ring.read(stage, kGate, i), gt);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    to[k] = d[k] * (vy[k] * rp * factor[i][k]);
-                    d[k] *= gt[k];
-                }
-                store_out(reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.a.dgate) + row * p.a.ld_dgate + c),
-                          pack8(to), p.x_gate);
+                store8<false>(row_of(p.a.dgate, row, p.a.ld_dgate), c, mul8(d, mul8(a, factor[i])), p.x_gate);
+                d = mul8(d, bf16_values(ring.read(stage, kGate, i)));
             }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                // (of a gate per channel the columns' sum takes the factor at the end)
-                dpost[i][k] = fmaf(d[k], vy[k] * rp, dpost[i][k]);
-                to[k] = d[k] * factor[i][k];
-                if (has_post) to[k] = rp * fmaf(-vy[k], mean, to[k]);
-            }
-            store_out(reinterpret_cast<uint4*>(p.a.dbranch + row * p.a.ld_dbranch + c), pack8(to), p.x_branch);
+            // (of a gate per channel the columns' sum takes the factor at the end)
+            dpost[i] = fma8(d, a, dpost[i]);
+            Eight t = mul8(d, factor[i]);
+            if (has_post) t = mul8(fma8(y, less_mean, t), rp2);
+            store8<false>(dbranch, c, t, p.x_branch);
         }
-        load(row + p.ahead * step, stage);
+        load(row + p.ahead * gridDim.x, stage);
         if (++stage == p.ahead) stage = 0;
     }
-
-    if (!p.a.partials) return;
-    // the block's sums of each column: its rows in order, over the ring
-    float* columns = reinterpret_cast<float*>(smem);   // [2][width]
     asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncthreads();
-    for (uint32_t m = 0; m < p.rows; ++m) {
-        if (m == mine) {
+    if (!p.a.partials) return;
+    // the block's sums of each column
+    float* share = p.a.partials + (uint64_t)blockIdx.x * 2u * H;
+    const Extent all{0, ~(uintptr_t)0};
 #pragma unroll
-            for (int i = 0; i < kV; ++i) {
-                const uint32_t c = (l + i * lanes) * 8u;
-                if (c >= H) continue;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    columns[c + k] = m ? columns[c + k] + dpre[i][k] : dpre[i][k];
-                    columns[H + c + k] = m ? columns[H + c + k] + dpost[i][k] : dpost[i][k];
-                }
-            }
-        }
-        __syncthreads();
+    for (int i = 0; i < kV; ++i) {
+        const uint32_t c = column(i);
+        if (c >= H) continue;
+        store_fp32(share + c, dpre[i], all);
+        store_fp32(share + H + c, dpost[i], all);
     }
-    for (uint32_t c = threadIdx.x; c < 2u * H; c += blockDim.x)
-        p.a.partials[(uint64_t)blockIdx.x * 2u * H + c] = columns[c];
 }
 
 // The weights' gradients: the blocks' shares summed in a fixed order, 32
@@ -522,8 +525,10 @@ __global__ void __launch_bounds__(1024) weight_kernel(const float* partials, uin
     const uint32_t i = blockIdx.x * 32 + threadIdx.x, half = blockIdx.y;
     if (half == 0 ? dpre == nullptr : dpost == nullptr && dgate == nullptr) return;
     float t = 0.0f;
-    if (i < H)
+    if (i < H) {
+#pragma unroll 8
         for (uint32_t b = threadIdx.y; b < blocks; b += 32) t += partials[((uint64_t)b * 2 + half) * H + i];
+    }
     sums[threadIdx.y][threadIdx.x] = t;
     __syncthreads();
     if (threadIdx.y == 0 && i < H) {
@@ -539,21 +544,6 @@ __global__ void __launch_bounds__(1024) weight_kernel(const float* partials, uin
     }
 }
 
-// Warps of a row and rows of a block: one vector of 8 columns per lane up to
-// 12 warps, then two; rows of fewer than 8 warps share a block.
-struct Shape {
-    int vectors;
-    uint32_t row_warps, rows;
-};
-Shape shape_for(int width) {
-    Shape s;
-    const int pieces = (width + 7) / 8;
-    s.vectors = pieces > most_threads(1) ? 2 : 1;
-    s.row_warps = (uint32_t)((pieces + 32 * s.vectors - 1) / (32 * s.vectors));
-    s.rows = s.row_warps >= 8 ? 1u : 8u / s.row_warps;
-    return s;
-}
-
 // Shared memory of an SM that blocks may share, and what one keeps besides its ring.
 constexpr size_t kSmemOfSm = 227 * 1024, kSmemBesides = 4 * 1024;
 
@@ -564,11 +554,13 @@ struct Residence {
     int blocks;
     size_t smem;
 };
-Residence residence_for(const Params& p, bool fp32, int vectors, bool backward) {
-    const int threads = 32 * (int)(p.row_warps * p.rows);
+Residence residence_for(const Params& p, bool fp32, int width_class, bool backward) {
+    const int threads = 32 * (int)p.warps;
     Residence r;
-    r.blocks = most_threads(vectors) * blocks_at_most_threads(backward, vectors) / threads;
-    const size_t row = (size_t)row_slots(fp32, backward, p.a.gate_kind == kGateToken) * vectors * threads * 16;
+    r.blocks = most_threads(width_class, backward) * blocks_of(width_class, backward) / threads;
+    if (r.blocks > 24) r.blocks = 24;
+    const size_t row = (size_t)row_slots(fp32, backward, p.a.gate_kind == kGateToken) * vectors_of(width_class, backward) *
+                       threads * 16;
     while (r.blocks > 1 && r.blocks * (2 * row + kSmemBesides) > kSmemOfSm) --r.blocks;
     const size_t rows = (kSmemOfSm / r.blocks - kSmemBesides) / row;
     r.ahead = (uint32_t)(rows < 1 ? 1 : rows > kMostAhead ? kMostAhead : rows);
@@ -576,35 +568,22 @@ Residence residence_for(const Params& p, bool fp32, int vectors, bool backward) 
     return r;
 }
 
-template <typename Kernel>
-cudaError_t launch_rows(Kernel* kernel, Params& p, bool fp32, int vectors, bool backward, int64_t most_blocks,
-                        uint32_t* blocks, cudaStream_t stream) {
-    const Residence r = residence_for(p, fp32, vectors, backward);
+template <bool kFp32, int kClass, bool kBackward>
+cudaError_t launch_rows(Params& p, cudaStream_t stream) {
+    auto* kernel = kBackward ? backward_kernel<kFp32, kClass> : forward_kernel<kFp32, kClass>;
+    const uint32_t H = (uint32_t)p.a.width, columns = 256u * vectors_of(kClass, kBackward);
+    p.warps = (H + columns - 1) / columns;
+    const Residence r = residence_for(p, kFp32, kClass, kBackward);
     p.ahead = r.ahead;
-    if (r.smem + kSmemBesides > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)(kSmemOfSm - kSmemBesides));
-        if (e != cudaSuccess) return e;
-    }
+    cudaError_t e = cudaSuccess;
+    if (r.smem + kSmemBesides > 48 * 1024)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kSmemOfSm - kSmemBesides));
+    if (e != cudaSuccess) return e;
     int64_t most = (int64_t)device_sm_count() * r.blocks;
-    if (most > most_blocks) most = most_blocks;
-    const int64_t need = (p.a.tokens + p.rows - 1) / p.rows;
-    *blocks = (uint32_t)(need < most ? need : most);
-    return launch_early(kernel, dim3(*blocks), dim3(32 * p.row_warps * p.rows), r.smem, stream, p);
-}
-
-template <bool kFp32, int kV>
-cudaError_t launch_forward(Params& p, cudaStream_t stream) {
-    uint32_t blocks;
-    return launch_rows(forward_kernel<kFp32, kV>, p, kFp32, kV, false, 1 << 30, &blocks, stream);
-}
-
-template <bool kFp32, int kV>
-cudaError_t launch_backward(Params& p, cudaStream_t stream) {
-    uint32_t blocks;
-    cudaError_t e = launch_rows(backward_kernel<kFp32, kV>, p, kFp32, kV, true, kBlockNormMaxBlocks, &blocks, stream);
-    if (e == cudaSuccess && p.a.partials) {
-        const uint32_t H = (uint32_t)p.a.width;
+    if (kBackward && most > block_norm_max_blocks(p.a.width)) most = block_norm_max_blocks(p.a.width);
+    const uint32_t blocks = (uint32_t)(p.a.tokens < most ? p.a.tokens : most);
+    e = launch_early(kernel, dim3(blocks), dim3(32 * p.warps), r.smem, stream, p);
+    if (kBackward && e == cudaSuccess && p.a.partials) {
         const bool channel = p.a.gate_kind == kGateChannel;
         e = launch_early(weight_kernel, dim3((H + 31) / 32, 2), dim3(32, 32), 0, stream,
                          static_cast<const float*>(p.a.partials), blocks, H, p.a.post,
@@ -612,6 +591,15 @@ cudaError_t launch_backward(Params& p, cudaStream_t stream) {
                          channel ? static_cast<float*>(p.a.dgate) : nullptr);
     }
     return e;
+}
+
+template <bool kBackward>
+cudaError_t launch_width(Params& p, cudaStream_t stream) {
+    if (p.a.width <= 256)
+        return p.a.fp32 ? launch_rows<true, kNarrow, kBackward>(p, stream) : launch_rows<false, kNarrow, kBackward>(p, stream);
+    if (p.a.width <= 8 * vectors_of(kMedium, kBackward) * most_threads(kMedium, kBackward))
+        return p.a.fp32 ? launch_rows<true, kMedium, kBackward>(p, stream) : launch_rows<false, kMedium, kBackward>(p, stream);
+    return p.a.fp32 ? launch_rows<true, kWide, kBackward>(p, stream) : launch_rows<false, kWide, kBackward>(p, stream);
 }
 
 Extent extent_of_kind(const void* p, int64_t tokens, int64_t ld, int64_t width, int64_t esz) {
@@ -623,24 +611,22 @@ Extent extent_of_kind(const void* p, int64_t tokens, int64_t ld, int64_t width, 
 cudaError_t launch_block_norm(const BlockNorm& a, bool backward, cudaStream_t stream) {
     Params p{};
     p.a = a;
-    const Shape s = shape_for(a.width);
-    p.row_warps = s.row_warps;
-    p.rows = s.rows;
     const int64_t T = a.tokens, H = a.width, esz = a.fp32 ? 4 : 2;
     if (!backward) {
         p.x_residual = extent_of_kind(a.residual_out, T, a.ld_residual_out, H, esz);
         p.x_normed = extent_of_kind(a.normed, T, a.ld_normed, H, 2);
         p.x_codes = extent_of_kind(a.kept.data, T, a.kept.ld, H, 1);
         p.x_scales = extent_of_kind(a.kept.scales, T, a.kept.ld_scales, (H + 31) / 32, 1);
-        if (a.fp32)
-            return s.vectors == 1 ? launch_forward<true, 1>(p, stream) : launch_forward<true, 2>(p, stream);
-        return s.vectors == 1 ? launch_forward<false, 1>(p, stream) : launch_forward<false, 2>(p, stream);
+    } else {
+        p.x_residual = extent_of_kind(a.dresidual_out, T, a.ld_dresidual_out, H, esz);
+        p.x_branch = extent_of_kind(a.dbranch, T, a.ld_dbranch, H, 2);
+        if (a.gate_kind == kGateToken) p.x_gate = extent_of_kind(a.dgate, T, a.ld_dgate, H, 2);
     }
-    p.x_residual = extent_of_kind(a.dresidual_out, T, a.ld_dresidual_out, H, esz);
-    p.x_branch = extent_of_kind(a.dbranch, T, a.ld_dbranch, H, 2);
-    if (a.gate_kind == kGateToken) p.x_gate = extent_of_kind(a.dgate, T, a.ld_dgate, H, 2);
-    if (a.fp32) return s.vectors == 1 ? launch_backward<true, 1>(p, stream) : launch_backward<true, 2>(p, stream);
-    return s.vectors == 1 ? launch_backward<false, 1>(p, stream) : launch_backward<false, 2>(p, stream);
+    // the kernels take leading dimensions in bytes
+    for (int64_t* ld : {&p.a.ld_residual, &p.a.ld_residual_out, &p.a.ld_dresidual, &p.a.ld_dresidual_out}) *ld *= esz;
+    for (int64_t* ld : {&p.a.ld_branch, &p.a.ld_gate, &p.a.ld_normed, &p.a.ld_dnormed, &p.a.ld_dbranch, &p.a.ld_dgate})
+        *ld *= 2;
+    return backward ? launch_width<true>(p, stream) : launch_width<false>(p, stream);
 }
 
 cudaError_t block_norm_bounds_read_and_clear(uint64_t* n) { return bounds_read_and_clear_local(n); }

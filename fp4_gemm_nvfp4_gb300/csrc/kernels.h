@@ -178,7 +178,11 @@ cudaError_t launch_gemm_gated_backward(const GemmOperand& a, const GemmOperand& 
 // elements; optional parts are null.
 enum GateKind { kGateNone = 0, kGateChannel = 1, kGateToken = 2 };
 constexpr int kBlockNormMaxWidth = 8192;
-constexpr int kBlockNormMaxBlocks = 1024;  // partial sums of the weights' gradients: 2 * width floats each
+// Blocks of the backward pass, each with 2 * width floats of the weights' gradients.
+inline int block_norm_max_blocks(int width) {
+    const int n = 160 * 48 / ((width + 255) / 256);
+    return n < 4096 ? n : 4096;
+}
 struct BlockNorm {
     int64_t tokens;
     int width;
