@@ -98,14 +98,15 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;
 enum EpiMode { kEpiPlain = 0, kEpiAmax = 1, kEpiC = 2, kEpiGated = 3, kEpiGatedBack = 4 };
 
 // The gated backward pass reads two matrices through its slices and writes two
-// back: two slices per epilogue warp, paid for with a stage of operands.
-__host__ __device__ constexpr int stages_of(int mode) { return mode == kEpiGatedBack ? 4 : 5; }
-__host__ __device__ constexpr uint32_t slices_of(int mode) { return mode == kEpiGatedBack ? 2 : 1; }
+// back: three slices per epilogue warp, paid for with two stages of operands.
+constexpr uint32_t kBackSlices = 3;
+__host__ __device__ constexpr int stages_of(int mode) { return mode == kEpiGatedBack ? 3 : 5; }
+__host__ __device__ constexpr uint32_t slices_of(int mode) { return mode == kEpiGatedBack ? kBackSlices : 1; }
 __host__ __device__ constexpr uint32_t staging_of(int mode) {
     return kNumEpiWarpsStaging * slices_of(mode) * kSliceBytes;
 }
 __host__ __device__ constexpr size_t smem_of(int mode) {
-    return (size_t)stages_of(mode) * kStageBytes + staging_of(mode) + 1024 /*align*/ + 256 /*barriers*/;
+    return (size_t)stages_of(mode) * kStageBytes + staging_of(mode) + 1024 /*align*/ + 512 /*barriers*/;
 }
 
 static_assert(kStageBytes % 1024 == 0, "stages must keep 1024-byte alignment for the 128B swizzle");
@@ -418,7 +419,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile uint32_t* abort_flag = tmem_slot + 1;
     volatile uint32_t* sf_ok = tmem_slot + 4;    // [2]: scales-landed verdicts, by stage-count parity
-    uint64_t* loaded = reinterpret_cast<uint64_t*>(tmem_slot + 6);   // gated backward: an epilogue warp's gate and up
+    uint64_t* loaded = reinterpret_cast<uint64_t*>(tmem_slot + 6);   // gated backward: the epilogue warps' slices
 
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
     const uint32_t rank = cluster_ctarank();
@@ -433,7 +434,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         mbar_init(acc_empty, 2 * kNumEpiWarps);
         mbar_init(drain, 1);
         if constexpr (kGatedBack) {
-            for (int w = 0; w < kNumEpiWarps; ++w) mbar_init(&loaded[w], 1);
+            for (uint32_t w = 0; w < kNumEpiWarps * kBackSlices; ++w) mbar_init(&loaded[w], 1);
         }
         *abort_flag = 0u;
         fence_barrier_init();
@@ -741,7 +742,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t half = (warp - kFirstEpiWarp) >> 2;     // 128-column half of the tile
         const float alpha = __fmul_rn(__fmul_rn(*p.sga, *p.sgb), p.alpha);
         uint8_t* const own_slice = staging + (half * 4 + q) * (slices_of(kMode) * kSliceBytes);
-        GatedWarp gated{&loaded[half * 4 + q]};   // (of the gated modes)
+        GatedWarp gated{&loaded[(half * 4 + q) * kBackSlices], own_slice, q, half};   // (of the gated backward mode)
+        if constexpr (kGatedBack) {
+            gated.in_tile = first_tile;
+            gated_load<0>(p, extra, gated, lane, rank, num_tiles, tile_stride);
+            gated_load<0>(p, extra, gated, lane, rank, num_tiles, tile_stride);
+            gated_scales(p, gated, lane, rank, first_tile, num_tiles);
+        }
         constexpr bool kAmax = kMode == kEpiAmax;
         constexpr bool has_c = kMode == kEpiC;
         const uint32_t leader_acc_empty = map_to_cta(smem_u32(acc_empty), 0);
@@ -758,9 +765,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tile_coords(tile, p, mt, nt);
             if constexpr (has_c)
                 prefetch_c_row(p, mt * kPairM + rank * kCtaM + row_local, nt * kBN + half * 128);
-            if constexpr (kGatedBack)
-                gated_backward_load(p, extra, gated, own_slice, lane, mt * kPairM + rank * kCtaM + q * 32,
-                                    nt * kBN + half * 128);
+            if constexpr (kGatedBack) {
+                gated.scales[0] = gated.next_scales[0];
+                gated.scales[1] = gated.next_scales[1];
+                gated_scales(p, gated, lane, rank, tile + tile_stride, num_tiles);
+            }
             // One thread per warp waits for the accumulator, suspended in the
             // barrier's try_wait (no issue slots taken from the MMA issuer);
             // each warp wakes on the barrier itself, not behind a named
@@ -800,8 +809,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(leader_acc_empty);
-                if (!gated_backward_epilogue(p, extra, gated, &tma_d, &tma_u, own_slice, lane, row0 + q * 32, nbase, v,
-                                             alpha, abort_flag, amax_plain, amax_rht))
+                if (!gated_backward_epilogue(p, extra, gated, &tma_d, &tma_u, lane, rank, num_tiles, tile_stride,
+                                             row0 + q * 32, nbase, v, alpha, abort_flag, amax_plain, amax_rht))
                     break;
             } else if (has_c && p.c_staged) {
                 // C through this warp's 4 KiB slice: each round the lanes copy
@@ -1005,7 +1014,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             ++tiles_done;
         }
-        if constexpr (kGatedBack) gated_backward_drain(p, gated, lane);
+        if constexpr (kGatedBack) gated_drain(p, gated, lane);
         if (p.tma_store && lane == 0) bulk_wait_all();
         if (kAmax || ((kGated || kGatedBack) && p.amax_out)) {
             amax_plain = warp_max(amax_plain);
@@ -1247,24 +1256,30 @@ int gemm_grid(const Params& p) {
     return 2 * (int)(tiles < pairs ? tiles : pairs);
 }
 
-// 2-D map over a matrix kept for the backward pass: 64 columns by 32 rows per
-// box, BF16 (128-byte swizzle) or 8-bit codes (64-byte swizzle).
-bool make_checkpoint_map(CUtensorMap* map, const CheckpointView& t, int64_t rows, int64_t cols) {
-    if (!t.scales) return make_output_map(map, t.data, rows, cols, t.ld, false);
+// 2-D map over a row-major matrix of BF16 or 8-bit codes, `box_cols` columns by
+// 32 rows per box, swizzled over the box's row of 32, 64 or 128 bytes.
+bool make_piece_map(CUtensorMap* map, void* base, int64_t rows, int64_t cols, int64_t ld_bytes, bool codes,
+                    uint32_t box_cols) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
+    const uint32_t row = box_cols * (codes ? 1u : 2u);
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)t.ld};
-    const cuuint32_t box[2] = {64, 32};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld_bytes};
+    const cuuint32_t box[2] = {box_cols, 32};
     const cuuint32_t elem[2] = {1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, t.data, dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return fn(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides,
+              box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                         : row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool make_checkpoint_map(CUtensorMap* map, const CheckpointView& t, int64_t rows, int64_t cols, uint32_t box_cols) {
+    return make_piece_map(map, t.data, rows, cols, t.scales ? t.ld : 2 * t.ld, t.scales != nullptr, box_cols);
 }
 
 // Gate and up as kept, of the call's M x N.
 bool set_checkpoints(Params& p, CUtensorMap* gate_map, CUtensorMap* up_map, const CheckpointView& gate,
-                     const CheckpointView& up) {
+                     const CheckpointView& up, uint32_t box_cols) {
     p.kept = gate.scales ? 2 : 1;
     p.scale_blocks = (p.N + 31) / 32;
     p.gate_scales = gate.scales;
@@ -1275,7 +1290,7 @@ bool set_checkpoints(Params& p, CUtensorMap* gate_map, CUtensorMap* up_map, cons
         p.x_gate_scales = extent_rows(gate.scales, p.M, gate.ld_scales, p.scale_blocks);
         p.x_up_scales = extent_rows(up.scales, p.M, up.ld_scales, p.scale_blocks);
     }
-    return make_checkpoint_map(gate_map, gate, p.M, p.N) && make_checkpoint_map(up_map, up, p.M, p.N);
+    return make_checkpoint_map(gate_map, gate, p.M, p.N, box_cols) && make_checkpoint_map(up_map, up, p.M, p.N, box_cols);
 }
 
 }  // namespace
@@ -1293,7 +1308,7 @@ cudaError_t launch_gemm_gated(const GemmOperand& a, const GemmOperand& gate, con
         !make_output_map(&mh, h, a.rows, gate.rows, ldh, false))
         return cudaErrorInvalidValue;
     extra.gate = extra.up = mh;   // (not read unless they are kept)
-    if (gate_kept && !set_checkpoints(p, &extra.gate, &extra.up, *gate_kept, *up_kept)) return cudaErrorInvalidValue;
+    if (gate_kept && !set_checkpoints(p, &extra.gate, &extra.up, *gate_kept, *up_kept, 64)) return cudaErrorInvalidValue;
     p.gelu = gelu ? 1 : 0;
     p.sgu = up.sg;
     p.tma_store = 1;
@@ -1313,9 +1328,9 @@ cudaError_t launch_gemm_gated_backward(const GemmOperand& a, const GemmOperand& 
     ExtraMaps<kEpiGatedBack> extra;
     Params p = gemm_params(a, b, kBN);
     if (!make_codes_map(&ma, a, kCtaM) || !make_codes_map(&mb, b, kCtaN) || !make_scale_map(&msa, a, 1) ||
-        !make_scale_map(&msb, b, 2) || !make_output_map(&mg, dgate, a.rows, b.rows, ld_dgate, false) ||
-        !make_output_map(&mu, dup, a.rows, b.rows, ld_dup, false) ||
-        !set_checkpoints(p, &extra.gate, &extra.up, gate, up))
+        !make_scale_map(&msb, b, 2) || !make_piece_map(&mg, dgate, a.rows, b.rows, 2 * ld_dgate, false, 32) ||
+        !make_piece_map(&mu, dup, a.rows, b.rows, 2 * ld_dup, false, 32) ||
+        !set_checkpoints(p, &extra.gate, &extra.up, gate, up, 32))
         return cudaErrorInvalidValue;
     p.gelu = gelu ? 1 : 0;
     p.tma_store = 1;

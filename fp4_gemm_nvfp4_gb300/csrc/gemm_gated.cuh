@@ -14,9 +14,13 @@
 // Everything is binary32 up to the one rounding of each output; kept values
 // are rounded once from binary32 (BF16, or 8 bits as in checkpoint.cuh).
 //
-// A warp's piece is 32 rows x 64 columns, staged in a 4 KiB slice of shared
-// memory as the TMA unit reads and writes it (128-byte swizzle; 8-bit codes:
-// 64-byte swizzle, gate and up in the slice's halves).
+// Forward, a warp's piece is 32 rows x 64 columns, staged in a 4 KiB slice of
+// shared memory as the TMA unit reads it (128-byte swizzle; 8-bit codes: 64-byte
+// swizzle, gate and up in the slice's halves).  Backward, where gate and up come
+// in the same way, it is 32 columns, gate's and then dgate's in a slice's first
+// half and up's and dup's in the second (64-byte swizzle, codes 32-byte), and a
+// warp has three slices: two pieces are on their way, those of its next tile
+// among them, while it works on the third.
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluSlope = 1.5957691216057308f;   // 2 sqrt(2 / pi)
@@ -42,13 +46,17 @@ __device__ __forceinline__ float gate_slope(float g, float s) {
     return fmaf(s, r, s);
 }
 
-// The place of a lane's 16-byte piece i in a slice of 128-byte rows, and in a
-// half slice of 64-byte rows.
+// The place of a lane's 16-byte piece i in a slice of 128-byte rows, in a half
+// slice of 64-byte rows,
 __device__ __forceinline__ uint4* piece128(uint8_t* slice, uint32_t lane, int i) {
     return reinterpret_cast<uint4*>(slice + lane * 128u + ((uint32_t)i ^ (lane & 7u)) * 16u);
 }
 __device__ __forceinline__ uint4* piece64(uint8_t* slice, uint32_t lane, int i) {
     return reinterpret_cast<uint4*>(slice + lane * 64u + ((uint32_t)i ^ ((lane >> 1) & 3u)) * 16u);
+}
+// ... and among 32-byte rows.
+__device__ __forceinline__ uint4* piece32(uint8_t* slice, uint32_t lane, int i) {
+    return reinterpret_cast<uint4*>(slice + lane * 32u + ((uint32_t)i ^ ((lane >> 2) & 1u)) * 16u);
 }
 
 // The scale bytes of a lane's two blocks, the second only inside the row.
@@ -152,13 +160,7 @@ __device__ __forceinline__ void gated_epilogue(const Params& p, const ExtraMaps<
     }
 }
 
-// An epilogue warp's loads of gate and up in the backward pass.
-struct GatedWarp {
-    uint64_t* loaded;
-    uint32_t parity = 0;
-    bool pending = false;        // a load that has not been waited for
-    uint32_t scales[2];          // this lane's row: four blocks of gate, of up
-};
+constexpr uint32_t kHalfSlice = kSliceBytes / 2;
 
 // The four scale bytes from `block` on of a row, ones past its end.
 __device__ __forceinline__ uint32_t load_scales(const uint8_t* scales, int64_t ld, uint32_t row, uint32_t block,
@@ -170,53 +172,125 @@ __device__ __forceinline__ uint32_t load_scales(const uint8_t* scales, int64_t l
     return w;
 }
 
-// Gate's and up's 64 columns from x on, rows y .. y + 31, into the warp's two
-// slices (rows and columns outside read as zero).
-__device__ __forceinline__ void gated_backward_issue(const Params& p, const ExtraMaps<kEpiGatedBack>& extra,
-                                                     const GatedWarp& w, uint8_t* slices, uint32_t x, uint32_t y) {
-    bulk_wait_read_all();   // the slices' last stores have read them
-    mbar_arrive_expect_tx(w.loaded, p.kept == 2 ? kSliceBytes : 2u * kSliceBytes);
-    tma_load_2d(slices, &extra.gate, w.loaded, (int32_t)x, (int32_t)y);
-    tma_load_2d(slices + kSliceBytes, &extra.up, w.loaded, (int32_t)x, (int32_t)y);
+// An epilogue warp's pieces of gate and up in the backward pass: piece n of the
+// warp's tiles, four of 32 columns each, goes through slice n % kBackSlices.
+struct GatedWarp {
+    uint64_t* loaded;            // one barrier per slice
+    uint8_t* slices;
+    uint32_t q, half;            // the warp's rows and columns of its CTA's tile
+    uint32_t in = 0, in_slice = 0, in_tile = 0, in_piece = 0;   // the next piece to load
+    uint32_t out = 0, out_slice = 0, out_parity = 0;            // the next to work on
+    uint32_t scales[2], next_scales[2];   // this lane's row: four blocks of gate, of up
+};
+
+__device__ __forceinline__ void gated_place(const Params& p, const GatedWarp& w, uint32_t tile, uint32_t rank,
+                                            uint32_t& x, uint32_t& y) {
+    uint32_t mt, nt;
+    tile_coords(tile, p, mt, nt);
+    x = nt * kBN + w.half * 128;
+    y = mt * kPairM + rank * kCtaM + w.q * 32;
+}
+// Pieces of the 128 columns from x on that lie in the matrix.
+__device__ __forceinline__ uint32_t gated_pieces(const Params& p, uint32_t x) {
+    return x >= p.N ? 0u : p.N - x >= 128u ? 4u : (p.N - x + 31u) / 32u;
 }
 
-// Before the wait for the accumulator: the first half of the tile's columns is
-// loaded, the second brought to L2, and the rows' scales read.
-__device__ __forceinline__ void gated_backward_load(const Params& p, const ExtraMaps<kEpiGatedBack>& extra,
-                                                    GatedWarp& w, uint8_t* slices, uint32_t lane, uint32_t y,
-                                                    uint32_t x) {
+// Lets the next piece come into its slice, whose last store but `stores` must
+// have been read (rows outside the matrix come as zeros).
+template <int kStores>
+__device__ __forceinline__ void gated_load(const Params& p, const ExtraMaps<kEpiGatedBack>& extra, GatedWarp& w,
+                                           uint32_t lane, uint32_t rank, uint32_t num_tiles, uint32_t tile_stride) {
+    uint32_t x = 0, y = 0;
+    while (w.in_tile < num_tiles) {
+        gated_place(p, w, w.in_tile, rank, x, y);
+        if (w.in_piece < gated_pieces(p, x)) break;
+        w.in_tile += tile_stride;
+        w.in_piece = 0;
+    }
+    if (w.in_tile >= num_tiles) return;
     if (lane == 0) {
-        gated_backward_issue(p, extra, w, slices, x, y);
-        if (x + 64 < p.N) {
-            prefetch_tile(&extra.gate, (int32_t)(x + 64), (int32_t)y);
-            prefetch_tile(&extra.up, (int32_t)(x + 64), (int32_t)y);
-        }
+        asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kStores) : "memory");
+        uint8_t* slice = w.slices + w.in_slice * kSliceBytes;
+        uint64_t* bar = &w.loaded[w.in_slice];
+        mbar_arrive_expect_tx(bar, p.kept == 2 ? kHalfSlice : kSliceBytes);
+        tma_load_2d(slice, &extra.gate, bar, (int32_t)(x + 32u * w.in_piece), (int32_t)y);
+        tma_load_2d(slice + kHalfSlice, &extra.up, bar, (int32_t)(x + 32u * w.in_piece), (int32_t)y);
     }
-    w.pending = true;
-    w.scales[0] = w.scales[1] = 0x7F7F7F7Fu;
-    if (p.kept == 2 && y + lane < p.M) {
-        w.scales[0] = load_scales(p.gate_scales, p.ld_gate_scales, y + lane, x / 32u, p.scale_blocks);
-        w.scales[1] = load_scales(p.up_scales, p.ld_up_scales, y + lane, x / 32u, p.scale_blocks);
-    }
+    ++w.in;
+    ++w.in_piece;
+    if (++w.in_slice == kBackSlices) w.in_slice = 0;
 }
 
-__device__ __forceinline__ bool gated_backward_wait(const Params& p, GatedWarp& w, uint32_t lane,
-                                                    volatile uint32_t* abort_flag) {
+// The scales of a tile's row, a tile ahead of their use.
+__device__ __forceinline__ void gated_scales(const Params& p, GatedWarp& w, uint32_t lane, uint32_t rank,
+                                             uint32_t tile, uint32_t num_tiles) {
+    w.next_scales[0] = w.next_scales[1] = 0x7F7F7F7Fu;
+    if (p.kept != 2 || tile >= num_tiles) return;
+    uint32_t x, y;
+    gated_place(p, w, tile, rank, x, y);
+    if (y + lane >= p.M || x >= p.N) return;
+    w.next_scales[0] = load_scales(p.gate_scales, p.ld_gate_scales, y + lane, x / 32u, p.scale_blocks);
+    w.next_scales[1] = load_scales(p.up_scales, p.ld_up_scales, y + lane, x / 32u, p.scale_blocks);
+}
+
+// Until the next piece has landed; false if the wait ran out.
+__device__ __forceinline__ bool gated_landed(const Params& p, GatedWarp& w, uint32_t lane,
+                                             volatile uint32_t* abort_flag) {
     uint32_t ready = 0;
     if (lane == 0) {
-        ready = mbar_wait(w.loaded, w.parity, p.timeout_ns) ? 1u : 0u;
+        ready = mbar_wait(&w.loaded[w.out_slice], w.out_parity, p.timeout_ns) ? 1u : 0u;
         if (!ready) record_timeout(abort_flag);
     }
     ready = __shfl_sync(0xFFFFFFFFu, ready, 0);
     __syncwarp();
-    w.parity ^= 1u;
-    w.pending = false;
-    return ready != 0;
+    if (!ready) return false;   // (gated_drain waits once more)
+    ++w.out;
+    if (++w.out_slice == kBackSlices) {
+        w.out_slice = 0;
+        w.out_parity ^= 1u;
+    }
+    return true;
 }
 
-// A load in flight lands before the CTA ends.
-__device__ __forceinline__ void gated_backward_drain(const Params& p, const GatedWarp& w, uint32_t lane) {
-    if (w.pending && lane == 0) (void)mbar_wait(w.loaded, w.parity, p.timeout_ns);
+// Loads in flight land before the CTA ends.
+__device__ __forceinline__ void gated_drain(const Params& p, GatedWarp& w, uint32_t lane) {
+    while (w.out != w.in) {
+        if (lane == 0) (void)mbar_wait(&w.loaded[w.out_slice], w.out_parity, p.timeout_ns);
+        ++w.out;
+        if (++w.out_slice == kBackSlices) {
+            w.out_slice = 0;
+            w.out_parity ^= 1u;
+        }
+    }
+}
+
+// slice_amax of a half slice, 32 rows x 32 columns: a lane takes two columns of
+// one 16-row block.
+__device__ __forceinline__ void half_slice_amax(const uint8_t* slice, uint32_t lane, const Params& p,
+                                                float& amax_plain, float& amax_rht) {
+    const uint32_t chunk = (lane & 15u) >> 2, word = (lane & 3u) * 4u;
+    uint64_t t[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t j = (lane & 16u) + i;
+        uint32_t w = *reinterpret_cast<const uint32_t*>(slice + j * 64u + ((chunk ^ ((j >> 1) & 3u)) << 4) + word);
+        w ^= p.rht_sgn[i];
+        const float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xFFFF0000u);
+        amax_plain = fmax3(amax_plain, fabsf(lo), fabsf(hi));
+        t[i] = f32x2_pack(lo, hi);
+    }
+#pragma unroll
+    for (int st = 0; st < 4; ++st) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (!(i & (1 << st))) f32x2_butterfly(t[i], t[i | (1 << st)]);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float lo, hi;
+        f32x2_unpack(t[i], lo, hi);
+        amax_rht = fmax3(amax_rht, fabsf(lo), fabsf(hi));
+    }
 }
 
 // Eight columns: dg and du over gate and up.
@@ -239,59 +313,56 @@ __device__ __forceinline__ void bf16_x8(const uint4& w, float* v) {
     v[4] = bf16lo(w.z), v[5] = bf16hi(w.z), v[6] = bf16lo(w.w), v[7] = bf16hi(w.w);
 }
 
-// Backward: columns x .. x + 127 of rows y .. y + 31 in two rounds; v: dh.
+// Backward: a tile's 128 columns from x0 on, rows y .. y + 31, piece by piece;
+// v: dh, used up: a turn of the loop takes v[0] and moves the others down, so
+// that its code is there once (unrolled it did not fit the instruction cache).
 // False if a wait ran out.
 __device__ __forceinline__ bool gated_backward_epilogue(const Params& p, const ExtraMaps<kEpiGatedBack>& extra,
                                                         GatedWarp& w, const CUtensorMap* dgate_map,
-                                                        const CUtensorMap* dup_map, uint8_t* slices, uint32_t lane,
-                                                        uint32_t y, uint32_t x0, uint32_t (&v)[4][32], float alpha,
+                                                        const CUtensorMap* dup_map, uint32_t lane, uint32_t rank,
+                                                        uint32_t num_tiles, uint32_t tile_stride, uint32_t y,
+                                                        uint32_t x0, uint32_t (&v)[4][32], float alpha,
                                                         volatile uint32_t* abort_flag, float& amax_plain,
                                                         float& amax_rht) {
-    uint8_t* gate_slice = slices;
-    uint8_t* up_slice = slices + kSliceBytes;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const uint32_t x = x0 + 64u * r;
-        if (r && x >= p.N) break;   // warp-uniform
-        if (r) {
-            if (lane == 0) gated_backward_issue(p, extra, w, slices, x, y);
-            w.pending = true;
-        }
-        if (!gated_backward_wait(p, w, lane, abort_flag)) return false;
+    const uint32_t pieces = gated_pieces(p, x0);
+#pragma unroll 1
+    for (uint32_t r = 0; r < pieces; ++r) {
+        uint8_t* gate_slice = w.slices + w.out_slice * kSliceBytes;
+        uint8_t* up_slice = gate_slice + kHalfSlice;
+        if (!gated_landed(p, w, lane, abort_flag)) return false;
         auto gradients = [&](auto gelu) {
             constexpr bool kGelu = decltype(gelu)::value;
             if (p.kept == 2) {
-                uint4 gc[4], uc[4];
+                uint4 gc[2], uc[2];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    gc[i] = *piece64(gate_slice, lane, i);
-                    uc[i] = *piece64(up_slice, lane, i);
+                for (int i = 0; i < 2; ++i) {
+                    gc[i] = *piece32(gate_slice, lane, i);
+                    uc[i] = *piece32(up_slice, lane, i);
                 }
                 __syncwarp();   // every lane has read its codes: the slices take the gradients
+                const float fg = checkpoint_factor((w.scales[0] >> (8u * r)) & 0xFFu);
+                const float fu = checkpoint_factor((w.scales[1] >> (8u * r)) & 0xFFu);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int j = 2 * r + (i >> 2);   // the block in the lane's four
-                    const float fg = checkpoint_factor((w.scales[0] >> (8 * j)) & 0xFFu);
-                    const float fu = checkpoint_factor((w.scales[1] >> (8 * j)) & 0xFFu);
+                for (int i = 0; i < 4; ++i) {
                     float g[8], u[8];
                     e4m3_values_x4((i & 1) ? gc[i >> 1].z : gc[i >> 1].x, fg, g);
                     e4m3_values_x4((i & 1) ? gc[i >> 1].w : gc[i >> 1].y, fg, g + 4);
                     e4m3_values_x4((i & 1) ? uc[i >> 1].z : uc[i >> 1].x, fu, u);
                     e4m3_values_x4((i & 1) ? uc[i >> 1].w : uc[i >> 1].y, fu, u + 4);
                     uint4 dg, du;
-                    gated_gradients<kGelu>(g, u, &v[2 * r + (i >> 2)][8 * (i & 3)], alpha, dg, du);
-                    *piece128(gate_slice, lane, i) = dg;
-                    *piece128(up_slice, lane, i) = du;
+                    gated_gradients<kGelu>(g, u, &v[0][8 * i], alpha, dg, du);
+                    *piece64(gate_slice, lane, i) = dg;
+                    *piece64(up_slice, lane, i) = du;
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    uint4 *gp = piece128(gate_slice, lane, i), *up = piece128(up_slice, lane, i);
+                for (int i = 0; i < 4; ++i) {
+                    uint4 *gp = piece64(gate_slice, lane, i), *up = piece64(up_slice, lane, i);
                     float g[8], u[8];
                     bf16_x8(*gp, g);
                     bf16_x8(*up, u);
                     uint4 dg, du;
-                    gated_gradients<kGelu>(g, u, &v[2 * r + (i >> 2)][8 * (i & 3)], alpha, dg, du);
+                    gated_gradients<kGelu>(g, u, &v[0][8 * i], alpha, dg, du);
                     *gp = dg;
                     *up = du;
                 }
@@ -302,17 +373,25 @@ __device__ __forceinline__ bool gated_backward_epilogue(const Params& p, const E
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-            if (y < p.M && x < p.N) {
-                tma_store_2d(dgate_map, gate_slice, (int32_t)x, (int32_t)y);
-                tma_store_2d(dup_map, up_slice, (int32_t)x, (int32_t)y);
+            if (y < p.M) {
+                tma_store_2d(dgate_map, gate_slice, (int32_t)(x0 + 32u * r), (int32_t)y);
+                tma_store_2d(dup_map, up_slice, (int32_t)(x0 + 32u * r), (int32_t)y);
             }
             bulk_commit_group();
         }
         if (p.amax_out) {
-            slice_amax(gate_slice, lane, p, amax_plain, amax_rht);
-            slice_amax(up_slice, lane, p, amax_plain, amax_rht);
+            half_slice_amax(gate_slice, lane, p, amax_plain, amax_rht);
+            half_slice_amax(up_slice, lane, p, amax_plain, amax_rht);
         }
-        __syncwarp();   // (before lane 0 lets the next load into the slices)
+        // the piece after the next, into the slice that the last turn stored
+        // (and whose amax every lane has read)
+        __syncwarp();
+        gated_load<1>(p, extra, w, lane, rank, num_tiles, tile_stride);
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[j][i] = v[j + 1][i];
+        }
     }
     return true;
 }
