@@ -409,10 +409,10 @@ __global__ void __launch_bounds__(most_threads(kClass, true), blocks_of(kClass, 
         const uint4 w = ring.read(stage, kBranch, i);
         if (!coded) return bf16_values(w);
         const float f = checkpoint_factor((w.z >> (8u * ((column(i) / 32u) & 3u))) & 0xFFu);
-        float v[8];
-        e4m3_values_x4(w.x, f, v);
-        e4m3_values_x4(w.y, f, v + 4);
-        return Eight{{pair(v[0], v[1]), pair(v[2], v[3]), pair(v[4], v[5]), pair(v[6], v[7])}};
+        Eight v;
+        e4m3_pairs_x4(w.x, f, v.p);
+        e4m3_pairs_x4(w.y, f, v.p + 2);
+        return v;
     };
     const uint64_t scale = both(p.a.scale);
     uint32_t turn = 0, stage = 0;

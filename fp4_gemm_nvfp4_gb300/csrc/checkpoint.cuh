@@ -17,6 +17,7 @@
 #include <cstdint>
 
 #include "device_common.cuh"
+#include "mma_common.cuh"
 
 namespace nvfp4 {
 
@@ -130,6 +131,12 @@ __device__ __forceinline__ void e4m3_values_x4(uint32_t codes, float factor, flo
         v[2 * i] = lo * factor;
         v[2 * i + 1] = hi * factor;
     }
+}
+__device__ __forceinline__ void e4m3_pairs_x4(uint32_t codes, float factor, uint64_t* v) {
+    float f[4];
+    e4m3_values_x4(codes, factor, f);
+    v[0] = pair(f[0], f[1]);
+    v[1] = pair(f[2], f[3]);
 }
 
 }  // namespace nvfp4

@@ -111,7 +111,8 @@ __host__ __device__ constexpr size_t smem_of(int mode) {
 
 static_assert(kStageBytes % 1024 == 0, "stages must keep 1024-byte alignment for the 128B swizzle");
 static_assert(kSfCol0 + stages_of(kEpiPlain) * kSfColsPerStage <= kTmemCols, "tensor memory budget");
-static_assert(smem_of(kEpiPlain) <= 232448 && smem_of(kEpiGatedBack) <= 232448, "shared memory budget");
+static_assert(smem_of(kEpiPlain) <= 232448 && smem_of(kEpiGated) <= 232448 && smem_of(kEpiGatedBack) <= 232448,
+              "shared memory budget");
 
 struct Params {
     uint32_t M, N;

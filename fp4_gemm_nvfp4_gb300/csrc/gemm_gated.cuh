@@ -26,24 +26,47 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluSlope = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 constexpr float kGeluCube = 0.044715f;
 
+// Two values in a pair throughout (half the instructions of the FMA pipe).
+__device__ __forceinline__ uint64_t both(float x) { return pair(x, x); }
+
 // s(p(g)); past the type's ends e^-x is infinity or 0, s 0 or 1.
 template <bool kGelu>
-__device__ __forceinline__ float gate_sigmoid(float g) {
-    float x = -kLog2e * g;
-    if constexpr (kGelu) x *= kGeluSlope * fmaf(kGeluCube * g, g, 1.0f);
-    return rcp(1.0f + ex2(x));
+__device__ __forceinline__ uint64_t gate_sigmoid(uint64_t g) {
+    uint64_t x;
+    if constexpr (kGelu)
+        x = mul2(mul2(g, both(-kLog2e * kGeluSlope)), fma2(mul2(g, both(kGeluCube)), g, both(1.0f)));
+    else
+        x = mul2(g, both(-kLog2e));
+    float lo, hi;
+    unpair(x, lo, hi);
+    unpair(add2(pair(ex2(lo), ex2(hi)), both(1.0f)), lo, hi);
+    return pair(rcp(lo), rcp(hi));
 }
 
 // act'(g), from s = gate_sigmoid(g).  From |g| = 14 on GELU's s is 0 or 1 and
 // p' of no account: g is cut at 100 there, so that p' stays finite.
 template <bool kGelu>
-__device__ __forceinline__ float gate_slope(float g, float s) {
-    float r = g * (1.0f - s);
+__device__ __forceinline__ uint64_t gate_slope(uint64_t g, uint64_t s) {
+    const uint64_t rest = fma2(s, both(-1.0f), both(1.0f));
+    uint64_t r;
     if constexpr (kGelu) {
-        const float c = fminf(fmaxf(g, -100.0f), 100.0f);
-        r = c * (1.0f - s) * (kGeluSlope * fmaf(3.0f * kGeluCube * c, c, 1.0f));
+        float lo, hi;
+        unpair(g, lo, hi);
+        const uint64_t c = pair(fminf(fmaxf(lo, -100.0f), 100.0f), fminf(fmaxf(hi, -100.0f), 100.0f));
+        r = mul2(mul2(c, rest), fma2(mul2(c, both(3.0f * kGeluCube * kGeluSlope)), c, both(kGeluSlope)));
+    } else {
+        r = mul2(g, rest);
     }
-    return fmaf(s, r, s);
+    return fma2(s, r, s);
+}
+
+__device__ __forceinline__ uint32_t pack_pair(uint64_t p) {
+    float lo, hi;
+    unpair(p, lo, hi);
+    return pack_bf16(lo, hi);
+}
+__device__ __forceinline__ uint64_t word_pair(const uint32_t* v) {
+    return pair(__uint_as_float(v[0]), __uint_as_float(v[1]));
 }
 
 // The place of a lane's 16-byte piece i in a slice of 128-byte rows, in a half
@@ -69,7 +92,9 @@ __device__ __forceinline__ void store_scales(uint8_t* scales, int64_t ld, uint32
         store_out(to, (uint8_t)b0, e);
 }
 
-// Before a slice is written again its last store must have read it.
+// Before a slice is written again its last store must have read it.  (Two
+// slices in turn, which cost a stage of operands, took 446 us for 409 with gate
+// and up kept in BF16, 361 for 335 without.)
 __device__ __forceinline__ void slice_free(uint32_t lane) {
     if (lane == 0) bulk_wait_read_all();
     __syncwarp();
@@ -91,15 +116,14 @@ __device__ __forceinline__ void gated_epilogue(const Params& p, const ExtraMaps<
     auto product = [&](auto gelu) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float h[8];
+            uint32_t h[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int c = 8 * (i & 3) + k;
-                const float g = __uint_as_float(v[i >> 2][c]);
-                h[k] = g * gate_sigmoid<decltype(gelu)::value>(g) * __uint_as_float(v[2 + (i >> 2)][c]);
+            for (int k = 0; k < 4; ++k) {
+                const int c = 8 * (i & 3) + 2 * k;
+                const uint64_t g = word_pair(&v[i >> 2][c]);
+                h[k] = pack_pair(mul2(mul2(g, gate_sigmoid<decltype(gelu)::value>(g)), word_pair(&v[2 + (i >> 2)][c])));
             }
-            *piece128(slice, lane, i) = make_uint4(pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3]), pack_bf16(h[4], h[5]),
-                                                   pack_bf16(h[6], h[7]));
+            *piece128(slice, lane, i) = make_uint4(h[0], h[1], h[2], h[3]);
         }
     };
     if (p.gelu) product(std::true_type{});
@@ -295,22 +319,22 @@ __device__ __forceinline__ void half_slice_amax(const uint8_t* slice, uint32_t l
 
 // Eight columns: dg and du over gate and up.
 template <bool kGelu>
-__device__ __forceinline__ void gated_gradients(const float* g, const float* u, const uint32_t* dh, float alpha,
-                                                uint4& dg_out, uint4& du_out) {
-    float dg[8], du[8];
+__device__ __forceinline__ void gated_gradients(const uint64_t* g, const uint64_t* u, const uint32_t* dh,
+                                                uint64_t alpha, uint4& dg_out, uint4& du_out) {
+    uint32_t dg[4], du[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const float d = __uint_as_float(dh[k]) * alpha, s = gate_sigmoid<kGelu>(g[k]);
-        dg[k] = d * u[k] * gate_slope<kGelu>(g[k], s);
-        du[k] = d * (g[k] * s);
+    for (int k = 0; k < 4; ++k) {
+        const uint64_t d = mul2(word_pair(&dh[2 * k]), alpha), s = gate_sigmoid<kGelu>(g[k]);
+        dg[k] = pack_pair(mul2(mul2(d, u[k]), gate_slope<kGelu>(g[k], s)));
+        du[k] = pack_pair(mul2(d, mul2(g[k], s)));
     }
-    dg_out = make_uint4(pack_bf16(dg[0], dg[1]), pack_bf16(dg[2], dg[3]), pack_bf16(dg[4], dg[5]), pack_bf16(dg[6], dg[7]));
-    du_out = make_uint4(pack_bf16(du[0], du[1]), pack_bf16(du[2], du[3]), pack_bf16(du[4], du[5]), pack_bf16(du[6], du[7]));
+    dg_out = make_uint4(dg[0], dg[1], dg[2], dg[3]);
+    du_out = make_uint4(du[0], du[1], du[2], du[3]);
 }
 
-__device__ __forceinline__ void bf16_x8(const uint4& w, float* v) {
-    v[0] = bf16lo(w.x), v[1] = bf16hi(w.x), v[2] = bf16lo(w.y), v[3] = bf16hi(w.y);
-    v[4] = bf16lo(w.z), v[5] = bf16hi(w.z), v[6] = bf16lo(w.w), v[7] = bf16hi(w.w);
+__device__ __forceinline__ void bf16_pairs(const uint4& w, uint64_t* v) {
+    v[0] = pair(bf16lo(w.x), bf16hi(w.x)), v[1] = pair(bf16lo(w.y), bf16hi(w.y));
+    v[2] = pair(bf16lo(w.z), bf16hi(w.z)), v[3] = pair(bf16lo(w.w), bf16hi(w.w));
 }
 
 // Backward: a tile's 128 columns from x0 on, rows y .. y + 31, piece by piece;
@@ -344,13 +368,13 @@ __device__ __forceinline__ bool gated_backward_epilogue(const Params& p, const E
                 const float fu = checkpoint_factor((w.scales[1] >> (8u * r)) & 0xFFu);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float g[8], u[8];
-                    e4m3_values_x4((i & 1) ? gc[i >> 1].z : gc[i >> 1].x, fg, g);
-                    e4m3_values_x4((i & 1) ? gc[i >> 1].w : gc[i >> 1].y, fg, g + 4);
-                    e4m3_values_x4((i & 1) ? uc[i >> 1].z : uc[i >> 1].x, fu, u);
-                    e4m3_values_x4((i & 1) ? uc[i >> 1].w : uc[i >> 1].y, fu, u + 4);
+                    uint64_t g[4], u[4];
+                    e4m3_pairs_x4((i & 1) ? gc[i >> 1].z : gc[i >> 1].x, fg, g);
+                    e4m3_pairs_x4((i & 1) ? gc[i >> 1].w : gc[i >> 1].y, fg, g + 2);
+                    e4m3_pairs_x4((i & 1) ? uc[i >> 1].z : uc[i >> 1].x, fu, u);
+                    e4m3_pairs_x4((i & 1) ? uc[i >> 1].w : uc[i >> 1].y, fu, u + 2);
                     uint4 dg, du;
-                    gated_gradients<kGelu>(g, u, &v[0][8 * i], alpha, dg, du);
+                    gated_gradients<kGelu>(g, u, &v[0][8 * i], both(alpha), dg, du);
                     *piece64(gate_slice, lane, i) = dg;
                     *piece64(up_slice, lane, i) = du;
                 }
@@ -358,11 +382,11 @@ __device__ __forceinline__ bool gated_backward_epilogue(const Params& p, const E
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint4 *gp = piece64(gate_slice, lane, i), *up = piece64(up_slice, lane, i);
-                    float g[8], u[8];
-                    bf16_x8(*gp, g);
-                    bf16_x8(*up, u);
+                    uint64_t g[4], u[4];
+                    bf16_pairs(*gp, g);
+                    bf16_pairs(*up, u);
                     uint4 dg, du;
-                    gated_gradients<kGelu>(g, u, &v[0][8 * i], alpha, dg, du);
+                    gated_gradients<kGelu>(g, u, &v[0][8 * i], both(alpha), dg, du);
                     *gp = dg;
                     *up = du;
                 }

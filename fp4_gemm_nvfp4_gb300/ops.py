@@ -516,10 +516,11 @@ class Checkpoint:
 
 def _leading(x: torch.Tensor, rows: int, cols: int, dtype, what: str) -> int:
     """The leading dimension of a matrix with at least `cols` contiguous columns."""
-    if x.dtype != dtype or x.dim() != 2 or x.shape[0] != rows or x.shape[1] < cols:
-        raise ValueError(f"{what}: {dtype} [{rows}, {cols}] expected, got {x.dtype} {list(x.shape)}")
+    shape = x.shape
+    if x.dtype is not dtype or len(shape) != 2 or shape[0] != rows or shape[1] < cols:
+        raise ValueError(f"{what}: {dtype} [{rows}, {cols}] expected, got {x.dtype} {list(shape)}")
     ld, one = x.stride()
-    if one != 1 and x.shape[1] > 1:
+    if one != 1 and shape[1] > 1:
         raise ValueError(f"{what}: the columns must be contiguous")
     # the stride of one row says nothing
     return ld if rows > 1 else (cols + 15) // 16 * 16
@@ -527,28 +528,35 @@ def _leading(x: torch.Tensor, rows: int, cols: int, dtype, what: str) -> int:
 
 def _matrix(x: torch.Tensor, rows: int, cols: int, dtype, what: str) -> Tuple[int, int]:
     """Address and leading dimension of a [rows, cols] matrix."""
-    if x.shape != (rows, cols):
-        raise ValueError(f"{what}: [{rows}, {cols}] expected, got {list(x.shape)}")
-    return x.data_ptr(), _leading(x, rows, cols, dtype, what)
+    if x.dtype is not dtype or x.shape != (rows, cols):
+        raise ValueError(f"{what}: {dtype} [{rows}, {cols}] expected, got {x.dtype} {list(x.shape)}")
+    ld, one = x.stride()
+    if one != 1 and cols > 1:
+        raise ValueError(f"{what}: the columns must be contiguous")
+    return x.data_ptr(), ld if rows > 1 else (cols + 15) // 16 * 16
 
 
 def _check_here(*tensors: Optional[torch.Tensor]) -> None:
     """Every tensor on the current device, where the kernels run."""
+    here = None
     for t in tensors:
         if t is not None:
-            _check_on_gpu(t.is_cuda)
-            if t.get_device() != torch._C._cuda_getDevice():
-                raise ValueError(f"tensors on the current device expected, got one on {t.device}")
+            at = t.get_device()
+            if at != here:
+                _check_on_gpu(at >= 0)
+                here = torch._C._cuda_getDevice()
+                if at != here:
+                    raise ValueError(f"tensors on the current device expected, got one on {t.device}")
 
 
 def alloc_checkpoint(rows: int, cols: int, kind: str = "e4m3", device="cuda") -> Checkpoint:
     """A checkpoint's memory: kind "e4m3" (8 bits) or "bf16"."""
     if kind == "bf16":
-        return Checkpoint(torch.empty((rows, _round_up(cols, 8)), dtype=torch.bfloat16, device=device), None, rows, cols)
+        return Checkpoint(torch.empty((rows, (cols + 7) // 8 * 8), dtype=torch.bfloat16, device=device), None, rows, cols)
     if kind != "e4m3":
         raise ValueError(f'"bf16" or "e4m3" expected, got {kind!r}')
-    return Checkpoint(torch.empty((rows, _round_up(cols, 16)), dtype=torch.uint8, device=device),
-                      torch.empty((rows, _round_up((cols + 31) // 32, 16)), dtype=torch.uint8, device=device), rows, cols)
+    return Checkpoint(torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.uint8, device=device),
+                      torch.empty((rows, (cols + 511) // 512 * 16), dtype=torch.uint8, device=device), rows, cols)
 
 
 def checkpoint_encode(x: torch.Tensor, out: Optional[Checkpoint] = None, stream=None) -> Checkpoint:
@@ -669,9 +677,10 @@ def _block_norm_desc(tokens, width, dtype, post_weight, pre_weight, gate, residu
         kind = capi.NVFP4_OUT_FP32
     else:
         raise ValueError(f"residual: bfloat16 or float32 expected, got {dtype}")
-    for w, what in ((post_weight, "post_weight"), (pre_weight, "pre_weight")):
-        if w is not None:
-            _check_float32(w, (width,), what)
+    if post_weight is not None:
+        _check_float32(post_weight, (width,), "post_weight")
+    if pre_weight is not None:
+        _check_float32(pre_weight, (width,), "pre_weight")
     gate_kind, gate_ptr, ld_gate = capi.NVFP4_GATE_NONE, None, 0
     if gate is not None:
         if gate.dim() == 1:
