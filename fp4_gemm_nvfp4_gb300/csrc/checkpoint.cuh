@@ -93,28 +93,31 @@ __device__ __forceinline__ uint2 bf16_codes(const uint4& w, uint32_t b, bool spe
     return make_uint2(e4m3_codes_x4(v[0], v[1], v[2], v[3]), e4m3_codes_x4(v[4], v[5], v[6], v[7]));
 }
 
-// 32 FP32 values as the codes of one block; returns its scale byte.  v is used up.
-__device__ __forceinline__ uint32_t fp32_codes(uint32_t* v, uint32_t* codes) {
+// 32 FP32 values as the codes of one block; returns its scale byte.
+__device__ __forceinline__ uint32_t fp32_codes(const uint32_t* v, uint32_t* codes) {
     float m = 0.0f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(__uint_as_float(v[i]))));
     uint32_t bits = __float_as_uint(m) & 0x7FFFFFFFu;
     uint32_t b = checkpoint_scale(bits);
-    float f = checkpoint_inverse(b);
-    if (bits >= kOrdinaryBelow) {
+    if (bits < kOrdinaryBelow) {
+        const float f = checkpoint_inverse(b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            codes[i] = e4m3_codes_x4(__uint_as_float(v[4 * i]) * f, __uint_as_float(v[4 * i + 1]) * f,
+                                     __uint_as_float(v[4 * i + 2]) * f, __uint_as_float(v[4 * i + 3]) * f);
+    } else {
         bits = 0;
 #pragma unroll
         for (int i = 0; i < 32; ++i) bits = max(bits, finite_magnitude(__uint_as_float(v[i])));
         b = checkpoint_scale(bits);
-        f = 1.0f;
+        const float f = checkpoint_inverse(b);
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            v[i] = __float_as_uint(checkpoint_scaled(__uint_as_float(v[i]), checkpoint_inverse(b)));
+        for (int i = 0; i < 8; ++i)
+            codes[i] = e4m3_codes_x4(
+                checkpoint_scaled(__uint_as_float(v[4 * i]), f), checkpoint_scaled(__uint_as_float(v[4 * i + 1]), f),
+                checkpoint_scaled(__uint_as_float(v[4 * i + 2]), f), checkpoint_scaled(__uint_as_float(v[4 * i + 3]), f));
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        codes[i] = e4m3_codes_x4(__uint_as_float(v[4 * i]) * f, __uint_as_float(v[4 * i + 1]) * f,
-                                 __uint_as_float(v[4 * i + 2]) * f, __uint_as_float(v[4 * i + 3]) * f);
     return b;
 }
 

@@ -94,8 +94,9 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 // Epilogue variants: the plain product; the product plus the output's two
 // tensor amaxes (p.amax_out); alpha times the product plus beta C (p.c); the
-// gated pair of products and its backward pass (gemm_gated.cuh).
-enum EpiMode { kEpiPlain = 0, kEpiAmax = 1, kEpiC = 2, kEpiGated = 3, kEpiGatedBack = 4 };
+// gated pair of products, alone and with gate and up kept, and its backward pass
+// (gemm_gated.cuh).
+enum EpiMode { kEpiPlain = 0, kEpiAmax = 1, kEpiC = 2, kEpiGated = 3, kEpiGatedKept = 4, kEpiGatedBack = 5 };
 
 // The gated backward pass reads two matrices through its slices and writes two
 // back: three slices per epilogue warp, paid for with two stages of operands.
@@ -145,19 +146,18 @@ struct Params {
     int gelu;                    // the gate's activation: SiLU or GELU
     int kept;                    // gate and up: 0 not kept, 1 BF16, 2 in 8 bits
     const float* sgu;            // B's second operand's tensor scale (forward)
+    uint8_t* lane_out[2];        // forward: gate and up as kept
+    int64_t ld_lane_out[2];      // bytes
+    Extent x_lane_out[2];
     uint8_t *gate_scales, *up_scales;
     int64_t ld_gate_scales, ld_up_scales;
     uint32_t scale_blocks;       // 1x32 blocks of a row
     Extent x_gate_scales, x_up_scales;
 };
 
-// Tensor maps that only some modes have: gate and up as kept.
+// Tensor maps that only one mode has: gate and up as kept.
 template <int kMode>
 struct ExtraMaps {};
-template <>
-struct ExtraMaps<kEpiGated> {
-    CUtensorMap gate, up;
-};
 template <>
 struct ExtraMaps<kEpiGatedBack> {
     CUtensorMap gate, up;
@@ -407,7 +407,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                      const __grid_constant__ CUtensorMap tma_v, const Params p,
                      const __grid_constant__ ExtraMaps<kMode> extra) {
     constexpr int kStages = stages_of(kMode);
-    constexpr bool kGated = kMode == kEpiGated, kGatedBack = kMode == kEpiGatedBack;
+    constexpr bool kGated = kMode == kEpiGated || kMode == kEpiGatedKept, kGatedBack = kMode == kEpiGatedBack;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* staging = smem + kStages * kStageBytes;
@@ -800,7 +800,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(leader_acc_empty);
-                gated_epilogue(p, extra, &tma_d, own_slice, lane, row0 + q * 32, nt * kCtaN + half * 64, v, alpha,
+                gated_epilogue<kMode == kEpiGatedKept>(p, &tma_d, own_slice, lane, row0 + q * 32, nt * kCtaN + half * 64, v, alpha,
                                __fmul_rn(*p.sga, *p.sgu), amax_plain, amax_rht);
             } else if constexpr (kGatedBack) {
                 uint32_t v[4][32];
@@ -1135,7 +1135,7 @@ bool register_split_ok() {
         };
         ok = (split(gemm_nvf4_kernel<kEpiPlain>) && split(gemm_nvf4_kernel<kEpiAmax>) &&
               split(gemm_nvf4_kernel<kEpiC>) && split(gemm_nvf4_kernel<kEpiGated>) &&
-              split(gemm_nvf4_kernel<kEpiGatedBack>))
+              split(gemm_nvf4_kernel<kEpiGatedKept>) && split(gemm_nvf4_kernel<kEpiGatedBack>))
                  ? 1
                  : 0;
     }
@@ -1212,6 +1212,7 @@ cudaError_t prepare_gemm() {
         allow(gemm_nvf4_kernel<kEpiAmax>, kEpiAmax);
         allow(gemm_nvf4_kernel<kEpiC>, kEpiC);
         allow(gemm_nvf4_kernel<kEpiGated>, kEpiGated);
+        allow(gemm_nvf4_kernel<kEpiGatedKept>, kEpiGatedKept);
         allow(gemm_nvf4_kernel<kEpiGatedBack>, kEpiGatedBack);
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
@@ -1257,30 +1258,30 @@ int gemm_grid(const Params& p) {
     return 2 * (int)(tiles < pairs ? tiles : pairs);
 }
 
-// 2-D map over a row-major matrix of BF16 or 8-bit codes, `box_cols` columns by
-// 32 rows per box, swizzled over the box's row of 32, 64 or 128 bytes.
-bool make_piece_map(CUtensorMap* map, void* base, int64_t rows, int64_t cols, int64_t ld_bytes, bool codes,
-                    uint32_t box_cols) {
+// 2-D map over a row-major matrix of BF16 or 8-bit codes, 32 columns by 32 rows
+// per box (64-byte swizzle; codes 32-byte).
+bool make_piece_map(CUtensorMap* map, void* base, int64_t rows, int64_t cols, int64_t ld, bool codes) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
-    const uint32_t row = box_cols * (codes ? 1u : 2u);
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)ld_bytes};
-    const cuuint32_t box[2] = {box_cols, 32};
+    const cuuint64_t strides[1] = {(cuuint64_t)(codes ? ld : 2 * ld)};
+    const cuuint32_t box[2] = {32, 32};
     const cuuint32_t elem[2] = {1, 1};
     return fn(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides,
               box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
-                         : row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
-              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              codes ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-bool make_checkpoint_map(CUtensorMap* map, const CheckpointView& t, int64_t rows, int64_t cols, uint32_t box_cols) {
-    return make_piece_map(map, t.data, rows, cols, t.scales ? t.ld : 2 * t.ld, t.scales != nullptr, box_cols);
+
+// Matrix t that the lanes store, M x N of `esz` bytes.
+void set_lane_out(Params& p, int t, void* data, int64_t ld, int64_t esz) {
+    p.lane_out[t] = static_cast<uint8_t*>(data);
+    p.ld_lane_out[t] = ld * esz;
+    p.x_lane_out[t] = extent_rows(data, p.M, ld * esz, p.N * esz);
 }
 
 // Gate and up as kept, of the call's M x N.
-bool set_checkpoints(Params& p, CUtensorMap* gate_map, CUtensorMap* up_map, const CheckpointView& gate,
-                     const CheckpointView& up, uint32_t box_cols) {
+void set_checkpoints(Params& p, const CheckpointView& gate, const CheckpointView& up) {
     p.kept = gate.scales ? 2 : 1;
     p.scale_blocks = (p.N + 31) / 32;
     p.gate_scales = gate.scales;
@@ -1291,7 +1292,6 @@ bool set_checkpoints(Params& p, CUtensorMap* gate_map, CUtensorMap* up_map, cons
         p.x_gate_scales = extent_rows(gate.scales, p.M, gate.ld_scales, p.scale_blocks);
         p.x_up_scales = extent_rows(up.scales, p.M, up.ld_scales, p.scale_blocks);
     }
-    return make_checkpoint_map(gate_map, gate, p.M, p.N, box_cols) && make_checkpoint_map(up_map, up, p.M, p.N, box_cols);
 }
 
 }  // namespace
@@ -1302,20 +1302,26 @@ cudaError_t launch_gemm_gated(const GemmOperand& a, const GemmOperand& gate, con
     cudaError_t e = prepare_gemm();
     if (e != cudaSuccess) return e;
     CUtensorMap ma, mg, mu, msa, msg, msu, mh;
-    ExtraMaps<kEpiGated> extra;
     Params p = gemm_params(a, gate, kCtaN);
     if (!make_codes_map(&ma, a, kCtaM) || !make_codes_map(&mg, gate, kCtaN) || !make_codes_map(&mu, up, kCtaN) ||
         !make_scale_map(&msa, a, 1) || !make_scale_map(&msg, gate, 1) || !make_scale_map(&msu, up, 1) ||
         !make_output_map(&mh, h, a.rows, gate.rows, ldh, false))
         return cudaErrorInvalidValue;
-    extra.gate = extra.up = mh;   // (not read unless they are kept)
-    if (gate_kept && !set_checkpoints(p, &extra.gate, &extra.up, *gate_kept, *up_kept, 64)) return cudaErrorInvalidValue;
+    if (gate_kept) {
+        set_checkpoints(p, *gate_kept, *up_kept);
+        set_lane_out(p, 0, gate_kept->data, gate_kept->ld, gate_kept->scales ? 1 : 2);
+        set_lane_out(p, 1, up_kept->data, up_kept->ld, up_kept->scales ? 1 : 2);
+    }
     p.gelu = gelu ? 1 : 0;
     p.sgu = up.sg;
     p.tma_store = 1;
     if (amax_out && (e = set_amax(p, amax_out, rht_mask, stream)) != cudaSuccess) return e;
-    gemm_nvf4_kernel<kEpiGated>
-        <<<gemm_grid(p), kThreads, smem_of(kEpiGated), stream>>>(ma, mg, msa, msg, mh, mu, msu, p, extra);
+    if (gate_kept)
+        gemm_nvf4_kernel<kEpiGatedKept>
+            <<<gemm_grid(p), kThreads, smem_of(kEpiGatedKept), stream>>>(ma, mg, msa, msg, mh, mu, msu, p, {});
+    else
+        gemm_nvf4_kernel<kEpiGated>
+            <<<gemm_grid(p), kThreads, smem_of(kEpiGated), stream>>>(ma, mg, msa, msg, mh, mu, msu, p, {});
     return cudaGetLastError();
 }
 
@@ -1329,10 +1335,12 @@ cudaError_t launch_gemm_gated_backward(const GemmOperand& a, const GemmOperand& 
     ExtraMaps<kEpiGatedBack> extra;
     Params p = gemm_params(a, b, kBN);
     if (!make_codes_map(&ma, a, kCtaM) || !make_codes_map(&mb, b, kCtaN) || !make_scale_map(&msa, a, 1) ||
-        !make_scale_map(&msb, b, 2) || !make_piece_map(&mg, dgate, a.rows, b.rows, 2 * ld_dgate, false, 32) ||
-        !make_piece_map(&mu, dup, a.rows, b.rows, 2 * ld_dup, false, 32) ||
-        !set_checkpoints(p, &extra.gate, &extra.up, gate, up, 32))
+        !make_scale_map(&msb, b, 2) || !make_piece_map(&mg, dgate, a.rows, b.rows, ld_dgate, false) ||
+        !make_piece_map(&mu, dup, a.rows, b.rows, ld_dup, false) ||
+        !make_piece_map(&extra.gate, gate.data, a.rows, b.rows, gate.ld, gate.scales != nullptr) ||
+        !make_piece_map(&extra.up, up.data, a.rows, b.rows, up.ld, up.scales != nullptr))
         return cudaErrorInvalidValue;
+    set_checkpoints(p, gate, up);
     p.gelu = gelu ? 1 : 0;
     p.tma_store = 1;
     if (amax_out && (e = set_amax(p, amax_out, rht_mask, stream)) != cudaSuccess) return e;

@@ -26,6 +26,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluSlope = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 constexpr float kGeluCube = 0.044715f;
 
+constexpr uint32_t kHalfSlice = kSliceBytes / 2;
+
 // Two values in a pair throughout (half the instructions of the FMA pipe).
 __device__ __forceinline__ uint64_t both(float x) { return pair(x, x); }
 
@@ -92,20 +94,40 @@ __device__ __forceinline__ void store_scales(uint8_t* scales, int64_t ld, uint32
         store_out(to, (uint8_t)b0, e);
 }
 
-// Before a slice is written again its last store must have read it.  (Two
-// slices in turn, which cost a stage of operands, took 446 us for 409 with gate
-// and up kept in BF16, 361 for 335 without.)
+// Before a slice is written again its last TMA store must have read it.
 __device__ __forceinline__ void slice_free(uint32_t lane) {
     if (lane == 0) bulk_wait_read_all();
     __syncwarp();
 }
 
-// Forward: columns x .. x + 63 of rows y .. y + 31; v: gate (2 x 32), up, used up.
-__device__ __forceinline__ void gated_epilogue(const Params& p, const ExtraMaps<kEpiGated>& extra,
-                                               const CUtensorMap* h_map, uint8_t* slice, uint32_t lane, uint32_t y,
-                                               uint32_t x, uint32_t (&v)[4][32], float alpha_gate, float alpha_up,
-                                               float& amax_plain, float& amax_rht) {
-    const bool inside = y < p.M && x < p.N;
+// A slice's 32 rows of kRowBytes (swizzled as above) to byte x of the rows from
+// y on of output t, `bytes` to a row, by the lanes, whole rows at a time: the
+// slice is free when they are done, where a TMA store would have to be waited for.
+template <uint32_t kRowBytes>
+__device__ __forceinline__ void copy_out(const Params& p, int t, const uint8_t* slice, uint32_t lane, uint32_t x,
+                                         uint32_t y, uint32_t bytes) {
+    constexpr uint32_t kPieces = kRowBytes / 16, kRows = 32 / kPieces;
+    const uint32_t ch = lane % kPieces, first = lane / kPieces;
+    const bool inside = x + 16u * ch < bytes;
+    uint8_t* to = p.lane_out[t] + (int64_t)(y + first) * p.ld_lane_out[t] + x + 16u * ch;
+#pragma unroll
+    for (uint32_t i = 0; i < 32 / kRows; ++i) {
+        const uint32_t rr = i * kRows + first;
+        const uint32_t at = kRowBytes == 128 ? rr & 7u : (rr >> 1) & 3u;
+        const uint4 w = *reinterpret_cast<const uint4*>(slice + rr * kRowBytes + ((ch ^ at) << 4));
+        if (inside && y + rr < p.M) store_out(reinterpret_cast<uint4*>(to), w, p.x_lane_out[t]);
+        to += (int64_t)kRows * p.ld_lane_out[t];
+    }
+}
+
+// Forward: columns x .. x + 63 of rows y .. y + 31; v: gate (2 x 32), up.  What
+// is kept goes first, copied out by the lanes, and H last, whose TMA store the
+// next tile waits for (all three by TMA, each waiting for the one before: 409 us
+// for 381 with BF16 kept).
+template <bool kKept>
+__device__ __forceinline__ void gated_epilogue(const Params& p, const CUtensorMap* h_map, uint8_t* slice,
+                                               uint32_t lane, uint32_t y, uint32_t x, uint32_t (&v)[4][32],
+                                               float alpha_gate, float alpha_up, float& amax_plain, float& amax_rht) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
 #pragma unroll
@@ -113,6 +135,43 @@ __device__ __forceinline__ void gated_epilogue(const Params& p, const ExtraMaps<
             v[j][i] = __float_as_uint(__uint_as_float(v[j][i]) * (j < 2 ? alpha_gate : alpha_up));
     }
     slice_free(lane);
+    if (kKept && p.kept == 1) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t* a = &v[2 * t + (i >> 2)][8 * (i & 3)];
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = pack_bf16(__uint_as_float(a[2 * k]), __uint_as_float(a[2 * k + 1]));
+                *piece128(slice, lane, i) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            __syncwarp();
+            copy_out<128>(p, t, slice, lane, 2u * x, y, 2u * p.N);
+            __syncwarp();
+        }
+    } else if (kKept) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            uint32_t b[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                uint32_t codes[8];
+                b[j] = fp32_codes(v[2 * t + j], codes);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    *piece64(slice + t * kHalfSlice, lane, 2 * j + i) =
+                        make_uint4(codes[4 * i], codes[4 * i + 1], codes[4 * i + 2], codes[4 * i + 3]);
+            }
+            if (y + lane < p.M && x < p.N)
+                store_scales(t ? p.up_scales : p.gate_scales, t ? p.ld_up_scales : p.ld_gate_scales, y + lane, x / 32u,
+                             p.scale_blocks, b[0], b[1], t ? p.x_up_scales : p.x_gate_scales);
+        }
+        __syncwarp();
+        copy_out<64>(p, 0, slice, lane, x, y, p.N);
+        copy_out<64>(p, 1, slice + kHalfSlice, lane, x, y, p.N);
+        __syncwarp();
+    }
     auto product = [&](auto gelu) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -131,60 +190,11 @@ __device__ __forceinline__ void gated_epilogue(const Params& p, const ExtraMaps<
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-        if (inside) tma_store_2d(h_map, slice, (int32_t)x, (int32_t)y);
+        if (y < p.M && x < p.N) tma_store_2d(h_map, slice, (int32_t)x, (int32_t)y);
         bulk_commit_group();
     }
     if (p.amax_out) slice_amax(slice, lane, p, amax_plain, amax_rht);
-    if (p.kept == 1) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            slice_free(lane);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t* a = &v[2 * t + (i >> 2)][8 * (i & 3)];
-                uint32_t w[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) w[k] = pack_bf16(__uint_as_float(a[2 * k]), __uint_as_float(a[2 * k + 1]));
-                *piece128(slice, lane, i) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                if (inside) tma_store_2d(t ? &extra.up : &extra.gate, slice, (int32_t)x, (int32_t)y);
-                bulk_commit_group();
-            }
-        }
-    } else if (p.kept == 2) {
-        slice_free(lane);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            uint32_t b[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                uint32_t codes[8];
-                b[j] = fp32_codes(v[2 * t + j], codes);
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    *piece64(slice + t * (kSliceBytes / 2), lane, 2 * j + i) =
-                        make_uint4(codes[4 * i], codes[4 * i + 1], codes[4 * i + 2], codes[4 * i + 3]);
-            }
-            if (y + lane < p.M && x < p.N)
-                store_scales(t ? p.up_scales : p.gate_scales, t ? p.ld_up_scales : p.ld_gate_scales, y + lane, x / 32u,
-                             p.scale_blocks, b[0], b[1], t ? p.x_up_scales : p.x_gate_scales);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            if (inside) {
-                tma_store_2d(&extra.gate, slice, (int32_t)x, (int32_t)y);
-                tma_store_2d(&extra.up, slice + kSliceBytes / 2, (int32_t)x, (int32_t)y);
-            }
-            bulk_commit_group();
-        }
-    }
 }
-
-constexpr uint32_t kHalfSlice = kSliceBytes / 2;
 
 // The four scale bytes from `block` on of a row, ones past its end.
 __device__ __forceinline__ uint32_t load_scales(const uint8_t* scales, int64_t ld, uint32_t row, uint32_t block,
