@@ -622,7 +622,8 @@ typedef struct {
  * Requirements: width as above, leading dimensions >= width [SHAPE]; every
  * pointer 16-byte aligned, rows a multiple of 16 bytes apart [ALIGNMENT]; finite
  * eps >= 0 and residual_scale [INVALID_ARG].  tokens = 0 enqueues nothing.
- * A NaN or infinity stays in its token's row.
+ * A NaN or infinity stays in its token's row.  The sums of squares are FP32: a
+ * row whose squares overflow it (magnitudes from about 1e18 on) is normed to 0.
  */
 NVFP4_API nvfp4_status nvfp4_block_norm(const nvfp4_block_norm_desc *desc, const void *residual, int64_t ld_residual,
                                         const void *branch, int64_t ld_branch, void *residual_out,
