@@ -4,7 +4,9 @@
 // Bound by HBM: 3.03 bytes per value each way.  A lane takes 8 columns (16
 // bytes of BF16, 8 of codes), four lanes a 1x32 block, whose maximum takes two
 // shuffles; a warp's accesses are whole lines.  A lane loads kAhead pieces, a
-// grid apart, before it computes (bytes in flight).
+// grid apart, before it computes (bytes in flight).  16384 x 9216: 83 and 80 us
+// (5.5 and 5.7 TB/s, 81 and 85 % of a copy); maxima of packed halves instead of
+// FP32 values took encode from 130.
 #include <cuda_runtime.h>
 
 #include "bounds.cuh"

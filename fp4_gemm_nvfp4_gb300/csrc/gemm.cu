@@ -107,7 +107,7 @@ __host__ __device__ constexpr uint32_t staging_of(int mode) {
     return kNumEpiWarpsStaging * slices_of(mode) * kSliceBytes;
 }
 __host__ __device__ constexpr size_t smem_of(int mode) {
-    return (size_t)stages_of(mode) * kStageBytes + staging_of(mode) + 1024 /*align*/ + 512 /*barriers*/;
+    return (size_t)stages_of(mode) * kStageBytes + staging_of(mode) + 1024 /*align*/ + 256 /*barriers*/;
 }
 
 static_assert(kStageBytes % 1024 == 0, "stages must keep 1024-byte alignment for the 128B swizzle");
@@ -146,21 +146,13 @@ struct Params {
     int gelu;                    // the gate's activation: SiLU or GELU
     int kept;                    // gate and up: 0 not kept, 1 BF16, 2 in 8 bits
     const float* sgu;            // B's second operand's tensor scale (forward)
-    uint8_t* lane_out[2];        // forward: gate and up as kept
-    int64_t ld_lane_out[2];      // bytes
-    Extent x_lane_out[2];
+    uint8_t* pair[2];            // gate and up as kept: written forward, read backward
+    int64_t ld_pair[2];          // bytes
+    Extent x_pair[2];
     uint8_t *gate_scales, *up_scales;
     int64_t ld_gate_scales, ld_up_scales;
     uint32_t scale_blocks;       // 1x32 blocks of a row
     Extent x_gate_scales, x_up_scales;
-};
-
-// Tensor maps that only one mode has: gate and up as kept.
-template <int kMode>
-struct ExtraMaps {};
-template <>
-struct ExtraMaps<kEpiGatedBack> {
-    CUtensorMap gate, up;
 };
 
 // 32 consecutive values of C's row `row` from column n0 (zeros past M or N):
@@ -404,8 +396,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_nvf4_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_constant__ CUtensorMap tma_b,
                      const __grid_constant__ CUtensorMap tma_sfa, const __grid_constant__ CUtensorMap tma_sfb,
                      const __grid_constant__ CUtensorMap tma_d, const __grid_constant__ CUtensorMap tma_u,
-                     const __grid_constant__ CUtensorMap tma_v, const Params p,
-                     const __grid_constant__ ExtraMaps<kMode> extra) {
+                     const __grid_constant__ CUtensorMap tma_v, const Params p) {
     constexpr int kStages = stages_of(kMode);
     constexpr bool kGated = kMode == kEpiGated || kMode == kEpiGatedKept, kGatedBack = kMode == kEpiGatedBack;
     extern __shared__ uint8_t smem_raw[];
@@ -420,7 +411,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile uint32_t* abort_flag = tmem_slot + 1;
     volatile uint32_t* sf_ok = tmem_slot + 4;    // [2]: scales-landed verdicts, by stage-count parity
-    uint64_t* loaded = reinterpret_cast<uint64_t*>(tmem_slot + 6);   // gated backward: the epilogue warps' slices
 
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
     const uint32_t rank = cluster_ctarank();
@@ -434,9 +424,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         mbar_init(acc_full, 1);
         mbar_init(acc_empty, 2 * kNumEpiWarps);
         mbar_init(drain, 1);
-        if constexpr (kGatedBack) {
-            for (uint32_t w = 0; w < kNumEpiWarps * kBackSlices; ++w) mbar_init(&loaded[w], 1);
-        }
         *abort_flag = 0u;
         fence_barrier_init();
     }
@@ -743,11 +730,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t half = (warp - kFirstEpiWarp) >> 2;     // 128-column half of the tile
         const float alpha = __fmul_rn(__fmul_rn(*p.sga, *p.sgb), p.alpha);
         uint8_t* const own_slice = staging + (half * 4 + q) * (slices_of(kMode) * kSliceBytes);
-        GatedWarp gated{&loaded[(half * 4 + q) * kBackSlices], own_slice, q, half};   // (of the gated backward mode)
+        GatedWarp gated{own_slice, q, half};   // (of the gated backward mode)
         if constexpr (kGatedBack) {
             gated.in_tile = first_tile;
-            gated_load<0>(p, extra, gated, lane, rank, num_tiles, tile_stride);
-            gated_load<0>(p, extra, gated, lane, rank, num_tiles, tile_stride);
+            gated_load<0>(p, gated, lane, rank, num_tiles, tile_stride);
+            gated_load<0>(p, gated, lane, rank, num_tiles, tile_stride);
             gated_scales(p, gated, lane, rank, first_tile, num_tiles);
         }
         constexpr bool kAmax = kMode == kEpiAmax;
@@ -810,9 +797,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(leader_acc_empty);
-                if (!gated_backward_epilogue(p, extra, gated, &tma_d, &tma_u, lane, rank, num_tiles, tile_stride,
-                                             row0 + q * 32, nbase, v, alpha, abort_flag, amax_plain, amax_rht))
-                    break;
+                gated_backward_epilogue(p, gated, &tma_d, &tma_u, lane, rank, num_tiles, tile_stride, row0 + q * 32,
+                                        nbase, v, alpha, amax_plain, amax_rht);
             } else if (has_c && p.c_staged) {
                 // C through this warp's 4 KiB slice: each round the lanes copy
                 // the round's 32 rows of C into the slice (the output map's
@@ -1015,7 +1001,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             ++tiles_done;
         }
-        if constexpr (kGatedBack) gated_drain(p, gated, lane);
+        if constexpr (kGatedBack) asm volatile("cp.async.wait_all;" ::: "memory");
         if (p.tma_store && lane == 0) bulk_wait_all();
         if (kAmax || ((kGated || kGatedBack) && p.amax_out)) {
             amax_plain = warp_max(amax_plain);
@@ -1258,31 +1244,29 @@ int gemm_grid(const Params& p) {
     return 2 * (int)(tiles < pairs ? tiles : pairs);
 }
 
-// 2-D map over a row-major matrix of BF16 or 8-bit codes, 32 columns by 32 rows
-// per box (64-byte swizzle; codes 32-byte).
-bool make_piece_map(CUtensorMap* map, void* base, int64_t rows, int64_t cols, int64_t ld, bool codes) {
+// 2-D map over a BF16 output of 32 columns by 32 rows per box (64-byte swizzle).
+bool make_piece_map(CUtensorMap* map, void* base, int64_t rows, int64_t cols, int64_t ld) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)(codes ? ld : 2 * ld)};
+    const cuuint64_t strides[1] = {(cuuint64_t)(2 * ld)};
     const cuuint32_t box[2] = {32, 32};
     const cuuint32_t elem[2] = {1, 1};
-    return fn(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides,
-              box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              codes ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Matrix t that the lanes store, M x N of `esz` bytes.
-void set_lane_out(Params& p, int t, void* data, int64_t ld, int64_t esz) {
-    p.lane_out[t] = static_cast<uint8_t*>(data);
-    p.ld_lane_out[t] = ld * esz;
-    p.x_lane_out[t] = extent_rows(data, p.M, ld * esz, p.N * esz);
 }
 
 // Gate and up as kept, of the call's M x N.
 void set_checkpoints(Params& p, const CheckpointView& gate, const CheckpointView& up) {
+    const int64_t esz = gate.scales ? 1 : 2;
     p.kept = gate.scales ? 2 : 1;
+    p.pair[0] = static_cast<uint8_t*>(gate.data);
+    p.pair[1] = static_cast<uint8_t*>(up.data);
+    p.ld_pair[0] = gate.ld * esz;
+    p.ld_pair[1] = up.ld * esz;
+    p.x_pair[0] = extent_rows(gate.data, p.M, gate.ld * esz, p.N * esz);
+    p.x_pair[1] = extent_rows(up.data, p.M, up.ld * esz, p.N * esz);
     p.scale_blocks = (p.N + 31) / 32;
     p.gate_scales = gate.scales;
     p.up_scales = up.scales;
@@ -1307,21 +1291,17 @@ cudaError_t launch_gemm_gated(const GemmOperand& a, const GemmOperand& gate, con
         !make_scale_map(&msa, a, 1) || !make_scale_map(&msg, gate, 1) || !make_scale_map(&msu, up, 1) ||
         !make_output_map(&mh, h, a.rows, gate.rows, ldh, false))
         return cudaErrorInvalidValue;
-    if (gate_kept) {
-        set_checkpoints(p, *gate_kept, *up_kept);
-        set_lane_out(p, 0, gate_kept->data, gate_kept->ld, gate_kept->scales ? 1 : 2);
-        set_lane_out(p, 1, up_kept->data, up_kept->ld, up_kept->scales ? 1 : 2);
-    }
+    if (gate_kept) set_checkpoints(p, *gate_kept, *up_kept);
     p.gelu = gelu ? 1 : 0;
     p.sgu = up.sg;
     p.tma_store = 1;
     if (amax_out && (e = set_amax(p, amax_out, rht_mask, stream)) != cudaSuccess) return e;
     if (gate_kept)
         gemm_nvf4_kernel<kEpiGatedKept>
-            <<<gemm_grid(p), kThreads, smem_of(kEpiGatedKept), stream>>>(ma, mg, msa, msg, mh, mu, msu, p, {});
+            <<<gemm_grid(p), kThreads, smem_of(kEpiGatedKept), stream>>>(ma, mg, msa, msg, mh, mu, msu, p);
     else
         gemm_nvf4_kernel<kEpiGated>
-            <<<gemm_grid(p), kThreads, smem_of(kEpiGated), stream>>>(ma, mg, msa, msg, mh, mu, msu, p, {});
+            <<<gemm_grid(p), kThreads, smem_of(kEpiGated), stream>>>(ma, mg, msa, msg, mh, mu, msu, p);
     return cudaGetLastError();
 }
 
@@ -1332,20 +1312,17 @@ cudaError_t launch_gemm_gated_backward(const GemmOperand& a, const GemmOperand& 
     cudaError_t e = prepare_gemm();
     if (e != cudaSuccess) return e;
     CUtensorMap ma, mb, msa, msb, mg, mu;
-    ExtraMaps<kEpiGatedBack> extra;
     Params p = gemm_params(a, b, kBN);
     if (!make_codes_map(&ma, a, kCtaM) || !make_codes_map(&mb, b, kCtaN) || !make_scale_map(&msa, a, 1) ||
-        !make_scale_map(&msb, b, 2) || !make_piece_map(&mg, dgate, a.rows, b.rows, ld_dgate, false) ||
-        !make_piece_map(&mu, dup, a.rows, b.rows, ld_dup, false) ||
-        !make_piece_map(&extra.gate, gate.data, a.rows, b.rows, gate.ld, gate.scales != nullptr) ||
-        !make_piece_map(&extra.up, up.data, a.rows, b.rows, up.ld, up.scales != nullptr))
+        !make_scale_map(&msb, b, 2) || !make_piece_map(&mg, dgate, a.rows, b.rows, ld_dgate) ||
+        !make_piece_map(&mu, dup, a.rows, b.rows, ld_dup))
         return cudaErrorInvalidValue;
     set_checkpoints(p, gate, up);
     p.gelu = gelu ? 1 : 0;
     p.tma_store = 1;
     if (amax_out && (e = set_amax(p, amax_out, rht_mask, stream)) != cudaSuccess) return e;
     gemm_nvf4_kernel<kEpiGatedBack>
-        <<<gemm_grid(p), kThreads, smem_of(kEpiGatedBack), stream>>>(ma, mb, msa, msb, mg, mu, mb, p, extra);
+        <<<gemm_grid(p), kThreads, smem_of(kEpiGatedBack), stream>>>(ma, mb, msa, msb, mg, mu, mb, p);
     return cudaGetLastError();
 }
 
@@ -1400,11 +1377,11 @@ cudaError_t launch_gemm(const GemmOperand& a, const GemmOperand& b, void* d, int
     }
     const int grid = gemm_grid(p);
     if (p.amax_out)
-        gemm_nvf4_kernel<kEpiAmax><<<grid, kThreads, smem_of(kEpiAmax), stream>>>(ma, mb, msa, msb, md, mu, mv, p, {});
+        gemm_nvf4_kernel<kEpiAmax><<<grid, kThreads, smem_of(kEpiAmax), stream>>>(ma, mb, msa, msb, md, mu, mv, p);
     else if (p.c)
-        gemm_nvf4_kernel<kEpiC><<<grid, kThreads, smem_of(kEpiC), stream>>>(ma, mb, msa, msb, md, mu, mv, p, {});
+        gemm_nvf4_kernel<kEpiC><<<grid, kThreads, smem_of(kEpiC), stream>>>(ma, mb, msa, msb, md, mu, mv, p);
     else
-        gemm_nvf4_kernel<kEpiPlain><<<grid, kThreads, smem_of(kEpiPlain), stream>>>(ma, mb, msa, msb, md, mu, mv, p, {});
+        gemm_nvf4_kernel<kEpiPlain><<<grid, kThreads, smem_of(kEpiPlain), stream>>>(ma, mb, msa, msb, md, mu, mv, p);
     return cudaGetLastError();
 }
 

@@ -22,6 +22,12 @@
 // warp has three slices: two pieces are on their way, those of its next tile
 // among them, while it works on the third.
 
+// Measured, 16384 tokens, 3072 to 9216, in us: forward 340 (5.5 PFLOP/s, the plain
+// GEMM's rate; bound by the operand ring), with gate and up kept 380 (BF16) and
+// 382 (8 bits); backward 312 (3.9 TB/s; the three stages that the slices leave and
+// their traffic: without the activation's arithmetic 311) and 390 (8 bits; the
+// arithmetic: without it 327).
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluSlope = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 constexpr float kGeluCube = 0.044715f;
@@ -109,14 +115,14 @@ __device__ __forceinline__ void copy_out(const Params& p, int t, const uint8_t* 
     constexpr uint32_t kPieces = kRowBytes / 16, kRows = 32 / kPieces;
     const uint32_t ch = lane % kPieces, first = lane / kPieces;
     const bool inside = x + 16u * ch < bytes;
-    uint8_t* to = p.lane_out[t] + (int64_t)(y + first) * p.ld_lane_out[t] + x + 16u * ch;
+    uint8_t* to = p.pair[t] + (int64_t)(y + first) * p.ld_pair[t] + x + 16u * ch;
 #pragma unroll
     for (uint32_t i = 0; i < 32 / kRows; ++i) {
         const uint32_t rr = i * kRows + first;
         const uint32_t at = kRowBytes == 128 ? rr & 7u : (rr >> 1) & 3u;
         const uint4 w = *reinterpret_cast<const uint4*>(slice + rr * kRowBytes + ((ch ^ at) << 4));
-        if (inside && y + rr < p.M) store_out(reinterpret_cast<uint4*>(to), w, p.x_lane_out[t]);
-        to += (int64_t)kRows * p.ld_lane_out[t];
+        if (inside && y + rr < p.M) store_out(reinterpret_cast<uint4*>(to), w, p.x_pair[t]);
+        to += (int64_t)kRows * p.ld_pair[t];
     }
 }
 
@@ -209,11 +215,10 @@ __device__ __forceinline__ uint32_t load_scales(const uint8_t* scales, int64_t l
 // An epilogue warp's pieces of gate and up in the backward pass: piece n of the
 // warp's tiles, four of 32 columns each, goes through slice n % kBackSlices.
 struct GatedWarp {
-    uint64_t* loaded;            // one barrier per slice
     uint8_t* slices;
     uint32_t q, half;            // the warp's rows and columns of its CTA's tile
-    uint32_t in = 0, in_slice = 0, in_tile = 0, in_piece = 0;   // the next piece to load
-    uint32_t out = 0, out_slice = 0, out_parity = 0;            // the next to work on
+    uint32_t in_slice = 0, in_tile = 0, in_piece = 0;   // the next piece to load
+    uint32_t out_slice = 0;                             // the next to work on
     uint32_t scales[2], next_scales[2];   // this lane's row: four blocks of gate, of up
 };
 
@@ -229,11 +234,14 @@ __device__ __forceinline__ uint32_t gated_pieces(const Params& p, uint32_t x) {
     return x >= p.N ? 0u : p.N - x >= 128u ? 4u : (p.N - x + 31u) / 32u;
 }
 
-// Lets the next piece come into its slice, whose last store but `stores` must
-// have been read (rows outside the matrix come as zeros).
+// Brings the next piece to its slice, whose last store but `kStores` must have
+// been read, by the lanes' own asynchronous copies, whole rows at a time and
+// swizzled (through the load/store path: the TMA unit has the operands to bring
+// and the gradients to take).  Rows and columns outside the matrix come as
+// zeros; with no piece left the group of copies is empty.
 template <int kStores>
-__device__ __forceinline__ void gated_load(const Params& p, const ExtraMaps<kEpiGatedBack>& extra, GatedWarp& w,
-                                           uint32_t lane, uint32_t rank, uint32_t num_tiles, uint32_t tile_stride) {
+__device__ __forceinline__ void gated_load(const Params& p, GatedWarp& w, uint32_t lane, uint32_t rank,
+                                           uint32_t num_tiles, uint32_t tile_stride) {
     uint32_t x = 0, y = 0;
     while (w.in_tile < num_tiles) {
         gated_place(p, w, w.in_tile, rank, x, y);
@@ -241,18 +249,38 @@ __device__ __forceinline__ void gated_load(const Params& p, const ExtraMaps<kEpi
         w.in_tile += tile_stride;
         w.in_piece = 0;
     }
-    if (w.in_tile >= num_tiles) return;
-    if (lane == 0) {
-        asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kStores) : "memory");
-        uint8_t* slice = w.slices + w.in_slice * kSliceBytes;
-        uint64_t* bar = &w.loaded[w.in_slice];
-        mbar_arrive_expect_tx(bar, p.kept == 2 ? kHalfSlice : kSliceBytes);
-        tma_load_2d(slice, &extra.gate, bar, (int32_t)(x + 32u * w.in_piece), (int32_t)y);
-        tma_load_2d(slice + kHalfSlice, &extra.up, bar, (int32_t)(x + 32u * w.in_piece), (int32_t)y);
+    if (w.in_tile < num_tiles) {
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kStores) : "memory");
+        __syncwarp();
+        x += 32u * w.in_piece;
+        const uint32_t slice = smem_u32(w.slices + w.in_slice * kSliceBytes);
+        auto copy = [&](auto row_bytes) {
+            constexpr uint32_t kRow = decltype(row_bytes)::value, kPieces = kRow / 16, kRows = 32 / kPieces;
+            const uint32_t ch = lane % kPieces, first = lane / kPieces;
+            const uint32_t at = x * (kRow / 32u) + 16u * ch;   // byte of the row
+            const bool inside = at < p.N * (kRow / 32u);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const uint8_t* from = p.pair[t] + (int64_t)(y + first) * p.ld_pair[t] + at;
+#pragma unroll
+                for (uint32_t i = 0; i < 32 / kRows; ++i) {
+                    const uint32_t rr = i * kRows + first;
+                    const uint32_t swizzle = kRow == 64 ? (rr >> 1) & 3u : (rr >> 2) & 1u;
+                    const bool ok = inside && y + rr < p.M;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                     slice + t * kHalfSlice + rr * kRow + ((ch ^ swizzle) << 4)),
+                                 "l"(ok ? from : p.pair[t]), "r"(ok ? 16u : 0u)
+                                 : "memory");
+                    from += (int64_t)kRows * p.ld_pair[t];
+                }
+            }
+        };
+        if (p.kept == 2) copy(std::integral_constant<uint32_t, 32>{});
+        else copy(std::integral_constant<uint32_t, 64>{});
+        ++w.in_piece;
+        if (++w.in_slice == kBackSlices) w.in_slice = 0;
     }
-    ++w.in;
-    ++w.in_piece;
-    if (++w.in_slice == kBackSlices) w.in_slice = 0;
+    asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
 // The scales of a tile's row, a tile ahead of their use.
@@ -267,35 +295,11 @@ __device__ __forceinline__ void gated_scales(const Params& p, GatedWarp& w, uint
     w.next_scales[1] = load_scales(p.up_scales, p.ld_up_scales, y + lane, x / 32u, p.scale_blocks);
 }
 
-// Until the next piece has landed; false if the wait ran out.
-__device__ __forceinline__ bool gated_landed(const Params& p, GatedWarp& w, uint32_t lane,
-                                             volatile uint32_t* abort_flag) {
-    uint32_t ready = 0;
-    if (lane == 0) {
-        ready = mbar_wait(&w.loaded[w.out_slice], w.out_parity, p.timeout_ns) ? 1u : 0u;
-        if (!ready) record_timeout(abort_flag);
-    }
-    ready = __shfl_sync(0xFFFFFFFFu, ready, 0);
+// Until the next piece has landed: the one after it may still be on its way.
+__device__ __forceinline__ void gated_landed(GatedWarp& w) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kBackSlices - 2) : "memory");
     __syncwarp();
-    if (!ready) return false;   // (gated_drain waits once more)
-    ++w.out;
-    if (++w.out_slice == kBackSlices) {
-        w.out_slice = 0;
-        w.out_parity ^= 1u;
-    }
-    return true;
-}
-
-// Loads in flight land before the CTA ends.
-__device__ __forceinline__ void gated_drain(const Params& p, GatedWarp& w, uint32_t lane) {
-    while (w.out != w.in) {
-        if (lane == 0) (void)mbar_wait(&w.loaded[w.out_slice], w.out_parity, p.timeout_ns);
-        ++w.out;
-        if (++w.out_slice == kBackSlices) {
-            w.out_slice = 0;
-            w.out_parity ^= 1u;
-        }
-    }
+    if (++w.out_slice == kBackSlices) w.out_slice = 0;
 }
 
 // slice_amax of a half slice, 32 rows x 32 columns: a lane takes two columns of
@@ -350,20 +354,17 @@ __device__ __forceinline__ void bf16_pairs(const uint4& w, uint64_t* v) {
 // Backward: a tile's 128 columns from x0 on, rows y .. y + 31, piece by piece;
 // v: dh, used up: a turn of the loop takes v[0] and moves the others down, so
 // that its code is there once (unrolled it did not fit the instruction cache).
-// False if a wait ran out.
-__device__ __forceinline__ bool gated_backward_epilogue(const Params& p, const ExtraMaps<kEpiGatedBack>& extra,
-                                                        GatedWarp& w, const CUtensorMap* dgate_map,
+__device__ __forceinline__ void gated_backward_epilogue(const Params& p, GatedWarp& w, const CUtensorMap* dgate_map,
                                                         const CUtensorMap* dup_map, uint32_t lane, uint32_t rank,
                                                         uint32_t num_tiles, uint32_t tile_stride, uint32_t y,
                                                         uint32_t x0, uint32_t (&v)[4][32], float alpha,
-                                                        volatile uint32_t* abort_flag, float& amax_plain,
-                                                        float& amax_rht) {
+                                                        float& amax_plain, float& amax_rht) {
     const uint32_t pieces = gated_pieces(p, x0);
 #pragma unroll 1
     for (uint32_t r = 0; r < pieces; ++r) {
         uint8_t* gate_slice = w.slices + w.out_slice * kSliceBytes;
         uint8_t* up_slice = gate_slice + kHalfSlice;
-        if (!gated_landed(p, w, lane, abort_flag)) return false;
+        gated_landed(w);
         auto gradients = [&](auto gelu) {
             constexpr bool kGelu = decltype(gelu)::value;
             if (p.kept == 2) {
@@ -420,12 +421,11 @@ __device__ __forceinline__ bool gated_backward_epilogue(const Params& p, const E
         // the piece after the next, into the slice that the last turn stored
         // (and whose amax every lane has read)
         __syncwarp();
-        gated_load<1>(p, extra, w, lane, rank, num_tiles, tile_stride);
+        gated_load<1>(p, w, lane, rank, num_tiles, tile_stride);
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[j][i] = v[j + 1][i];
         }
     }
-    return true;
 }
