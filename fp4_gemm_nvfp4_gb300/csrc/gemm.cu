@@ -112,6 +112,7 @@ __host__ __device__ constexpr size_t smem_of(int mode) {
 
 static_assert(kStageBytes % 1024 == 0, "stages must keep 1024-byte alignment for the 128B swizzle");
 static_assert(kSfCol0 + stages_of(kEpiPlain) * kSfColsPerStage <= kTmemCols, "tensor memory budget");
+static_assert(smem_of(kEpiGated) == smem_of(kEpiGatedKept));
 static_assert(smem_of(kEpiPlain) <= 232448 && smem_of(kEpiGated) <= 232448 && smem_of(kEpiGatedBack) <= 232448,
               "shared memory budget");
 
@@ -448,6 +449,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_before();
     cluster_sync();
     tc_fence_after();
+    if constexpr (kGated || kGatedBack) {
+        // what precedes needs nothing of the kernel before
+        wait_for_prior_grid();
+        let_next_grid_start();
+    }
     const uint32_t tmem = *tmem_slot;
     const uint32_t num_tiles = p.m_tiles * p.n_tiles;
     const uint32_t first_tile = cluster_id_x(), tile_stride = num_clusters_x();
@@ -1296,13 +1302,8 @@ cudaError_t launch_gemm_gated(const GemmOperand& a, const GemmOperand& gate, con
     p.sgu = up.sg;
     p.tma_store = 1;
     if (amax_out && (e = set_amax(p, amax_out, rht_mask, stream)) != cudaSuccess) return e;
-    if (gate_kept)
-        gemm_nvf4_kernel<kEpiGatedKept>
-            <<<gemm_grid(p), kThreads, smem_of(kEpiGatedKept), stream>>>(ma, mg, msa, msg, mh, mu, msu, p);
-    else
-        gemm_nvf4_kernel<kEpiGated>
-            <<<gemm_grid(p), kThreads, smem_of(kEpiGated), stream>>>(ma, mg, msa, msg, mh, mu, msu, p);
-    return cudaGetLastError();
+    return launch_early(gate_kept ? gemm_nvf4_kernel<kEpiGatedKept> : gemm_nvf4_kernel<kEpiGated>, dim3(gemm_grid(p)),
+                        dim3(kThreads), smem_of(kEpiGated), stream, ma, mg, msa, msg, mh, mu, msu, p);
 }
 
 cudaError_t launch_gemm_gated_backward(const GemmOperand& a, const GemmOperand& b, bool gelu,
@@ -1321,9 +1322,8 @@ cudaError_t launch_gemm_gated_backward(const GemmOperand& a, const GemmOperand& 
     p.gelu = gelu ? 1 : 0;
     p.tma_store = 1;
     if (amax_out && (e = set_amax(p, amax_out, rht_mask, stream)) != cudaSuccess) return e;
-    gemm_nvf4_kernel<kEpiGatedBack>
-        <<<gemm_grid(p), kThreads, smem_of(kEpiGatedBack), stream>>>(ma, mb, msa, msb, mg, mu, mb, p);
-    return cudaGetLastError();
+    return launch_early(gemm_nvf4_kernel<kEpiGatedBack>, dim3(gemm_grid(p)), dim3(kThreads), smem_of(kEpiGatedBack),
+                        stream, ma, mb, msa, msb, mg, mu, mb, p);
 }
 
 cudaError_t launch_gemm(const GemmOperand& a, const GemmOperand& b, void* d, int64_t ldd, bool out_fp32,
