@@ -1284,6 +1284,15 @@ void set_checkpoints(Params& p, const CheckpointView& gate, const CheckpointView
     }
 }
 
+// The gated kernels start under the tail of the kernel before, but for the
+// clearing of the amaxes, which is none.
+template <typename Kernel, typename... Maps>
+cudaError_t launch_gated(Kernel* kernel, int mode, const Params& p, cudaStream_t stream, const Maps&... maps) {
+    if (!p.amax_out) return launch_early(kernel, dim3(gemm_grid(p)), dim3(kThreads), smem_of(mode), stream, maps..., p);
+    kernel<<<gemm_grid(p), kThreads, smem_of(mode), stream>>>(maps..., p);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_gemm_gated(const GemmOperand& a, const GemmOperand& gate, const GemmOperand& up, bool gelu, void* h,
@@ -1302,8 +1311,8 @@ cudaError_t launch_gemm_gated(const GemmOperand& a, const GemmOperand& gate, con
     p.sgu = up.sg;
     p.tma_store = 1;
     if (amax_out && (e = set_amax(p, amax_out, rht_mask, stream)) != cudaSuccess) return e;
-    return launch_early(gate_kept ? gemm_nvf4_kernel<kEpiGatedKept> : gemm_nvf4_kernel<kEpiGated>, dim3(gemm_grid(p)),
-                        dim3(kThreads), smem_of(kEpiGated), stream, ma, mg, msa, msg, mh, mu, msu, p);
+    return launch_gated(gate_kept ? gemm_nvf4_kernel<kEpiGatedKept> : gemm_nvf4_kernel<kEpiGated>, kEpiGated, p, stream,
+                        ma, mg, msa, msg, mh, mu, msu);
 }
 
 cudaError_t launch_gemm_gated_backward(const GemmOperand& a, const GemmOperand& b, bool gelu,
@@ -1322,8 +1331,7 @@ cudaError_t launch_gemm_gated_backward(const GemmOperand& a, const GemmOperand& 
     p.gelu = gelu ? 1 : 0;
     p.tma_store = 1;
     if (amax_out && (e = set_amax(p, amax_out, rht_mask, stream)) != cudaSuccess) return e;
-    return launch_early(gemm_nvf4_kernel<kEpiGatedBack>, dim3(gemm_grid(p)), dim3(kThreads), smem_of(kEpiGatedBack),
-                        stream, ma, mb, msa, msb, mg, mu, mb, p);
+    return launch_gated(gemm_nvf4_kernel<kEpiGatedBack>, kEpiGatedBack, p, stream, ma, mb, msa, msb, mg, mu, mb);
 }
 
 cudaError_t launch_gemm(const GemmOperand& a, const GemmOperand& b, void* d, int64_t ldd, bool out_fp32,

@@ -165,6 +165,20 @@ def test_amaxes_feed_the_quantizer(M, K, N):
             assert torch.equal(p.codes[:, :n], q.codes[:, :n]) and torch.equal(p.scales, q.scales)
 
 
+def test_amaxes_of_calls_in_a_row():
+    """A large product and then a small one into the same two floats, without a wait between."""
+    M, K, N = 512, 512, 768
+    _, bg, bu, dy, wd = _case(M, K, N, 12)
+    big, small = _operand(M, K, 13, 50.0), _operand(M, K, 14, 0.01)
+    _, gate, up = ops.gemm_gated(small, bg, bu, keep="bf16")
+    amax, dmax = (torch.empty(2, device="cuda") for _ in range(2))
+    for _ in range(10):
+        for a in (big, small):
+            h, _, _ = ops.gemm_gated(a, bg, bu, amax=amax, rht_mask=MASK)
+            dgu = ops.gemm_gated_backward(dy, wd, gate, up, amax=dmax, rht_mask=MASK)
+        assert amax[0] == h.abs().max().float() and dmax[0] == dgu.abs().max().float()
+
+
 def test_halves_of_one_weight_matrix():
     M, K, N = 200, 512, 384
     g = torch.Generator(device="cuda").manual_seed(3)
