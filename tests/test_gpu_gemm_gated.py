@@ -137,6 +137,40 @@ def test_far_gates(kind):
             _check_backward(dy, wd, gate, up, ops.gemm_gated_backward(dy, wd, gate, up, activation=kind), kind)
 
 
+def test_gates_past_the_type_are_kept_as_nan():
+    """Gates around FP32's end: what overflows is kept as NaN and leaves its block's scale to the others, what
+    reaches 2^127 takes the last scale."""
+    a, bg, bu = _operand(64, 256, 5, 3e37), _operand(160, 256, 6, 0.5), _operand(160, 256, 7, 1e-30)   # (finite in bf16)
+    _, gate, _ = ops.gemm_gated(a, bg, bu, keep="e4m3")
+    (g, ge), got = _product(a, bg), _values(gate)
+    limit = float(torch.finfo(torch.float32).max)
+    over, under = g.abs() - ge > limit, g.abs() + ge < limit
+    assert over.any() and (g.abs() > 2.0 ** 127)[under].any()
+    assert torch.isnan(got[over]).all() and torch.isfinite(got[under]).all()
+    # 1.875 2^127 stands for what would round to 2^128
+    want = g.clamp(-1.875 * 2.0 ** 127, 1.875 * 2.0 ** 127)
+    b = gate.scales[:, :5].double().repeat_interleave(32, 1)
+    tol = ge + 2.0 ** -4 * (want.abs() + ge) + torch.exp2(b - 137)
+    assert ((got - want).abs() <= tol)[under].all()
+
+
+@pytest.mark.parametrize("keep", ["bf16", "e4m3"])
+def test_a_nan_that_is_kept_stays_alone(keep):
+    _, _, _, dy, wd = _case(70, 128, 112, 8)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x, y = (torch.randn(70, 112, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    kept = (lambda t: t) if keep == "bf16" else ops.checkpoint_encode
+    clean = ops.gemm_gated_backward(dy, wd, kept(x), kept(y))
+    x[3, 40], y[69, 111] = float("nan"), float("nan")
+    dgu = ops.gemm_gated_backward(dy, wd, kept(x), kept(y))
+    bad = torch.zeros_like(dgu, dtype=torch.bool)
+    bad[3, 40] = bad[3, 152] = bad[69, 111] = True
+    assert torch.isnan(dgu[bad]).all()
+    if keep == "bf16":   # (in 8 bits the block's other values may have another scale)
+        assert torch.equal(dgu[~bad], clean[~bad])
+    assert torch.isfinite(dgu[~bad]).all()
+
+
 def test_zeros():
     a, bg, bu, dy, wd = _case(48, 256, 96)
     zero = _operand(48, 256, 0, 0.0)
