@@ -4,9 +4,10 @@
 // Bound by HBM: 3.03 bytes per value each way.  A lane takes 8 columns (16
 // bytes of BF16, 8 of codes), four lanes a 1x32 block, whose maximum takes two
 // shuffles; a warp's accesses are whole lines.  A lane loads kAhead pieces, a
-// grid apart, before it computes (bytes in flight).  16384 x 9216: 83 and 80 us
-// (5.5 and 5.7 TB/s, 81 and 85 % of a copy); maxima of packed halves instead of
-// FP32 values took encode from 130.
+// grid apart, before it computes (bytes in flight).  16384 x 9216: 74 us each way
+// (6.2 TB/s, 91 % of a copy).  Six blocks per SM with four pieces ahead 83 and 80,
+// eight with one or three 82 and 76, 80 and 73, a grid without a loop 78 and 76;
+// maxima of FP32 values instead of packed halves 130.
 #include <cuda_runtime.h>
 
 #include "bounds.cuh"
@@ -18,8 +19,8 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;
-constexpr int kBlocksPerSm = 6;
+constexpr int kAhead = 2;
+constexpr int kBlocksPerSm = 8;
 
 struct Params {
     const void* in;
