@@ -581,13 +581,14 @@ def checkpoint_decode(kept: Checkpoint, out_dtype=torch.bfloat16, out: Optional[
     rows, cols = kept.rows, kept.cols
     if kept.scales is None:
         raise ValueError("kept: an 8-bit checkpoint expected")
+    what, dtype = ("out_dtype", out_dtype) if out is None else ("out", out.dtype)
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{what}: bfloat16 or float32 expected, got {dtype}")
     if out is None:
-        out = torch.empty((rows, cols), dtype=out_dtype, device=kept.data.device)
-    elif out.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"out: bfloat16 or float32 expected, got {out.dtype}")
-    ptr, ld = _matrix(out, rows, cols, out.dtype, "out")
+        out = torch.empty((rows, cols), dtype=dtype, device=kept.data.device)
+    ptr, ld = _matrix(out, rows, cols, dtype, "out")
     _check_here(kept.data, kept.scales, out)
-    dt = capi.NVFP4_OUT_FP32 if out.dtype == torch.float32 else capi.NVFP4_OUT_BF16
+    dt = capi.NVFP4_OUT_FP32 if dtype == torch.float32 else capi.NVFP4_OUT_BF16
     capi.check(capi.nvfp4_checkpoint_decode(kept.struct(), rows, cols, ptr, ld, dt, stream_handle(stream)),
                "nvfp4_checkpoint_decode")
     return out
