@@ -536,6 +536,18 @@ def _matrix(x: torch.Tensor, rows: int, cols: int, dtype, what: str) -> Tuple[in
     return x.data_ptr(), ld if rows > 1 else (cols + 15) // 16 * 16
 
 
+def _as_kept(x: Union[torch.Tensor, Checkpoint], rows: int, cols: int, what: str) -> Checkpoint:
+    """What stands for a kept matrix of this size: a tensor of it, or a Checkpoint that says so (whose rows may
+    be padded)."""
+    if isinstance(x, Checkpoint):
+        size = x.rows, x.cols
+    else:
+        size, x = tuple(x.shape), Checkpoint(x, None, rows, cols)
+    if size != (rows, cols):
+        raise ValueError(f"{what}: [{rows}, {cols}] expected, got {list(size)}")
+    return x
+
+
 def _check_here(*tensors: Optional[torch.Tensor]) -> None:
     """Every tensor on the current device, where the kernels run."""
     here = None
@@ -655,10 +667,7 @@ def gemm_gated_backward(dy: NVFP4Operand, w_down: NVFP4Operand, gate: Union[torc
     act = _activation(activation)
     _check_amax(amax, rht_mask)
     rows, cols = dy.rows, w_down.rows
-    gate, up = (x if isinstance(x, Checkpoint) else Checkpoint(x, None, rows, cols) for x in (gate, up))
-    for x, what in ((gate, "gate"), (up, "up")):
-        if (x.rows, x.cols) != (rows, cols):
-            raise ValueError(f"{what}: [{rows}, {cols}] expected, got [{x.rows}, {x.cols}]")
+    gate, up = _as_kept(gate, rows, cols, "gate"), _as_kept(up, rows, cols, "up")
     if out is None:
         out = torch.empty((rows, 2 * cols), dtype=torch.bfloat16, device=dy.codes.device)
     ptr, ld = _matrix(out, rows, 2 * cols, torch.bfloat16, "out")
@@ -780,10 +789,7 @@ def block_norm_backward(dresidual_out: Optional[torch.Tensor], dnormed: Optional
     dr, ld_dr = _matrix(dresidual, tokens, width, kind, "dresidual")
     kept = data = scales = None
     if branch is not None:
-        if not isinstance(branch, Checkpoint):
-            branch = Checkpoint(branch, None, tokens, width)
-        if (branch.rows, branch.cols) != (tokens, width):
-            raise ValueError(f"branch: [{tokens}, {width}] expected, got [{branch.rows}, {branch.cols}]")
+        branch = _as_kept(branch, tokens, width, "branch")
         kept, data, scales = branch.struct(), branch.data, branch.scales
         if dbranch is None:
             dbranch = torch.empty((tokens, width), dtype=torch.bfloat16, device=device)
