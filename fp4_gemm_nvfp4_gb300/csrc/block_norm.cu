@@ -459,13 +459,16 @@ __global__ void __launch_bounds__(most_threads(kClass, true), blocks_of(kClass, 
             }
 #pragma unroll
             for (int j = 0; j < kUsedSums; ++j) s[j] = __shfl_sync(kAll, t, j);
+            // (a row whose squares overflow has 1 / rms = 0, and nothing goes back
+            // through that norm whatever its other sums are: infinities, too)
             if (has_pre) {
                 rq = rsqrtf(fmaf(s[kSumX2], inv_h, p.a.eps));
-                along = rq * rq * (s[kSumGx] * inv_h) * rq;
+                along = rq == 0.0f ? 0.0f : rq * rq * (s[kSumGx] * inv_h) * rq;
             }
             if (has_post) {
                 rp = rsqrtf(fmaf(s[kSumY2], inv_h, p.a.eps));
-                mean = rp * rp * (fmaf(rq, s[kSumGy], s[kSumRy]) - along * s[kSumXy]) * inv_h;
+                const float back = along == 0.0f ? 0.0f : along * s[kSumXy];
+                mean = rp == 0.0f ? 0.0f : rp * rp * (fmaf(rq, s[kSumGy], s[kSumRy]) - back) * inv_h;
             }
         }
         ++turn;

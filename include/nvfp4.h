@@ -646,7 +646,8 @@ NVFP4_API nvfp4_status nvfp4_block_norm(const nvfp4_block_norm_desc *desc, const
  *  workspace    nvfp4_block_norm_backward_workspace_size(width) bytes, 16-byte
  *               aligned.
  * The weights' gradients sum over every token, padding included; sums run in a
- * fixed order: equal inputs give equal bits.
+ * fixed order: equal inputs give equal bits.  A row that the forward pass norms
+ * to 0 passes nothing back through that norm.
  */
 NVFP4_API size_t nvfp4_block_norm_backward_workspace_size(int32_t width);
 NVFP4_API nvfp4_status nvfp4_block_norm_backward(const nvfp4_block_norm_desc *desc, const void *dresidual_out,
