@@ -25,8 +25,9 @@
 // it copies to its own places in shared memory ahead of time (cp.async; no
 // other thread reads them, so no barrier stands between).  Columns are worked
 // on in packed pairs.  Forward 8 bytes per element (BF16 residual), backward 12;
-// 16384 x 3072 with a gate per channel 71 us (5.6 TB/s, HBM) and 115 us (5.3 TB/s;
-// the instructions and the exchange of a row; 6.4 TB/s with a gate per token).
+// 16384 x 3072 with a gate per channel 71 us (5.6 TB/s, HBM) and 116 us (5.2 TB/s;
+// the instructions and the exchange of a row; 6.4 TB/s with a gate per token);
+// 16384 x 8192 172 us (6.2 TB/s) and 272 us (5.9 TB/s).
 #include <cuda_runtime.h>
 
 #include "bounds.cuh"
@@ -460,7 +461,8 @@ __global__ void __launch_bounds__(most_threads(kClass, true), blocks_of(kClass, 
 #pragma unroll
             for (int j = 0; j < kUsedSums; ++j) s[j] = __shfl_sync(kAll, t, j);
             // (a row whose squares overflow has 1 / rms = 0, and nothing goes back
-            // through that norm whatever its other sums are: infinities, too)
+            // through that norm whatever its other sums are: infinities, too;
+            // 0 to 1 % of the pass, as by a branch or by clearing the sums)
             if (has_pre) {
                 rq = rsqrtf(fmaf(s[kSumX2], inv_h, p.a.eps));
                 along = rq == 0.0f ? 0.0f : rq * rq * (s[kSumGx] * inv_h) * rq;
@@ -552,7 +554,10 @@ __global__ void __launch_bounds__(1024) weight_kernel(const float* partials, uin
 constexpr size_t kSmemOfSm = 227 * 1024, kSmemBesides = 4 * 1024;
 
 // Rows ahead (as many as the SM's shared memory holds for the blocks that its
-// registers hold, two at least), blocks resident and bytes of a block's ring.
+// registers hold, fewer blocks where there would not be two rows), blocks resident
+// and bytes of a block's ring.  One block may hold a single row: backward with an
+// FP32 residual and a gate per token from 7688 columns on a row takes 112 KiB, and
+// nothing is on its way while it is worked on.
 struct Residence {
     uint32_t ahead;
     int blocks;

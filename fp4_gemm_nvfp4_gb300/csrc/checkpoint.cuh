@@ -4,7 +4,8 @@
 // finite magnitude to at most 448 (E4M3's largest value).
 //
 // A power of two makes x / scale and code * scale exact, so the code's rounding
-// (3 bits after the leading one: at most 2^-4 of the value) is the only one.
+// (3 bits after the leading one: at most 2^-4 of the value, or half the smallest
+// code, 2^(b - 137), where that is more) is the only one.
 // From b = 10 on the smallest code, 2^-9, stands for 2^-126: every kept value is
 // a normal FP32 and BF16 number.  At the other end 2^128 is none: what would
 // round to it (magnitudes past 1.9375 * 2^127) is kept as 1.875 * 2^127.

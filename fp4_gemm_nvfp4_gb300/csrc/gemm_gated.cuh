@@ -22,11 +22,12 @@
 // warp has three slices: two pieces are on their way, those of its next tile
 // among them, while it works on the third.
 
-// Measured, 16384 tokens, 3072 to 9216, in us: forward 340 (5.5 PFLOP/s, the plain
-// GEMM's rate; bound by the operand ring), with gate and up kept 380 (BF16) and
-// 382 (8 bits); backward 312 (3.9 TB/s; the three stages that the slices leave and
-// their traffic: without the activation's arithmetic 311) and 390 (8 bits; the
-// arithmetic: without it 327).
+// Measured, 16384 tokens, 3072 to 9216, in us, calls of one kind in a row: forward
+// 338 (5.5 PFLOP/s, the plain GEMM's rate; bound by the operand ring), with gate and
+// up kept 378 (BF16) and 379 (8 bits); backward 311 (3.9 TB/s; the three stages that
+// the slices leave and their traffic: without the activation's arithmetic 311) and
+// 383 (8 bits; the arithmetic: without it 327).  With the amaxes 355 forward, 360 and
+// 460 backward.
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluSlope = 1.5957691216057308f;   // 2 sqrt(2 / pi)
